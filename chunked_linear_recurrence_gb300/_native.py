@@ -28,7 +28,10 @@ EXPORTS = ("sf_last_error", "sf_version", "sf_gdn_fwd_workspace", "sf_gdn_chunk_
            "sf_gdn_chunk_bwd_noalloc_status",
            "sf_gdn_reverse_summary_workspace", "sf_gdn_segment_reverse_summary",
            "sf_state_scan_reverse", "sf_validate_cu_seqlens", "sf_workspace_status",
-           "sf_testing_inject_timeout")
+           "sf_testing_inject_timeout",
+           "sf_linattn_fwd_workspace", "sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd",
+           "sf_linattn_bwd_workspace", "sf_linattn_chunk_bwd", "sf_linattn_step", "sf_gdn_step",
+           "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd_workspace", "sf_qk_norm_rope_bwd")
 
 
 class SfError(RuntimeError):
@@ -41,6 +44,15 @@ class sf_gdn_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("K", ctypes.c_int), ("V", ctypes.c_int), ("N", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("HK", ctypes.c_int)]
+
+
+class sf_qk_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("H", ctypes.c_int), ("HK", ctypes.c_int),
+                ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("norm", ctypes.c_int),
+                ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("table_rows", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4),
+                ("rows_stride_q", ctypes.c_int64), ("rows_stride_k", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -84,7 +96,26 @@ def load(path: str = LIB_PATH):
         lib.sf_workspace_status.argtypes = [vp, vp]
         lib.sf_gdn_chunk_bwd_noalloc_status.argtypes = [vp]
         lib.sf_testing_inject_timeout.argtypes = [ctypes.c_longlong, ctypes.c_longlong]
-        for f in ("sf_gdn_chunk_fwd", "sf_gdn_paged_chunk_fwd", "sf_gdn_segment_summary",
+        qp = ctypes.POINTER(sf_qk_shape)
+        lib.sf_linattn_fwd_workspace.argtypes = [sp, I]
+        lib.sf_linattn_fwd_workspace.restype = sz
+        lib.sf_linattn_bwd_workspace.argtypes = [sp, I]
+        lib.sf_linattn_bwd_workspace.restype = sz
+        lib.sf_linattn_chunk_fwd.argtypes = [sp, vp, vp, vp, vp, vp, vp, I, vp, vp, vp, sz, vp]
+        lib.sf_linattn_paged_chunk_fwd.argtypes = [sp, vp, vp, vp, vp, vp, I, vp, vp, vp, vp, vp,
+                                                   sz, vp]
+        lib.sf_linattn_chunk_bwd.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                             vp, sz, vp]
+        lib.sf_linattn_step.argtypes = [sp, vp, vp, vp, vp, vp, I, vp, vp, vp]
+        lib.sf_gdn_step.argtypes = [sp, vp, vp, vp, vp, vp, vp, I, vp, vp, vp]
+        lib.sf_qk_norm_rope_fwd.argtypes = [qp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.sf_qk_norm_rope_bwd_workspace.argtypes = [qp]
+        lib.sf_qk_norm_rope_bwd_workspace.restype = sz
+        lib.sf_qk_norm_rope_bwd.argtypes = [qp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                            sz, vp]
+        for f in ("sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd", "sf_linattn_chunk_bwd",
+                  "sf_linattn_step", "sf_gdn_step", "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd",
+                  "sf_gdn_chunk_fwd", "sf_gdn_paged_chunk_fwd", "sf_gdn_segment_summary",
                   "sf_state_scan",
                   "sf_gdn_chunk_bwd", "sf_gdn_chunk_bwd_noalloc",
                   "sf_gdn_chunk_bwd_noalloc_status", "sf_testing_inject_timeout",

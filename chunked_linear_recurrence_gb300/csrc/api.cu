@@ -1,11 +1,6 @@
 // api.cu -- the C ABI (include/sf_gdn.h): argument checks, workspace layout and
 // kernel dispatch.  No entry point allocates memory or synchronises the host
 // (except the two documented synchronous helpers at the end).
-#if __has_include(<nvtx3/nvToolsExt.h>)
-#include <nvtx3/nvToolsExt.h>
-#define SF_HAVE_NVTX 1
-#endif
-
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -47,19 +42,7 @@ sf_status sfg::report(sf_status s, const char* fmt, ...) {
 
 namespace {
 
-// An NVTX range around each compute entry point, so that timelines (Nsight Systems, ncu's
-// range filters) show the library's calls; without a tool attached it does nothing.
-// (Without the NVTX headers it compiles to nothing.)
-struct Range {
-#ifdef SF_HAVE_NVTX
-  explicit Range(const char* name) { nvtxRangePushA(name); }
-  ~Range() { nvtxRangePop(); }
-#else
-  explicit Range(const char*) {}
-#endif
-  Range(const Range&) = delete;
-  Range& operator=(const Range&) = delete;
-};
+using sfg::Range;
 
 sf_status cuda_fail(cudaError_t e, const char* where) {
   return fail(SF_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));

@@ -1,0 +1,385 @@
+// linattn_api.cu -- the C ABI of include/sf_linattn.h: argument checks, workspace layout and
+// dispatch.  No entry point allocates memory or synchronises the host.
+#include <cmath>
+
+#include "../../include/sf_linattn.h"
+#include "api_internal.cuh"
+#include "linattn.cuh"
+#include "simt_chunk.cuh"
+
+using sfg::report;
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+constexpr int kSms = 152;   // the segment rule's machine: workspace sizes do not ask the device
+
+size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+sf_status cuda_status(cudaError_t e, const char* fn) {
+  return e == cudaSuccess ? SF_OK : report(SF_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+int eff_hk(const sf_gdn_shape* s) { return s->HK > 0 ? s->HK : s->H; }
+float eff_scale(const sf_gdn_shape* s) {
+  return s->scale > 0.f ? s->scale : 1.0f / std::sqrt((float)s->K);
+}
+
+// Head counts, head size and type: what the token streams and the steps share.
+sf_status check_heads(const sf_gdn_shape* s, const char* fn) {
+  if (!s) return report(SF_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  if (s->H < 1 || s->K < 1 || s->V < 1)
+    return report(SF_ERR_INVALID_ARG, "%s: need H>=1, K>=1, V>=1 (got H=%d K=%d V=%d)", fn, s->H,
+                  s->K, s->V);
+  if (s->dtype != SF_F32 && s->dtype != SF_BF16)
+    return report(SF_ERR_INVALID_ARG, "%s: dtype must be SF_F32 or SF_BF16", fn);
+  if (s->HK < 0 || s->H % (s->HK > 0 ? s->HK : s->H))
+    return report(SF_ERR_INVALID_ARG, "%s: query/key heads HK = %d must divide H = %d", fn, s->HK,
+                  s->H);
+  if (s->K != s->V || (s->K != 64 && s->K != 128))
+    return report(SF_ERR_UNSUPPORTED, "%s: head sizes K == V in {64, 128} only (got K=%d V=%d)", fn,
+                  s->K, s->V);
+  return SF_OK;
+}
+
+sf_status check_tokens(const sf_gdn_shape* s, bool packed, const char* fn) {
+  const sf_status st = check_heads(s, fn);
+  if (st != SF_OK) return st;
+  if (s->B < 1 || s->T < 0)
+    return report(SF_ERR_INVALID_ARG, "%s: need B>=1, T>=0 (got B=%d T=%d)", fn, s->B, s->T);
+  const long long elems = (long long)s->B * s->T * s->H * s->K;
+  if (elems >= (1LL << 31))
+    return report(SF_ERR_UNSUPPORTED, "%s: tensors need int64 element offsets (%lld elements)", fn,
+                  elems);
+  if (packed) {
+    if (s->B != 1) return report(SF_ERR_INVALID_ARG, "%s: cu_seqlens requires B == 1", fn);
+    if (s->N < 1) return report(SF_ERR_INVALID_ARG, "%s: cu_seqlens requires N >= 1", fn);
+  } else if (s->N != s->B) {
+    return report(SF_ERR_INVALID_ARG, "%s: without cu_seqlens N must equal B (N=%d B=%d)", fn, s->N,
+                  s->B);
+  }
+  return SF_OK;
+}
+
+// Rows of a segment (linattn.cuh), a multiple of 64: as many segments as it takes to give
+// every SM a CTA, none shorter than 256 rows; a walk that needs no cut is one segment.
+int seg_rows(const sf_gdn_shape* s, bool packed, int npass) {
+  const int64_t chains = (int64_t)(packed ? 1 : s->N) * s->H * npass * (s->K / 64);
+  const int64_t want = (kSms + chains - 1) / chains;       // segments of the longest walk
+  int64_t rows = (s->T + want - 1) / want;
+  rows = (rows + 63) / 64 * 64;
+  if (rows < 256) rows = 256;
+  return (int)rows;
+}
+
+struct Layout {
+  int seg;
+  int64_t units;
+  size_t states, gqa, total;   // segment states of one pass; one FP32 [B,T,H,K] area
+};
+
+Layout layout(const sf_gdn_shape* s, bool packed, int npass) {
+  Layout l{0, 0, 0, 0, kStatusBytes};
+  if (!s || s->K < 1 || s->H < 1 || s->T < 0 || s->N < 1) return l;
+  l.seg = seg_rows(s, packed, npass);
+  l.units = sfg::la_units(s->B, s->T, s->N, packed, l.seg);
+  if (l.seg < s->T) l.states = round_up((size_t)l.units * s->H * s->K * s->V * sizeof(float));
+  if (npass > 1 && eff_hk(s) < s->H)
+    l.gqa = round_up((size_t)s->B * s->T * s->H * s->K * sizeof(float));
+  l.total = kStatusBytes + npass * l.states + 2 * l.gqa;
+  return l;
+}
+
+cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, int D,
+                       cudaStream_t cs) {
+  p.seg = l.seg;
+  p.units = (int)l.units;
+  p.status = reinterpret_cast<int*>(ws);
+  for (int i = 0; i < p.npass; ++i)
+    p.pass[i].seg_state =
+        l.states ? reinterpret_cast<float*>(ws + kStatusBytes + i * l.states) : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (l.states) {
+    e = sfg::launch_la_simt(p, bf16, D, /*state_only=*/true, cs);
+    if (e == cudaSuccess) e = sfg::launch_la_carry(p, D, cs);
+  }
+  if (e == cudaSuccess) e = sfg::launch_la_simt(p, bf16, D, /*state_only=*/false, cs);
+  return e;
+}
+
+sf_status chunk_fwd(const char* fn, const sf_gdn_shape* shape, const void* q, const void* k,
+                    const void* v, const float* decay, const float* initial_state,
+                    const int32_t* cu, float* final_state, void* out, float* pool, int num_slots,
+                    const int32_t* idx, const uint8_t* has, void* workspace, size_t ws_bytes,
+                    sf_stream_t stream) {
+  const bool packed = cu != nullptr;
+  const sf_status st = check_tokens(shape, packed, fn);
+  if (st != SF_OK) return st;
+  if (!decay) return report(SF_ERR_INVALID_ARG, "%s: decay must be non-NULL", fn);
+  if (shape->T > 0 && (!q || !k || !v || !out))
+    return report(SF_ERR_INVALID_ARG, "%s: q, k, v and out must be non-NULL", fn);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+      !aligned16(initial_state) || !aligned16(final_state))
+    return report(SF_ERR_INVALID_ARG, "%s: q, k, v, out and states must be 16-byte aligned", fn);
+  const Layout l = layout(shape, packed, 1);
+  if (!workspace || ws_bytes < l.total)
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, l.total);
+  sfg::LaParams p{};
+  p.npass = 1;
+  p.decay = decay;
+  p.cu = cu;
+  p.pool = pool; p.state_idx = idx; p.has_init = has; p.num_slots = num_slots;
+  p.B = shape->B; p.T = shape->T; p.H = shape->H; p.N = shape->N;
+  const float sc = eff_scale(shape);
+  const int hk = eff_hk(shape);
+  p.pass[0] = sfg::LaPass{q, k, v, out, initial_state, final_state, nullptr, hk, hk, shape->H,
+                          0, 0, 0, sc, sc, 1.f};
+  return cuda_status(run_passes(p, l, static_cast<char*>(workspace), shape->dtype == SF_BF16,
+                                shape->K, reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+sf_status step(const char* fn, const sf_gdn_shape* s, const void* q, const void* k, const void* v,
+               const float* decay, const float* gate, const float* beta, float* pool, int num_slots,
+               const int32_t* idx, void* out, sf_stream_t stream) {
+  const sf_status st = check_heads(s, fn);
+  if (st != SF_OK) return st;
+  if (s->N < 0 || num_slots < 0 || (!idx && num_slots < s->N))
+    return report(SF_ERR_INVALID_ARG,
+                  "%s: need N >= 0 and, without state_indices, num_slots >= N (N=%d num_slots=%d)",
+                  fn, s->N, num_slots);
+  if (s->N == 0) return SF_OK;
+  if (!q || !k || !v || !out || !pool || (!decay && (!gate || !beta)))
+    return report(SF_ERR_INVALID_ARG, "%s: inputs, state_cache and out must be non-NULL", fn);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(pool))
+    return report(SF_ERR_INVALID_ARG, "%s: q, k, v, out and state_cache must be 16-byte aligned", fn);
+  if ((long long)s->N * s->H * (s->K / 64) > 0x7fffffffLL)
+    return report(SF_ERR_UNSUPPORTED, "%s: N * H is too large for one launch", fn);
+  sfg::StepParams p{};
+  p.q = q; p.k = k; p.v = v; p.decay = decay; p.gate = gate; p.beta = beta; p.pool = pool;
+  p.idx = idx; p.out = out; p.N = s->N; p.H = s->H; p.HK = eff_hk(s); p.num_slots = num_slots;
+  p.scale = eff_scale(s);
+  return cuda_status(sfg::launch_state_step(p, s->dtype == SF_BF16, s->K,
+                                            reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+sf_status check_qk(const sf_qk_shape* s, const void* q, const void* k, const float* qw,
+                   const float* kw, const float* cs, const int32_t* pos, const char* fn,
+                   sfg::QkParams& p) {
+  if (!s) return report(SF_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  if (s->rows < 0 || s->H < 1 || s->HK < 1)
+    return report(SF_ERR_INVALID_ARG, "%s: need rows>=0, H>=1, HK>=1", fn);
+  if (s->dtype != SF_F32 && s->dtype != SF_BF16)
+    return report(SF_ERR_INVALID_ARG, "%s: dtype must be SF_F32 or SF_BF16", fn);
+  if (s->norm != SF_NORM_RMS && s->norm != SF_NORM_L2)
+    return report(SF_ERR_INVALID_ARG, "%s: norm must be SF_NORM_RMS or SF_NORM_L2", fn);
+  if (!(s->eps >= 0.f)) return report(SF_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+  if (s->D != 64 && s->D != 128)
+    return report(SF_ERR_UNSUPPORTED, "%s: head size 64 or 128 only (got %d)", fn, s->D);
+  if (s->rotary_dim < 0 || s->rotary_dim > s->D || s->rotary_dim % 8)
+    return report(SF_ERR_UNSUPPORTED, "%s: rotary_dim must be a multiple of 8 in [0, D] (got %d)",
+                  fn, s->rotary_dim);
+  const int el = s->dtype == SF_BF16 ? 8 : 4;   // elements of 16 bytes
+  if (s->rows_stride_q % el || s->rows_stride_k % el ||
+      s->rows_stride_q < (int64_t)s->H * s->D || s->rows_stride_k < (int64_t)s->HK * s->D)
+    return report(SF_ERR_INVALID_ARG,
+                  "%s: token strides must be multiples of 16 bytes and hold every head", fn);
+  if (s->rows > 0 && (!q || !k)) return report(SF_ERR_INVALID_ARG, "%s: q and k must be non-NULL", fn);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(qw) || !aligned16(kw) || !aligned16(cs))
+    return report(SF_ERR_INVALID_ARG, "%s: q, k, weights and cos_sin must be 16-byte aligned", fn);
+  p.axes = 1;
+  p.bound[0] = 0;
+  if (s->rotary_dim > 0) {
+    if (s->axes < 1 || s->axes > 4)
+      return report(SF_ERR_INVALID_ARG, "%s: 1 to 4 position axes (got %d)", fn, s->axes);
+    int sum = 0;
+    for (int a = 0; a < s->axes; ++a) {
+      if (s->sections[a] < 0)
+        return report(SF_ERR_INVALID_ARG, "%s: sections[%d] = %d is negative", fn, a, s->sections[a]);
+      p.bound[a] = sum += s->sections[a];
+    }
+    if (sum != s->rotary_dim / 2)
+      return report(SF_ERR_INVALID_ARG, "%s: sections sum to %d, rotary_dim / 2 is %d", fn, sum,
+                    s->rotary_dim / 2);
+    if (s->table_rows < 1 || !cs || (s->rows > 0 && !pos))
+      return report(SF_ERR_INVALID_ARG, "%s: cos_sin (table_rows >= 1) and positions needed", fn);
+    p.axes = s->axes;
+  }
+  p.q = q; p.k = k; p.qw = qw; p.kw = kw; p.cs = cs; p.pos = pos;
+  p.rows = s->rows; p.sq = s->rows_stride_q; p.sk = s->rows_stride_k;
+  p.H = s->H; p.HK = s->HK; p.half = s->rotary_dim / 2; p.inter = s->interleaved != 0;
+  p.table_rows = s->table_rows; p.l2 = s->norm == SF_NORM_L2; p.eps = s->eps;
+  return SF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sf_linattn_fwd_workspace(const sf_gdn_shape* shape, int packed) {
+  return layout(shape, packed != 0, 1).total;
+}
+
+sf_status sf_linattn_chunk_fwd(const sf_gdn_shape* shape, const void* q, const void* k,
+                               const void* v, const float* decay, const float* initial_state,
+                               const int32_t* cu_seqlens, int output_final_state, void* out,
+                               float* final_state, void* workspace, size_t ws_bytes,
+                               sf_stream_t stream) {
+  const char* fn = "sf_linattn_chunk_fwd";
+  const sfg::Range range(fn);
+  if (output_final_state && !final_state)
+    return report(SF_ERR_INVALID_ARG, "%s: output_final_state requires final_state", fn);
+  return chunk_fwd(fn, shape, q, k, v, decay, initial_state, cu_seqlens,
+                   output_final_state ? final_state : nullptr, out, nullptr, 0, nullptr, nullptr,
+                   workspace, ws_bytes, stream);
+}
+
+sf_status sf_linattn_paged_chunk_fwd(const sf_gdn_shape* shape, const void* q, const void* k,
+                                     const void* v, const float* decay, float* state_cache,
+                                     int num_slots, const int32_t* state_indices,
+                                     const uint8_t* has_initial_state, const int32_t* cu_seqlens,
+                                     void* out, void* workspace, size_t ws_bytes,
+                                     sf_stream_t stream) {
+  const char* fn = "sf_linattn_paged_chunk_fwd";
+  const sfg::Range range(fn);
+  if (!state_cache || !state_indices || num_slots < 1)
+    return report(SF_ERR_INVALID_ARG, "%s: state_cache, state_indices and num_slots >= 1 needed", fn);
+  if (!aligned16(state_cache))
+    return report(SF_ERR_INVALID_ARG, "%s: state_cache must be 16-byte aligned", fn);
+  return chunk_fwd(fn, shape, q, k, v, decay, nullptr, cu_seqlens, nullptr, out, state_cache,
+                   num_slots, state_indices, has_initial_state, workspace, ws_bytes, stream);
+}
+
+size_t sf_linattn_bwd_workspace(const sf_gdn_shape* shape, int packed) {
+  return layout(shape, packed != 0, 3).total;
+}
+
+sf_status sf_linattn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const void* k,
+                               const void* v, const float* decay, const float* initial_state,
+                               const int32_t* cu_seqlens, const void* d_out,
+                               const float* d_final_state, void* dq, void* dk, void* dv,
+                               float* d_initial_state, void* workspace, size_t ws_bytes,
+                               sf_stream_t stream) {
+  const char* fn = "sf_linattn_chunk_bwd";
+  const sfg::Range range(fn);
+  const bool packed = cu_seqlens != nullptr;
+  const sf_status st = check_tokens(shape, packed, fn);
+  if (st != SF_OK) return st;
+  if (!decay) return report(SF_ERR_INVALID_ARG, "%s: decay must be non-NULL", fn);
+  if (shape->T > 0 && (!q || !k || !v || !d_out || !dq || !dk || !dv))
+    return report(SF_ERR_INVALID_ARG, "%s: inputs and gradient outputs must be non-NULL", fn);
+  const void* al[] = {q, k, v, d_out, dq, dk, dv, initial_state, d_final_state, d_initial_state};
+  for (const void* a : al)
+    if (!aligned16(a))
+      return report(SF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const Layout l = layout(shape, packed, 3);
+  if (!workspace || ws_bytes < l.total)
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, l.total);
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = shape->dtype == SF_BF16;
+  sfg::LaParams p{};
+  p.npass = 3;
+  p.decay = decay;
+  p.cu = cu_seqlens;
+  p.B = shape->B; p.T = shape->T; p.H = shape->H; p.N = shape->N;
+  const float sc = eff_scale(shape);
+  const int hk = eff_hk(shape), H = shape->H;
+  float* gq = nullptr;
+  float* gk = nullptr;
+  if (l.gqa) {   // per-value-head parts in FP32, summed below
+    gq = reinterpret_cast<float*>(ws + kStatusBytes + 3 * l.states);
+    gk = reinterpret_cast<float*>(ws + kStatusBytes + 3 * l.states + l.gqa);
+  }
+  const int f32 = gq != nullptr;
+  p.pass[0] = sfg::LaPass{d_out, v, k, f32 ? gq : dq, initial_state, nullptr, nullptr, H, H, hk,
+                          1, f32, 0, sc, sc, 1.f};
+  p.pass[1] = sfg::LaPass{k, q, d_out, dv, d_final_state, d_initial_state, nullptr, hk, hk, H,
+                          0, 0, 1, sc, 1.f, sc};
+  p.pass[2] = sfg::LaPass{v, d_out, q, f32 ? gk : dk, d_final_state, nullptr, nullptr, H, H, hk,
+                          1, f32, 1, sc, 1.f, sc};
+  cudaError_t e = run_passes(p, l, ws, bf16, shape->K, cs);
+  if (e == cudaSuccess && f32) {
+    const int64_t rows = (int64_t)shape->B * shape->T;
+    e = sfg::launch_group_sum(gq, dq, bf16, rows, H, hk, shape->K, cu_seqlens, shape->N, cs);
+    if (e == cudaSuccess)
+      e = sfg::launch_group_sum(gk, dk, bf16, rows, H, hk, shape->K, cu_seqlens, shape->N, cs);
+  }
+  return cuda_status(e, fn);
+}
+
+sf_status sf_linattn_step(const sf_gdn_shape* shape, const void* q, const void* k, const void* v,
+                          const float* decay, float* state_cache, int num_slots,
+                          const int32_t* state_indices, void* out, sf_stream_t stream) {
+  const char* fn = "sf_linattn_step";
+  const sfg::Range range(fn);
+  if (!decay) return report(SF_ERR_INVALID_ARG, "%s: decay must be non-NULL", fn);
+  return step(fn, shape, q, k, v, decay, nullptr, nullptr, state_cache, num_slots, state_indices,
+              out, stream);
+}
+
+sf_status sf_gdn_step(const sf_gdn_shape* shape, const void* q, const void* k, const void* v,
+                      const float* gate, const float* beta, float* state_cache, int num_slots,
+                      const int32_t* state_indices, void* out, sf_stream_t stream) {
+  const char* fn = "sf_gdn_step";
+  const sfg::Range range(fn);
+  return step(fn, shape, q, k, v, nullptr, gate, beta, state_cache, num_slots, state_indices, out,
+              stream);
+}
+
+sf_status sf_qk_norm_rope_fwd(const sf_qk_shape* shape, const void* q, const void* k,
+                              const float* q_weight, const float* k_weight, const float* cos_sin,
+                              const int32_t* positions, void* q_out, void* k_out,
+                              sf_stream_t stream) {
+  const char* fn = "sf_qk_norm_rope_fwd";
+  const sfg::Range range(fn);
+  sfg::QkParams p{};
+  const sf_status st = check_qk(shape, q, k, q_weight, k_weight, cos_sin, positions, fn, p);
+  if (st != SF_OK) return st;
+  if (shape->rows == 0) return SF_OK;
+  if (!q_out || !k_out || !aligned16(q_out) || !aligned16(k_out))
+    return report(SF_ERR_INVALID_ARG, "%s: q_out and k_out must be non-NULL, 16-byte aligned", fn);
+  if ((q_out == q && shape->rows_stride_q != (int64_t)shape->H * shape->D) ||
+      (k_out == k && shape->rows_stride_k != (int64_t)shape->HK * shape->D))
+    return report(SF_ERR_INVALID_ARG, "%s: in place needs contiguous q and k", fn);
+  p.q_out = q_out;
+  p.k_out = k_out;
+  return cuda_status(sfg::launch_qk_norm_rope(p, shape->dtype == SF_BF16, shape->D,
+                                              reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+size_t sf_qk_norm_rope_bwd_workspace(const sf_qk_shape* shape) {
+  // sums of at most sfg::QK_PARTS CTAs, whatever the device has
+  if (!shape || shape->D < 1) return 256;
+  return (size_t)sfg::QK_PARTS * 2 * shape->D * sizeof(float);
+}
+
+sf_status sf_qk_norm_rope_bwd(const sf_qk_shape* shape, const void* q, const void* k,
+                              const float* q_weight, const float* k_weight, const float* cos_sin,
+                              const int32_t* positions, const void* d_q_out, const void* d_k_out,
+                              void* dq, void* dk, float* dq_weight, float* dk_weight,
+                              void* workspace, size_t ws_bytes, sf_stream_t stream) {
+  const char* fn = "sf_qk_norm_rope_bwd";
+  const sfg::Range range(fn);
+  sfg::QkParams p{};
+  const sf_status st = check_qk(shape, q, k, q_weight, k_weight, cos_sin, positions, fn, p);
+  if (st != SF_OK) return st;
+  if (shape->rows > 0 && (!d_q_out || !d_k_out || !dq || !dk))
+    return report(SF_ERR_INVALID_ARG, "%s: cotangents and gradients must be non-NULL", fn);
+  if (!aligned16(d_q_out) || !aligned16(d_k_out) || !aligned16(dq) || !aligned16(dk))
+    return report(SF_ERR_INVALID_ARG, "%s: cotangents and gradients must be 16-byte aligned", fn);
+  const bool weights = dq_weight || dk_weight;
+  if (weights && (!workspace || !aligned16(workspace) || ws_bytes < sf_qk_norm_rope_bwd_workspace(shape)))
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn,
+                  sf_qk_norm_rope_bwd_workspace(shape));
+  p.q_out = dq;
+  p.k_out = dk;
+  p.dqo = d_q_out;
+  p.dko = d_k_out;
+  p.part = weights ? static_cast<float*>(workspace) : nullptr;
+  return cuda_status(sfg::launch_qk_norm_rope_bwd(p, shape->dtype == SF_BF16, shape->D, dq_weight,
+                                                  dk_weight, reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+}  // extern "C"

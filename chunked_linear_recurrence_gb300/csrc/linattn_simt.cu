@@ -1,0 +1,339 @@
+// linattn_simt.cu -- the decayed linear attention's product (linattn.cuh) on the CUDA cores:
+// FP32 tokens, and BF16 tokens with head size 64.  FP32 multiply-adds throughout.
+//
+// One CTA of 256 threads walks one (segment, head, 64-column slice of z).  Per 64-row chunk
+//     P  = a (X Y^T) o lam^|r-s|       64 x 64, each thread 4 x 4
+//     O  = b lam^e diag (X S^T) + P Z  64 x 64, each thread 4 x 4
+//     S' = lam^L S + c (lam^f Y)^T Z   D x 64, each thread D/16 x 4, kept in registers
+// Every product reads one operand as rows that sixteen threads share (a broadcast) and the
+// other as consecutive float4 of the row that the sixteen divide among them.  The state is
+// copied to shared memory once a chunk for the second product.  Powers of lam come from a
+// table formed in FP64; lam^64 is carried as a sum of two floats, so that a state kept over
+// thousands of chunks does not drift by the rounding of one factor.
+// Bound by the FP32 rate: about 5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, two
+// thirds of it in S and O, against 2 KB of tokens.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "linattn.cuh"
+
+namespace sfg {
+namespace {
+
+constexpr int ZT = 64;   // columns of z per CTA
+constexpr int C = LA_CHUNK;
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<uint32_t*>(&a);
+  u.y = *reinterpret_cast<uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+template <int D>
+struct Smem {
+  float X[C][D + 4], Y[C][D + 4], Z[C][ZT + 4], P[C][ZT + 4], S[D][ZT + 4], tab[C + 4];
+};
+
+// Rows [r0, r0 + L) of one head's columns [c0, c0 + W) into dst (leading dimension ld); the
+// other rows of the 64 become zero.
+template <typename T, int W>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t r0, int L,
+                                          int heads, int head, int D, int c0, int tid) {
+  for (int idx = tid; idx < C * (W / 4); idx += 256) {
+    const int r = idx / (W / 4), c = (idx % (W / 4)) * 4;
+    const float4 v = r < L ? ld4(src + ((size_t)(r0 + r) * heads + head) * D + c0 + c)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(dst + r * ld + c) = v;
+  }
+}
+
+template <typename T, int D, bool kState>
+__global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  constexpr int NZ = D / ZT, YR = D / 16;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  int id = blockIdx.x;
+  const int zt = id % NZ; id /= NZ;
+  const int pi = id % p.npass; id /= p.npass;
+  const int h = id % p.H, u = id / p.H;
+  const LaPass& q = p.pass[pi];
+  int n, w;
+  int64_t bos, eos;
+  if (!la_locate(u, p, n, w, bos, eos)) return;
+  const int64_t len = eos - bos;
+  const bool split = p.seg < p.T;
+  const bool last = (int64_t)(w + 1) * p.seg >= len;
+  if (kState && last) return;                     // nobody enters from its end
+  const int64_t off = (int64_t)w * p.seg;
+  const int64_t rows = len - off < p.seg ? len - off : p.seg;
+  const int64_t sb = q.reverse ? eos - off - rows : bos + off, se = sb + rows;
+  bool skip;
+  const float* s_in = la_entry(p, q, n, h, D, skip);
+  const int zc = zt * ZT;
+  if (skip) {                                     // padding of the paged pool
+    if (kState) return;
+    T* o = reinterpret_cast<T*>(q.out);
+    for (int64_t idx = tid; idx < rows * (ZT / 4); idx += 256)
+      st4(o + ((size_t)(sb + idx / (ZT / 4)) * p.H + h) * D + zc + (int)(idx % (ZT / 4)) * 4,
+          make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
+  const float d = p.decay[h];
+  if (tid <= C) sm.tab[tid] = (float)la_pow(d, tid);
+
+  // S[y = ty YR + e][z = zc + 4 tx ..]: zeros, the caller's state, or the segment's entry
+  float4 s[YR];
+  size_t uoff = ((size_t)u * p.H + h) * D * D;
+  const float* src = kState ? nullptr : split ? q.seg_state + uoff : s_in;
+  const bool st = q.s_t && !split;                // segment states are stored [z][y]
+#pragma unroll
+  for (int e = 0; e < YR; ++e) {
+    const int y = ty * YR + e, z = zc + 4 * tx;
+    if (!src) s[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    else if (st) s[e] = ld4(src + (size_t)y * D + z);
+    else s[e] = make_float4(src[(size_t)z * D + y], src[(size_t)(z + 1) * D + y],
+                            src[(size_t)(z + 2) * D + y], src[(size_t)(z + 3) * D + y]);
+  }
+  const int G_x = p.H / q.hx, G_y = p.H / q.hy, G_z = p.H / q.hz;
+  const int nc = (int)((rows + C - 1) / C);
+  float hi = 1.f, lo = 0.f;                       // lam^carry_rows
+  int carry_rows = 0;
+  for (int ci = 0; ci < nc; ++ci) {
+    const int64_t done = (int64_t)ci * C;
+    const int L = (int)(rows - done < C ? rows - done : C);
+    const int64_t r0 = q.reverse ? se - done - L : sb + done;
+    __syncthreads();                              // the last chunk's readers; the table
+    if (!kState)
+      load_rows<T, D>(&sm.X[0][0], D + 4, reinterpret_cast<const T*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
+    load_rows<T, D>(&sm.Y[0][0], D + 4, reinterpret_cast<const T*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
+    load_rows<T, ZT>(&sm.Z[0][0], ZT + 4, reinterpret_cast<const T*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
+    if (!kState) {
+#pragma unroll
+      for (int e = 0; e < YR; ++e) st4(&sm.S[ty * YR + e][4 * tx], s[e]);
+    }
+    __syncthreads();
+    if (!kState) {
+      // P rows 4 ty + i, columns tx + 16 j
+      float acc[4][4] = {};
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float4 xv[4], yv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[i] = ld4(&sm.X[4 * ty + i][c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) yv[j] = ld4(&sm.Y[tx + 16 * j][c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[i][j] = fmaf(xv[i].x, yv[j].x, fmaf(xv[i].y, yv[j].y,
+                        fmaf(xv[i].z, yv[j].z, fmaf(xv[i].w, yv[j].w, acc[i][j]))));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 4 * ty + i, c = tx + 16 * j, gap = q.reverse ? c - r : r - c;
+          sm.P[r][c] = gap >= 0 ? acc[i][j] * (q.a * sm.tab[gap]) : 0.f;
+        }
+      __syncthreads();
+      // O rows 4 ty + i, columns 4 tx ..
+      float4 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int c = 0; c < D; c += 4) {
+        float4 sv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sv[e] = ld4(&sm.S[c + e][4 * tx]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 xv = ld4(&sm.X[4 * ty + i][c]);
+          o[i].x = fmaf(xv.x, sv[0].x, fmaf(xv.y, sv[1].x, fmaf(xv.z, sv[2].x, fmaf(xv.w, sv[3].x, o[i].x))));
+          o[i].y = fmaf(xv.x, sv[0].y, fmaf(xv.y, sv[1].y, fmaf(xv.z, sv[2].y, fmaf(xv.w, sv[3].y, o[i].y))));
+          o[i].z = fmaf(xv.x, sv[0].z, fmaf(xv.y, sv[1].z, fmaf(xv.z, sv[2].z, fmaf(xv.w, sv[3].z, o[i].z))));
+          o[i].w = fmaf(xv.x, sv[0].w, fmaf(xv.y, sv[1].w, fmaf(xv.z, sv[2].w, fmaf(xv.w, sv[3].w, o[i].w))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        const float f = r < L ? q.b * sm.tab[q.reverse ? L - 1 - r : r + 1] : 0.f;
+        o[i].x *= f; o[i].y *= f; o[i].z *= f; o[i].w *= f;
+      }
+#pragma unroll 2
+      for (int c = 0; c < C; c += 4) {
+        float4 zv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zv[e] = ld4(&sm.Z[c + e][4 * tx]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 pv = ld4(&sm.P[4 * ty + i][c]);
+          o[i].x = fmaf(pv.x, zv[0].x, fmaf(pv.y, zv[1].x, fmaf(pv.z, zv[2].x, fmaf(pv.w, zv[3].x, o[i].x))));
+          o[i].y = fmaf(pv.x, zv[0].y, fmaf(pv.y, zv[1].y, fmaf(pv.z, zv[2].y, fmaf(pv.w, zv[3].y, o[i].y))));
+          o[i].z = fmaf(pv.x, zv[0].z, fmaf(pv.y, zv[1].z, fmaf(pv.z, zv[2].z, fmaf(pv.w, zv[3].z, o[i].z))));
+          o[i].w = fmaf(pv.x, zv[0].w, fmaf(pv.y, zv[1].w, fmaf(pv.z, zv[2].w, fmaf(pv.w, zv[3].w, o[i].w))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (r >= L) continue;
+        const size_t at = ((size_t)(r0 + r) * p.H + h) * D + zc + 4 * tx;
+        if (q.out_f32) st4(reinterpret_cast<float*>(q.out) + at, o[i]);
+        else st4(reinterpret_cast<T*>(q.out) + at, o[i]);
+      }
+    }
+    // S = lam^L S + c sum_r lam^f(r) y_r z_r
+    if (L != carry_rows) {
+      const double full = la_pow(d, L);
+      hi = (float)full;
+      lo = (float)(full - (double)hi);
+      carry_rows = L;
+    }
+    float4 acc[YR];
+#pragma unroll
+    for (int e = 0; e < YR; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < L; ++r) {
+      const float wgt = q.c * sm.tab[q.reverse ? r + 1 : L - 1 - r];
+      float4 zv = ld4(&sm.Z[r][4 * tx]);
+      zv.x *= wgt; zv.y *= wgt; zv.z *= wgt; zv.w *= wgt;
+#pragma unroll
+      for (int e = 0; e < YR; ++e) {
+        const float yv = sm.Y[r][ty * YR + e];
+        acc[e].x = fmaf(yv, zv.x, acc[e].x);
+        acc[e].y = fmaf(yv, zv.y, acc[e].y);
+        acc[e].z = fmaf(yv, zv.z, acc[e].z);
+        acc[e].w = fmaf(yv, zv.w, acc[e].w);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < YR; ++e) {
+      s[e].x = fmaf(hi, s[e].x, fmaf(lo, s[e].x, acc[e].x));
+      s[e].y = fmaf(hi, s[e].y, fmaf(lo, s[e].y, acc[e].y));
+      s[e].z = fmaf(hi, s[e].z, fmaf(lo, s[e].z, acc[e].z));
+      s[e].w = fmaf(hi, s[e].w, fmaf(lo, s[e].w, acc[e].w));
+    }
+  }
+  float* dst = kState ? q.seg_state + uoff : last ? la_exit(p, q, n, h, D) : nullptr;
+  if (!dst) return;
+  const bool dt = q.s_t && !kState;
+#pragma unroll
+  for (int e = 0; e < YR; ++e) {
+    const int y = ty * YR + e, z = zc + 4 * tx;
+    if (dt) {
+      st4(dst + (size_t)y * D + z, s[e]);
+    } else {
+      dst[(size_t)z * D + y] = s[e].x;
+      dst[(size_t)(z + 1) * D + y] = s[e].y;
+      dst[(size_t)(z + 2) * D + y] = s[e].z;
+      dst[(size_t)(z + 3) * D + y] = s[e].w;
+    }
+  }
+}
+
+// Entry states of the segments of one (sequence, head, pass): e_0 = the caller's state,
+// e_{w+1} = lam^seg e_w + sum_w; seg_state holds sum_w before and e_w after.  Each thread
+// carries one float4 of the state over the segments.
+template <int D>
+__global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
+  const int tid = threadIdx.x;
+  int id = blockIdx.x;
+  constexpr int PARTS = D * D / 1024;
+  const int part = id % PARTS; id /= PARTS;
+  const int pi = id % p.npass; id /= p.npass;
+  const int h = id % p.H, n = id / p.H;
+  const LaPass& q = p.pass[pi];
+  int64_t len = p.T;
+  int u0 = 0;
+  if (!p.cu) {
+    u0 = n * ((p.T + p.seg - 1) / p.seg);
+  } else {
+    const int lane = tid & 31;
+    int sum = 0;
+    for (int m = lane; m < n; m += 32) {
+      int64_t b, e;
+      seq_span(m, p.B, p.T, p.cu, b, e);
+      sum += e > b ? (int)((e - b + p.seg - 1) / p.seg) : 1;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    u0 = sum;
+    int64_t b, e;
+    seq_span(n, p.B, p.T, p.cu, b, e);
+    len = e - b;
+  }
+  const int segs = len > 0 ? (int)((len + p.seg - 1) / p.seg) : 1;
+  if (u0 + segs > p.units) return;                // malformed offsets
+  bool skip;
+  const float* s_in = la_entry(p, q, n, h, D, skip);
+  if (skip) return;
+  const int at = (part * 256 + tid) * 4, z = at / D, y = at % D;
+  float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (s_in) {
+    if (q.s_t) e = make_float4(s_in[(size_t)y * D + z], s_in[(size_t)(y + 1) * D + z],
+                               s_in[(size_t)(y + 2) * D + z], s_in[(size_t)(y + 3) * D + z]);
+    else e = ld4(s_in + at);
+  }
+  const double full = la_pow(p.decay[h], p.seg);
+  const float hi = (float)full, lo = (float)(full - (double)hi);
+  float* base = q.seg_state + ((size_t)u0 * p.H + h) * D * D + at;
+  const size_t step = (size_t)p.H * D * D;
+  float4 cur = segs > 1 ? ld4(base) : e;
+  for (int w = 0; w < segs; ++w) {
+    float4 nxt = e;
+    if (w + 2 < segs) nxt = ld4(base + (size_t)(w + 1) * step);
+    st4(base + (size_t)w * step, e);
+    e.x = fmaf(hi, e.x, fmaf(lo, e.x, cur.x));
+    e.y = fmaf(hi, e.y, fmaf(lo, e.y, cur.y));
+    e.z = fmaf(hi, e.z, fmaf(lo, e.z, cur.z));
+    e.w = fmaf(hi, e.w, fmaf(lo, e.w, cur.w));
+    cur = nxt;
+  }
+}
+
+template <typename T, int D, bool kState>
+cudaError_t go(const LaParams& p, cudaStream_t st) {
+  const int64_t grid = (int64_t)p.units * p.H * p.npass * (D / ZT);
+  if (grid <= 0) return cudaSuccess;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  auto kern = la_simt_kernel<T, D, kState>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(Smem<D>));
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)grid, 256, sizeof(Smem<D>), st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_la_simt(const LaParams& p, bool bf16, int D, bool state_only, cudaStream_t st) {
+  if (bf16) {
+    if (D == 64) return state_only ? go<__nv_bfloat16, 64, true>(p, st) : go<__nv_bfloat16, 64, false>(p, st);
+    return state_only ? go<__nv_bfloat16, 128, true>(p, st) : go<__nv_bfloat16, 128, false>(p, st);
+  }
+  if (D == 64) return state_only ? go<float, 64, true>(p, st) : go<float, 64, false>(p, st);
+  return state_only ? go<float, 128, true>(p, st) : go<float, 128, false>(p, st);
+}
+
+cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st) {
+  const int64_t grid = (int64_t)p.N * p.H * p.npass * (D * D / 1024);
+  if (grid <= 0) return cudaSuccess;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  if (D == 64) la_carry_kernel<64><<<(unsigned)grid, 256, 0, st>>>(p);
+  else la_carry_kernel<128><<<(unsigned)grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace sfg

@@ -6,6 +6,7 @@
 #include "api_internal.cuh"
 #include "linattn.cuh"
 #include "simt_chunk.cuh"
+#include "tmap.cuh"
 
 using sfg::report;
 
@@ -62,10 +63,21 @@ sf_status check_tokens(const sf_gdn_shape* s, bool packed, const char* fn) {
   return SF_OK;
 }
 
+// BF16 with K = V = 128 runs on the tensor-core kernel alone, which needs TMA descriptors.
+sf_status check_encoder(const sf_gdn_shape* s, const char* fn) {
+  if (s->dtype == SF_BF16 && s->K == 128 && s->T > 0 && !sfg::tc_fwd_available())
+    return report(SF_ERR_UNSUPPORTED,
+                  "%s: BF16 with K = V = 128 needs the tensor-core kernels, but the driver entry "
+                  "point cuTensorMapEncodeTiled is unavailable (or disabled by "
+                  "SF_GDN_DISABLE_TMA_ENCODER)", fn);
+  return SF_OK;
+}
+
 // Rows of a segment (linattn.cuh), a multiple of 64: as many segments as it takes to give
 // every SM a CTA, none shorter than 256 rows; a walk that needs no cut is one segment.
 int seg_rows(const sf_gdn_shape* s, bool packed, int npass) {
-  const int64_t chains = (int64_t)(packed ? 1 : s->N) * s->H * npass * (s->K / 64);
+  const bool tc = s->dtype == SF_BF16 && s->K == 128;   // one CTA a walk, else one per 64 columns
+  const int64_t chains = (int64_t)(packed ? 1 : s->N) * s->H * npass * (tc ? 1 : s->K / 64);
   const int64_t want = (kSms + chains - 1) / chains;       // segments of the longest walk
   int64_t rows = (s->T + want - 1) / want;
   rows = (rows + 63) / 64 * 64;
@@ -99,12 +111,17 @@ cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, i
   for (int i = 0; i < p.npass; ++i)
     p.pass[i].seg_state =
         l.states ? reinterpret_cast<float*>(ws + kStatusBytes + i * l.states) : nullptr;
+  // (T = 0: no token is read or written, only the states move; either kernel does)
+  const bool tc = bf16 && D == 128 && p.T > 0;
+  auto walk = [&](bool state_only) {
+    return tc ? sfg::launch_la_tc(p, state_only, cs) : sfg::launch_la_simt(p, bf16, D, state_only, cs);
+  };
   cudaError_t e = cudaSuccess;
   if (l.states) {
-    e = sfg::launch_la_simt(p, bf16, D, /*state_only=*/true, cs);
+    e = walk(true);
     if (e == cudaSuccess) e = sfg::launch_la_carry(p, D, cs);
   }
-  if (e == cudaSuccess) e = sfg::launch_la_simt(p, bf16, D, /*state_only=*/false, cs);
+  if (e == cudaSuccess) e = walk(false);
   return e;
 }
 
@@ -125,6 +142,8 @@ sf_status chunk_fwd(const char* fn, const sf_gdn_shape* shape, const void* q, co
   const Layout l = layout(shape, packed, 1);
   if (!workspace || ws_bytes < l.total)
     return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, l.total);
+  const sf_status enc = check_encoder(shape, fn);
+  if (enc != SF_OK) return enc;
   sfg::LaParams p{};
   p.npass = 1;
   p.decay = decay;
@@ -275,6 +294,8 @@ sf_status sf_linattn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const v
   const Layout l = layout(shape, packed, 3);
   if (!workspace || ws_bytes < l.total)
     return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, l.total);
+  const sf_status enc = check_encoder(shape, fn);
+  if (enc != SF_OK) return enc;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = shape->dtype == SF_BF16;

@@ -1,0 +1,515 @@
+// linattn_tc.cu -- the decayed linear attention's product (linattn.cuh) on tcgen05: BF16 tokens
+// with head size 128.
+//
+// One CTA walks one (segment, head) in 64-row chunks.  Rows r, s of a chunk, the state S [z][y]:
+//     QK  = [Y; X] Y^T           M = 128, N = 64, K = 128   (rows 64-127: X Y^T)
+//     P   = a QK o lam^|r-s|     BF16, by two warps, to shared memory
+//     E   = (lam^f c Z)^T Y      M = 128, N = 128, K = 64   three times (below)
+//     O1^T = S X^T               M = 128, N = 64,  K = 128  (S as BF16 in TMEM)
+//     O2^T = Z^T P^T             M = 128, N = 64,  K = 64
+//     out = b lam^e O1 + O2,     S <- lam^L S + E           (FP32)
+// Everything is laid out as the TMA brings it: [rows][128] BF16 tiles of two swizzled 64-column
+// panels, read K-major or MN-major as each product needs.
+//
+// The state stays in the registers of eight warps (64 floats a thread), not in TMEM: every
+// chunk's E is a product of its own, so E of the next chunks never waits for S, no FP32 state
+// is read and written back around the products, and the sum over the chunks is rounded in
+// FP32 to nearest.  E's left operand is exact enough to keep FP32 accuracy of the state: the
+// weighted rows are split into three BF16 summands (8 bits each, 24 together), each multiplied
+// with the exact Y.  A launch that returns no state takes two of them (16 bits): its state
+// only ever reaches BF16 results.
+//
+// Warps: 0 loads (three chunks in flight), 1 issues, 2-3 form P, 4-11 hold the state and write
+// the results (two warpgroups: columns y 0-63 and 64-127 of the state, rows 0-31 and 32-63 of
+// the results), 12-15 split the weighted rows.  Per chunk the issuer queues QK, E, then O1 (once
+// the state is there), then O2 (once P is there): while the state warps turn E into the next
+// entry state, the tensor pipe works on the next chunk's QK and E.  Warps meet through
+// mbarriers alone; every wait is bounded, and a thread that gives up writes SF_ERR_TIMEOUT to
+// the status word and raises the CTA's abort flag; copies and products in flight land before
+// the CTA leaves.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "linattn.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace sfg {
+namespace {
+
+using namespace tc;
+
+constexpr int D = 128, C = LA_CHUNK, NT = 512, NS = 3;
+constexpr uint32_t PANEL = 8192;                 // 64 rows x 128 bytes
+constexpr uint32_t B_Y = 0, B_X = PANEL;         // panel 0 of Y and X; panel 1 two panels on
+constexpr uint32_t B_Z = 4 * PANEL, STAGE = 6 * PANEL;
+constexpr uint32_t O_SPLIT = NS * STAGE;         // three weighted tiles of two panels
+constexpr uint32_t O_P = O_SPLIT + 6 * PANEL;    // P [64][64]
+constexpr uint32_t O_TAB = O_P + PANEL;          // lam^n [64], b lam^e [128], c lam^f [128], carry [4]
+constexpr uint32_t O_BAR = O_TAB + 1536;
+constexpr uint32_t SMEM = O_BAR + 256 + 1024;
+static_assert(SMEM <= 232448, "shared memory");
+
+constexpr uint32_t TM_E = 0, TM_SB = 256, TM_P = 320, TM_O1 = 384, TM_O2 = 448;
+
+constexpr uint32_t ID_QK = idesc_bf16(128, 64, false, false);
+constexpr uint32_t ID_E = idesc_bf16(128, 128, true, true);
+constexpr uint32_t ID_O1 = idesc_bf16(128, 64, false, false);   // A in TMEM
+constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
+
+enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY, SPLIT, EDONE,
+       EFREE = EDONE + 2, ODONE = EFREE + 2, GO, TBL, DRAIN, NBAR };
+static_assert(8 * NBAR + 8 <= 256, "barriers");
+
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+struct Maps {
+  CUtensorMap m[3][3];   // x, y, z of each pass
+};
+
+struct Cx {
+  int* status;
+  volatile int* abort;
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Cx& cx) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (*cx.abort) return false;
+    if (globaltimer_ns() - t0 > WAIT_NS) {
+      *cx.abort = 1;
+      if (cx.status) {
+        atomicCAS(cx.status, 0, (int)SF_ERR_TIMEOUT);
+        atomicCAS(cx.status + 1, 0, (int)(0x40000000u | ((blockIdx.x & 0x3ffffu) << 12) |
+                                          ((threadIdx.x >> 5) << 6) | ((smem_u32(bar) & 255u) >> 3)));
+      }
+      return false;
+    }
+  }
+}
+// The lanes of a warp wait together and agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Cx& cx) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, cx));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint64_t kstep_k(int kk) {   // panels 16 KB apart
+  return (uint64_t)(((uint32_t)(kk >> 2) * 2 * PANEL + (uint32_t)(kk & 3) * 32u) >> 4);
+}
+__device__ __forceinline__ uint64_t kstep_mn(int kk) { return (uint64_t)(kk * 2048 >> 4); }
+
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+template <bool kState>
+__global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Maps maps,
+                                                      const LaParams p, const int nsplit) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(sm);
+  float* tab = reinterpret_cast<float*>(sm + O_TAB);
+  float* rd = tab + 64;
+  float* wr = tab + 192;
+  float* carry = tab + 320;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + O_BAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR);
+  int* abort_s = reinterpret_cast<int*>(sm + O_BAR + 8 * NBAR + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  int id = blockIdx.x;
+  const int pi = id % p.npass; id /= p.npass;
+  const int h = id % p.H, u = id / p.H;
+  const LaPass& q = p.pass[pi];
+  int n, w;
+  int64_t bos, eos;
+  if (!la_locate(u, p, n, w, bos, eos)) return;
+  const int64_t len = eos - bos;
+  const bool split = p.seg < p.T;
+  const bool last = (int64_t)(w + 1) * p.seg >= len;
+  if (kState && last) return;                     // nobody enters from its end
+  const int64_t off = (int64_t)w * p.seg;
+  const int64_t rows = len - off < p.seg ? len - off : p.seg;
+  const bool rev = q.reverse != 0;
+  const int64_t s0 = rev ? eos - off - rows : bos + off, s1 = s0 + rows;
+  bool skip;
+  const float* s_in = la_entry(p, q, n, h, D, skip);
+  if (skip) {                                     // padding of the paged pool: zero rows
+    if (kState) return;
+    uint4* o = reinterpret_cast<uint4*>(q.out);
+    for (int64_t i = tid; i < rows * 16; i += NT)
+      o[((size_t)(s0 + (i >> 4)) * p.H + h) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int nc = (int)((rows + C - 1) / C);
+  const int tail = (int)(rows - (int64_t)(nc - 1) * C);   // rows of the walk's last chunk
+  const float d = p.decay[h];
+  const Cx cx{p.status, abort_s};
+
+  if (tid == 0) {
+    for (int i = 0; i < NBAR; ++i)
+      mbar_init(&bars[i], i == PREADY ? 2 : i == SPLIT ? 4 : i == GO || i == EFREE || i == EFREE + 1 ? 8 : 1);
+    *abort_s = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.m[pi][1]);
+    prefetch_tmap(&maps.m[pi][2]);
+    if (!kState) prefetch_tmap(&maps.m[pi][0]);
+  }
+  if (warp == 0) tmem_alloc(tslot, 512);
+  if (tid >= 64 && tid < 128) {
+    const int i = tid - 64;
+    auto pw = [&](int e) { return e == 0 ? 1.f : expf(d * (float)e); };
+    tab[i] = pw(i);
+    rd[i] = q.b * pw(rev ? 63 - i : i + 1);
+    wr[i] = q.c * pw(rev ? i + 1 : 63 - i);
+    rd[64 + i] = wr[64 + i] = 0.f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tslot;
+
+  if (warp < 4) {
+    reg_dealloc<88>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- loader
+      const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
+      bool ok = true;
+      int issued = 0;
+      for (int c = 0; c < nc && ok; ++c) {
+        const int b = c % NS;
+        const int L = c + 1 == nc ? tail : C;
+        const int r0 = (int)(rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C);
+        uint8_t* st = sm + b * STAGE;
+        if (c >= NS) {
+          bool f = true;
+          if (lane == 0) f = wait_bar(&bars[FREE + b], ((c - NS) / NS) & 1, cx);
+          if (!(ok = __shfl_sync(0xffffffffu, f, 0) != 0)) break;
+        }
+        uint64_t* bar = L < C ? &bars[LANDED + b] : &bars[FULL + b];   // (the last chunk only)
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, (kState ? 4 : 6) * PANEL);
+#pragma unroll
+          for (int pp = 0; pp < 2; ++pp) {
+            tma_load_3d(st + B_Y + 2 * pp * PANEL, &maps.m[pi][1], bar, 64 * pp, hy, r0);
+            if (!kState) tma_load_3d(st + B_X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
+            tma_load_3d(st + B_Z + pp * PANEL, &maps.m[pi][2], bar, 64 * pp, hz, r0);
+          }
+        }
+        issued = c + 1;
+        if (L < C) {
+          // rows past the end (other tokens, or NaN padding) must not reach the products
+          bool f = true;
+          if (lane == 0) f = wait_bar(bar, 0, cx);
+          if (!(ok = __shfl_sync(0xffffffffu, f, 0) != 0)) break;
+          const int per = (C - L) * 8;               // 16-byte pieces of a panel
+          for (int i = lane; i < 4 * per; i += 32) {
+            const int t = i / per, rr = i % per;
+            uint8_t* base = st + (t < 2 ? B_Y + 2 * t * PANEL : B_Z + (t - 2) * PANEL);
+            *reinterpret_cast<uint4*>(base + (L + rr / 8) * 128 + (rr % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[FULL + b]);
+        }
+      }
+      if (lane == 0 && !ok)   // let the copies in flight land
+        for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
+          if (c + 1 == nc && tail < C) mbar_wait(&bars[LANDED + c % NS], 0, 100000000ull);
+          else mbar_wait(&bars[FULL + c % NS], (c / NS) & 1, 100000000ull);
+        }
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- issuer
+      if (lane == 0) {
+        bool ok = true;
+        const uint64_t dp = sdesc_sw128(sb + O_P, 0, 1024);
+        for (int c = 0; c < nc && ok; ++c) {
+          const int b = c % NS;
+          const uint32_t st = sb + b * STAGE;
+          if (!(ok = wait_bar(&bars[FULL + b], (c / NS) & 1, cx))) break;
+          tc_fence_after();
+          if (!kState) {
+            const uint64_t dy = sdesc_sw128(st + B_Y, 0, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16(tm + TM_P, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
+            mma_commit(&bars[QKDONE]);
+          }
+          if (!(ok = wait_bar(&bars[SPLIT], c & 1, cx))) break;
+          if (kState && c >= 2 && !(ok = wait_bar(&bars[EFREE + (c & 1)], ((c - 2) >> 1) & 1, cx))) break;
+          tc_fence_after();
+          {
+            const uint32_t e = tm + TM_E + 128 * (c & 1);
+            const uint64_t dy = sdesc_sw128(st + B_Y, 2 * PANEL, 1024);
+            const uint64_t dz = sdesc_sw128(sb + O_SPLIT, PANEL, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              for (int sp = 0; sp < nsplit; ++sp)
+                mma_bf16(e, dz + kstep_mn(kk) + (uint64_t)(sp * 2 * PANEL >> 4), dy + kstep_mn(kk), ID_E,
+                         kk + sp > 0);
+            mma_commit(&bars[EDONE + (c & 1)]);
+          }
+          if (!kState) {
+            if (!(ok = wait_bar(&bars[GO], c & 1, cx))) break;
+            tc_fence_after();
+            const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
+            if (!(ok = wait_bar(&bars[PREADY], c & 1, cx))) break;
+            tc_fence_after();
+            const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)(kk * 2), ID_O2, kk > 0);
+            mma_commit(&bars[ODONE]);
+          }
+          mma_commit(&bars[FREE + b]);
+        }
+        // leave no product running into the TMEM and barriers that go away
+        mma_commit(&bars[DRAIN]);
+        mbar_wait(&bars[DRAIN], 0, 100000000ull);
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- P
+      if (warp == 3) {
+        // lam^64 and lam^tail as sums of two floats: a state carried over thousands of chunks
+        // must not drift by the rounding of one factor
+        if (lane < 2) {
+          const double f = la_pow(d, lane ? tail : C);
+          carry[2 * lane] = (float)f;
+          carry[2 * lane + 1] = (float)(f - (double)(float)f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[TBL]);
+      }
+      if (!kState) {
+        const int r = (warp - 2) * 32 + lane;          // TMEM lane 64 + r
+        const uint32_t tl = tm + TM_P + ((uint32_t)(warp * 32) << 16);
+        uint8_t* row = sm + O_P + r * 128;
+        const float a = q.a;
+        for (int c = 0; c < nc; ++c) {
+          if (!warp_wait(&bars[QKDONE], c & 1, cx)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            // 32 columns; the half on the far side of the diagonal is all masked
+            const bool none = rev ? half == 0 && warp == 3 : half == 1 && warp == 2;
+            float x[32];
+            if (none) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = 0.f;
+            } else {
+              tmem_ld32(tl + 32 * half, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int gap = rev ? 32 * half + e - r : r - (32 * half + e);
+                x[e] = gap >= 0 ? x[e] * (a * tab[gap & 63]) : 0.f;
+              }
+            }
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint4 v;
+              v.x = pack_bf16x2(x[8 * ch], x[8 * ch + 1]);
+              v.y = pack_bf16x2(x[8 * ch + 2], x[8 * ch + 3]);
+              v.z = pack_bf16x2(x[8 * ch + 4], x[8 * ch + 5]);
+              v.w = pack_bf16x2(x[8 * ch + 6], x[8 * ch + 7]);
+              *reinterpret_cast<uint4*>(row + (((4 * half + ch) ^ (r & 7)) << 4)) = v;
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          warp_arrive(&bars[PREADY], lane);
+        }
+      }
+    }
+  } else if (warp < 12) {
+    reg_alloc<168>();
+    // ---------------------------------------------------------------- state and results
+    const int wg = (warp - 4) >> 2;
+    const int z = ((warp & 3) << 5) + lane;
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    float s[64];
+    const size_t uoff = ((size_t)u * p.H + h) * D * D;
+    {
+      const float* src = kState ? nullptr : split ? q.seg_state + uoff : s_in;
+      if (!src) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) s[e] = 0.f;
+      } else if (q.s_t && !split) {                   // stored [y][z]
+#pragma unroll
+        for (int e = 0; e < 64; ++e) s[e] = src[(size_t)(64 * wg + e) * D + z];
+      } else {
+        const float4* v = reinterpret_cast<const float4*>(src + (size_t)z * D + 64 * wg);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 f = v[e];
+          s[4 * e] = f.x; s[4 * e + 1] = f.y; s[4 * e + 2] = f.z; s[4 * e + 3] = f.w;
+        }
+      }
+    }
+    auto put_state = [&]() {                          // BF16 copy, the A operand of S X^T
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]);
+        tmem_st16(tl + TM_SB + 32 * wg + 16 * k, v);
+      }
+    };
+    if (!kState && nc > 0) {
+      put_state();
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&bars[GO], lane);
+    }
+    bool ok = nc == 0 || warp_wait(&bars[TBL], 0, cx);
+    for (int c = 0; c < nc && ok; ++c) {
+      const bool end = c + 1 == nc;
+      const int L = end ? tail : C;
+      if (!(ok = warp_wait(&bars[EDONE + (c & 1)], (c >> 1) & 1, cx))) break;
+      tc_fence_after();
+      const float fh = carry[end ? 2 : 0], fl = carry[end ? 3 : 1];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x[32];
+        tmem_ld32(tl + TM_E + 128 * (c & 1) + 64 * wg + 32 * k, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[32 * k + e] = fmaf(fh, s[32 * k + e], fmaf(fl, s[32 * k + e], x[e]));
+      }
+      if (kState) {
+        tc_fence_before();
+        warp_arrive(&bars[EFREE + (c & 1)], lane);
+        continue;
+      }
+      if (!(ok = warp_wait(&bars[ODONE], c & 1, cx))) break;
+      tc_fence_after();
+      float o1[32], o2[32];
+      if (!end) put_state();                          // S X^T of this chunk has read the old copy
+      tmem_ld32(tl + TM_O1 + 32 * wg, o1);
+      tmem_ld32(tl + TM_O2 + 32 * wg, o2);
+      tmem_ld_wait();
+      if (!end) {
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&bars[GO], lane);
+      }
+      // rows [32 wg, + 32) of the chunk, column z
+      const int64_t r0 = (rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C) + 32 * wg;
+      const float* f = rd + 32 * wg + (rev ? C - L : 0);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o1[e] = fmaf(f[e], o1[e], o2[e]);
+      const int cnt = L - 32 * wg;                    // rows that exist
+      if (q.out_f32) {
+        float* o = reinterpret_cast<float*>(q.out) + ((size_t)r0 * p.H + h) * D + z;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e < cnt) o[(size_t)e * p.H * D] = o1[e];
+      } else {
+        // lane pairs swap a value: the even lane stores columns z, z + 1 of row e, the odd one
+        // those of row e + 1
+        const int odd = lane & 1;
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(q.out) +
+                           ((size_t)(r0 + odd) * p.H + h) * D + (z & ~1);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? o1[e] : o1[e + 1], 1);
+          const uint32_t v = odd ? pack_bf16x2(got, o1[e + 1]) : pack_bf16x2(o1[e], got);
+          if (e + odd < cnt) *reinterpret_cast<uint32_t*>(o + (size_t)e * p.H * D) = v;
+        }
+      }
+    }
+    float* dst = !ok ? nullptr : kState ? q.seg_state + uoff : last ? la_exit(p, q, n, h, D) : nullptr;
+    if (dst) {
+      if (q.s_t && !kState) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) dst[(size_t)(64 * wg + e) * D + z] = s[e];
+      } else {
+        float4* v = reinterpret_cast<float4*>(dst + (size_t)z * D + 64 * wg);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          v[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
+      }
+    }
+  } else {
+    reg_dealloc<88>();
+    // ---------------------------------------------------------------- weighted rows in BF16 parts
+    const int t = tid - 384, j0 = t >> 4, ch = t & 15;
+    const uint32_t panel = (uint32_t)(ch >> 3) * PANEL;
+    for (int c = 0; c < nc; ++c) {
+      const int b = c % NS;
+      if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
+      if (c > 0 && !warp_wait(&bars[EDONE + ((c - 1) & 1)], ((c - 1) >> 1) & 1, cx)) break;
+      const int shift = rev ? 0 : (c + 1 == nc ? C - tail : 0);
+      const uint8_t* src = sm + b * STAGE + B_Z + panel;
+      uint8_t* dst = sm + O_SPLIT + panel;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + 8 * k;
+        const uint32_t at = (uint32_t)j * 128u + (uint32_t)(((ch & 7) ^ (j & 7)) << 4);
+        const uint4 v = *reinterpret_cast<const uint4*>(src + at);
+        const float wgt = wr[j + shift];
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = lo_f(in[e]) * wgt, y = hi_f(in[e]) * wgt;
+          o[0][e] = pack_bf16x2(x, y);
+          x -= lo_f(o[0][e]);
+          y -= hi_f(o[0][e]);
+          o[1][e] = pack_bf16x2(x, y);
+          x -= lo_f(o[1][e]);
+          y -= hi_f(o[1][e]);
+          o[2][e] = pack_bf16x2(x, y);
+        }
+        *reinterpret_cast<uint4*>(dst + at) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+        *reinterpret_cast<uint4*>(dst + 2 * PANEL + at) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+        if (nsplit > 2)
+          *reinterpret_cast<uint4*>(dst + 4 * PANEL + at) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bars[SPLIT], lane);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {
+    tmem_relinquish();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
+  const int64_t grid = (int64_t)p.units * p.H * p.npass;
+  if (grid <= 0) return cudaSuccess;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  Maps maps;
+  const int rows = p.B * p.T;
+  bool returns = p.pool != nullptr;
+  for (int i = 0; i < p.npass; ++i) {
+    const LaPass& q = p.pass[i];
+    returns = returns || q.s_out;
+    if (!make_bf16_map(&maps.m[i][0], q.x, rows, q.hx) || !make_bf16_map(&maps.m[i][1], q.y, rows, q.hy) ||
+        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz))
+      return cudaErrorInvalidValue;
+  }
+  auto kern = state_only ? la_tc_kernel<true> : la_tc_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)grid, NT, SMEM, st>>>(maps, p, returns ? 3 : 2);
+  return cudaGetLastError();
+}
+
+}  // namespace sfg

@@ -7,8 +7,7 @@
 //     S' = lam^L S + c (lam^f Y)^T Z   D x 64, each thread D/16 x 4, kept in registers
 // Every product reads one operand as rows that sixteen threads share (a broadcast) and the
 // other as consecutive float4 of the row that the sixteen divide among them.  The state is
-// copied to shared memory once a chunk for the second product.  Powers of lam come from a
-// table formed in FP64; lam^64 is carried as a sum of two floats, so that a state kept over
+// copied to shared memory once a chunk for the second product.  lam^64 is formed in FP64 and carried as a sum of two floats, so that a state kept over
 // thousands of chunks does not drift by the rounding of one factor.
 // Bound by the FP32 rate: about 5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, two
 // thirds of it in S and O, against 2 KB of tokens.
@@ -41,7 +40,7 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
 
 template <int D>
 struct Smem {
-  float X[C][D + 4], Y[C][D + 4], Z[C][ZT + 4], P[C][ZT + 4], S[D][ZT + 4], tab[C + 4];
+  float X[C][D + 4], Y[C][D + 4], Z[C][ZT + 4], P[C][ZT + 4], S[D][ZT + 4], tab[C + 4], carry[4];
 };
 
 // Rows [r0, r0 + L) of one head's columns [c0, c0 + W) into dst (leading dimension ld); the
@@ -90,7 +89,14 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
     return;
   }
   const float d = p.decay[h];
-  if (tid <= C) sm.tab[tid] = (float)la_pow(d, tid);
+  const int nc = (int)((rows + C - 1) / C);
+  const int tail = (int)(rows - (int64_t)(nc - 1) * C);
+  if (tid <= C) sm.tab[tid] = tid == 0 ? 1.f : expf(d * (float)tid);
+  if (tid >= 128 && tid < 130) {                  // lam^64 and lam^tail as sums of two floats
+    const double f = la_pow(d, tid == 128 ? C : tail);
+    sm.carry[2 * (tid - 128)] = (float)f;
+    sm.carry[2 * (tid - 128) + 1] = (float)(f - (double)(float)f);
+  }
 
   // S[y = ty YR + e][z = zc + 4 tx ..]: zeros, the caller's state, or the segment's entry
   float4 s[YR];
@@ -106,9 +112,6 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
                             src[(size_t)(z + 2) * D + y], src[(size_t)(z + 3) * D + y]);
   }
   const int G_x = p.H / q.hx, G_y = p.H / q.hy, G_z = p.H / q.hz;
-  const int nc = (int)((rows + C - 1) / C);
-  float hi = 1.f, lo = 0.f;                       // lam^carry_rows
-  int carry_rows = 0;
   for (int ci = 0; ci < nc; ++ci) {
     const int64_t done = (int64_t)ci * C;
     const int L = (int)(rows - done < C ? rows - done : C);
@@ -196,12 +199,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
       }
     }
     // S = lam^L S + c sum_r lam^f(r) y_r z_r
-    if (L != carry_rows) {
-      const double full = la_pow(d, L);
-      hi = (float)full;
-      lo = (float)(full - (double)hi);
-      carry_rows = L;
-    }
+    const float hi = sm.carry[ci + 1 == nc ? 2 : 0], lo = sm.carry[ci + 1 == nc ? 3 : 1];
     float4 acc[YR];
 #pragma unroll
     for (int e = 0; e < YR; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -286,8 +284,14 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
                                s_in[(size_t)(y + 2) * D + z], s_in[(size_t)(y + 3) * D + z]);
     else e = ld4(s_in + at);
   }
-  const double full = la_pow(p.decay[h], p.seg);
-  const float hi = (float)full, lo = (float)(full - (double)hi);
+  __shared__ float pow_s[2];
+  if (tid == 0) {
+    const double full = la_pow(p.decay[h], p.seg);
+    pow_s[0] = (float)full;
+    pow_s[1] = (float)(full - (double)pow_s[0]);
+  }
+  __syncthreads();
+  const float hi = pow_s[0], lo = pow_s[1];
   float* base = q.seg_state + ((size_t)u0 * p.H + h) * D * D + at;
   const size_t step = (size_t)p.H * D * D;
   float4 cur = segs > 1 ? ld4(base) : e;

@@ -45,27 +45,29 @@ constexpr uint32_t PANEL = 8192;                 // 64 rows x 128 bytes
 constexpr uint32_t B_Y = 0, B_X = PANEL;         // panel 0 of Y and X; panel 1 two panels on
 constexpr uint32_t B_Z = 4 * PANEL, STAGE = 6 * PANEL;
 constexpr uint32_t O_SPLIT = NS * STAGE;         // three weighted tiles of two panels
-constexpr uint32_t O_P = O_SPLIT + 6 * PANEL;    // P [64][64]
-constexpr uint32_t O_TAB = O_P + PANEL;          // lam^n [64], b lam^e [128], c lam^f [128], carry [4]
-constexpr uint32_t O_BAR = O_TAB + 1536;
+constexpr uint32_t O_P = O_SPLIT + 6 * PANEL;    // P [64][64], two buffers
+constexpr uint32_t O_OUT = O_P + 2 * PANEL;      // results, [32 rows][32 columns] of each warp
+// b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4]
+constexpr uint32_t O_TAB = O_OUT + 16384;
+constexpr uint32_t O_BAR = O_TAB + 1280;
 constexpr uint32_t SMEM = O_BAR + 256 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
 
-constexpr uint32_t TM_E = 0, TM_SB = 256, TM_P = 320, TM_O1 = 384, TM_O2 = 448;
+constexpr uint32_t TM_E = 0, TM_SB = 128, TM_P = 192, TM_O1 = 320, TM_O2 = 384;   // P: two
 
 constexpr uint32_t ID_QK = idesc_bf16(128, 64, false, false);
 constexpr uint32_t ID_E = idesc_bf16(128, 128, true, true);
 constexpr uint32_t ID_O1 = idesc_bf16(128, 64, false, false);   // A in TMEM
 constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 
-enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY, SPLIT, EDONE,
-       EFREE = EDONE + 2, ODONE = EFREE + 2, GO, TBL, DRAIN, NBAR };
+enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY = QKDONE + 2,
+       SPLIT = PREADY + 2, EHALF = SPLIT + 2, EDONE, EFREE, ODONE, GO, TBL, DRAIN, NBAR };
 static_assert(8 * NBAR + 8 <= 256, "barriers");
 
-constexpr unsigned long long WAIT_NS = 2000000000ull;
+constexpr long long WAIT_CYCLES = 4000000000ll;   // about 2 s
 
 struct Maps {
-  CUtensorMap m[3][3];   // x, y, z of each pass
+  CUtensorMap m[3][4];   // x, y, z and the output of each pass
 };
 
 struct Cx {
@@ -75,11 +77,11 @@ struct Cx {
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Cx& cx) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
     if (*cx.abort) return false;
-    if (globaltimer_ns() - t0 > WAIT_NS) {
+    if (clock64() - t0 > WAIT_CYCLES) {
       *cx.abort = 1;
       if (cx.status) {
         atomicCAS(cx.status, 0, (int)SF_ERR_TIMEOUT);
@@ -104,6 +106,15 @@ __device__ __forceinline__ uint64_t kstep_k(int kk) {   // panels 16 KB apart
 }
 __device__ __forceinline__ uint64_t kstep_mn(int kk) { return (uint64_t)(kk * 2048 >> 4); }
 
+// Two FP32 multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -113,10 +124,9 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(sm);
-  float* tab = reinterpret_cast<float*>(sm + O_TAB);
-  float* rd = tab + 64;
-  float* wr = tab + 192;
-  float* carry = tab + 320;
+  float* rd = reinterpret_cast<float*>(sm + O_TAB);   // [2][64]
+  float* wr = rd + 128;                               // [2][64]
+  float* carry = rd + 256;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + O_BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR);
   int* abort_s = reinterpret_cast<int*>(sm + O_BAR + 8 * NBAR + 4);
@@ -153,29 +163,35 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i)
-      mbar_init(&bars[i], i == PREADY ? 2 : i == SPLIT ? 4 : i == GO || i == EFREE || i == EFREE + 1 ? 8 : 1);
+      mbar_init(&bars[i], i == PREADY || i == PREADY + 1 ? 2 : i == SPLIT || i == SPLIT + 1 ? 4
+                          : i == GO || i == EFREE ? 8 : 1);
     *abort_s = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.m[pi][1]);
     prefetch_tmap(&maps.m[pi][2]);
-    if (!kState) prefetch_tmap(&maps.m[pi][0]);
+    if (!kState) {
+      prefetch_tmap(&maps.m[pi][0]);
+      prefetch_tmap(&maps.m[pi][3]);
+    }
   }
   if (warp == 0) tmem_alloc(tslot, 512);
-  if (tid >= 64 && tid < 128) {
-    const int i = tid - 64;
-    auto pw = [&](int e) { return e == 0 ? 1.f : expf(d * (float)e); };
-    tab[i] = pw(i);
-    rd[i] = q.b * pw(rev ? 63 - i : i + 1);
-    wr[i] = q.c * pw(rev ? i + 1 : 63 - i);
-    rd[64 + i] = wr[64 + i] = 0.f;
+  auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
+  if (tid >= 128 && tid < 256) {
+    const int i = tid & 63, L = tid < 192 ? C : tail, t = tid - 128;
+    rd[t] = i < L ? q.b * pw(rev ? L - 1 - i : i + 1) : 0.f;
+    wr[t] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
   }
+  if (!kState)   // P on the far side of the diagonal stays zero
+    for (int i = tid; i < 2 * (int)PANEL / 16; i += NT)
+      *reinterpret_cast<uint4*>(sm + O_P + 16 * i) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tslot;
 
   if (warp < 4) {
-    reg_dealloc<88>();
+    reg_dealloc<104>();
     if (warp == 0) {
       // -------------------------------------------------------------- loader
       const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
@@ -226,56 +242,87 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------------- issuer
-      if (lane == 0) {
-        bool ok = true;
-        const uint64_t dp = sdesc_sw128(sb + O_P, 0, 1024);
-        for (int c = 0; c < nc && ok; ++c) {
-          const int b = c % NS;
-          const uint32_t st = sb + b * STAGE;
-          if (!(ok = wait_bar(&bars[FULL + b], (c / NS) & 1, cx))) break;
-          tc_fence_after();
-          if (!kState) {
-            const uint64_t dy = sdesc_sw128(st + B_Y, 0, 1024);
+      // (the whole warp waits; one elected lane issues)
+      const uint64_t dw = sdesc_sw128(sb + O_SPLIT, PANEL, 1024);
+      auto issue_qk = [&](int c) {
+        const uint64_t dy = sdesc_sw128(sb + (c % NS) * STAGE + B_Y, 0, 1024);
+        const uint32_t t = tm + TM_P + 64 * (c & 1);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16(tm + TM_P, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
-            mma_commit(&bars[QKDONE]);
-          }
-          if (!(ok = wait_bar(&bars[SPLIT], c & 1, cx))) break;
-          if (kState && c >= 2 && !(ok = wait_bar(&bars[EFREE + (c & 1)], ((c - 2) >> 1) & 1, cx))) break;
-          tc_fence_after();
-          {
-            const uint32_t e = tm + TM_E + 128 * (c & 1);
-            const uint64_t dy = sdesc_sw128(st + B_Y, 2 * PANEL, 1024);
-            const uint64_t dz = sdesc_sw128(sb + O_SPLIT, PANEL, 1024);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16(t, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
+          mma_commit(&bars[QKDONE + (c & 1)]);
+        }
+        __syncwarp();
+      };
+      auto full = [&](int c) { return warp_wait(&bars[FULL + c % NS], (c / NS) & 1, cx); };
+      bool ok = nc == 0 || full(0);
+      if (!kState && nc > 0 && ok) issue_qk(0);
+      for (int c = 0; c < nc && ok; ++c) {
+        const int b = c % NS;
+        const uint32_t st = sb + b * STAGE;
+        if (kState && !(ok = full(c))) break;
+        // E, in two halves of 32 rows: the split warps refill the first under the second
+        const uint64_t dy = sdesc_sw128(st + B_Y, 2 * PANEL, 1024);
+        if (c > 0 && !(ok = warp_wait(&bars[EFREE], (c - 1) & 1, cx))) break;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              for (int sp = 0; sp < nsplit; ++sp)
-                mma_bf16(e, dz + kstep_mn(kk) + (uint64_t)(sp * 2 * PANEL >> 4), dy + kstep_mn(kk), ID_E,
-                         kk + sp > 0);
-            mma_commit(&bars[EDONE + (c & 1)]);
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!(ok = warp_wait(&bars[SPLIT + hf], c & 1, cx))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int sp = 0; sp < 3; ++sp)
+              if (sp < nsplit) {
+#pragma unroll
+                for (int kk = 2 * hf; kk < 2 * hf + 2; ++kk)
+                  mma_bf16(tm + TM_E, dw + kstep_mn(kk) + (uint64_t)(sp * 2 * PANEL >> 4),
+                           dy + kstep_mn(kk), ID_E, kk + sp > 0);
+              }
+            mma_commit(&bars[hf ? EDONE : EHALF]);
+            if (kState && hf) mma_commit(&bars[FREE + b]);
           }
-          if (!kState) {
-            if (!(ok = wait_bar(&bars[GO], c & 1, cx))) break;
-            tc_fence_after();
-            const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (!kState) {
+          if (!(ok = warp_wait(&bars[GO], c & 1, cx))) break;
+          tc_fence_after();
+          const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
-            if (!(ok = wait_bar(&bars[PREADY], c & 1, cx))) break;
-            tc_fence_after();
-            const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
+          }
+          __syncwarp();
+          // the next chunk's QK goes ahead of this one's O2 (P takes as long as a step) if its
+          // rows are there
+          bool ahead = false;
+          if (c + 1 < nc) {
+            ahead = __all_sync(0xffffffffu, mbar_test(&bars[FULL + (c + 1) % NS], ((c + 1) / NS) & 1));
+            if (ahead) issue_qk(c + 1);
+          }
+          if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
+          tc_fence_after();
+          const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
+          const uint64_t dp = sdesc_sw128(sb + O_P + (c & 1) * PANEL, 0, 1024);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)(kk * 2), ID_O2, kk > 0);
             mma_commit(&bars[ODONE]);
+            mma_commit(&bars[FREE + b]);
           }
-          mma_commit(&bars[FREE + b]);
+          __syncwarp();
+          if (c + 1 < nc && !ahead) {
+            if (!(ok = full(c + 1))) break;
+            issue_qk(c + 1);
+          }
         }
-        // leave no product running into the TMEM and barriers that go away
-        mma_commit(&bars[DRAIN]);
-        mbar_wait(&bars[DRAIN], 0, 100000000ull);
       }
+      // leave no product running into the TMEM and barriers that go away
+      if (elect_one()) mma_commit(&bars[DRAIN]);
+      if (lane == 0) mbar_wait(&bars[DRAIN], 0, 100000000ull);
       __syncwarp();
     } else {
       // -------------------------------------------------------------- P
@@ -291,68 +338,73 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         if (lane == 0) mbar_arrive(&bars[TBL]);
       }
       if (!kState) {
+        // row r of P; the factors a lam^|r-s| stay in registers.  The half on the far side of
+        // the diagonal (32 columns of one warp) is never touched: it stays zero.
         const int r = (warp - 2) * 32 + lane;          // TMEM lane 64 + r
+        float f[2][32];
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int s = 32 * half + e, gap = rev ? s - r : r - s;
+            f[half][e] = gap >= 0 ? q.a * pw(gap) : 0.f;
+          }
         const uint32_t tl = tm + TM_P + ((uint32_t)(warp * 32) << 16);
-        uint8_t* row = sm + O_P + r * 128;
-        const float a = q.a;
         for (int c = 0; c < nc; ++c) {
-          if (!warp_wait(&bars[QKDONE], c & 1, cx)) break;
+          if (!warp_wait(&bars[QKDONE + (c & 1)], (c >> 1) & 1, cx)) break;
           tc_fence_after();
+          uint8_t* row = sm + O_P + (c & 1) * PANEL + r * 128;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            // 32 columns; the half on the far side of the diagonal is all masked
-            const bool none = rev ? half == 0 && warp == 3 : half == 1 && warp == 2;
-            float x[32];
-            if (none) {
+            if (rev ? half == 0 && warp == 3 : half == 1 && warp == 2) continue;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = 0.f;
-            } else {
-              tmem_ld32(tl + 32 * half, x);
+            for (int k = 0; k < 2; ++k) {
+              float x[16];
+              tmem_ld16(tl + 64 * (c & 1) + 32 * half + 16 * k, x);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int gap = rev ? 32 * half + e - r : r - (32 * half + e);
-                x[e] = gap >= 0 ? x[e] * (a * tab[gap & 63]) : 0.f;
+              for (int ch = 0; ch < 2; ++ch) {
+                const float* g = &f[half][16 * k + 8 * ch];
+                const float* y = x + 8 * ch;
+                uint4 v;
+                v.x = pack_bf16x2(y[0] * g[0], y[1] * g[1]);
+                v.y = pack_bf16x2(y[2] * g[2], y[3] * g[3]);
+                v.z = pack_bf16x2(y[4] * g[4], y[5] * g[5]);
+                v.w = pack_bf16x2(y[6] * g[6], y[7] * g[7]);
+                *reinterpret_cast<uint4*>(row + (((4 * half + 2 * k + ch) ^ (r & 7)) << 4)) = v;
               }
-            }
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              uint4 v;
-              v.x = pack_bf16x2(x[8 * ch], x[8 * ch + 1]);
-              v.y = pack_bf16x2(x[8 * ch + 2], x[8 * ch + 3]);
-              v.z = pack_bf16x2(x[8 * ch + 4], x[8 * ch + 5]);
-              v.w = pack_bf16x2(x[8 * ch + 6], x[8 * ch + 7]);
-              *reinterpret_cast<uint4*>(row + (((4 * half + ch) ^ (r & 7)) << 4)) = v;
             }
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          warp_arrive(&bars[PREADY], lane);
+          warp_arrive(&bars[PREADY + (c & 1)], lane);
         }
       }
     }
   } else if (warp < 12) {
-    reg_alloc<168>();
+    reg_alloc<160>();
     // ---------------------------------------------------------------- state and results
     const int wg = (warp - 4) >> 2;
     const int z = ((warp & 3) << 5) + lane;
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    float s[64];
+    float2 s[32];                                       // columns 64 wg + 2 e, + 1 of row z
     const size_t uoff = ((size_t)u * p.H + h) * D * D;
     {
       const float* src = kState ? nullptr : split ? q.seg_state + uoff : s_in;
       if (!src) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) s[e] = 0.f;
+        for (int e = 0; e < 32; ++e) s[e] = make_float2(0.f, 0.f);
       } else if (q.s_t && !split) {                   // stored [y][z]
 #pragma unroll
-        for (int e = 0; e < 64; ++e) s[e] = src[(size_t)(64 * wg + e) * D + z];
+        for (int e = 0; e < 32; ++e)
+          s[e] = make_float2(src[(size_t)(64 * wg + 2 * e) * D + z], src[(size_t)(64 * wg + 2 * e + 1) * D + z]);
       } else {
         const float4* v = reinterpret_cast<const float4*>(src + (size_t)z * D + 64 * wg);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float4 f = v[e];
-          s[4 * e] = f.x; s[4 * e + 1] = f.y; s[4 * e + 2] = f.z; s[4 * e + 3] = f.w;
+          s[2 * e] = make_float2(f.x, f.y);
+          s[2 * e + 1] = make_float2(f.z, f.w);
         }
       }
     }
@@ -361,7 +413,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       for (int k = 0; k < 2; ++k) {
         uint32_t v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]);
+        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(s[16 * k + e].x, s[16 * k + e].y);
         tmem_st16(tl + TM_SB + 32 * wg + 16 * k, v);
       }
     };
@@ -372,25 +424,28 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       warp_arrive(&bars[GO], lane);
     }
     bool ok = nc == 0 || warp_wait(&bars[TBL], 0, cx);
+    uint8_t* stage = sm + O_OUT + (warp - 4) * 2048;
     for (int c = 0; c < nc && ok; ++c) {
       const bool end = c + 1 == nc;
       const int L = end ? tail : C;
-      if (!(ok = warp_wait(&bars[EDONE + (c & 1)], (c >> 1) & 1, cx))) break;
+      if (!(ok = warp_wait(&bars[EDONE], c & 1, cx))) break;
       tc_fence_after();
-      const float fh = carry[end ? 2 : 0], fl = carry[end ? 3 : 1];
+      const float2 fh = make_float2(carry[end ? 2 : 0], carry[end ? 2 : 0]);
+      const float2 fl = make_float2(carry[end ? 3 : 1], carry[end ? 3 : 1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x[32];
-        tmem_ld32(tl + TM_E + 128 * (c & 1) + 64 * wg + 32 * k, x);
+        tmem_ld32(tl + TM_E + 64 * wg + 32 * k, x);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s[32 * k + e] = fmaf(fh, s[32 * k + e], fmaf(fl, s[32 * k + e], x[e]));
+        for (int e = 0; e < 16; ++e) {
+          float2& v = s[16 * k + e];
+          v = fma2(fh, v, fma2(fl, v, make_float2(x[2 * e], x[2 * e + 1])));
+        }
       }
-      if (kState) {
-        tc_fence_before();
-        warp_arrive(&bars[EFREE + (c & 1)], lane);
-        continue;
-      }
+      tc_fence_before();
+      warp_arrive(&bars[EFREE], lane);
+      if (kState) continue;
       if (!(ok = warp_wait(&bars[ODONE], c & 1, cx))) break;
       tc_fence_after();
       float o1[32], o2[32];
@@ -405,26 +460,46 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       }
       // rows [32 wg, + 32) of the chunk, column z
       const int64_t r0 = (rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C) + 32 * wg;
-      const float* f = rd + 32 * wg + (rev ? C - L : 0);
+      const float4* f4 = reinterpret_cast<const float4*>(rd + (end ? 64 : 0) + 32 * wg);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o1[e] = fmaf(f[e], o1[e], o2[e]);
+      for (int e = 0; e < 32; e += 4) {
+        const float4 f = f4[e / 4];
+        o1[e] = fmaf(f.x, o1[e], o2[e]);
+        o1[e + 1] = fmaf(f.y, o1[e + 1], o2[e + 1]);
+        o1[e + 2] = fmaf(f.z, o1[e + 2], o2[e + 2]);
+        o1[e + 3] = fmaf(f.w, o1[e + 3], o2[e + 3]);
+      }
       const int cnt = L - 32 * wg;                    // rows that exist
       if (q.out_f32) {
         float* o = reinterpret_cast<float*>(q.out) + ((size_t)r0 * p.H + h) * D + z;
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           if (e < cnt) o[(size_t)e * p.H * D] = o1[e];
-      } else {
-        // lane pairs swap a value: the even lane stores columns z, z + 1 of row e, the odd one
-        // those of row e + 1
-        const int odd = lane & 1;
-        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(q.out) +
-                           ((size_t)(r0 + odd) * p.H + h) * D + (z & ~1);
+        continue;
+      }
+      // lane pairs swap a value: the even lane gets columns z, z + 1 of row e, the odd one those
+      // of row e + 1.  A warp's 32 rows go out as one bulk store of 64-byte rows; the rows of a
+      // short chunk one by one.
+      const int odd = lane & 1;
+      if (lane == 0) bulk_wait_read_all();            // the last chunk's store has left the stage
+      __syncwarp();
+      uint32_t* sr = reinterpret_cast<uint32_t*>(stage + odd * 64 + (lane >> 1) * 4);
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(q.out) +
+                         ((size_t)(r0 + odd) * p.H + h) * D + (z & ~1);
+      const bool whole = L == C;
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? o1[e] : o1[e + 1], 1);
-          const uint32_t v = odd ? pack_bf16x2(got, o1[e + 1]) : pack_bf16x2(o1[e], got);
-          if (e + odd < cnt) *reinterpret_cast<uint32_t*>(o + (size_t)e * p.H * D) = v;
+      for (int e = 0; e < 32; e += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? o1[e] : o1[e + 1], 1);
+        const uint32_t v = odd ? pack_bf16x2(got, o1[e + 1]) : pack_bf16x2(o1[e], got);
+        if (whole) sr[16 * e] = v;
+        else if (e + odd < cnt) *reinterpret_cast<uint32_t*>(o + (size_t)e * p.H * D) = v;
+      }
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.m[pi][3], stage, 32 * (warp & 3), h, (int)r0);
+          bulk_commit();
         }
       }
     }
@@ -432,14 +507,18 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     if (dst) {
       if (q.s_t && !kState) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) dst[(size_t)(64 * wg + e) * D + z] = s[e];
+        for (int e = 0; e < 32; ++e) {
+          dst[(size_t)(64 * wg + 2 * e) * D + z] = s[e].x;
+          dst[(size_t)(64 * wg + 2 * e + 1) * D + z] = s[e].y;
+        }
       } else {
         float4* v = reinterpret_cast<float4*>(dst + (size_t)z * D + 64 * wg);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          v[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
+        for (int e = 0; e < 16; ++e) v[e] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
       }
     }
+    if (lane == 0) bulk_wait_all();                   // the stores have landed
+    __syncwarp();
   } else {
     reg_dealloc<88>();
     // ---------------------------------------------------------------- weighted rows in BF16 parts
@@ -448,36 +527,41 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     for (int c = 0; c < nc; ++c) {
       const int b = c % NS;
       if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
-      if (c > 0 && !warp_wait(&bars[EDONE + ((c - 1) & 1)], ((c - 1) >> 1) & 1, cx)) break;
-      const int shift = rev ? 0 : (c + 1 == nc ? C - tail : 0);
+      const float* wt = wr + (c + 1 == nc ? 64 : 0) + j0;
       const uint8_t* src = sm + b * STAGE + B_Z + panel;
       uint8_t* dst = sm + O_SPLIT + panel;
+      bool ok = true;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = j0 + 8 * k;
-        const uint32_t at = (uint32_t)j * 128u + (uint32_t)(((ch & 7) ^ (j & 7)) << 4);
-        const uint4 v = *reinterpret_cast<const uint4*>(src + at);
-        const float wgt = wr[j + shift];
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[3][4];
+      for (int hf = 0; hf < 2; ++hf) {                // the last chunk's products are done with it
+        if (c > 0 && !(ok = warp_wait(&bars[hf ? EDONE : EHALF], (c - 1) & 1, cx))) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = lo_f(in[e]) * wgt, y = hi_f(in[e]) * wgt;
-          o[0][e] = pack_bf16x2(x, y);
-          x -= lo_f(o[0][e]);
-          y -= hi_f(o[0][e]);
-          o[1][e] = pack_bf16x2(x, y);
-          x -= lo_f(o[1][e]);
-          y -= hi_f(o[1][e]);
-          o[2][e] = pack_bf16x2(x, y);
+        for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
+          const int j = j0 + 8 * k;
+          const uint32_t at = (uint32_t)j * 128u + (uint32_t)(((ch & 7) ^ (j & 7)) << 4);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + at);
+          const float wgt = wt[8 * k];
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[3][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = lo_f(in[e]) * wgt, y = hi_f(in[e]) * wgt;
+            o[0][e] = pack_bf16x2(x, y);
+            x -= lo_f(o[0][e]);
+            y -= hi_f(o[0][e]);
+            o[1][e] = pack_bf16x2(x, y);
+            x -= lo_f(o[1][e]);
+            y -= hi_f(o[1][e]);
+            o[2][e] = pack_bf16x2(x, y);
+          }
+          *reinterpret_cast<uint4*>(dst + at) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          *reinterpret_cast<uint4*>(dst + 2 * PANEL + at) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+          if (nsplit > 2)
+            *reinterpret_cast<uint4*>(dst + 4 * PANEL + at) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
         }
-        *reinterpret_cast<uint4*>(dst + at) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-        *reinterpret_cast<uint4*>(dst + 2 * PANEL + at) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-        if (nsplit > 2)
-          *reinterpret_cast<uint4*>(dst + 4 * PANEL + at) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+        fence_proxy_async_smem();
+        warp_arrive(&bars[SPLIT + hf], lane);
       }
-      fence_proxy_async_smem();
-      warp_arrive(&bars[SPLIT], lane);
+      if (!ok) break;
     }
   }
   tc_fence_before();
@@ -502,7 +586,8 @@ cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
     const LaPass& q = p.pass[i];
     returns = returns || q.s_out;
     if (!make_bf16_map(&maps.m[i][0], q.x, rows, q.hx) || !make_bf16_map(&maps.m[i][1], q.y, rows, q.hy) ||
-        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz))
+        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz) ||
+        (!q.out_f32 && !make_bf16_store_map(&maps.m[i][3], q.out, rows, p.H)))
       return cudaErrorInvalidValue;
   }
   auto kern = state_only ? la_tc_kernel<true> : la_tc_kernel<false>;

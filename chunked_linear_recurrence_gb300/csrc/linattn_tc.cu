@@ -61,13 +61,13 @@ constexpr uint32_t ID_O1 = idesc_bf16(128, 64, false, false);   // A in TMEM
 constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 
 enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY = QKDONE + 2,
-       SPLIT = PREADY + 2, EHALF = SPLIT + 2, EDONE, EFREE, ODONE, GO, TBL, DRAIN, NBAR };
+       SPLIT = PREADY + 2, EHALF = SPLIT + 2, EDONE, EFREE, ODONE, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
 static_assert(8 * NBAR + 8 <= 256, "barriers");
 
 constexpr long long WAIT_CYCLES = 4000000000ll;   // about 2 s
 
 struct Maps {
-  CUtensorMap m[3][4];   // x, y, z and the output of each pass
+  CUtensorMap m[3][3];   // x, y, z of each pass
 };
 
 struct Cx {
@@ -115,12 +115,25 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         "l"(reinterpret_cast<unsigned long long&>(c)));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+// a - b
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  return fma2(b, make_float2(-1.f, -1.f), a);
+}
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-template <bool kState>
+__device__ __forceinline__ float2 unpack2(uint32_t u) { return make_float2(lo_f(u), hi_f(u)); }
+
+template <bool kState, int NSP>
 __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Maps maps,
-                                                      const LaParams p, const int nsplit) {
+                                                      const LaParams p) {
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(sm);
@@ -164,15 +177,12 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i)
       mbar_init(&bars[i], i == PREADY || i == PREADY + 1 ? 2 : i == SPLIT || i == SPLIT + 1 ? 4
-                          : i == GO || i == EFREE ? 8 : 1);
+                          : i == GO || i == EFREE ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
     *abort_s = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.m[pi][1]);
     prefetch_tmap(&maps.m[pi][2]);
-    if (!kState) {
-      prefetch_tmap(&maps.m[pi][0]);
-      prefetch_tmap(&maps.m[pi][3]);
-    }
+    if (!kState) prefetch_tmap(&maps.m[pi][0]);
   }
   if (warp == 0) tmem_alloc(tslot, 512);
   auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
@@ -193,57 +203,85 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   if (warp < 4) {
     reg_dealloc<104>();
     if (warp == 0) {
-      // -------------------------------------------------------------- loader
+      // -------------------------------------------------------------- loader, issuer of E
       const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
-      bool ok = true;
+      const uint64_t dw = sdesc_sw128(sb + O_SPLIT, PANEL, 1024);
       int issued = 0;
-      for (int c = 0; c < nc && ok; ++c) {
-        const int b = c % NS;
-        const int L = c + 1 == nc ? tail : C;
+      auto load = [&](int c) {
+        const int b = c % NS, L = c + 1 == nc ? tail : C;
         const int r0 = (int)(rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C);
         uint8_t* st = sm + b * STAGE;
-        if (c >= NS) {
-          bool f = true;
-          if (lane == 0) f = wait_bar(&bars[FREE + b], ((c - NS) / NS) & 1, cx);
-          if (!(ok = __shfl_sync(0xffffffffu, f, 0) != 0)) break;
-        }
         uint64_t* bar = L < C ? &bars[LANDED + b] : &bars[FULL + b];   // (the last chunk only)
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, (kState ? 4 : 6) * PANEL);
 #pragma unroll
           for (int pp = 0; pp < 2; ++pp) {
             tma_load_3d(st + B_Y + 2 * pp * PANEL, &maps.m[pi][1], bar, 64 * pp, hy, r0);
-            if (!kState) tma_load_3d(st + B_X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
             tma_load_3d(st + B_Z + pp * PANEL, &maps.m[pi][2], bar, 64 * pp, hz, r0);
+            if (!kState) tma_load_3d(st + B_X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
           }
         }
+        __syncwarp();
         issued = c + 1;
-        if (L < C) {
-          // rows past the end (other tokens, or NaN padding) must not reach the products
-          bool f = true;
-          if (lane == 0) f = wait_bar(bar, 0, cx);
-          if (!(ok = __shfl_sync(0xffffffffu, f, 0) != 0)) break;
-          const int per = (C - L) * 8;               // 16-byte pieces of a panel
-          for (int i = lane; i < 4 * per; i += 32) {
-            const int t = i / per, rr = i % per;
-            uint8_t* base = st + (t < 2 ? B_Y + 2 * t * PANEL : B_Z + (t - 2) * PANEL);
-            *reinterpret_cast<uint4*>(base + (L + rr / 8) * 128 + (rr % 8) * 16) = make_uint4(0, 0, 0, 0);
+      };
+      // A short last chunk: rows past the end (other tokens, or NaN padding) must not reach the
+      // products.
+      auto trim = [&]() {
+        const int b = (nc - 1) % NS;
+        if (!warp_wait(&bars[LANDED + b], 0, cx)) return false;
+        uint8_t* st = sm + b * STAGE;
+        const int per = (C - tail) * 8;                // 16-byte pieces of a panel
+        for (int i = lane; i < 4 * per; i += 32) {
+          const int t = i / per, rr = i % per;
+          uint8_t* base = st + (t < 2 ? B_Y + 2 * t * PANEL : B_Z + (t - 2) * PANEL);
+          *reinterpret_cast<uint4*>(base + (tail + rr / 8) * 128 + (rr % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&bars[FULL + b], lane);
+        return true;
+      };
+      for (int c = 0; c < NS && c < nc; ++c) load(c);
+      bool ok = nc != 1 || tail == C || trim();
+      for (int c = 0; c < nc && ok; ++c) {
+        const int b = c % NS;
+        // E in two halves of 32 rows: the split warps refill the first under the second
+        const uint64_t dy = sdesc_sw128(sb + b * STAGE + B_Y, 2 * PANEL, 1024);
+        if (c > 0 && !(ok = warp_wait(&bars[EFREE], (c - 1) & 1, cx))) break;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          // (the split warps have waited for the rows themselves)
+          if (!(ok = warp_wait(&bars[SPLIT + hf], c & 1, cx))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int sp = 0; sp < NSP; ++sp)
+#pragma unroll
+              for (int kk = 2 * hf; kk < 2 * hf + 2; ++kk)
+                mma_bf16(tm + TM_E, dw + kstep_mn(kk) + (uint64_t)(sp * 2 * PANEL >> 4),
+                         dy + kstep_mn(kk), ID_E, kk + sp > 0);
+            mma_commit(&bars[hf ? EDONE : EHALF]);
+            if (hf) mma_commit(&bars[FREE + b]);
           }
-          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[FULL + b]);
+        }
+        if (!ok) break;
+        if (c + 2 == nc && tail < C && !(ok = trim())) break;
+        if (c > 0 && c + 2 < nc) {
+          if (!(ok = warp_wait(&bars[FREE + (c + 2) % NS], ((c - 1) / NS) & 1, cx))) break;
+          load(c + 2);
         }
       }
-      if (lane == 0 && !ok)   // let the copies in flight land
+      if (!ok)   // let the copies in flight land
         for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
           if (c + 1 == nc && tail < C) mbar_wait(&bars[LANDED + c % NS], 0, 100000000ull);
           else mbar_wait(&bars[FULL + c % NS], (c / NS) & 1, 100000000ull);
         }
+      if (elect_one()) mma_commit(&bars[DRAIN]);
+      mbar_wait(&bars[DRAIN], 0, 100000000ull);
       __syncwarp();
     } else if (warp == 1) {
-      // -------------------------------------------------------------- issuer
+      // -------------------------------------------------------------- issuer of QK, O1, O2
       // (the whole warp waits; one elected lane issues)
-      const uint64_t dw = sdesc_sw128(sb + O_SPLIT, PANEL, 1024);
       auto issue_qk = [&](int c) {
         const uint64_t dy = sdesc_sw128(sb + (c % NS) * STAGE + B_Y, 0, 1024);
         const uint32_t t = tm + TM_P + 64 * (c & 1);
@@ -257,72 +295,40 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         __syncwarp();
       };
       auto full = [&](int c) { return warp_wait(&bars[FULL + c % NS], (c / NS) & 1, cx); };
-      bool ok = nc == 0 || full(0);
-      if (!kState && nc > 0 && ok) issue_qk(0);
+      bool ok = !kState && nc > 0 && full(0);
+      if (ok) issue_qk(0);
       for (int c = 0; c < nc && ok; ++c) {
         const int b = c % NS;
         const uint32_t st = sb + b * STAGE;
-        if (kState && !(ok = full(c))) break;
-        // E, in two halves of 32 rows: the split warps refill the first under the second
-        const uint64_t dy = sdesc_sw128(st + B_Y, 2 * PANEL, 1024);
-        if (c > 0 && !(ok = warp_wait(&bars[EFREE], (c - 1) & 1, cx))) break;
+        if (!(ok = warp_wait(&bars[GO], c & 1, cx))) break;
+        tc_fence_after();
+        const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!(ok = warp_wait(&bars[SPLIT + hf], c & 1, cx))) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int sp = 0; sp < 3; ++sp)
-              if (sp < nsplit) {
-#pragma unroll
-                for (int kk = 2 * hf; kk < 2 * hf + 2; ++kk)
-                  mma_bf16(tm + TM_E, dw + kstep_mn(kk) + (uint64_t)(sp * 2 * PANEL >> 4),
-                           dy + kstep_mn(kk), ID_E, kk + sp > 0);
-              }
-            mma_commit(&bars[hf ? EDONE : EHALF]);
-            if (kState && hf) mma_commit(&bars[FREE + b]);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
         }
-        if (!ok) break;
-        if (!kState) {
-          if (!(ok = warp_wait(&bars[GO], c & 1, cx))) break;
-          tc_fence_after();
-          const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
-          if (elect_one()) {
+        __syncwarp();
+        if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
+        tc_fence_after();
+        const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
+        const uint64_t dp = sdesc_sw128(sb + O_P + (c & 1) * PANEL, 0, 1024);
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
-          }
-          __syncwarp();
-          // the next chunk's QK goes ahead of this one's O2 (P takes as long as a step) if its
-          // rows are there
-          bool ahead = false;
-          if (c + 1 < nc) {
-            ahead = __all_sync(0xffffffffu, mbar_test(&bars[FULL + (c + 1) % NS], ((c + 1) / NS) & 1));
-            if (ahead) issue_qk(c + 1);
-          }
-          if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
-          tc_fence_after();
-          const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
-          const uint64_t dp = sdesc_sw128(sb + O_P + (c & 1) * PANEL, 0, 1024);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)(kk * 2), ID_O2, kk > 0);
-            mma_commit(&bars[ODONE]);
-            mma_commit(&bars[FREE + b]);
-          }
-          __syncwarp();
-          if (c + 1 < nc && !ahead) {
-            if (!(ok = full(c + 1))) break;
-            issue_qk(c + 1);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)(kk * 2), ID_O2, kk > 0);
+          mma_commit(&bars[ODONE]);
+          mma_commit(&bars[FREE + b]);
+        }
+        __syncwarp();
+        // the next chunk's QK, under the state warps' turn
+        if (c + 1 < nc) {
+          if (!(ok = full(c + 1))) break;
+          issue_qk(c + 1);
         }
       }
-      // leave no product running into the TMEM and barriers that go away
-      if (elect_one()) mma_commit(&bars[DRAIN]);
-      if (lane == 0) mbar_wait(&bars[DRAIN], 0, 100000000ull);
+      if (elect_one()) mma_commit(&bars[DRAIN + 1]);
+      mbar_wait(&bars[DRAIN + 1], 0, 100000000ull);
       __syncwarp();
     } else {
       // -------------------------------------------------------------- P
@@ -477,31 +483,27 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           if (e < cnt) o[(size_t)e * p.H * D] = o1[e];
         continue;
       }
-      // lane pairs swap a value: the even lane gets columns z, z + 1 of row e, the odd one those
-      // of row e + 1.  A warp's 32 rows go out as one bulk store of 64-byte rows; the rows of a
-      // short chunk one by one.
+      // lane pairs swap a value (the even lane gets columns z, z + 1 of row e, the odd one those
+      // of row e + 1) and the warp's 32 x 32 tile is turned in shared memory, so that the rows
+      // leave 16 bytes a lane, eight rows a store
       const int odd = lane & 1;
-      if (lane == 0) bulk_wait_read_all();            // the last chunk's store has left the stage
-      __syncwarp();
       uint32_t* sr = reinterpret_cast<uint32_t*>(stage + odd * 64 + (lane >> 1) * 4);
-      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(q.out) +
-                         ((size_t)(r0 + odd) * p.H + h) * D + (z & ~1);
-      const bool whole = L == C;
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
         const float got = __shfl_xor_sync(0xffffffffu, odd ? o1[e] : o1[e + 1], 1);
-        const uint32_t v = odd ? pack_bf16x2(got, o1[e + 1]) : pack_bf16x2(o1[e], got);
-        if (whole) sr[16 * e] = v;
-        else if (e + odd < cnt) *reinterpret_cast<uint32_t*>(o + (size_t)e * p.H * D) = v;
+        sr[16 * e] = odd ? pack_bf16x2(got, o1[e + 1]) : pack_bf16x2(o1[e], got);
       }
-      if (whole) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&maps.m[pi][3], stage, 32 * (warp & 3), h, (int)r0);
-          bulk_commit();
-        }
+      __syncwarp();
+      const int rr = lane >> 2;
+      uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(q.out) +
+                                          ((size_t)(r0 + rr) * p.H + h) * D + 32 * (warp & 3) +
+                                          8 * (lane & 3));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + e * 512 + lane * 16);
+        if (rr + 8 * e < cnt) o[(size_t)e * p.H * D] = v;   // 8 rows of H D elements, 8 a uint4
       }
+      __syncwarp();
     }
     float* dst = !ok ? nullptr : kState ? q.seg_state + uoff : last ? la_exit(p, q, n, h, D) : nullptr;
     if (dst) {
@@ -517,8 +519,6 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         for (int e = 0; e < 16; ++e) v[e] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
       }
     }
-    if (lane == 0) bulk_wait_all();                   // the stores have landed
-    __syncwarp();
   } else {
     reg_dealloc<88>();
     // ---------------------------------------------------------------- weighted rows in BF16 parts
@@ -541,22 +541,19 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           const uint4 v = *reinterpret_cast<const uint4*>(src + at);
           const float wgt = wt[8 * k];
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[3][4];
+          uint32_t o[NSP][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float x = lo_f(in[e]) * wgt, y = hi_f(in[e]) * wgt;
-            o[0][e] = pack_bf16x2(x, y);
-            x -= lo_f(o[0][e]);
-            y -= hi_f(o[0][e]);
-            o[1][e] = pack_bf16x2(x, y);
-            x -= lo_f(o[1][e]);
-            y -= hi_f(o[1][e]);
-            o[2][e] = pack_bf16x2(x, y);
+            float2 x = mul2(unpack2(in[e]), make_float2(wgt, wgt));
+#pragma unroll
+            for (int sp = 0; sp < NSP; ++sp) {
+              o[sp][e] = pack_bf16x2(x.x, x.y);
+              if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][e]));
+            }
           }
-          *reinterpret_cast<uint4*>(dst + at) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-          *reinterpret_cast<uint4*>(dst + 2 * PANEL + at) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-          if (nsplit > 2)
-            *reinterpret_cast<uint4*>(dst + 4 * PANEL + at) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+#pragma unroll
+          for (int sp = 0; sp < NSP; ++sp)
+            *reinterpret_cast<uint4*>(dst + 2 * sp * PANEL + at) = make_uint4(o[sp][0], o[sp][1], o[sp][2], o[sp][3]);
         }
         fence_proxy_async_smem();
         warp_arrive(&bars[SPLIT + hf], lane);
@@ -586,14 +583,14 @@ cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
     const LaPass& q = p.pass[i];
     returns = returns || q.s_out;
     if (!make_bf16_map(&maps.m[i][0], q.x, rows, q.hx) || !make_bf16_map(&maps.m[i][1], q.y, rows, q.hy) ||
-        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz) ||
-        (!q.out_f32 && !make_bf16_store_map(&maps.m[i][3], q.out, rows, p.H)))
+        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz))
       return cudaErrorInvalidValue;
   }
-  auto kern = state_only ? la_tc_kernel<true> : la_tc_kernel<false>;
+  auto kern = state_only ? (returns ? la_tc_kernel<true, 3> : la_tc_kernel<true, 2>)
+                         : (returns ? la_tc_kernel<false, 3> : la_tc_kernel<false, 2>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)grid, NT, SMEM, st>>>(maps, p, returns ? 3 : 2);
+  kern<<<(unsigned)grid, NT, SMEM, st>>>(maps, p);
   return cudaGetLastError();
 }
 

@@ -40,28 +40,31 @@ namespace {
 
 using namespace tc;
 
-constexpr int D = 128, C = LA_CHUNK, NT = 512, NS = 3;
+constexpr int D = 128, C = LA_CHUNK, NT = 512, NS = 4;
 constexpr uint32_t PANEL = 8192;                 // 64 rows x 128 bytes
 constexpr uint32_t B_Y = 0, B_X = PANEL;         // panel 0 of Y and X; panel 1 two panels on
 constexpr uint32_t B_Z = 4 * PANEL, STAGE = 6 * PANEL;
-constexpr uint32_t O_SPLIT = NS * STAGE;         // three weighted tiles of two panels
-constexpr uint32_t O_P = O_SPLIT + 6 * PANEL;    // P [64][64], two buffers
-constexpr uint32_t O_OUT = O_P + 2 * PANEL;      // results, [32 rows][32 columns] of each warp
+constexpr uint32_t O_P = NS * STAGE;             // P [64][64]
+constexpr uint32_t O_OUT = O_P + PANEL;          // results, [32 rows][32 columns] of each warp
 // b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4]
 constexpr uint32_t O_TAB = O_OUT + 16384;
 constexpr uint32_t O_BAR = O_TAB + 1280;
 constexpr uint32_t SMEM = O_BAR + 256 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
 
-constexpr uint32_t TM_E = 0, TM_SB = 128, TM_P = 192, TM_O1 = 320, TM_O2 = 384;   // P: two
+// TMEM columns: E, the state's BF16 copy, QK, O1, O2, the weighted rows' parts (32 columns
+// each); a launch that computes states alone has two buffers of E and of the parts.
+constexpr uint32_t TM_E = 0, TM_SB = 128, TM_P = 192, TM_O1 = 256, TM_O2 = 320;
+template <bool kState>
+__device__ __forceinline__ uint32_t tm_w(int buf) { return kState ? 256 + 96 * buf : 384; }
 
 constexpr uint32_t ID_QK = idesc_bf16(128, 64, false, false);
-constexpr uint32_t ID_E = idesc_bf16(128, 128, true, true);
+constexpr uint32_t ID_E = idesc_bf16(128, 128, false, true);   // A in TMEM
 constexpr uint32_t ID_O1 = idesc_bf16(128, 64, false, false);   // A in TMEM
 constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 
-enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY = QKDONE + 2,
-       SPLIT = PREADY + 2, EHALF = SPLIT + 2, EDONE, EFREE, ODONE, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
+enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY, SPLIT,
+       EDONE = SPLIT + 2, EFREE = EDONE + 2, ODONE = EFREE + 2, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
 static_assert(8 * NBAR + 8 <= 256, "barriers");
 
 constexpr long long WAIT_CYCLES = 4000000000ll;   // about 2 s
@@ -169,6 +172,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       o[((size_t)(s0 + (i >> 4)) * p.H + h) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
     return;
   }
+  constexpr int NE = kState ? 2 : 1;              // buffers of E and of the weighted rows
   const int nc = (int)((rows + C - 1) / C);
   const int tail = (int)(rows - (int64_t)(nc - 1) * C);   // rows of the walk's last chunk
   const float d = p.decay[h];
@@ -176,8 +180,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i)
-      mbar_init(&bars[i], i == PREADY || i == PREADY + 1 ? 2 : i == SPLIT || i == SPLIT + 1 ? 4
-                          : i == GO || i == EFREE ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
+      mbar_init(&bars[i], i == PREADY ? 2 : i == SPLIT || i == SPLIT + 1 ? 4
+                          : i == GO || i == EFREE || i == EFREE + 1 ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
     *abort_s = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.m[pi][1]);
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     wr[t] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
   }
   if (!kState)   // P on the far side of the diagonal stays zero
-    for (int i = tid; i < 2 * (int)PANEL / 16; i += NT)
+    for (int i = tid; i < (int)PANEL / 16; i += NT)
       *reinterpret_cast<uint4*>(sm + O_P + 16 * i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -205,7 +209,6 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     if (warp == 0) {
       // -------------------------------------------------------------- loader, issuer of E
       const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
-      const uint64_t dw = sdesc_sw128(sb + O_SPLIT, PANEL, 1024);
       int issued = 0;
       auto load = [&](int c) {
         const int b = c % NS, L = c + 1 == nc ? tail : C;
@@ -244,31 +247,27 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       bool ok = nc != 1 || tail == C || trim();
       for (int c = 0; c < nc && ok; ++c) {
         const int b = c % NS;
-        // E in two halves of 32 rows: the split warps refill the first under the second
+        const int eb = c % NE, ph = (c / NE) & 1;
         const uint64_t dy = sdesc_sw128(sb + b * STAGE + B_Y, 2 * PANEL, 1024);
-        if (c > 0 && !(ok = warp_wait(&bars[EFREE], (c - 1) & 1, cx))) break;
+        if (c >= NE && !(ok = warp_wait(&bars[EFREE + eb], ph ^ 1, cx))) break;
+        // (the split warps have waited for the rows themselves)
+        if (!(ok = warp_wait(&bars[SPLIT + eb], ph, cx))) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          // (the split warps have waited for the rows themselves)
-          if (!(ok = warp_wait(&bars[SPLIT + hf], c & 1, cx))) break;
-          tc_fence_after();
-          if (elect_one()) {
+          for (int sp = 0; sp < NSP; ++sp)
 #pragma unroll
-            for (int sp = 0; sp < NSP; ++sp)
-#pragma unroll
-              for (int kk = 2 * hf; kk < 2 * hf + 2; ++kk)
-                mma_bf16(tm + TM_E, dw + kstep_mn(kk) + (uint64_t)(sp * 2 * PANEL >> 4),
-                         dy + kstep_mn(kk), ID_E, kk + sp > 0);
-            mma_commit(&bars[hf ? EDONE : EHALF]);
-            if (hf) mma_commit(&bars[FREE + b]);
-          }
-          __syncwarp();
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ta(tm + TM_E + 128 * eb, tm + tm_w<kState>(eb) + 32 * sp + 8 * kk,
+                          dy + kstep_mn(kk), ID_E, kk + sp > 0);
+          mma_commit(&bars[EDONE + eb]);
+          mma_commit(&bars[FREE + b]);
         }
-        if (!ok) break;
+        __syncwarp();
         if (c + 2 == nc && tail < C && !(ok = trim())) break;
-        if (c > 0 && c + 2 < nc) {
-          if (!(ok = warp_wait(&bars[FREE + (c + 2) % NS], ((c - 1) / NS) & 1, cx))) break;
-          load(c + 2);
+        if (c > 0 && c + NS - 1 < nc) {
+          if (!(ok = warp_wait(&bars[FREE + (c - 1) % NS], ((c - 1) / NS) & 1, cx))) break;
+          load(c + NS - 1);
         }
       }
       if (!ok)   // let the copies in flight land
@@ -284,13 +283,13 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       // (the whole warp waits; one elected lane issues)
       auto issue_qk = [&](int c) {
         const uint64_t dy = sdesc_sw128(sb + (c % NS) * STAGE + B_Y, 0, 1024);
-        const uint32_t t = tm + TM_P + 64 * (c & 1);
+        const uint32_t t = tm + TM_P;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16(t, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
-          mma_commit(&bars[QKDONE + (c & 1)]);
+          mma_commit(&bars[QKDONE]);
         }
         __syncwarp();
       };
@@ -309,10 +308,10 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
             mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
         }
         __syncwarp();
-        if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
+        if (!(ok = warp_wait(&bars[PREADY], c & 1, cx))) break;
         tc_fence_after();
         const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
-        const uint64_t dp = sdesc_sw128(sb + O_P + (c & 1) * PANEL, 0, 1024);
+        const uint64_t dp = sdesc_sw128(sb + O_P, 0, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -356,17 +355,17 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
             f[half][e] = gap >= 0 ? q.a * pw(gap) : 0.f;
           }
         const uint32_t tl = tm + TM_P + ((uint32_t)(warp * 32) << 16);
+        uint8_t* row = sm + O_P + r * 128;
         for (int c = 0; c < nc; ++c) {
-          if (!warp_wait(&bars[QKDONE + (c & 1)], (c >> 1) & 1, cx)) break;
+          if (!warp_wait(&bars[QKDONE], c & 1, cx)) break;
           tc_fence_after();
-          uint8_t* row = sm + O_P + (c & 1) * PANEL + r * 128;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (rev ? half == 0 && warp == 3 : half == 1 && warp == 2) continue;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float x[16];
-              tmem_ld16(tl + 64 * (c & 1) + 32 * half + 16 * k, x);
+              tmem_ld16(tl + 32 * half + 16 * k, x);
               tmem_ld_wait();
 #pragma unroll
               for (int ch = 0; ch < 2; ++ch) {
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          warp_arrive(&bars[PREADY + (c & 1)], lane);
+          warp_arrive(&bars[PREADY], lane);
         }
       }
     }
@@ -434,14 +433,14 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     for (int c = 0; c < nc && ok; ++c) {
       const bool end = c + 1 == nc;
       const int L = end ? tail : C;
-      if (!(ok = warp_wait(&bars[EDONE], c & 1, cx))) break;
+      if (!(ok = warp_wait(&bars[EDONE + c % NE], (c / NE) & 1, cx))) break;
       tc_fence_after();
       const float2 fh = make_float2(carry[end ? 2 : 0], carry[end ? 2 : 0]);
       const float2 fl = make_float2(carry[end ? 3 : 1], carry[end ? 3 : 1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x[32];
-        tmem_ld32(tl + TM_E + 64 * wg + 32 * k, x);
+        tmem_ld32(tl + TM_E + 128 * (c % NE) + 64 * wg + 32 * k, x);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         }
       }
       tc_fence_before();
-      warp_arrive(&bars[EFREE], lane);
+      warp_arrive(&bars[EFREE + c % NE], lane);
       if (kState) continue;
       if (!(ok = warp_wait(&bars[ODONE], c & 1, cx))) break;
       tc_fence_after();
@@ -522,43 +521,52 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   } else {
     reg_dealloc<88>();
     // ---------------------------------------------------------------- weighted rows in BF16 parts
-    const int t = tid - 384, j0 = t >> 4, ch = t & 15;
-    const uint32_t panel = (uint32_t)(ch >> 3) * PANEL;
+    // Each warp weights and splits the 32 columns z of its TMEM lanes: 16 at a time, transposed
+    // on the way from shared memory (8 x 8 tiles), the rows j along the TMEM columns.  The first
+    // 16 are ready before the buffer is free.
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const int m = lane >> 3, i = lane & 7;
+    // lane's source row of K step 0: j = 8 (m / 2) + i, columns z0 + 8 (m % 2) ..; z0 of either
+    // half differs in bit 1 of the 16-byte chunk
+    const uint32_t ch = (uint32_t)(4 * (warp & 1) + (m & 1));
+    const uint32_t src = sb + B_Z + (uint32_t)((warp & 3) >> 1) * PANEL + (uint32_t)(8 * (m >> 1) + i) * 128u;
+    const uint32_t c0 = (ch ^ (uint32_t)i) << 4, c1 = ((ch + 2) ^ (uint32_t)i) << 4;
     for (int c = 0; c < nc; ++c) {
-      const int b = c % NS;
+      const int b = c % NS, eb = c % NE;
       if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
-      const float* wt = wr + (c + 1 == nc ? 64 : 0) + j0;
-      const uint8_t* src = sm + b * STAGE + B_Z + panel;
-      uint8_t* dst = sm + O_SPLIT + panel;
+      const float2* wt = reinterpret_cast<const float2*>(wr + (c + 1 == nc ? 64 : 0)) + (lane & 3);
+      float2 wv[8];                                   // rows 8 g + 2 (lane % 4), + 1
+#pragma unroll
+      for (int g = 0; g < 8; ++g) wv[g] = wt[4 * g];
       bool ok = true;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {                // the last chunk's products are done with it
-        if (c > 0 && !(ok = warp_wait(&bars[hf ? EDONE : EHALF], (c - 1) & 1, cx))) break;
+      for (int hz = 0; hz < 2; ++hz) {
+        uint32_t o[NSP][16];
 #pragma unroll
-        for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
-          const int j = j0 + 8 * k;
-          const uint32_t at = (uint32_t)j * 128u + (uint32_t)(((ch & 7) ^ (j & 7)) << 4);
-          const uint4 v = *reinterpret_cast<const uint4*>(src + at);
-          const float wgt = wt[8 * k];
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[NSP][4];
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t v[4];
+          ldmatrix_x4_trans(src + b * STAGE + kk * 2048 + (hz ? c1 : c0), v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float2 x = mul2(unpack2(in[e]), make_float2(wgt, wgt));
+            float2 x = mul2(unpack2(v[e]), wv[2 * kk + (e >> 1)]);
 #pragma unroll
             for (int sp = 0; sp < NSP; ++sp) {
-              o[sp][e] = pack_bf16x2(x.x, x.y);
-              if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][e]));
+              o[sp][4 * kk + e] = pack_bf16x2(x.x, x.y);
+              if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][4 * kk + e]));
             }
           }
-#pragma unroll
-          for (int sp = 0; sp < NSP; ++sp)
-            *reinterpret_cast<uint4*>(dst + 2 * sp * PANEL + at) = make_uint4(o[sp][0], o[sp][1], o[sp][2], o[sp][3]);
         }
-        fence_proxy_async_smem();
-        warp_arrive(&bars[SPLIT + hf], lane);
+        // the products of the chunk that had the buffer are done
+        if (hz == 0 && c >= NE && !(ok = warp_wait(&bars[EDONE + eb], ((c / NE) & 1) ^ 1, cx))) break;
+        if (hz == 0) tc_fence_after();
+#pragma unroll
+        for (int sp = 0; sp < NSP; ++sp)
+          tmem_st_16x32(tl + ((uint32_t)(16 * hz) << 16) + tm_w<kState>(eb) + 32 * sp, o[sp]);
       }
       if (!ok) break;
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&bars[SPLIT + eb], lane);
     }
   }
   tc_fence_before();

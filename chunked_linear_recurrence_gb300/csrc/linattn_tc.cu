@@ -46,9 +46,9 @@ constexpr uint32_t B_Y = 0, B_X = PANEL;         // panel 0 of Y and X; panel 1 
 constexpr uint32_t B_Z = 4 * PANEL, STAGE = 6 * PANEL;
 constexpr uint32_t O_P = NS * STAGE;             // P [64][64]
 constexpr uint32_t O_OUT = O_P + PANEL;          // results, [32 rows][32 columns] of each warp
-// b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4]
+// b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, a lam^n [64], carry [4]
 constexpr uint32_t O_TAB = O_OUT + 16384;
-constexpr uint32_t O_BAR = O_TAB + 1280;
+constexpr uint32_t O_BAR = O_TAB + 1536;
 constexpr uint32_t SMEM = O_BAR + 256 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
 
@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const uint32_t sb = smem_u32(sm);
   float* rd = reinterpret_cast<float*>(sm + O_TAB);   // [2][64]
   float* wr = rd + 128;                               // [2][64]
-  float* carry = rd + 256;
+  float* pq = rd + 256;                               // [64]
+  float* carry = rd + 320;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + O_BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR);
   int* abort_s = reinterpret_cast<int*>(sm + O_BAR + 8 * NBAR + 4);
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     const int i = tid & 63, L = tid < 192 ? C : tail, t = tid - 128;
     rd[t] = i < L ? q.b * pw(rev ? L - 1 - i : i + 1) : 0.f;
     wr[t] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
+    if (t < 64) pq[t] = q.a * pw(t);
   }
   if (!kState)   // P on the far side of the diagonal stays zero
     for (int i = tid; i < (int)PANEL / 16; i += NT)
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int s = 32 * half + e, gap = rev ? s - r : r - s;
-            f[half][e] = gap >= 0 ? q.a * pw(gap) : 0.f;
+            f[half][e] = gap >= 0 ? pq[gap & 63] : 0.f;
           }
         const uint32_t tl = tm + TM_P + ((uint32_t)(warp * 32) << 16);
         uint8_t* row = sm + O_P + r * 128;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       warp_arrive(&bars[GO], lane);
     }
     bool ok = nc == 0 || warp_wait(&bars[TBL], 0, cx);
-    uint8_t* stage = sm + O_OUT + (warp - 4) * 2048;
+    const uint32_t stage = sb + O_OUT + (warp - 4) * 2048;
     for (int c = 0; c < nc && ok; ++c) {
       const bool end = c + 1 == nc;
       const int L = end ? tail : C;
@@ -437,60 +439,69 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       tc_fence_after();
       const float2 fh = make_float2(carry[end ? 2 : 0], carry[end ? 2 : 0]);
       const float2 fl = make_float2(carry[end ? 3 : 1], carry[end ? 3 : 1]);
+      float x[2][32];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x[32];
-        tmem_ld32(tl + TM_E + 128 * (c % NE) + 64 * wg + 32 * k, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2& v = s[16 * k + e];
-          v = fma2(fh, v, fma2(fl, v, make_float2(x[2 * e], x[2 * e + 1])));
-        }
-      }
+      for (int k = 0; k < 2; ++k) tmem_ld32(tl + TM_E + 128 * (c % NE) + 64 * wg + 32 * k, x[k]);
+      tmem_ld_wait();
       tc_fence_before();
       warp_arrive(&bars[EFREE + c % NE], lane);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const float* y = &x[e >> 4][2 * (e & 15)];
+        s[e] = fma2(fh, s[e], fma2(fl, s[e], make_float2(y[0], y[1])));
+      }
       if (kState) continue;
       if (!(ok = warp_wait(&bars[ODONE], c & 1, cx))) break;
       tc_fence_after();
-      float o1[32], o2[32];
+      // O1, O2 rows [32 wg, + 32) as 8 x 8 tiles: of row pairs 8 g + 2 (lane % 4), + 1, columns
+      // 16 hz + 8 k + lane / 4 of the warp's 32
+      float o1[2][16], o2[2][16];
       if (!end) put_state();                          // S X^T of this chunk has read the old copy
-      tmem_ld32(tl + TM_O1 + 32 * wg, o1);
-      tmem_ld32(tl + TM_O2 + 32 * wg, o2);
+#pragma unroll
+      for (int hz = 0; hz < 2; ++hz) {
+        tmem_ld_16x32(tl + ((uint32_t)(16 * hz) << 16) + TM_O1 + 32 * wg, o1[hz]);
+        tmem_ld_16x32(tl + ((uint32_t)(16 * hz) << 16) + TM_O2 + 32 * wg, o2[hz]);
+      }
       tmem_ld_wait();
       if (!end) {
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&bars[GO], lane);
       }
-      // rows [32 wg, + 32) of the chunk, column z
       const int64_t r0 = (rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C) + 32 * wg;
-      const float4* f4 = reinterpret_cast<const float4*>(rd + (end ? 64 : 0) + 32 * wg);
-#pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 f = f4[e / 4];
-        o1[e] = fmaf(f.x, o1[e], o2[e]);
-        o1[e + 1] = fmaf(f.y, o1[e + 1], o2[e + 1]);
-        o1[e + 2] = fmaf(f.z, o1[e + 2], o2[e + 2]);
-        o1[e + 3] = fmaf(f.w, o1[e + 3], o2[e + 3]);
-      }
       const int cnt = L - 32 * wg;                    // rows that exist
-      if (q.out_f32) {
-        float* o = reinterpret_cast<float*>(q.out) + ((size_t)r0 * p.H + h) * D + z;
+      const float2* f2 = reinterpret_cast<const float2*>(rd + (end ? 64 : 0) + 32 * wg) + (lane & 3);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e < cnt) o[(size_t)e * p.H * D] = o1[e];
-        continue;
+      for (int g = 0; g < 4; ++g) {
+        const float2 f = f2[4 * g];
+        uint32_t v[4];                                // tiles of columns 0, 8, 16, 24
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float* y = &o1[k >> 1][4 * g + 2 * (k & 1)];
+          const float* y2 = &o2[k >> 1][4 * g + 2 * (k & 1)];
+          const float2 t = fma2(f, make_float2(y[0], y[1]), make_float2(y2[0], y2[1]));
+          v[k] = pack_bf16x2(t.x, t.y);
+          y[0] = t.x;
+          y[1] = t.y;
+        }
+        // row 8 g + i of the 64-byte rows, its 16-byte pieces in the order that keeps eight rows
+        // on different banks
+        if (!q.out_f32) {
+          const int i = lane & 7, m = lane >> 3;
+          stmatrix_x4_trans(stage + (8 * g + i) * 64 + ((m ^ ((i >> 1) & 3)) << 4), v);
+        }
       }
-      // lane pairs swap a value (the even lane gets columns z, z + 1 of row e, the odd one those
-      // of row e + 1) and the warp's 32 x 32 tile is turned in shared memory, so that the rows
-      // leave 16 bytes a lane, eight rows a store
-      const int odd = lane & 1;
-      uint32_t* sr = reinterpret_cast<uint32_t*>(stage + odd * 64 + (lane >> 1) * 4);
+      if (q.out_f32) {
+        float* o = reinterpret_cast<float*>(q.out) +
+                   ((size_t)(r0 + 2 * (lane & 3)) * p.H + h) * D + 32 * (warp & 3) + (lane >> 2);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? o1[e] : o1[e + 1], 1);
-        sr[16 * e] = odd ? pack_bf16x2(got, o1[e + 1]) : pack_bf16x2(o1[e], got);
+        for (int hz = 0; hz < 2; ++hz)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int row = 8 * (e >> 2) + (e & 1), col = 16 * hz + 8 * ((e >> 1) & 1);
+            if (2 * (lane & 3) + row < cnt) o[(size_t)row * p.H * D + col] = o1[hz][e];
+          }
+        continue;
       }
       __syncwarp();
       const int rr = lane >> 2;
@@ -499,7 +510,10 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
                                           8 * (lane & 3));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + e * 512 + lane * 16);
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stage + (8 * e + rr) * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4)) : "memory");
         if (rr + 8 * e < cnt) o[(size_t)e * p.H * D] = v;   // 8 rows of H D elements, 8 a uint4
       }
       __syncwarp();

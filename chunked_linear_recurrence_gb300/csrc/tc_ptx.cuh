@@ -342,6 +342,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         "=r"(u[14]), "=r"(u[15])
       : "r"(taddr));
 }
+// TMEM -> registers: 16 lanes x 32 consecutive 32-bit columns.  Lane T receives, of columns 8 g +
+// 2 (T % 4) and the next, row T / 4 (r[4 g], r[4 g + 1]) and row 8 + T / 4 (r[4 g + 2], r[4 g + 3]).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&r)[16]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr));
+}
+// Four 8 x 8 tiles of 16-bit elements, transposed: lane T gives the elements (2 (T % 4), T / 4)
+// and (2 (T % 4) + 1, T / 4) of tile m in u[m]; lanes 8 m .. 8 m + 7 the addresses of its rows.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&u)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }

@@ -170,14 +170,15 @@ struct QkParams {
   void* k_out;
   const void* dqo;      // backward: cotangents of q_out, k_out
   const void* dko;
-  float* part;          // backward: per-CTA sums of the weights' gradients [parts][2][D]
+  float* part;          // backward: per-CTA sums of the weights' gradients [blocks][D]
   int64_t rows, sq, sk; // tokens; element strides between tokens of q and k
   int H, HK, half, inter, table_rows, axes, l2;
+  int q_blocks;         // CTAs that take queries; the rest take keys
   int bound[4];         // pairs below bound[a] belong to axes 0 .. a
   float eps;
 };
-// Most CTAs of the backward: parts of the weights' gradients, [QK_PARTS][2][D].
-constexpr int QK_PARTS = 608;
+// Most CTAs of the backward: parts of the weights' gradients, [QK_PARTS][D].
+constexpr int QK_PARTS = 152 * 4;
 cudaError_t launch_qk_norm_rope(const QkParams& p, bool bf16, int D, cudaStream_t st);
 cudaError_t launch_qk_norm_rope_bwd(const QkParams& p, bool bf16, int D, float* dqw, float* dkw,
                                     cudaStream_t st);

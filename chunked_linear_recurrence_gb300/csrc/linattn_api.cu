@@ -372,7 +372,7 @@ sf_status sf_qk_norm_rope_fwd(const sf_qk_shape* shape, const void* q, const voi
 size_t sf_qk_norm_rope_bwd_workspace(const sf_qk_shape* shape) {
   // sums of at most sfg::QK_PARTS CTAs, whatever the device has
   if (!shape || shape->D < 1) return 256;
-  return (size_t)sfg::QK_PARTS * 2 * shape->D * sizeof(float);
+  return (size_t)sfg::QK_PARTS * shape->D * sizeof(float);
 }
 
 sf_status sf_qk_norm_rope_bwd(const sf_qk_shape* shape, const void* q, const void* k,

@@ -31,6 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "linattn.cuh"
 #include "tc_ptx.cuh"
 #include "tmap.cuh"
@@ -108,31 +109,6 @@ __device__ __forceinline__ uint64_t kstep_k(int kk) {   // panels 16 KB apart
   return (uint64_t)(((uint32_t)(kk >> 2) * 2 * PANEL + (uint32_t)(kk & 3) * 32u) >> 4);
 }
 __device__ __forceinline__ uint64_t kstep_mn(int kk) { return (uint64_t)(kk * 2048 >> 4); }
-
-// Two FP32 multiply-adds in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-        "l"(reinterpret_cast<unsigned long long&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
-// a - b
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-  return fma2(b, make_float2(-1.f, -1.f), a);
-}
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-
-__device__ __forceinline__ float2 unpack2(uint32_t u) { return make_float2(lo_f(u), hi_f(u)); }
 
 template <bool kState, int NSP>
 __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Maps maps,

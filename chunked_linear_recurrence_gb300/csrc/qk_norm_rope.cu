@@ -7,67 +7,100 @@
 //               dw = sum over tokens and heads of dy x r
 //
 // Bound by memory: every element is read and written once (the backward reads two).  A row of
-// D elements belongs to D / 8 lanes, each with both members of its four pairs (two groups of
-// four consecutive elements; eight consecutive ones where the pairs are neighbours), so norm
-// and rotation stay in registers.  A group of lanes takes UNROLL heads of one token at a
-// time: its loads are in flight together, and the token's cosines and sines are read once
-// for all of them.  The weights' gradients are summed per lane over everything a CTA takes,
-// then over its lanes, then (a second kernel) over the CTAs, each in a fixed order.
+// D elements belongs to D / (2 VEC) lanes, each with both members of its VEC pairs: two groups of
+// VEC consecutive elements (2 VEC consecutive ones where the pairs are neighbours), so norm and
+// rotation stay in registers.  VEC is 8 (16-byte accesses of BF16) unless the rotated part ends
+// inside such a group.  A group of lanes takes U heads of one token at a time: its loads are in
+// flight together and the token's cosines and sines serve all of them.  A CTA takes queries or
+// keys, not both (the grid is shared in proportion), so it keeps one weight and one gradient of
+// it.  Arithmetic goes two elements an instruction.  The weights' gradients are summed per lane
+// over everything a CTA takes, then over its lanes, then (a second kernel) over the CTAs, each
+// in a fixed order.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "linattn.cuh"
 
 namespace sfg {
 namespace {
 
 constexpr int NT = 256;
-constexpr int UNROLL = 4;
 
-__device__ __forceinline__ void ld4(const float* p, float* x) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float* x) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-}
-__device__ __forceinline__ void st4(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float* x) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  uint2 u;
-  u.x = *reinterpret_cast<uint32_t*>(&a);
-  u.y = *reinterpret_cast<uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
+// VEC consecutive elements as they come from memory, and as VEC / 2 pairs of floats.
+template <typename T, int VEC>
+struct Raw {
+  static constexpr int W = VEC * sizeof(T) / 8;   // 8-byte words
+  uint2 u[W];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (W % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 2) {
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint2*>(p) + i);
+        u[i] = make_uint2(v.x, v.y);
+        u[i + 1] = make_uint2(v.z, v.w);
+      }
+    } else {
+      u[0] = *reinterpret_cast<const uint2*>(p);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) u[i] = make_uint2(0, 0);
+  }
+  __device__ __forceinline__ void get(float2* x) const {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        x[2 * i] = unpack2(u[i].x);
+        x[2 * i + 1] = unpack2(u[i].y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = make_float2(__uint_as_float(u[i].x), __uint_as_float(u[i].y));
+    }
+  }
+  __device__ __forceinline__ void put(const float2* x) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) u[i] = make_uint2(pack2(x[2 * i]), pack2(x[2 * i + 1]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) u[i] = make_uint2(__float_as_uint(x[i].x), __float_as_uint(x[i].y));
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (W % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 2)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint2*>(p) + i) =
+            make_uint4(u[i].x, u[i].y, u[i + 1].x, u[i + 1].y);
+    } else {
+      *reinterpret_cast<uint2*>(p) = u[0];
+    }
+  }
+};
 
-// What a lane holds of a row: elements [a, a+4) and [b, b+4), and its first pair (or no pair).
+// What a lane holds of a row: elements [a, a + VEC) and [b, b + VEC), and its first pair.
 struct Lane {
   int a, b, pair;
   bool turns;
 };
+template <int VEC>
 __device__ __forceinline__ Lane lane_of(int l, const QkParams& p) {
   Lane t;
-  const int lanes = p.half / 4;             // lanes that hold pairs
-  t.turns = l < lanes;
-  t.pair = 4 * l;
-  if (t.turns && !p.inter) {
-    t.a = 4 * l;
-    t.b = p.half + 4 * l;
-  } else {
-    t.a = 8 * l;
-    t.b = 8 * l + 4;
-  }
+  t.turns = l * VEC < p.half;
+  t.pair = VEC * l;
+  const bool halves = t.turns && !p.inter;
+  t.a = halves ? VEC * l : 2 * VEC * l;
+  t.b = halves ? p.half + VEC * l : 2 * VEC * l + VEC;
   return t;
 }
 
-// Cosines and sines of the lane's four pairs at a token.
-__device__ __forceinline__ void load_turn(const QkParams& p, const Lane& t, int64_t row, float* c,
-                                          float* s) {
+// Cosines and sines of the lane's VEC pairs at a token, two pairs to a float2.
+template <int VEC>
+__device__ __forceinline__ void load_turn(const QkParams& p, const Lane& t, int64_t row, float2* c,
+                                          float2* s) {
   if (!t.turns) return;
   int axis = 0;
   while (axis + 1 < p.axes && t.pair >= p.bound[axis]) ++axis;
@@ -77,36 +110,44 @@ __device__ __forceinline__ void load_turn(const QkParams& p, const Lane& t, int6
     return p.cs + ((size_t)pos * p.half + t.pair) * 2;
   };
   const float* cs = at(axis);
-  if (t.pair + 4 <= p.bound[axis]) {        // one axis for all four
-    const float4 u = *reinterpret_cast<const float4*>(cs), v = *reinterpret_cast<const float4*>(cs + 4);
-    c[0] = u.x; s[0] = u.y; c[1] = u.z; s[1] = u.w;
-    c[2] = v.x; s[2] = v.y; c[3] = v.z; s[3] = v.w;
+  if (t.pair + VEC <= p.bound[axis]) {        // one axis for all of them
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float4 v = *reinterpret_cast<const float4*>(cs + 4 * e);
+      c[e] = make_float2(v.x, v.z);
+      s[e] = make_float2(v.y, v.w);
+    }
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < VEC; ++e) {
     while (axis + 1 < p.axes && t.pair + e >= p.bound[axis]) cs = at(++axis);
-    const float2 u = *reinterpret_cast<const float2*>(cs + 2 * e);
-    c[e] = u.x;
-    s[e] = u.y;
+    const float2 v = *reinterpret_cast<const float2*>(cs + 2 * e);
+    if (e & 1) c[e / 2].y = v.x, s[e / 2].y = v.y;
+    else c[e / 2].x = v.x, s[e / 2].x = v.y;
   }
 }
 
-// Rotates the lane's eight elements by its four angles (sign -1: the opposite ones).
-__device__ __forceinline__ void turn(float* x, const Lane& t, bool inter, const float* c,
-                                     const float* s, float sign) {
+// Rotates the lane's elements by its angles (kBack: the opposite ones); xa, xb its two groups.
+template <int VEC, bool kBack>
+__device__ __forceinline__ void turn(float2* xa, float2* xb, const Lane& t, bool inter, const float2* c,
+                                     const float2* s) {
   if (!t.turns) return;
+  if (!inter) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float sn = sign * s[e];
-    if (inter) {
-      const float a = x[2 * e], b = x[2 * e + 1];
-      x[2 * e] = a * c[e] - b * sn;
-      x[2 * e + 1] = b * c[e] + a * sn;
-    } else {
-      const float a = x[e], b = x[e + 4];
-      x[e] = a * c[e] - b * sn;
-      x[e + 4] = b * c[e] + a * sn;
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 a = xa[e], b = xb[e], n = make_float2(-s[e].x, -s[e].y);
+      xa[e] = fma2(a, c[e], mul2(b, kBack ? s[e] : n));
+      xb[e] = fma2(b, c[e], mul2(a, kBack ? n : s[e]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {            // pair e is one float2
+      float2& v = e < VEC / 2 ? xa[e] : xb[e - VEC / 2];
+      const float ce = e & 1 ? c[e / 2].y : c[e / 2].x;
+      float se = e & 1 ? s[e / 2].y : s[e / 2].x;
+      if (kBack) se = -se;
+      v = make_float2(v.x * ce - v.y * se, v.y * ce + v.x * se);
     }
   }
 }
@@ -118,127 +159,140 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ void load_weight(const float* w, const Lane& t, float* x) {
-  if (w) {
-    ld4(w + t.a, x);
-    ld4(w + t.b, x + 4);
-  } else {
+template <int VEC>
+__device__ __forceinline__ void load_weight(const float* w, const Lane& t, float2* x) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 1.f;
+  for (int e = 0; e < VEC / 2; ++e) {
+    x[e] = w ? *reinterpret_cast<const float2*>(w + t.a + 2 * e) : make_float2(1.f, 1.f);
+    x[VEC / 2 + e] = w ? *reinterpret_cast<const float2*>(w + t.b + 2 * e) : make_float2(1.f, 1.f);
   }
 }
 
-// Item -> token and its UNROLL heads [h0, h0 + cnt) of q, or of k.
-struct Item {
-  int64_t row;
-  int h0, cnt;
+// The part of the grid that takes the queries, and the walk of one group of lanes over its
+// (token, U heads) items.
+struct Share {
   bool is_q;
+  int block, blocks, heads, per;
+  int64_t items;
 };
-__device__ __forceinline__ Item item_of(int64_t id, const QkParams& p, int per, int nq) {
-  Item it;
-  it.row = id / per;
-  const int g = (int)(id % per);
-  it.is_q = g < nq;
-  it.h0 = (it.is_q ? g : g - nq) * UNROLL;
-  const int left = (it.is_q ? p.H : p.HK) - it.h0;
-  it.cnt = left < UNROLL ? left : UNROLL;
-  return it;
+template <int U>
+__device__ __forceinline__ Share share_of(const QkParams& p) {
+  Share w;
+  w.is_q = (int)blockIdx.x < p.q_blocks;
+  w.block = w.is_q ? blockIdx.x : blockIdx.x - p.q_blocks;
+  w.blocks = w.is_q ? p.q_blocks : gridDim.x - p.q_blocks;
+  w.heads = w.is_q ? p.H : p.HK;
+  w.per = (w.heads + U - 1) / U;
+  w.items = p.rows * w.per;
+  return w;
 }
 
-template <typename T, int D>
+template <typename T, int D, int VEC, int U>
 __global__ void __launch_bounds__(NT) qk_fwd_kernel(const QkParams p) {
-  constexpr int LPR = D / 8, GROUPS = NT / LPR;
+  constexpr int LPR = D / (2 * VEC), GROUPS = NT / LPR, NP = VEC / 2;
   const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const Lane t = lane_of(l, p);
-  const int nq = (p.H + UNROLL - 1) / UNROLL, per = nq + (p.HK + UNROLL - 1) / UNROLL;
-  const int64_t items = p.rows * per, rounds = (items + (int64_t)gridDim.x * GROUPS - 1) / ((int64_t)gridDim.x * GROUPS);
-  float wq[8], wk[8];
-  load_weight(p.qw, t, wq);
-  load_weight(p.kw, t, wk);
-  for (int64_t rd = 0; rd < rounds; ++rd) {
-    const int64_t id = (rd * gridDim.x + blockIdx.x) * GROUPS + grp;
-    const bool live = id < items;            // whole warps stay for the shuffles
-    const Item it = item_of(live ? id : 0, p, per, nq);
-    const int heads = it.is_q ? p.H : p.HK;
-    const T* src = reinterpret_cast<const T*>(it.is_q ? p.q : p.k) +
-                   (size_t)it.row * (it.is_q ? p.sq : p.sk) + (size_t)it.h0 * D;
-    T* dst = reinterpret_cast<T*>(it.is_q ? p.q_out : p.k_out) + ((size_t)it.row * heads + it.h0) * D;
-    float x[UNROLL][8], c[4], s[4];
+  const Lane t = lane_of<VEC>(l, p);
+  const Share w = share_of<U>(p);
+  const T* const base = reinterpret_cast<const T*>(w.is_q ? p.q : p.k);
+  T* const obase = reinterpret_cast<T*>(w.is_q ? p.q_out : p.k_out);
+  const int64_t stride = w.is_q ? p.sq : p.sk;
+  float2 wt[VEC];
+  load_weight<VEC>(w.is_q ? p.qw : p.kw, t, wt);
+  for (int64_t first = (int64_t)w.block * GROUPS; first < w.items; first += (int64_t)w.blocks * GROUPS) {
+    const bool live = first + grp < w.items;       // whole warps stay for the shuffles
+    const int64_t id = live ? first + grp : w.items - 1;
+    const int64_t row = (id >> 31) ? id / w.per : (int64_t)((uint32_t)id / (uint32_t)w.per);
+    const int h0 = (int)(id - row * w.per) * U, cnt = live ? w.heads - h0 : 0;
+    const T* src = base + (size_t)row * stride + (size_t)h0 * D;
+    T* dst = obase + ((size_t)row * w.heads + h0) * D;
+    Raw<T, VEC> ra[U], rb[U];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (live && u < it.cnt) {
-        ld4(src + u * D + t.a, x[u]);
-        ld4(src + u * D + t.b, x[u] + 4);
+    for (int u = 0; u < U; ++u)
+      if (u < cnt) {
+        ra[u].load(src + u * D + t.a);
+        rb[u].load(src + u * D + t.b);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+        ra[u].zero();
+        rb[u].zero();
       }
-    load_turn(p, t, it.row, c, s);
+    float2 c[NP], s[NP];
+    load_turn<VEC>(p, t, row, c, s);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      float ss = 0.f;
+    for (int u = 0; u < U; ++u) {
+      float2 x[VEC];
+      ra[u].get(x);
+      rb[u].get(x + NP);
+      float2 q = mul2(x[0], x[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
-      ss = row_sum<LPR>(ss);
+      for (int e = 1; e < VEC; ++e) q = fma2(x[e], x[e], q);
+      const float ss = row_sum<LPR>(q.x + q.y);
       const float r = p.l2 ? 1.f / fmaxf(sqrtf(ss), p.eps) : rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] *= r * (it.is_q ? wq[e] : wk[e]);
-      turn(x[u], t, p.inter, c, s, 1.f);
-      if (live && u < it.cnt) {
-        st4(dst + u * D + t.a, x[u]);
-        st4(dst + u * D + t.b, x[u] + 4);
+      for (int e = 0; e < VEC; ++e) x[e] = mul2(x[e], mul2(wt[e], make_float2(r, r)));
+      turn<VEC, false>(x, x + NP, t, p.inter, c, s);
+      if (u < cnt) {
+        ra[u].put(x);
+        rb[u].put(x + NP);
+        ra[u].store(dst + u * D + t.a);
+        rb[u].store(dst + u * D + t.b);
       }
     }
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int VEC, int U>
 __global__ void __launch_bounds__(NT) qk_bwd_kernel(const QkParams p) {
-  constexpr int LPR = D / 8, GROUPS = NT / LPR;
+  constexpr int LPR = D / (2 * VEC), GROUPS = NT / LPR, NP = VEC / 2;
   __shared__ float red[GROUPS][D];
   const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const Lane t = lane_of(l, p);
-  const int nq = (p.H + UNROLL - 1) / UNROLL, per = nq + (p.HK + UNROLL - 1) / UNROLL;
-  const int64_t items = p.rows * per, rounds = (items + (int64_t)gridDim.x * GROUPS - 1) / ((int64_t)gridDim.x * GROUPS);
-  float wq[8], wk[8], gq[8], gk[8];
-  load_weight(p.qw, t, wq);
-  load_weight(p.kw, t, wk);
+  const Lane t = lane_of<VEC>(l, p);
+  const Share w = share_of<U>(p);
+  const T* const base = reinterpret_cast<const T*>(w.is_q ? p.q : p.k);
+  const T* const dbase = reinterpret_cast<const T*>(w.is_q ? p.dqo : p.dko);
+  T* const obase = reinterpret_cast<T*>(w.is_q ? p.q_out : p.k_out);
+  const int64_t stride = w.is_q ? p.sq : p.sk;
+  float2 wt[VEC], dw[VEC];
+  load_weight<VEC>(w.is_q ? p.qw : p.kw, t, wt);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 0.f;
-  for (int64_t rd = 0; rd < rounds; ++rd) {
-    const int64_t id = (rd * gridDim.x + blockIdx.x) * GROUPS + grp;
-    const bool live = id < items;
-    const Item it = item_of(live ? id : 0, p, per, nq);
-    const int heads = it.is_q ? p.H : p.HK;
-    const T* src = reinterpret_cast<const T*>(it.is_q ? p.q : p.k) +
-                   (size_t)it.row * (it.is_q ? p.sq : p.sk) + (size_t)it.h0 * D;
-    const size_t at = ((size_t)it.row * heads + it.h0) * D;
-    const T* dsrc = reinterpret_cast<const T*>(it.is_q ? p.dqo : p.dko) + at;
-    T* dst = reinterpret_cast<T*>(it.is_q ? p.q_out : p.k_out) + at;
-    float x[UNROLL][8], d[UNROLL][8], c[4], s[4];
+  for (int e = 0; e < VEC; ++e) dw[e] = make_float2(0.f, 0.f);
+  for (int64_t first = (int64_t)w.block * GROUPS; first < w.items; first += (int64_t)w.blocks * GROUPS) {
+    const bool live = first + grp < w.items;
+    const int64_t id = live ? first + grp : w.items - 1;
+    const int64_t row = (id >> 31) ? id / w.per : (int64_t)((uint32_t)id / (uint32_t)w.per);
+    const int h0 = (int)(id - row * w.per) * U, cnt = live ? w.heads - h0 : 0;
+    const T* src = base + (size_t)row * stride + (size_t)h0 * D;
+    const size_t at = ((size_t)row * w.heads + h0) * D;
+    Raw<T, VEC> ra[U], rb[U], da[U], db[U];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (live && u < it.cnt) {
-        ld4(src + u * D + t.a, x[u]);
-        ld4(src + u * D + t.b, x[u] + 4);
-        ld4(dsrc + u * D + t.a, d[u]);
-        ld4(dsrc + u * D + t.b, d[u] + 4);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = d[u][e] = 0.f;
+    for (int u = 0; u < U; ++u)
+      if (u < cnt) {
+        ra[u].load(src + u * D + t.a);
+        rb[u].load(src + u * D + t.b);
+        da[u].load(dbase + at + u * D + t.a);
+        db[u].load(dbase + at + u * D + t.b);
+      } else {                                     // adds nothing to the weight's gradient
+        ra[u].zero();
+        rb[u].zero();
+        da[u].zero();
+        db[u].zero();
       }
-    load_turn(p, t, it.row, c, s);
+    float2 c[NP], s[NP];
+    load_turn<VEC>(p, t, row, c, s);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      turn(d[u], t, p.inter, c, s, -1.f);
-      float ss = 0.f, gx = 0.f;
+    for (int u = 0; u < U; ++u) {
+      float2 x[VEC], d[VEC];
+      ra[u].get(x);
+      rb[u].get(x + NP);
+      da[u].get(d);
+      db[u].get(d + NP);
+      turn<VEC, true>(d, d + NP, t, p.inter, c, s);
+      float2 q = mul2(x[0], x[0]), g = mul2(mul2(d[0], wt[0]), x[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(x[u][e], x[u][e], ss);
-        gx = fmaf(d[u][e] * (it.is_q ? wq[e] : wk[e]), x[u][e], gx);
+      for (int e = 1; e < VEC; ++e) {
+        q = fma2(x[e], x[e], q);
+        g = fma2(mul2(d[e], wt[e]), x[e], g);
       }
-      ss = row_sum<LPR>(ss);
-      gx = row_sum<LPR>(gx);
+      const float ss = row_sum<LPR>(q.x + q.y), gx = row_sum<LPR>(g.x + g.y);
       float r, f;
       if (p.l2) {
         const float nrm = sqrtf(ss);
@@ -248,92 +302,116 @@ __global__ void __launch_bounds__(NT) qk_bwd_kernel(const QkParams p) {
         r = rsqrtf(ss * (1.f / D) + p.eps);
         f = r * r * (1.f / D) * gx;
       }
-      const bool on = live && u < it.cnt;
+      if (u >= cnt) continue;
+      const float2 r2 = make_float2(r, r), nrf = make_float2(-r * f, -r * f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float dw = on ? d[u][e] * (x[u][e] * r) : 0.f;
-        if (it.is_q) gq[e] += dw;
-        else gk[e] += dw;
-        d[u][e] = r * (d[u][e] * (it.is_q ? wq[e] : wk[e]) - x[u][e] * f);
+      for (int e = 0; e < VEC; ++e) {
+        const float2 dr = mul2(d[e], r2);
+        dw[e] = fma2(dr, x[e], dw[e]);
+        d[e] = fma2(dr, wt[e], mul2(x[e], nrf));   // r (g - x f)
       }
-      if (on) {
-        st4(dst + u * D + t.a, d[u]);
-        st4(dst + u * D + t.b, d[u] + 4);
-      }
+      ra[u].put(d);
+      rb[u].put(d + NP);
+      ra[u].store(obase + at + u * D + t.a);
+      rb[u].store(obase + at + u * D + t.b);
     }
   }
   if (!p.part) return;
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
+  for (int e = 0; e < NP; ++e) {
+    *reinterpret_cast<float2*>(&red[grp][t.a + 2 * e]) = dw[e];
+    *reinterpret_cast<float2*>(&red[grp][t.b + 2 * e]) = dw[NP + e];
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[grp][(e < 4 ? t.a : t.b) + (e & 3)] = which ? gk[e] : gq[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float sum = 0.f;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) sum += red[g][threadIdx.x];
-      p.part[((size_t)blockIdx.x * 2 + which) * D + threadIdx.x] = sum;
-    }
+    for (int g = 0; g < GROUPS; ++g) sum += red[g][threadIdx.x];
+    p.part[(size_t)blockIdx.x * D + threadIdx.x] = sum;
   }
 }
 
-// dw[c] = sum over the parts of part[.][which][c]: 32 columns a CTA, 32 threads a column.
-__global__ void __launch_bounds__(1024) qk_weight_kernel(const float* part, int parts, int D,
-                                                         float* dqw, float* dkw) {
+// dw[c] = sum of part[.][c] over the query blocks (dqw) and over the key blocks (dkw): 32 columns
+// a CTA, 32 threads a column.
+__global__ void __launch_bounds__(1024) qk_weight_kernel(const float* part, int q_blocks, int blocks,
+                                                         int D, float* dqw, float* dkw) {
   __shared__ float red[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + x;       // of 2 D
+  const bool is_q = (int)blockIdx.x < D / 32;
+  const int col = (blockIdx.x % (D / 32)) * 32;
+  const int lo = is_q ? 0 : q_blocks, hi = is_q ? q_blocks : blocks;
+  float* dst = is_q ? dqw : dkw;
+  if (!dst) return;
   float s = 0.f;
-  for (int i = y; i < parts; i += 32) s += part[(size_t)i * 2 * D + col];
+#pragma unroll 4
+  for (int i = lo + y; i < hi; i += 32) s += part[(size_t)i * D + col + x];
   red[y][x] = s;
   __syncthreads();
   s = red[x][y];
 #pragma unroll
   for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  const int c = blockIdx.x * 32 + y;
-  float* dst = c < D ? dqw : dkw;
-  if (x == 0 && dst) dst[c % D] = s;
+  if (x == 0) dst[col + y] = s;
 }
 
-// CTAs for the tokens' items, at most `cap`.
-unsigned qk_grid(const QkParams& p, int D, int64_t cap) {
-  const int per = (p.H + UNROLL - 1) / UNROLL + (p.HK + UNROLL - 1) / UNROLL;
-  const int64_t want = (p.rows * per + NT / (D / 8) - 1) / (NT / (D / 8));
-  return (unsigned)(want < cap ? want : cap);
+// Blocks for the queries' and the keys' items, at most `cap` together.
+template <int U>
+void share(QkParams& p, int groups, int64_t cap, unsigned& blocks) {
+  const int64_t qi = (p.rows * ((p.H + U - 1) / U) + groups - 1) / groups;
+  const int64_t ki = (p.rows * ((p.HK + U - 1) / U) + groups - 1) / groups;
+  int64_t qb = qi, kb = ki;
+  if (qi + ki > cap) {
+    qb = cap * qi / (qi + ki);
+    qb = qb < 1 ? 1 : qb > cap - 1 ? cap - 1 : qb;
+    kb = cap - qb;
+  }
+  p.q_blocks = (int)qb;
+  blocks = (unsigned)(qb + kb);
+}
+
+constexpr int FWD_U = 4, BWD_U = 2;
+
+template <typename T, int D, int VEC>
+cudaError_t fwd(QkParams p, cudaStream_t st) {
+  unsigned blocks;
+  share<FWD_U>(p, NT / (D / (2 * VEC)), 152 * 6, blocks);
+  qk_fwd_kernel<T, D, VEC, FWD_U><<<blocks, NT, 0, st>>>(p);
+  return cudaGetLastError();
+}
+template <typename T, int D, int VEC>
+cudaError_t bwd(QkParams p, float* dqw, float* dkw, cudaStream_t st) {
+  unsigned blocks = 0;
+  if (p.rows > 0) {
+    share<BWD_U>(p, NT / (D / (2 * VEC)), QK_PARTS, blocks);
+    qk_bwd_kernel<T, D, VEC, BWD_U><<<blocks, NT, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (dqw || dkw) qk_weight_kernel<<<2 * D / 32, 1024, 0, st>>>(p.part, p.q_blocks, (int)blocks, D, dqw, dkw);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+// Groups of 8 elements need a rotated part of a multiple of 16 elements.
 cudaError_t launch_qk_norm_rope(const QkParams& p, bool bf16, int D, cudaStream_t st) {
   if (p.rows <= 0) return cudaSuccess;
-  const unsigned g = qk_grid(p, D, 152 * 8);
+  const bool wide = p.half % 8 == 0;
   if (bf16) {
-    if (D == 128) qk_fwd_kernel<__nv_bfloat16, 128><<<g, NT, 0, st>>>(p);
-    else qk_fwd_kernel<__nv_bfloat16, 64><<<g, NT, 0, st>>>(p);
-  } else {
-    if (D == 128) qk_fwd_kernel<float, 128><<<g, NT, 0, st>>>(p);
-    else qk_fwd_kernel<float, 64><<<g, NT, 0, st>>>(p);
+    if (D == 128) return wide ? fwd<__nv_bfloat16, 128, 8>(p, st) : fwd<__nv_bfloat16, 128, 4>(p, st);
+    return wide ? fwd<__nv_bfloat16, 64, 8>(p, st) : fwd<__nv_bfloat16, 64, 4>(p, st);
   }
-  return cudaGetLastError();
+  return D == 128 ? fwd<float, 128, 4>(p, st) : fwd<float, 64, 4>(p, st);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const QkParams& p, bool bf16, int D, float* dqw, float* dkw,
                                     cudaStream_t st) {
-  const unsigned g = p.rows > 0 ? qk_grid(p, D, QK_PARTS) : 0;
-  if (g > 0) {
-    if (bf16) {
-      if (D == 128) qk_bwd_kernel<__nv_bfloat16, 128><<<g, NT, 0, st>>>(p);
-      else qk_bwd_kernel<__nv_bfloat16, 64><<<g, NT, 0, st>>>(p);
-    } else {
-      if (D == 128) qk_bwd_kernel<float, 128><<<g, NT, 0, st>>>(p);
-      else qk_bwd_kernel<float, 64><<<g, NT, 0, st>>>(p);
-    }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  const bool wide = p.half % 8 == 0;
+  if (bf16) {
+    if (D == 128)
+      return wide ? bwd<__nv_bfloat16, 128, 8>(p, dqw, dkw, st) : bwd<__nv_bfloat16, 128, 4>(p, dqw, dkw, st);
+    return wide ? bwd<__nv_bfloat16, 64, 8>(p, dqw, dkw, st) : bwd<__nv_bfloat16, 64, 4>(p, dqw, dkw, st);
   }
-  if (dqw || dkw) qk_weight_kernel<<<2 * D / 32, 1024, 0, st>>>(p.part, (int)g, D, dqw, dkw);
-  return cudaGetLastError();
+  return D == 128 ? bwd<float, 128, 4>(p, dqw, dkw, st) : bwd<float, 64, 4>(p, dqw, dkw, st);
 }
 
 }  // namespace sfg

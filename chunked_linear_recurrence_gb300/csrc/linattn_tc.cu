@@ -30,6 +30,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "linattn.cuh"
@@ -41,16 +43,19 @@ namespace {
 
 using namespace tc;
 
-constexpr int D = 128, C = LA_CHUNK, NT = 512, NS = 4;
+constexpr int D = 128, C = LA_CHUNK, NT = 640, NS = 4;
 constexpr uint32_t PANEL = 8192;                 // 64 rows x 128 bytes
 constexpr uint32_t B_Y = 0, B_X = PANEL;         // panel 0 of Y and X; panel 1 two panels on
 constexpr uint32_t B_Z = 4 * PANEL, STAGE = 6 * PANEL;
-constexpr uint32_t O_P = NS * STAGE;             // P [64][64]
-constexpr uint32_t O_OUT = O_P + PANEL;          // results, [32 rows][32 columns] of each warp
-// b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, a lam^n [64], carry [4]
-constexpr uint32_t O_TAB = O_OUT + 16384;
-constexpr uint32_t O_BAR = O_TAB + 1536;
-constexpr uint32_t SMEM = O_BAR + 256 + 1024;
+constexpr uint32_t O_P = NS * STAGE;             // P [64][64], two buffers
+constexpr uint32_t O_OUT = O_P + 2 * PANEL;      // results, [32 rows][32 columns] of each of four warps
+// b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4] (padded), the
+// weights of P by 64 + s - r in four copies, each a word further on, 8 banks apart
+constexpr uint32_t O_TAB = O_OUT + 8192;
+constexpr int PQ_LD = 136;
+constexpr uint32_t O_BAR = O_TAB + 3328;
+constexpr uint32_t SMEM = O_BAR + 320 + 1024;
+static_assert(256 * 4 + 64 + 4 * PQ_LD * 4 <= 3328 && O_BAR % 256 == 0, "tables");
 static_assert(SMEM <= 232448, "shared memory");
 
 // TMEM columns: E, the state's BF16 copy, QK, O1, O2, the weighted rows' parts (32 columns
@@ -64,40 +69,34 @@ constexpr uint32_t ID_E = idesc_bf16(128, 128, false, true);   // A in TMEM
 constexpr uint32_t ID_O1 = idesc_bf16(128, 64, false, false);   // A in TMEM
 constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 
-enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + NS, QKDONE = FREE + NS, PREADY, SPLIT,
-       EDONE = SPLIT + 2, EFREE = EDONE + 2, ODONE = EFREE + 2, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
-static_assert(8 * NBAR + 8 <= 256, "barriers");
+enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + 1, QKDONE = FREE + NS, PREADY,
+       PFREE = PREADY + 2, SPLIT, EHALF = SPLIT + 4, EDONE = EHALF + 2, EFREE = EDONE + 2,
+       O1DONE = EFREE + 2, ODONE, OFREE, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
+static_assert(8 * NBAR + 8 <= 320 && NBAR <= 32, "barriers");
 
-constexpr long long WAIT_CYCLES = 4000000000ll;   // about 2 s
+// Tries of a wait before it gives up: each may suspend the thread for up to 20 us (at the least
+// it takes the ~50 ns of the instruction), so between 0.2 and 80 s, where a wait that ends takes
+// microseconds.  (A count and not a clock: the waits are inlined into every role's loop, and
+// the loops run at the speed of instruction fetch.)
+constexpr int WAIT_TRIES = 4000000;
 
 struct Maps {
   CUtensorMap m[3][3];   // x, y, z of each pass
 };
 
-struct Cx {
-  int* status;
-  volatile int* abort;
-};
-
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Cx& cx) {
+// False when the wait gave up, or another thread of the CTA did (`abort`: where, once).
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
+#pragma unroll 1
+  for (int i = 0; i < WAIT_TRIES; ++i) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-    if (*cx.abort) return false;
-    if (clock64() - t0 > WAIT_CYCLES) {
-      *cx.abort = 1;
-      if (cx.status) {
-        atomicCAS(cx.status, 0, (int)SF_ERR_TIMEOUT);
-        atomicCAS(cx.status + 1, 0, (int)(0x40000000u | ((blockIdx.x & 0x3ffffu) << 12) |
-                                          ((threadIdx.x >> 5) << 6) | ((smem_u32(bar) & 255u) >> 3)));
-      }
-      return false;
-    }
+    if (*abort) return false;
   }
+  *abort = 0x40000000u | ((threadIdx.x >> 5) << 6) | ((smem_u32(bar) & 255u) >> 3);
+  return false;
 }
 // The lanes of a warp wait together and agree on the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Cx& cx) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* cx) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, cx));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -118,11 +117,11 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const uint32_t sb = smem_u32(sm);
   float* rd = reinterpret_cast<float*>(sm + O_TAB);   // [2][64]
   float* wr = rd + 128;                               // [2][64]
-  float* pq = rd + 256;                               // [64]
-  float* carry = rd + 320;
+  float* carry = rd + 256;
+  float* pq = rd + 272;                               // [4][PQ_LD]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + O_BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR);
-  int* abort_s = reinterpret_cast<int*>(sm + O_BAR + 8 * NBAR + 4);
+  volatile uint32_t* cx = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   int id = blockIdx.x;
@@ -145,6 +144,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   if (skip) {                                     // padding of the paged pool: zero rows
     if (kState) return;
     uint4* o = reinterpret_cast<uint4*>(q.out);
+#pragma unroll 1
     for (int64_t i = tid; i < rows * 16; i += NT)
       o[((size_t)(s0 + (i >> 4)) * p.H + h) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
     return;
@@ -153,13 +153,13 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const int nc = (int)((rows + C - 1) / C);
   const int tail = (int)(rows - (int64_t)(nc - 1) * C);   // rows of the walk's last chunk
   const float d = p.decay[h];
-  const Cx cx{p.status, abort_s};
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < NBAR; ++i)
-      mbar_init(&bars[i], i == PREADY ? 2 : i == SPLIT || i == SPLIT + 1 ? 4
+      mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? 4
                           : i == GO || i == EFREE || i == EFREE + 1 ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
-    *abort_s = 0;
+    *cx = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.m[pi][1]);
     prefetch_tmap(&maps.m[pi][2]);
@@ -171,10 +171,14 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     const int i = tid & 63, L = tid < 192 ? C : tail, t = tid - 128;
     rd[t] = i < L ? q.b * pw(rev ? L - 1 - i : i + 1) : 0.f;
     wr[t] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
-    if (t < 64) pq[t] = q.a * pw(t);
+    const int gap = rev ? t - 64 : 64 - t;          // |r - s| where s may contribute to r
+    const float f = gap >= 0 ? q.a * pw(gap) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pq[k * PQ_LD + t + k] = f;
   }
   if (!kState)   // P on the far side of the diagonal stays zero
-    for (int i = tid; i < (int)PANEL / 16; i += NT)
+#pragma unroll 1
+    for (int i = tid; i < 2 * (int)PANEL / 16; i += NT)
       *reinterpret_cast<uint4*>(sm + O_P + 16 * i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const uint32_t tm = *tslot;
 
   if (warp < 4) {
-    reg_dealloc<104>();
+    reg_dealloc<56>();
     if (warp == 0) {
       // -------------------------------------------------------------- loader, issuer of E
       const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         const int b = c % NS, L = c + 1 == nc ? tail : C;
         const int r0 = (int)(rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C);
         uint8_t* st = sm + b * STAGE;
-        uint64_t* bar = L < C ? &bars[LANDED + b] : &bars[FULL + b];   // (the last chunk only)
+        uint64_t* bar = L < C ? &bars[LANDED] : &bars[FULL + b];   // (the last chunk only)
         if (elect_one()) {
           mbar_arrive_expect_tx(bar, (kState ? 4 : 6) * PANEL);
 #pragma unroll
@@ -209,9 +213,10 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       // products.
       auto trim = [&]() {
         const int b = (nc - 1) % NS;
-        if (!warp_wait(&bars[LANDED + b], 0, cx)) return false;
+        if (!warp_wait(&bars[LANDED], 0, cx)) return false;
         uint8_t* st = sm + b * STAGE;
         const int per = (C - tail) * 8;                // 16-byte pieces of a panel
+#pragma unroll 1
         for (int i = lane; i < 4 * per; i += 32) {
           const int t = i / per, rr = i % per;
           uint8_t* base = st + (t < 2 ? B_Y + 2 * t * PANEL : B_Z + (t - 2) * PANEL);
@@ -221,27 +226,34 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         warp_arrive(&bars[FULL + b], lane);
         return true;
       };
+#pragma unroll 1
       for (int c = 0; c < NS && c < nc; ++c) load(c);
       bool ok = nc != 1 || tail == C || trim();
+#pragma unroll 1
       for (int c = 0; c < nc && ok; ++c) {
         const int b = c % NS;
         const int eb = c % NE, ph = (c / NE) & 1;
         const uint64_t dy = sdesc_sw128(sb + b * STAGE + B_Y, 2 * PANEL, 1024);
         if (c >= NE && !(ok = warp_wait(&bars[EFREE + eb], ph ^ 1, cx))) break;
-        // (the split warps have waited for the rows themselves)
-        if (!(ok = warp_wait(&bars[SPLIT + eb], ph, cx))) break;
-        tc_fence_after();
-        if (elect_one()) {
+        // E in two halves of 32 rows: the split warps refill the first under the second.  (They
+        // have waited for the rows themselves.)
 #pragma unroll
-          for (int sp = 0; sp < NSP; ++sp)
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!(ok = warp_wait(&bars[SPLIT + 2 * eb + hf], ph, cx))) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ta(tm + TM_E + 128 * eb, tm + tm_w<kState>(eb) + 32 * sp + 8 * kk,
-                          dy + kstep_mn(kk), ID_E, kk + sp > 0);
-          mma_commit(&bars[EDONE + eb]);
-          mma_commit(&bars[FREE + b]);
+            for (int sp = 0; sp < NSP; ++sp)
+#pragma unroll
+              for (int kk = 2 * hf; kk < 2 * hf + 2; ++kk)
+                mma_bf16_ta(tm + TM_E + 128 * eb, tm + tm_w<kState>(eb) + 32 * sp + 8 * kk,
+                            dy + kstep_mn(kk), ID_E, kk + sp > 0);
+            mma_commit(&bars[(hf ? EDONE : EHALF) + eb]);
+            if (hf) mma_commit(&bars[FREE + b]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
         if (c + 2 == nc && tail < C && !(ok = trim())) break;
         if (c > 0 && c + NS - 1 < nc) {
           if (!(ok = warp_wait(&bars[FREE + (c - 1) % NS], ((c - 1) / NS) & 1, cx))) break;
@@ -249,8 +261,9 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         }
       }
       if (!ok)   // let the copies in flight land
+#pragma unroll 1
         for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
-          if (c + 1 == nc && tail < C) mbar_wait(&bars[LANDED + c % NS], 0, 100000000ull);
+          if (c + 1 == nc && tail < C) mbar_wait(&bars[LANDED], 0, 100000000ull);
           else mbar_wait(&bars[FULL + c % NS], (c / NS) & 1, 100000000ull);
         }
       if (elect_one()) mma_commit(&bars[DRAIN]);
@@ -258,39 +271,51 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------------- issuer of QK, O1, O2
-      // (the whole warp waits; one elected lane issues)
-      auto issue_qk = [&](int c) {
-        const uint64_t dy = sdesc_sw128(sb + (c % NS) * STAGE + B_Y, 0, 1024);
-        const uint32_t t = tm + TM_P;
-        tc_fence_after();
-        if (elect_one()) {
+      // (the whole warp waits; one elected lane issues).  A batch of products costs ~200 cycles
+      // beyond the tensor pipe's own time, so O1 and O2 go together.  The next chunk's QK goes
+      // first, while the results of the last chunk are being read, if its rows are there (P takes
+      // as long as the rest of a step), else in its own turn.
+      int qn = 0;                                      // chunks whose QK is issued
+      auto put_qk = [&]() {                            // by the elected lane
+        const uint64_t dy = sdesc_sw128(sb + (qn % NS) * STAGE + B_Y, 0, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16(t, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
-          mma_commit(&bars[QKDONE]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16(tm + TM_P, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
+        mma_commit(&bars[QKDONE]);
       };
-      auto full = [&](int c) { return warp_wait(&bars[FULL + c % NS], (c / NS) & 1, cx); };
-      bool ok = !kState && nc > 0 && full(0);
-      if (ok) issue_qk(0);
+      bool ok = !kState;
+#pragma unroll 1
       for (int c = 0; c < nc && ok; ++c) {
         const int b = c % NS;
         const uint32_t st = sb + b * STAGE;
+        if (qn == c) {                                 // its own turn
+          if (!(ok = warp_wait(&bars[FULL + b], (c / NS) & 1, cx))) break;
+          tc_fence_after();
+          if (elect_one()) put_qk();
+          __syncwarp();
+          ++qn;
+        }
+        if (qn < nc) {
+          if (!(ok = warp_wait(&bars[PFREE], c & 1, cx))) break;   // P of this chunk has been read
+          if (__all_sync(0xffffffffu, mbar_test(&bars[FULL + qn % NS], (qn / NS) & 1))) {
+            tc_fence_after();
+            if (elect_one()) put_qk();
+            __syncwarp();
+            ++qn;
+          }
+        }
+        if (c > 0 && !(ok = warp_wait(&bars[OFREE], (c - 1) & 1, cx))) break;
         if (!(ok = warp_wait(&bars[GO], c & 1, cx))) break;
+        if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
         tc_fence_after();
         const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
+        const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
+        const uint64_t dp = sdesc_sw128(sb + O_P + (c & 1) * PANEL, 0, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
-        }
-        __syncwarp();
-        if (!(ok = warp_wait(&bars[PREADY], c & 1, cx))) break;
-        tc_fence_after();
-        const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
-        const uint64_t dp = sdesc_sw128(sb + O_P, 0, 1024);
-        if (elect_one()) {
+          mma_commit(&bars[O1DONE]);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)(kk * 2), ID_O2, kk > 0);
@@ -298,11 +323,6 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           mma_commit(&bars[FREE + b]);
         }
         __syncwarp();
-        // the next chunk's QK, under the state warps' turn
-        if (c + 1 < nc) {
-          if (!(ok = full(c + 1))) break;
-          issue_qk(c + 1);
-        }
       }
       if (elect_one()) mma_commit(&bars[DRAIN + 1]);
       mbar_wait(&bars[DRAIN + 1], 0, 100000000ull);
@@ -321,52 +341,51 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         if (lane == 0) mbar_arrive(&bars[TBL]);
       }
       if (!kState) {
-        // row r of P; the factors a lam^|r-s| stay in registers.  The half on the far side of
-        // the diagonal (32 columns of one warp) is never touched: it stays zero.
+        // row r of P.  The half on the far side of the diagonal (32 columns of one warp) is never
+        // touched: it stays zero.
         const int r = (warp - 2) * 32 + lane;          // TMEM lane 64 + r
-        float f[2][32];
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int s = 32 * half + e, gap = rev ? s - r : r - s;
-            f[half][e] = gap >= 0 ? pq[gap & 63] : 0.f;
-          }
+        // a lam^|r-s|, or 0, at f[s] (the copy in which that is 16-byte aligned)
+        const float* f = pq + (r & 3) * (PQ_LD + 1) + 64 - r;
         const uint32_t tl = tm + TM_P + ((uint32_t)(warp * 32) << 16);
-        uint8_t* row = sm + O_P + r * 128;
+        const int s0 = rev && warp == 3 ? 32 : 0, s1 = !rev && warp == 2 ? 32 : 64;
+#pragma unroll 1
         for (int c = 0; c < nc; ++c) {
           if (!warp_wait(&bars[QKDONE], c & 1, cx)) break;
           tc_fence_after();
+          uint8_t* row = sm + O_P + (c & 1) * PANEL + r * 128;
+#pragma unroll 1
+          for (int s = s0; s < s1; s += 16) {
+            float x[16];
+            tmem_ld16(tl + s, x);
+            float4 g[4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (rev ? half == 0 && warp == 3 : half == 1 && warp == 2) continue;
+            for (int e = 0; e < 4; ++e) g[e] = *reinterpret_cast<const float4*>(f + s + 4 * e);
+            tmem_ld_wait();
+            if (s + 16 >= s1) {
+              tc_fence_before();
+              warp_arrive(&bars[PFREE], lane);
+            }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float x[16];
-              tmem_ld16(tl + 32 * half + 16 * k, x);
-              tmem_ld_wait();
+            for (int ch = 0; ch < 2; ++ch) {
+              uint32_t v[4];
 #pragma unroll
-              for (int ch = 0; ch < 2; ++ch) {
-                const float* g = &f[half][16 * k + 8 * ch];
-                const float* y = x + 8 * ch;
-                uint4 v;
-                v.x = pack_bf16x2(y[0] * g[0], y[1] * g[1]);
-                v.y = pack_bf16x2(y[2] * g[2], y[3] * g[3]);
-                v.z = pack_bf16x2(y[4] * g[4], y[5] * g[5]);
-                v.w = pack_bf16x2(y[6] * g[6], y[7] * g[7]);
-                *reinterpret_cast<uint4*>(row + (((4 * half + 2 * k + ch) ^ (r & 7)) << 4)) = v;
+              for (int e = 0; e < 4; ++e) {
+                const float4 w = g[2 * ch + (e >> 1)];
+                v[e] = pack2(mul2(make_float2(x[8 * ch + 2 * e], x[8 * ch + 2 * e + 1]),
+                                  e & 1 ? make_float2(w.z, w.w) : make_float2(w.x, w.y)));
               }
+              *reinterpret_cast<uint4*>(row + ((((s >> 3) + ch) ^ (r & 7)) << 4)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
             }
           }
           fence_proxy_async_smem();
-          tc_fence_before();
-          warp_arrive(&bars[PREADY], lane);
+          warp_arrive(&bars[PREADY + (c & 1)], lane);
         }
       }
     }
   } else if (warp < 12) {
-    reg_alloc<160>();
-    // ---------------------------------------------------------------- state and results
+    reg_alloc<128>();
+    // ---------------------------------------------------------------- state
     const int wg = (warp - 4) >> 2;
     const int z = ((warp & 3) << 5) + lane;
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -407,92 +426,36 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       warp_arrive(&bars[GO], lane);
     }
     bool ok = nc == 0 || warp_wait(&bars[TBL], 0, cx);
-    const uint32_t stage = sb + O_OUT + (warp - 4) * 2048;
+#pragma unroll 1
     for (int c = 0; c < nc && ok; ++c) {
       const bool end = c + 1 == nc;
-      const int L = end ? tail : C;
       if (!(ok = warp_wait(&bars[EDONE + c % NE], (c / NE) & 1, cx))) break;
       tc_fence_after();
       const float2 fh = make_float2(carry[end ? 2 : 0], carry[end ? 2 : 0]);
       const float2 fl = make_float2(carry[end ? 3 : 1], carry[end ? 3 : 1]);
-      float x[2][32];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) tmem_ld32(tl + TM_E + 128 * (c % NE) + 64 * wg + 32 * k, x[k]);
-      tmem_ld_wait();
-      tc_fence_before();
-      warp_arrive(&bars[EFREE + c % NE], lane);
+      for (int k = 0; k < 2; ++k) {
+        float x[32];
+        tmem_ld32(tl + TM_E + 128 * (c % NE) + 64 * wg + 32 * k, x);
+        tmem_ld_wait();
+        if (k == 1) {
+          tc_fence_before();
+          warp_arrive(&bars[EFREE + c % NE], lane);
+        }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float* y = &x[e >> 4][2 * (e & 15)];
-        s[e] = fma2(fh, s[e], fma2(fl, s[e], make_float2(y[0], y[1])));
+        for (int e = 0; e < 16; ++e) {
+          float2& v = s[16 * k + e];
+          v = fma2(fh, v, fma2(fl, v, make_float2(x[2 * e], x[2 * e + 1])));
+        }
       }
-      if (kState) continue;
-      if (!(ok = warp_wait(&bars[ODONE], c & 1, cx))) break;
+      if (kState || end) continue;
+      // S X^T of this chunk has read the old copy
+      if (!(ok = warp_wait(&bars[O1DONE], c & 1, cx))) break;
       tc_fence_after();
-      // O1, O2 rows [32 wg, + 32) as 8 x 8 tiles: of row pairs 8 g + 2 (lane % 4), + 1, columns
-      // 16 hz + 8 k + lane / 4 of the warp's 32
-      float o1[2][16], o2[2][16];
-      if (!end) put_state();                          // S X^T of this chunk has read the old copy
-#pragma unroll
-      for (int hz = 0; hz < 2; ++hz) {
-        tmem_ld_16x32(tl + ((uint32_t)(16 * hz) << 16) + TM_O1 + 32 * wg, o1[hz]);
-        tmem_ld_16x32(tl + ((uint32_t)(16 * hz) << 16) + TM_O2 + 32 * wg, o2[hz]);
-      }
-      tmem_ld_wait();
-      if (!end) {
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&bars[GO], lane);
-      }
-      const int64_t r0 = (rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C) + 32 * wg;
-      const int cnt = L - 32 * wg;                    // rows that exist
-      const float2* f2 = reinterpret_cast<const float2*>(rd + (end ? 64 : 0) + 32 * wg) + (lane & 3);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float2 f = f2[4 * g];
-        uint32_t v[4];                                // tiles of columns 0, 8, 16, 24
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float* y = &o1[k >> 1][4 * g + 2 * (k & 1)];
-          const float* y2 = &o2[k >> 1][4 * g + 2 * (k & 1)];
-          const float2 t = fma2(f, make_float2(y[0], y[1]), make_float2(y2[0], y2[1]));
-          v[k] = pack_bf16x2(t.x, t.y);
-          y[0] = t.x;
-          y[1] = t.y;
-        }
-        // row 8 g + i of the 64-byte rows, its 16-byte pieces in the order that keeps eight rows
-        // on different banks
-        if (!q.out_f32) {
-          const int i = lane & 7, m = lane >> 3;
-          stmatrix_x4_trans(stage + (8 * g + i) * 64 + ((m ^ ((i >> 1) & 3)) << 4), v);
-        }
-      }
-      if (q.out_f32) {
-        float* o = reinterpret_cast<float*>(q.out) +
-                   ((size_t)(r0 + 2 * (lane & 3)) * p.H + h) * D + 32 * (warp & 3) + (lane >> 2);
-#pragma unroll
-        for (int hz = 0; hz < 2; ++hz)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int row = 8 * (e >> 2) + (e & 1), col = 16 * hz + 8 * ((e >> 1) & 1);
-            if (2 * (lane & 3) + row < cnt) o[(size_t)row * p.H * D + col] = o1[hz][e];
-          }
-        continue;
-      }
-      __syncwarp();
-      const int rr = lane >> 2;
-      uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(q.out) +
-                                          ((size_t)(r0 + rr) * p.H + h) * D + 32 * (warp & 3) +
-                                          8 * (lane & 3));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(stage + (8 * e + rr) * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4)) : "memory");
-        if (rr + 8 * e < cnt) o[(size_t)e * p.H * D] = v;   // 8 rows of H D elements, 8 a uint4
-      }
-      __syncwarp();
+      put_state();
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&bars[GO], lane);
     }
     float* dst = !ok ? nullptr : kState ? q.seg_state + uoff : last ? la_exit(p, q, n, h, D) : nullptr;
     if (dst) {
@@ -508,12 +471,11 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         for (int e = 0; e < 16; ++e) v[e] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
       }
     }
-  } else {
-    reg_dealloc<88>();
+  } else if (warp < 16) {
+    reg_dealloc<72>();
     // ---------------------------------------------------------------- weighted rows in BF16 parts
     // Each warp weights and splits the 32 columns z of its TMEM lanes: 16 at a time, transposed
-    // on the way from shared memory (8 x 8 tiles), the rows j along the TMEM columns.  The first
-    // 16 are ready before the buffer is free.
+    // on the way from shared memory (8 x 8 tiles), the rows j along the TMEM columns.
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const int m = lane >> 3, i = lane & 7;
     // lane's source row of K step 0: j = 8 (m / 2) + i, columns z0 + 8 (m % 2) ..; z0 of either
@@ -521,42 +483,131 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     const uint32_t ch = (uint32_t)(4 * (warp & 1) + (m & 1));
     const uint32_t src = sb + B_Z + (uint32_t)((warp & 3) >> 1) * PANEL + (uint32_t)(8 * (m >> 1) + i) * 128u;
     const uint32_t c0 = (ch ^ (uint32_t)i) << 4, c1 = ((ch + 2) ^ (uint32_t)i) << 4;
+#pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const int b = c % NS, eb = c % NE;
       if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
       const float2* wt = reinterpret_cast<const float2*>(wr + (c + 1 == nc ? 64 : 0)) + (lane & 3);
-      float2 wv[8];                                   // rows 8 g + 2 (lane % 4), + 1
-#pragma unroll
-      for (int g = 0; g < 8; ++g) wv[g] = wt[4 * g];
+      uint32_t from = src + b * STAGE, to = tl + tm_w<kState>(eb);
       bool ok = true;
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        // the products of the chunk that had this half of the buffer are done
+        if (c >= NE && !(ok = warp_wait(&bars[(hf ? EDONE : EHALF) + eb], ((c / NE) & 1) ^ 1, cx))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int kk = 0; kk < 2; ++kk) {
+          // 16 rows: 2 (lane % 4), + 1 and 8 more
+          const float2 wv[2] = {wt[0], wt[4]};
 #pragma unroll
-      for (int hz = 0; hz < 2; ++hz) {
-        uint32_t o[NSP][16];
+          for (int hz = 0; hz < 2; ++hz) {
+            uint32_t v[4], o[NSP][4];
+            ldmatrix_x4_trans(from + (hz ? c1 : c0), v);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          uint32_t v[4];
-          ldmatrix_x4_trans(src + b * STAGE + kk * 2048 + (hz ? c1 : c0), v);
+            for (int e = 0; e < 4; ++e) {
+              float2 x = mul2(unpack2(v[e]), wv[e >> 1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 x = mul2(unpack2(v[e]), wv[2 * kk + (e >> 1)]);
+              for (int sp = 0; sp < NSP; ++sp) {
+                o[sp][e] = pack2(x);
+                if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][e]));
+              }
+            }
 #pragma unroll
-            for (int sp = 0; sp < NSP; ++sp) {
-              o[sp][4 * kk + e] = pack_bf16x2(x.x, x.y);
-              if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][4 * kk + e]));
+            for (int sp = 0; sp < NSP; ++sp)
+              tmem_st_16x8(to + ((uint32_t)(16 * hz) << 16) + 32 * sp, o[sp][0], o[sp][1], o[sp][2],
+                           o[sp][3]);
+          }
+          wt += 8;
+          from += 2048;
+          to += 8;
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&bars[SPLIT + 2 * eb + hf], lane);
+      }
+      if (!ok) break;
+    }
+  } else {
+    // (as launched: 96 registers)
+    // ---------------------------------------------------------------- results
+    // A warp takes the 32 columns z of its TMEM lanes, 32 rows at a time, as 8 x 8 tiles: of the
+    // row pairs 8 g + 2 (lane % 4), + 1, columns 8 k + lane / 4.
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t stage = sb + O_OUT + (warp & 3) * 2048;
+    const int H = p.H;
+    // the lane's row and 16 bytes of a store (eight rows a store)
+    const int rr = lane >> 2;
+    const uint32_t sw = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    const uint32_t sr = stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4);
+    const size_t col = (size_t)h * D + 32 * (warp & 3);
+    auto walk = [&](auto f32) {
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c) {
+        const bool end = c + 1 == nc;
+        const int L = end ? tail : C;
+        const int64_t r0 = rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C;
+        const float2* f2 = reinterpret_cast<const float2*>(rd + (end ? 64 : 0)) + (lane & 3);
+        if (!warp_wait(&bars[ODONE], c & 1, cx)) break;
+        tc_fence_after();
+        uint32_t v[2][4][4];                            // [hf][g][k]
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int hz = 0; hz < 2; ++hz) {
+            float o1[16], o2[16];
+            tmem_ld_16x32(tl + ((uint32_t)(16 * hz) << 16) + TM_O1 + 32 * hf, o1);
+            tmem_ld_16x32(tl + ((uint32_t)(16 * hz) << 16) + TM_O2 + 32 * hf, o2);
+            tmem_ld_wait();
+            if (hf + hz == 2) {
+              tc_fence_before();
+              warp_arrive(&bars[OFREE], lane);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float2 f = f2[16 * hf + 4 * g];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int e = 4 * g + 2 * k;
+                const float2 t = fma2(f, make_float2(o1[e], o1[e + 1]), make_float2(o2[e], o2[e + 1]));
+                if constexpr (f32.value) {
+                  const int row = 32 * hf + 8 * g + 2 * (lane & 3);
+                  float* of = reinterpret_cast<float*>(q.out) + (size_t)(r0 + row) * H * D + col +
+                              16 * hz + 8 * k + rr;
+                  if (row < L) of[0] = t.x;
+                  if (row + 1 < L) of[(size_t)H * D] = t.y;
+                } else {
+                  v[hf][g][2 * hz + k] = pack2(t);
+                }
+              }
             }
           }
         }
-        // the products of the chunk that had the buffer are done
-        if (hz == 0 && c >= NE && !(ok = warp_wait(&bars[EDONE + eb], ((c / NE) & 1) ^ 1, cx))) break;
-        if (hz == 0) tc_fence_after();
+        if constexpr (!f32.value) {
+          // turned in shared memory: row 8 g + i of the 64-byte rows, its 16-byte pieces in the
+          // order that keeps eight rows on different banks
+          uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(q.out) +
+                                              (size_t)(r0 + rr) * H * D + col + 8 * (lane & 3));
 #pragma unroll
-        for (int sp = 0; sp < NSP; ++sp)
-          tmem_st_16x32(tl + ((uint32_t)(16 * hz) << 16) + tm_w<kState>(eb) + 32 * sp, o[sp]);
+          for (int hf = 0; hf < 2; ++hf) {
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) stmatrix_x4_trans(sw + 512 * g, v[hf][g]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 w4;
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w) : "r"(sr + 512 * e) : "memory");
+              if (32 * hf + rr + 8 * e < L) *o = w4;    // 8 rows of H D elements
+              o += (size_t)H * D;
+            }
+          }
+        }
       }
-      if (!ok) break;
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(&bars[SPLIT + eb], lane);
+    };
+    if (!kState) {
+      if (q.out_f32) walk(std::true_type());
+      else walk(std::false_type());
     }
   }
   tc_fence_before();
@@ -565,6 +616,10 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   if (warp == 0) {
     tmem_relinquish();
     tmem_dealloc(tm, 512);
+    if (lane == 0 && *cx && p.status) {
+      atomicCAS(p.status, 0, (int)SF_ERR_TIMEOUT);
+      atomicCAS(p.status + 1, 0, (int)(*cx | ((blockIdx.x & 0x3ffffu) << 12)));
+    }
   }
 }
 

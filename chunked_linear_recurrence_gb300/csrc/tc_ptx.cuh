@@ -387,16 +387,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16
       "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
 }
-// registers -> TMEM: 16 lanes x 32 consecutive 32-bit columns.  Lane T holds row T / 4 (u[2 g])
-// and row 8 + T / 4 (u[2 g + 1]) of column 4 g + T % 4: the layout that ldmatrix gives 8 x 8
-// tiles of 16-bit pairs.
-__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&u)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-      "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-      : "memory");
+// registers -> TMEM: 16 lanes x 8 consecutive 32-bit columns.  Lane T holds row T / 4 (a, c) and
+// row 8 + T / 4 (b, d) of columns T % 4 (a, b) and 4 + T % 4 (c, d): the layout that ldmatrix gives
+// 8 x 8 tiles of 16-bit pairs.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 // Four 8 x 8 tiles of 16-bit elements, transposed: lanes 8 m .. 8 m + 7 give the addresses of
 // tile m's rows; lane T receives the elements (2 (T % 4), T / 4) and (2 (T % 4) + 1, T / 4).

@@ -154,18 +154,40 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const int tail = (int)(rows - (int64_t)(nc - 1) * C);   // rows of the walk's last chunk
   const float d = p.decay[h];
 
-  if (tid == 0) {
-#pragma unroll 1
-    for (int i = 0; i < NBAR; ++i)
+  const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
+  int issued = 0;
+  auto load = [&](int c) {
+    const int b = c % NS, L = c + 1 == nc ? tail : C;
+    const int r0 = (int)(rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C);
+    uint8_t* st = sm + b * STAGE;
+    uint64_t* bar = L < C ? &bars[LANDED] : &bars[FULL + b];   // (the last chunk only)
+    if (elect_one()) {
+      mbar_arrive_expect_tx(bar, (kState ? 4 : 6) * PANEL);
+#pragma unroll
+      for (int pp = 0; pp < 2; ++pp) {
+        tma_load_3d(st + B_Y + 2 * pp * PANEL, &maps.m[pi][1], bar, 64 * pp, hy, r0);
+        tma_load_3d(st + B_Z + pp * PANEL, &maps.m[pi][2], bar, 64 * pp, hz, r0);
+        if (!kState) tma_load_3d(st + B_X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
+      }
+    }
+    __syncwarp();
+    issued = c + 1;
+  };
+  if (warp == 0) {
+    // the barriers, and the first chunks on their way before anything else
+    if (lane < NBAR) {
+      const int i = lane;
       mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? 4
                           : i == GO || i == EFREE || i == EFREE + 1 ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
-    *cx = 0;
+    }
+    if (lane == 0) *cx = 0;
     fence_mbar_init();
-    prefetch_tmap(&maps.m[pi][1]);
-    prefetch_tmap(&maps.m[pi][2]);
-    if (!kState) prefetch_tmap(&maps.m[pi][0]);
+    fence_proxy_async_smem();
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < NS && c < nc; ++c) load(c);
   }
-  if (warp == 0) tmem_alloc(tslot, 512);
+  if (warp == 1) tmem_alloc(tslot, 512);
   auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
   if (tid >= 128 && tid < 256) {
     const int i = tid & 63, L = tid < 192 ? C : tail, t = tid - 128;
@@ -186,29 +208,68 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   tc_fence_after();
   const uint32_t tm = *tslot;
 
+  // ------------------------------------------------------------------ weighted rows in BF16 parts
+  // (four warps; chunks first, first + step, ..)
+  auto split_rows = [&](int first, int step) {
+    // Each warp weights and splits the 32 columns z of its TMEM lanes: 16 at a time, transposed
+    // on the way from shared memory (8 x 8 tiles), the rows j along the TMEM columns.
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const int m = lane >> 3, i = lane & 7;
+    // lane's source row of K step 0: j = 8 (m / 2) + i, columns z0 + 8 (m % 2) ..; z0 of either
+    // half differs in bit 1 of the 16-byte chunk
+    const uint32_t ch = (uint32_t)(4 * (warp & 1) + (m & 1));
+    const uint32_t src = sb + B_Z + (uint32_t)((warp & 3) >> 1) * PANEL + (uint32_t)(8 * (m >> 1) + i) * 128u;
+    const uint32_t c0 = (ch ^ (uint32_t)i) << 4, c1 = ((ch + 2) ^ (uint32_t)i) << 4;
+#pragma unroll 1
+    for (int c = first; c < nc; c += step) {
+      const int b = c % NS, eb = c % NE;
+      if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
+      const float2* wt = reinterpret_cast<const float2*>(wr + (c + 1 == nc ? 64 : 0)) + (lane & 3);
+      uint32_t from = src + b * STAGE, to = tl + tm_w<kState>(eb);
+      bool ok = true;
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        // the products of the chunk that had this half of the buffer are done
+        if (c >= NE && !(ok = warp_wait(&bars[(hf ? EDONE : EHALF) + eb], ((c / NE) & 1) ^ 1, cx))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int kk = 0; kk < 2; ++kk) {
+          // 16 rows: 2 (lane % 4), + 1 and 8 more
+          const float2 wv[2] = {wt[0], wt[4]};
+#pragma unroll
+          for (int hz = 0; hz < 2; ++hz) {
+            uint32_t v[4], o[NSP][4];
+            ldmatrix_x4_trans(from + (hz ? c1 : c0), v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float2 x = mul2(unpack2(v[e]), wv[e >> 1]);
+#pragma unroll
+              for (int sp = 0; sp < NSP; ++sp) {
+                o[sp][e] = pack2(x);
+                if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][e]));
+              }
+            }
+#pragma unroll
+            for (int sp = 0; sp < NSP; ++sp)
+              tmem_st_16x8(to + ((uint32_t)(16 * hz) << 16) + 32 * sp, o[sp][0], o[sp][1], o[sp][2],
+                           o[sp][3]);
+          }
+          wt += 8;
+          from += 2048;
+          to += 8;
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&bars[SPLIT + 2 * eb + hf], lane);
+      }
+      if (!ok) break;
+    }
+  };
+
   if (warp < 4) {
     reg_dealloc<56>();
     if (warp == 0) {
       // -------------------------------------------------------------- loader, issuer of E
-      const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
-      int issued = 0;
-      auto load = [&](int c) {
-        const int b = c % NS, L = c + 1 == nc ? tail : C;
-        const int r0 = (int)(rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C);
-        uint8_t* st = sm + b * STAGE;
-        uint64_t* bar = L < C ? &bars[LANDED] : &bars[FULL + b];   // (the last chunk only)
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar, (kState ? 4 : 6) * PANEL);
-#pragma unroll
-          for (int pp = 0; pp < 2; ++pp) {
-            tma_load_3d(st + B_Y + 2 * pp * PANEL, &maps.m[pi][1], bar, 64 * pp, hy, r0);
-            tma_load_3d(st + B_Z + pp * PANEL, &maps.m[pi][2], bar, 64 * pp, hz, r0);
-            if (!kState) tma_load_3d(st + B_X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
-          }
-        }
-        __syncwarp();
-        issued = c + 1;
-      };
       // A short last chunk: rows past the end (other tokens, or NaN padding) must not reach the
       // products.
       auto trim = [&]() {
@@ -226,8 +287,6 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         warp_arrive(&bars[FULL + b], lane);
         return true;
       };
-#pragma unroll 1
-      for (int c = 0; c < NS && c < nc; ++c) load(c);
       bool ok = nc != 1 || tail == C || trim();
 #pragma unroll 1
       for (int c = 0; c < nc && ok; ++c) {
@@ -473,60 +532,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     }
   } else if (warp < 16) {
     reg_dealloc<72>();
-    // ---------------------------------------------------------------- weighted rows in BF16 parts
-    // Each warp weights and splits the 32 columns z of its TMEM lanes: 16 at a time, transposed
-    // on the way from shared memory (8 x 8 tiles), the rows j along the TMEM columns.
-    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const int m = lane >> 3, i = lane & 7;
-    // lane's source row of K step 0: j = 8 (m / 2) + i, columns z0 + 8 (m % 2) ..; z0 of either
-    // half differs in bit 1 of the 16-byte chunk
-    const uint32_t ch = (uint32_t)(4 * (warp & 1) + (m & 1));
-    const uint32_t src = sb + B_Z + (uint32_t)((warp & 3) >> 1) * PANEL + (uint32_t)(8 * (m >> 1) + i) * 128u;
-    const uint32_t c0 = (ch ^ (uint32_t)i) << 4, c1 = ((ch + 2) ^ (uint32_t)i) << 4;
-#pragma unroll 1
-    for (int c = 0; c < nc; ++c) {
-      const int b = c % NS, eb = c % NE;
-      if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
-      const float2* wt = reinterpret_cast<const float2*>(wr + (c + 1 == nc ? 64 : 0)) + (lane & 3);
-      uint32_t from = src + b * STAGE, to = tl + tm_w<kState>(eb);
-      bool ok = true;
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        // the products of the chunk that had this half of the buffer are done
-        if (c >= NE && !(ok = warp_wait(&bars[(hf ? EDONE : EHALF) + eb], ((c / NE) & 1) ^ 1, cx))) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int kk = 0; kk < 2; ++kk) {
-          // 16 rows: 2 (lane % 4), + 1 and 8 more
-          const float2 wv[2] = {wt[0], wt[4]};
-#pragma unroll
-          for (int hz = 0; hz < 2; ++hz) {
-            uint32_t v[4], o[NSP][4];
-            ldmatrix_x4_trans(from + (hz ? c1 : c0), v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float2 x = mul2(unpack2(v[e]), wv[e >> 1]);
-#pragma unroll
-              for (int sp = 0; sp < NSP; ++sp) {
-                o[sp][e] = pack2(x);
-                if (sp + 1 < NSP) x = sub2(x, unpack2(o[sp][e]));
-              }
-            }
-#pragma unroll
-            for (int sp = 0; sp < NSP; ++sp)
-              tmem_st_16x8(to + ((uint32_t)(16 * hz) << 16) + 32 * sp, o[sp][0], o[sp][1], o[sp][2],
-                           o[sp][3]);
-          }
-          wt += 8;
-          from += 2048;
-          to += 8;
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&bars[SPLIT + 2 * eb + hf], lane);
-      }
-      if (!ok) break;
-    }
+    split_rows(0, NE);
   } else {
     // (as launched: 96 registers)
     // ---------------------------------------------------------------- results
@@ -605,7 +611,9 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         }
       }
     };
-    if (!kState) {
+    if (kState) {
+      split_rows(1, 2);                               // no results: the other buffer's chunks
+    } else {
       if (q.out_f32) walk(std::true_type());
       else walk(std::false_type());
     }
@@ -613,7 +621,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {
+  if (warp == 1) {
     tmem_relinquish();
     tmem_dealloc(tm, 512);
     if (lane == 0 && *cx && p.status) {

@@ -173,6 +173,13 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     __syncwarp();
     issued = c + 1;
   };
+  auto land = [&]() {   // the copies in flight, when a wait has failed
+#pragma unroll 1
+    for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
+      if (c + 1 == nc && tail < C) mbar_wait(&bars[LANDED], 0, 100000000ull);
+      else mbar_wait(&bars[FULL + c % NS], (c / NS) & 1, 100000000ull);
+    }
+  };
   if (warp == 0) {
     // the barriers, and the first chunks on their way before anything else
     if (lane < NBAR) {
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         warp_arrive(&bars[FULL + b], lane);
         return true;
       };
-      bool ok = nc != 1 || tail == C || trim();
+      bool ok = kState || nc != 1 || tail == C || trim();
 #pragma unroll 1
       for (int c = 0; c < nc && ok; ++c) {
         const int b = c % NS;
@@ -313,18 +320,13 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           __syncwarp();
         }
         if (!ok) break;
-        if (c + 2 == nc && tail < C && !(ok = trim())) break;
-        if (c > 0 && c + NS - 1 < nc) {
+        if (!kState && c + 2 == nc && tail < C && !(ok = trim())) break;
+        if (!kState && c > 0 && c + NS - 1 < nc) {
           if (!(ok = warp_wait(&bars[FREE + (c - 1) % NS], ((c - 1) / NS) & 1, cx))) break;
           load(c + NS - 1);
         }
       }
-      if (!ok)   // let the copies in flight land
-#pragma unroll 1
-        for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
-          if (c + 1 == nc && tail < C) mbar_wait(&bars[LANDED], 0, 100000000ull);
-          else mbar_wait(&bars[FULL + c % NS], (c / NS) & 1, 100000000ull);
-        }
+      if (!kState && !ok) land();
       if (elect_one()) mma_commit(&bars[DRAIN]);
       mbar_wait(&bars[DRAIN], 0, 100000000ull);
       __syncwarp();
@@ -342,9 +344,18 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           mma_bf16(tm + TM_P, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
         mma_commit(&bars[QKDONE]);
       };
-      bool ok = !kState;
+      bool ok = true;
+      if (kState) {                                    // the loader, where E is the only product
+        issued = nc < NS ? nc : NS;
 #pragma unroll 1
-      for (int c = 0; c < nc && ok; ++c) {
+        for (int c = NS; c < nc; ++c) {
+          if (!(ok = warp_wait(&bars[FREE + c % NS], ((c - NS) / NS) & 1, cx))) break;
+          load(c);
+        }
+        if (!ok) land();
+      }
+#pragma unroll 1
+      for (int c = 0; !kState && c < nc && ok; ++c) {
         const int b = c % NS;
         const uint32_t st = sb + b * STAGE;
         if (qn == c) {                                 // its own turn

@@ -13,9 +13,9 @@
 //     dv:   k, q, do                reverse   a = c = scale, b = 1   S = cotangent
 //     dk:   v, do, q                reverse   a = c = scale, b = 1   S = cotangent^T
 //
-// A long walk is cut into segments of `seg` rows (in walk order) that run side by side: a
-// first launch computes what each segment adds to the state, a second carries the entry
-// states over the segments, a third runs the segments from them.
+// A long walk is cut into segments of `seg` rows (in walk order) that run side by side: a first
+// launch computes what each piece of `pre` rows (seg / pre to a segment) adds to the state, a
+// second carries the entry states over the pieces, a third runs the segments from them.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -31,7 +31,8 @@ struct LaPass {
   void* out;            // [rows, H, D]: the token type, or FP32 (out_f32)
   const float* s_in;    // [N,H,D,D] or NULL (zeros)
   float* s_out;         // [N,H,D,D] or NULL
-  float* seg_state;     // [units,H,D,D] (z rows): segment sums, then segment entry states
+  float* entry;         // [units,H,D,D] (z rows): entry states of the segments
+  float* sums;          // [pre_units,H,D,D] (z rows): what each piece adds to the state
   int hx, hy, hz;       // heads of x, y, z (each divides H)
   int s_t;              // the state is stored as [y][z] (s_in, s_out)
   int out_f32;
@@ -49,66 +50,161 @@ struct LaParams {
   const uint8_t* has_init;
   int num_slots;
   int B, T, H, N;
-  int seg;              // rows of a segment, a multiple of 64
-  int units;            // launched (sequence, segment) units; packed: an upper bound
+  int seg, pre;         // rows of a segment and of a piece, multiples of 64; pre divides seg
+  int units, pre_units; // launched (sequence, segment) and (sequence, piece) units; packed: bounds
   int* status;
 };
 
 constexpr int LA_CHUNK = 64;
 
-// (sequence, segment) units of a launch whose segments have `seg` rows.
-inline int64_t la_units(int B, int T, int N, bool packed, int seg) {
-  const int64_t per = T > 0 ? (T + (int64_t)seg - 1) / seg : 1;
-  return packed ? (int64_t)T / seg + N : (int64_t)N * (per > 0 ? per : 1);
+// (sequence, segment) units of a launch whose segments have `seg` rows, and (sequence, piece)
+// units of all segments but each walk's last.
+inline int64_t la_units(int64_t T, int64_t N, bool packed, int64_t seg) {
+  const int64_t per = T > seg ? (T + seg - 1) / seg : 1;
+  return packed ? T / seg + N : N * per;
+}
+inline int64_t la_pre_units(int64_t T, int64_t N, bool packed, int64_t seg, int64_t pre) {
+  const int64_t cuts = packed ? T / seg : N * ((T > seg ? (T + seg - 1) / seg : 1) - 1);
+  return cuts * (seg / pre);
 }
 
 #ifdef __CUDACC__
-// Unit u -> sequence n and its segment w in walk order; a warp calls it together.  False
-// when the unit holds nothing.  bos, eos: the sequence's rows, clamped into [0, B T].
-__device__ __forceinline__ bool la_locate(int u, const LaParams& p, int& n, int& w, int64_t& bos,
-                                          int64_t& eos) {
+struct LaUnit {
+  int n;                // sequence
+  int64_t bos, eos;     // its rows, clamped into [0, B T]
+  int64_t off, rows;    // the unit's rows in walk order
+  int at;               // its place in `entry` (segments) or `sums` (pieces)
+  bool last;            // the walk ends with it
+};
+
+__device__ __forceinline__ int la_segments(int64_t len, int seg) {
+  return len > seg ? (int)((len + seg - 1) / seg) : 1;
+}
+
+// Unit u of a launch; a warp calls it together.  False when the unit holds nothing.  Whole
+// segments come first, then the walks' remainders -- the longest first, for up to 64 packed
+// sequences -- so that the launch ends evenly.
+template <bool kPieces>
+__device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
   const int64_t total = (int64_t)p.B * p.T;
+  const int k = p.seg / p.pre;
   if (!p.cu) {
-    const int per = p.T > 0 ? (p.T + p.seg - 1) / p.seg : 1;
-    n = u / per;
-    w = u % per;
-    if (n >= p.N) return false;
-    bos = (int64_t)n * p.T;
-    eos = bos + p.T;
+    const int S = la_segments(p.T, p.seg);
+    int w;
+    if (kPieces) {
+      const int per = (S - 1) * k;
+      if (per == 0) return false;
+      t.n = u / per;
+      w = u % per;
+      t.at = u;
+    } else {
+      w = u / p.N;
+      t.n = u % p.N;
+      t.at = t.n * S + w;
+      if (w >= S) return false;
+    }
+    if (t.n >= p.N) return false;
+    t.bos = (int64_t)t.n * p.T;
+    t.eos = t.bos + p.T;
+    t.off = (int64_t)w * (kPieces ? p.pre : p.seg);
+    t.last = !kPieces && w + 1 == S;
+    t.rows = t.last ? p.T - t.off : (kPieces ? p.pre : p.seg);
     return true;
   }
   const int lane = threadIdx.x & 31;
-  int base = 0;
+  auto span = [&](int m, int64_t& b, int64_t& e) {
+    b = p.cu[m];
+    e = p.cu[m + 1];
+    b = b < 0 ? 0 : (b > total ? total : b);
+    e = e < b ? b : (e > total ? total : e);
+  };
+  // the place of u among the whole segments (pieces), or past them among the remainders
+  int base = 0, at = 0, found = -1, w = 0;
+#pragma unroll 1
   for (int m0 = 0; m0 < p.N; m0 += 32) {
     const int m = m0 + lane;
     int64_t b = 0, e = 0;
-    int cnt = 0;
+    int S = 0;
     if (m < p.N) {
-      b = p.cu[m];
-      e = p.cu[m + 1];
-      b = b < 0 ? 0 : (b > total ? total : b);
-      e = e < b ? b : (e > total ? total : e);
-      cnt = e > b ? (int)((e - b + p.seg - 1) / p.seg) : 1;
+      span(m, b, e);
+      S = la_segments(e - b, p.seg);
     }
-    int incl = cnt;
+    const int cnt = S > 0 ? (kPieces ? (S - 1) * k : S - 1) : 0;
+    int incl = cnt, slots = kPieces ? cnt : S;         // before the walk's last segment; stored
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      const int x = __shfl_up_sync(0xffffffffu, incl, o), y = __shfl_up_sync(0xffffffffu, slots, o);
+      if (lane >= o) incl += x, slots += y;
     }
-    const bool mine = m < p.N && u >= base + incl - cnt && u < base + incl;
-    const unsigned hit = __ballot_sync(0xffffffffu, mine);
+    const unsigned hit = __ballot_sync(0xffffffffu, u >= base + incl - cnt && u < base + incl);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      n = m0 + src;
+      found = m0 + src;
       w = u - __shfl_sync(0xffffffffu, base + incl - cnt, src);
-      bos = __shfl_sync(0xffffffffu, b, src);
-      eos = __shfl_sync(0xffffffffu, e, src);
-      return true;
+      at += __shfl_sync(0xffffffffu, slots - (kPieces ? cnt : S), src) + w;
+      break;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
+    at += __shfl_sync(0xffffffffu, slots, 31);
   }
-  return false;
+  if (kPieces) {
+    if (found < 0) return false;
+    t.n = found;
+    span(found, t.bos, t.eos);
+    t.off = (int64_t)w * p.pre;
+    t.rows = p.pre;
+    t.at = at;
+    t.last = false;
+    return true;
+  }
+  t.last = found < 0;
+  if (found < 0) {
+    const int r = u - base;                            // the r-th remainder
+    if (r >= p.N) return false;
+    found = r;
+    if (p.N <= 64) {
+      auto rem = [&](int m) {
+        int64_t b, e;
+        span(m, b, e);
+        return e - b - (int64_t)(la_segments(e - b, p.seg) - 1) * p.seg;
+      };
+#pragma unroll 1
+      for (int m0 = 0; m0 < p.N; m0 += 32) {
+        const int m = m0 + lane;
+        int rank = -1;
+        if (m < p.N) {
+          const int64_t mine = rem(m);
+          rank = 0;
+#pragma unroll 1
+          for (int o = 0; o < p.N; ++o) {
+            const int64_t other = rem(o);
+            rank += other > mine || (other == mine && o < m);
+          }
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, rank == r);
+        if (hit) found = m0 + __ffs(hit) - 1;
+      }
+    }
+    span(found, t.bos, t.eos);
+    const int S = la_segments(t.eos - t.bos, p.seg);
+    w = S - 1;
+    at = 0;                                            // segments of the sequences before it
+#pragma unroll 1
+    for (int m = lane; m < found; m += 32) {
+      int64_t b, e;
+      span(m, b, e);
+      at += la_segments(e - b, p.seg);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
+    at += w;
+  }
+  t.n = found;
+  span(found, t.bos, t.eos);
+  t.off = (int64_t)w * p.seg;
+  t.rows = t.last ? t.eos - t.bos - t.off : p.seg;
+  t.at = at;
+  return t.at < p.units;
 }
 
 // lam^n for a natural-log decay d (n = 0: 1 even for d = -inf).
@@ -136,12 +232,12 @@ __device__ __forceinline__ float* la_exit(const LaParams& p, const LaPass& q, in
 }
 #endif
 
-// The CUDA-core kernel (FP32 or BF16 tokens, D 64 or 128): state_only computes the segments'
-// sums into seg_state, otherwise the outputs.
+// The CUDA-core kernel (FP32 or BF16 tokens, D 64 or 128): state_only computes the pieces' sums,
+// otherwise the outputs.
 cudaError_t launch_la_simt(const LaParams& p, bool bf16, int D, bool state_only, cudaStream_t st);
 // The tcgen05 kernel (BF16 tokens, D = 128; needs tc_fwd_available()).
 cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st);
-// seg_state: segment sums -> entry states of every segment but the walk's first.
+// sums -> entry: the entry state of every segment.
 cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st);
 
 struct StepParams {

@@ -73,51 +73,114 @@ sf_status check_encoder(const sf_gdn_shape* s, const char* fn) {
   return SF_OK;
 }
 
-// Rows of a segment (linattn.cuh), a multiple of 64: as many segments as it takes to give
-// every SM a CTA, none shorter than 256 rows; a walk that needs no cut is one segment.
-int seg_rows(const sf_gdn_shape* s, bool packed, int npass) {
-  const bool tc = s->dtype == SF_BF16 && s->K == 128;   // one CTA a walk, else one per 64 columns
-  const int64_t chains = (int64_t)(packed ? 1 : s->N) * s->H * npass * (tc ? 1 : s->K / 64);
-  const int64_t want = (kSms + chains - 1) / chains;       // segments of the longest walk
-  int64_t rows = (s->T + want - 1) / want;
-  rows = (rows + 63) / 64 * 64;
-  if (rows < 256) rows = 256;
-  return (int)rows;
+// How a launch's walks are cut (linattn.cuh): whole, or into segments whose entry states a
+// state-only launch over pieces computes first.
+//
+// The times are a model of the kernels in microseconds for a 64-row chunk: `t0` a CTA's start
+// and end, `walk` and `state` a chunk of the two launches with every SM busy, `walk1` and
+// `state1` the same with few CTAs (bound by the chunk's own chain of steps instead of memory).
+// `least`: chunks of the shortest piece.  Measured: tcgen05 kernel, 152 walks of 64 chunks 103 us,
+// 128 of 32 chunks 54 us, state-only 54 us for 54 chunks on every SM; CUDA-core kernel, head
+// size 64, 4 chunks 48 us and 22 us (state-only) with few CTAs.
+struct Cost {
+  double slots, t0, walk, walk1, state, state1;
+  int least;
+};
+constexpr Cost kTc = {kSms, 4.5, 1.55, 1.35, 0.92, 0.80, 4};
+// The CUDA-core kernel (one CTA an SM at D = 128, two at 64).
+constexpr Cost kSimt128 = {kSms, 4.0, 19.0, 19.0, 8.0, 8.0, 2};
+constexpr Cost kSimt64 = {2 * kSms, 4.0, 14.0, 11.0, 7.0, 5.0, 2};
+
+double launch_time(const Cost& c, double ctas, double chunks, bool state) {
+  const double busy = ctas < c.slots ? ctas / c.slots : 1.0;
+  const double full = state ? c.state : c.walk, few = state ? c.state1 : c.walk1;
+  const double per = full * busy > few ? full * busy : few;
+  return std::ceil(ctas / c.slots) * (c.t0 + chunks * per);
+}
+
+struct Cut {
+  int seg, pre;   // rows
+};
+
+Cut cut_walks(const sf_gdn_shape* s, bool packed, int npass) {
+  const bool tc = s->dtype == SF_BF16 && s->K == 128;
+  const Cost c = tc ? kTc : s->K == 128 ? kSimt128 : kSimt64;
+  const int lanes = npass * (tc ? 1 : s->K / 64);            // CTAs of a (sequence, head) walk
+  const int64_t chunks = (s->T + 63) / 64;
+  const Cut whole = {(int)((chunks > 0 ? chunks : 1) * 64), (int)((chunks > 0 ? chunks : 1) * 64)};
+  if (chunks < 2 * c.least) return whole;
+  if (packed) {
+    // Lengths are on the device.  `share` chunks a CTA slot would be even; with at least a
+    // walk for every slot only walks far above it are cut, with fewer any walk above it.
+    const double share = (double)chunks * s->H * lanes / c.slots;
+    const bool many = (double)s->N * s->H * lanes >= c.slots;
+    int64_t seg = (int64_t)std::ceil(share * (many ? 1.5 : 1.1));
+    if (seg < 2 * c.least - 2) seg = 2 * c.least - 2;
+    if (seg >= chunks) return whole;
+    return {(int)seg * 64, (int)seg * 64};
+  }
+  const double walks = (double)s->N * s->H * lanes;
+  double best = launch_time(c, walks, (double)chunks, false);
+  Cut cut = whole;
+  for (int S = 2; S <= 128; ++S) {
+    for (int k = 1; k <= 4; ++k) {
+      int64_t seg = (chunks + S - 1) / S;
+      seg = (seg + k - 1) / k * k;
+      if (seg / k < c.least || (S - 1) * seg >= chunks) continue;
+      const double units = walks * S, pieces = walks * (S - 1) * k;
+      const double t = launch_time(c, units, (double)seg, false) +
+                       launch_time(c, pieces, (double)(seg / k), true) + 5.0 +
+                       (units + pieces) * s->K * s->K * 4.0 / 5e6;
+      if (t < best) {
+        best = t;
+        cut = {(int)seg * 64, (int)(seg / k) * 64};
+      }
+    }
+  }
+  return cut;
 }
 
 struct Layout {
-  int seg;
-  int64_t units;
-  size_t states, gqa, total;   // segment states of one pass; one FP32 [B,T,H,K] area
+  Cut cut;
+  int64_t units, pre_units;
+  size_t entry, sums, gqa, total;   // segment states of one pass; one FP32 [B,T,H,K] area
 };
 
 Layout layout(const sf_gdn_shape* s, bool packed, int npass) {
-  Layout l{0, 0, 0, 0, kStatusBytes};
-  if (!s || s->K < 1 || s->H < 1 || s->T < 0 || s->N < 1) return l;
-  l.seg = seg_rows(s, packed, npass);
-  l.units = sfg::la_units(s->B, s->T, s->N, packed, l.seg);
-  if (l.seg < s->T) l.states = round_up((size_t)l.units * s->H * s->K * s->V * sizeof(float));
+  Layout l{{64, 64}, 0, 0, 0, 0, 0, kStatusBytes};
+  if (!s || s->K < 1 || s->V < 1 || s->H < 1 || s->T < 0 || s->N < 1) return l;
+  l.cut = cut_walks(s, packed, npass);
+  l.units = sfg::la_units(s->T, s->N, packed, l.cut.seg);
+  if (l.cut.seg < s->T) {
+    l.pre_units = sfg::la_pre_units(s->T, s->N, packed, l.cut.seg, l.cut.pre);
+    const size_t state = (size_t)s->H * s->K * s->V * sizeof(float);
+    l.entry = round_up(l.units * state);
+    l.sums = round_up(l.pre_units * state);
+  }
   if (npass > 1 && eff_hk(s) < s->H)
     l.gqa = round_up((size_t)s->B * s->T * s->H * s->K * sizeof(float));
-  l.total = kStatusBytes + npass * l.states + 2 * l.gqa;
+  l.total = kStatusBytes + npass * (l.entry + l.sums) + 2 * l.gqa;
   return l;
 }
 
 cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, int D,
                        cudaStream_t cs) {
-  p.seg = l.seg;
+  p.seg = l.cut.seg;
+  p.pre = l.cut.pre;
   p.units = (int)l.units;
+  p.pre_units = (int)l.pre_units;
   p.status = reinterpret_cast<int*>(ws);
-  for (int i = 0; i < p.npass; ++i)
-    p.pass[i].seg_state =
-        l.states ? reinterpret_cast<float*>(ws + kStatusBytes + i * l.states) : nullptr;
+  for (int i = 0; i < p.npass; ++i) {
+    p.pass[i].entry = reinterpret_cast<float*>(ws + kStatusBytes + i * (l.entry + l.sums));
+    p.pass[i].sums = p.pass[i].entry + l.entry / sizeof(float);
+  }
   // (T = 0: no token is read or written, only the states move; either kernel does)
   const bool tc = bf16 && D == 128 && p.T > 0;
   auto walk = [&](bool state_only) {
     return tc ? sfg::launch_la_tc(p, state_only, cs) : sfg::launch_la_simt(p, bf16, D, state_only, cs);
   };
   cudaError_t e = cudaSuccess;
-  if (l.states) {
+  if (l.pre_units > 0) {
     e = walk(true);
     if (e == cudaSuccess) e = sfg::launch_la_carry(p, D, cs);
   }
@@ -152,7 +215,7 @@ sf_status chunk_fwd(const char* fn, const sf_gdn_shape* shape, const void* q, co
   p.B = shape->B; p.T = shape->T; p.H = shape->H; p.N = shape->N;
   const float sc = eff_scale(shape);
   const int hk = eff_hk(shape);
-  p.pass[0] = sfg::LaPass{q, k, v, out, initial_state, final_state, nullptr, hk, hk, shape->H,
+  p.pass[0] = sfg::LaPass{q, k, v, out, initial_state, final_state, nullptr, nullptr, hk, hk, shape->H,
                           0, 0, 0, sc, sc, 1.f};
   return cuda_status(run_passes(p, l, static_cast<char*>(workspace), shape->dtype == SF_BF16,
                                 shape->K, reinterpret_cast<cudaStream_t>(stream)), fn);
@@ -309,15 +372,15 @@ sf_status sf_linattn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const v
   float* gq = nullptr;
   float* gk = nullptr;
   if (l.gqa) {   // per-value-head parts in FP32, summed below
-    gq = reinterpret_cast<float*>(ws + kStatusBytes + 3 * l.states);
-    gk = reinterpret_cast<float*>(ws + kStatusBytes + 3 * l.states + l.gqa);
+    gq = reinterpret_cast<float*>(ws + kStatusBytes + 3 * (l.entry + l.sums));
+    gk = reinterpret_cast<float*>(ws + kStatusBytes + 3 * (l.entry + l.sums) + l.gqa);
   }
   const int f32 = gq != nullptr;
-  p.pass[0] = sfg::LaPass{d_out, v, k, f32 ? gq : dq, initial_state, nullptr, nullptr, H, H, hk,
+  p.pass[0] = sfg::LaPass{d_out, v, k, f32 ? gq : dq, initial_state, nullptr, nullptr, nullptr, H, H, hk,
                           1, f32, 0, sc, sc, 1.f};
-  p.pass[1] = sfg::LaPass{k, q, d_out, dv, d_final_state, d_initial_state, nullptr, hk, hk, H,
+  p.pass[1] = sfg::LaPass{k, q, d_out, dv, d_final_state, d_initial_state, nullptr, nullptr, hk, hk, H,
                           0, 0, 1, sc, 1.f, sc};
-  p.pass[2] = sfg::LaPass{v, d_out, q, f32 ? gk : dk, d_final_state, nullptr, nullptr, H, H, hk,
+  p.pass[2] = sfg::LaPass{v, d_out, q, f32 ? gk : dk, d_final_state, nullptr, nullptr, nullptr, H, H, hk,
                           1, f32, 1, sc, 1.f, sc};
   cudaError_t e = run_passes(p, l, ws, bf16, shape->K, cs);
   if (e == cudaSuccess && f32) {

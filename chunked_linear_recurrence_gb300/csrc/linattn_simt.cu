@@ -67,16 +67,12 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
   const int pi = id % p.npass; id /= p.npass;
   const int h = id % p.H, u = id / p.H;
   const LaPass& q = p.pass[pi];
-  int n, w;
-  int64_t bos, eos;
-  if (!la_locate(u, p, n, w, bos, eos)) return;
-  const int64_t len = eos - bos;
+  LaUnit t;
+  if (!la_locate<kState>(u, p, t)) return;
+  const int n = t.n;
   const bool split = p.seg < p.T;
-  const bool last = (int64_t)(w + 1) * p.seg >= len;
-  if (kState && last) return;                     // nobody enters from its end
-  const int64_t off = (int64_t)w * p.seg;
-  const int64_t rows = len - off < p.seg ? len - off : p.seg;
-  const int64_t sb = q.reverse ? eos - off - rows : bos + off, se = sb + rows;
+  const int64_t rows = t.rows;
+  const int64_t sb = q.reverse ? t.eos - t.off - rows : t.bos + t.off, se = sb + rows;
   bool skip;
   const float* s_in = la_entry(p, q, n, h, D, skip);
   const int zc = zt * ZT;
@@ -100,8 +96,8 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
 
   // S[y = ty YR + e][z = zc + 4 tx ..]: zeros, the caller's state, or the segment's entry
   float4 s[YR];
-  size_t uoff = ((size_t)u * p.H + h) * D * D;
-  const float* src = kState ? nullptr : split ? q.seg_state + uoff : s_in;
+  const size_t uoff = ((size_t)t.at * p.H + h) * D * D;
+  const float* src = kState ? nullptr : split ? q.entry + uoff : s_in;
   const bool st = q.s_t && !split;                // segment states are stored [z][y]
 #pragma unroll
   for (int e = 0; e < YR; ++e) {
@@ -224,7 +220,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
       s[e].w = fmaf(hi, s[e].w, fmaf(lo, s[e].w, acc[e].w));
     }
   }
-  float* dst = kState ? q.seg_state + uoff : last ? la_exit(p, q, n, h, D) : nullptr;
+  float* dst = kState ? q.sums + uoff : t.last ? la_exit(p, q, n, h, D) : nullptr;
   if (!dst) return;
   const bool dt = q.s_t && !kState;
 #pragma unroll
@@ -241,39 +237,42 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
   }
 }
 
-// Entry states of the segments of one (sequence, head, pass): e_0 = the caller's state,
-// e_{w+1} = lam^seg e_w + sum_w; seg_state holds sum_w before and e_w after.  Each thread
-// carries one float4 of the state over the segments.
+// Entry states of the segments of one (sequence, head, pass): e = the caller's state, then
+// e = lam^pre e + sum over the pieces, kept at every segment's start.  Each thread carries one
+// float4 of the state; the sums of eight pieces are in flight together.
 template <int D>
 __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   const int tid = threadIdx.x;
   int id = blockIdx.x;
-  constexpr int PARTS = D * D / 1024;
+  constexpr int PARTS = D * D / 1024, AHEAD = 8;
   const int part = id % PARTS; id /= PARTS;
   const int pi = id % p.npass; id /= p.npass;
   const int h = id % p.H, n = id / p.H;
   const LaPass& q = p.pass[pi];
+  const int k = p.seg / p.pre;
   int64_t len = p.T;
-  int u0 = 0;
+  int u0, s0;
   if (!p.cu) {
-    u0 = n * ((p.T + p.seg - 1) / p.seg);
+    const int S = la_segments(p.T, p.seg);
+    u0 = n * S;
+    s0 = n * (S - 1) * k;
   } else {
     const int lane = tid & 31;
     int sum = 0;
+    int64_t b, e;
     for (int m = lane; m < n; m += 32) {
-      int64_t b, e;
       seq_span(m, p.B, p.T, p.cu, b, e);
-      sum += e > b ? (int)((e - b + p.seg - 1) / p.seg) : 1;
+      sum += la_segments(e - b, p.seg);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     u0 = sum;
-    int64_t b, e;
+    s0 = (sum - n) * k;
     seq_span(n, p.B, p.T, p.cu, b, e);
     len = e - b;
   }
-  const int segs = len > 0 ? (int)((len + p.seg - 1) / p.seg) : 1;
-  if (u0 + segs > p.units) return;                // malformed offsets
+  const int S = la_segments(len, p.seg), pieces = (S - 1) * k;
+  if (u0 + S > p.units || s0 + pieces > p.pre_units) return;   // malformed offsets
   bool skip;
   const float* s_in = la_entry(p, q, n, h, D, skip);
   if (skip) return;
@@ -286,30 +285,41 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   }
   __shared__ float pow_s[2];
   if (tid == 0) {
-    const double full = la_pow(p.decay[h], p.seg);
+    const double full = la_pow(p.decay[h], p.pre);
     pow_s[0] = (float)full;
     pow_s[1] = (float)(full - (double)pow_s[0]);
   }
+  const size_t step = (size_t)p.H * D * D;
+  float* out = q.entry + ((size_t)u0 * p.H + h) * D * D + at;
+  const float* in = q.sums + ((size_t)s0 * p.H + h) * D * D + at;
+  st4(out, e);
   __syncthreads();
   const float hi = pow_s[0], lo = pow_s[1];
-  float* base = q.seg_state + ((size_t)u0 * p.H + h) * D * D + at;
-  const size_t step = (size_t)p.H * D * D;
-  float4 cur = segs > 1 ? ld4(base) : e;
-  for (int w = 0; w < segs; ++w) {
-    float4 nxt = e;
-    if (w + 2 < segs) nxt = ld4(base + (size_t)(w + 1) * step);
-    st4(base + (size_t)w * step, e);
-    e.x = fmaf(hi, e.x, fmaf(lo, e.x, cur.x));
-    e.y = fmaf(hi, e.y, fmaf(lo, e.y, cur.y));
-    e.z = fmaf(hi, e.z, fmaf(lo, e.z, cur.z));
-    e.w = fmaf(hi, e.w, fmaf(lo, e.w, cur.w));
-    cur = nxt;
+  int until = k;                                       // pieces to the next segment's start
+  for (int i = 0; i < pieces; i += AHEAD) {
+    float4 x[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i + j < pieces) x[j] = ld4(in + (size_t)(i + j) * step);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i + j < pieces) {
+        e.x = fmaf(hi, e.x, fmaf(lo, e.x, x[j].x));
+        e.y = fmaf(hi, e.y, fmaf(lo, e.y, x[j].y));
+        e.z = fmaf(hi, e.z, fmaf(lo, e.z, x[j].z));
+        e.w = fmaf(hi, e.w, fmaf(lo, e.w, x[j].w));
+        if (--until == 0) {
+          out += step;
+          st4(out, e);
+          until = k;
+        }
+      }
   }
 }
 
 template <typename T, int D, bool kState>
 cudaError_t go(const LaParams& p, cudaStream_t st) {
-  const int64_t grid = (int64_t)p.units * p.H * p.npass * (D / ZT);
+  const int64_t grid = (int64_t)(kState ? p.pre_units : p.units) * p.H * p.npass * (D / ZT);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   auto kern = la_simt_kernel<T, D, kState>;

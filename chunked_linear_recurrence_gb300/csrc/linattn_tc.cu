@@ -72,7 +72,7 @@ constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + 1, QKDONE = FREE + NS, PREADY,
        PFREE = PREADY + 2, SPLIT, EHALF = SPLIT + 4, EDONE = EHALF + 2, EFREE = EDONE + 2,
        O1DONE = EFREE + 2, ODONE, OFREE, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
-static_assert(8 * NBAR + 8 <= 320 && NBAR <= 32, "barriers");
+static_assert(8 * NBAR + 32 <= 320 && NBAR <= 32, "barriers");
 
 // Tries of a wait before it gives up: each may suspend the thread for up to 20 us (at the least
 // it takes the ~50 ns of the instruction), so between 0.2 and 80 s, where a wait that ends takes
@@ -122,43 +122,54 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + O_BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR);
   volatile uint32_t* cx = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR + 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   int id = blockIdx.x;
   const int pi = id % p.npass; id /= p.npass;
   const int h = id % p.H, u = id / p.H;
   const LaPass& q = p.pass[pi];
-  int n, w;
-  int64_t bos, eos;
-  if (!la_locate(u, p, n, w, bos, eos)) return;
-  const int64_t len = eos - bos;
-  const bool split = p.seg < p.T;
-  const bool last = (int64_t)(w + 1) * p.seg >= len;
-  if (kState && last) return;                     // nobody enters from its end
-  const int64_t off = (int64_t)w * p.seg;
-  const int64_t rows = len - off < p.seg ? len - off : p.seg;
   const bool rev = q.reverse != 0;
-  const int64_t s0 = rev ? eos - off - rows : bos + off, s1 = s0 + rows;
-  bool skip;
-  const float* s_in = la_entry(p, q, n, h, D, skip);
-  if (skip) {                                     // padding of the paged pool: zero rows
-    if (kState) return;
-    uint4* o = reinterpret_cast<uint4*>(q.out);
-#pragma unroll 1
-    for (int64_t i = tid; i < rows * 16; i += NT)
-      o[((size_t)(s0 + (i >> 4)) * p.H + h) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
-    return;
-  }
   constexpr int NE = kState ? 2 : 1;              // buffers of E and of the weighted rows
-  const int nc = (int)((rows + C - 1) / C);
-  const int tail = (int)(rows - (int64_t)(nc - 1) * C);   // rows of the walk's last chunk
-  const float d = p.decay[h];
-
+  // The unit, found by one warp: whether there is one (2: padding of the paged pool), its rows
+  // [s0, s1), its sequence, its place, whether the walk ends with it.
+  int* unit = reinterpret_cast<int*>(sm + O_BAR + 8 * NBAR + 8);
+  if (warp == 0) {
+    LaUnit t;
+    int code = la_locate<kState>(u, p, t);
+    if (code) {
+      bool skip;
+      la_entry(p, q, t.n, h, D, skip);
+      if (skip) code = 2;
+      const int first = (int)(rev ? t.eos - t.off - t.rows : t.bos + t.off);
+      if (lane == 0) {
+        unit[1] = first;
+        unit[2] = first + (int)t.rows;
+        unit[3] = t.n;
+        unit[4] = t.at;
+        unit[5] = t.last;
+      }
+    }
+    if (lane == 0) unit[0] = code, *cx = 0;
+    if (lane < NBAR) {
+      const int i = lane;
+      mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? 4
+                          : i == GO || i == EFREE || i == EFREE + 1 ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
+    }
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  if (warp != 0) __syncthreads();                 // warp 0: once the first chunks are on their way
+  // (the shuffles tell the compiler that these are the same in every lane: they stay out of the
+  // roles' registers)
+  const int s0 = __shfl_sync(0xffffffffu, unit[1], 0), s1 = __shfl_sync(0xffffffffu, unit[2], 0);
+  const int nc = (s1 - s0 + C - 1) / C;
+  const int tail = s1 - s0 - (nc - 1) * C;        // rows of the walk's last chunk
   const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
   int issued = 0;
   auto load = [&](int c) {
     const int b = c % NS, L = c + 1 == nc ? tail : C;
-    const int r0 = (int)(rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C);
+    const int r0 = rev ? s1 - c * C - L : s0 + c * C;
     uint8_t* st = sm + b * STAGE;
     uint64_t* bar = L < C ? &bars[LANDED] : &bars[FULL + b];   // (the last chunk only)
     if (elect_one()) {
@@ -181,29 +192,31 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     }
   };
   if (warp == 0) {
-    // the barriers, and the first chunks on their way before anything else
-    if (lane < NBAR) {
-      const int i = lane;
-      mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? 4
-                          : i == GO || i == EFREE || i == EFREE + 1 ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
-    }
-    if (lane == 0) *cx = 0;
-    fence_mbar_init();
-    fence_proxy_async_smem();
-    __syncwarp();
+    if (unit[0] == 1) {
 #pragma unroll 1
-    for (int c = 0; c < NS && c < nc; ++c) load(c);
+      for (int c = 0; c < NS && c < nc; ++c) load(c);
+    }
+    __syncthreads();
   }
+  if (unit[0] != 1) {
+    if (kState || unit[0] == 0) return;
+    uint4* o = reinterpret_cast<uint4*>(q.out);   // padding: zero rows
+#pragma unroll 1
+    for (int i = tid; i < (s1 - s0) * 16; i += NT)
+      o[((size_t)(s0 + (i >> 4)) * p.H + h) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float d = p.decay[h];
   if (warp == 1) tmem_alloc(tslot, 512);
   auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
   if (tid >= 128 && tid < 256) {
-    const int i = tid & 63, L = tid < 192 ? C : tail, t = tid - 128;
-    rd[t] = i < L ? q.b * pw(rev ? L - 1 - i : i + 1) : 0.f;
-    wr[t] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
-    const int gap = rev ? t - 64 : 64 - t;          // |r - s| where s may contribute to r
+    const int i = tid & 63, L = tid < 192 ? C : tail, j = tid - 128;
+    rd[j] = i < L ? q.b * pw(rev ? L - 1 - i : i + 1) : 0.f;
+    wr[j] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
+    const int gap = rev ? j - 64 : 64 - j;          // |r - s| where s may contribute to r
     const float f = gap >= 0 ? q.a * pw(gap) : 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) pq[k * PQ_LD + t + k] = f;
+    for (int k = 0; k < 4; ++k) pq[k * PQ_LD + j + k] = f;
   }
   if (!kState)   // P on the far side of the diagonal stays zero
 #pragma unroll 1
@@ -460,9 +473,11 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     const int z = ((warp & 3) << 5) + lane;
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     float2 s[32];                                       // columns 64 wg + 2 e, + 1 of row z
-    const size_t uoff = ((size_t)u * p.H + h) * D * D;
     {
-      const float* src = kState ? nullptr : split ? q.seg_state + uoff : s_in;
+      bool skip;
+      const bool split = p.seg < p.T;
+      const float* src = kState ? nullptr : split ? q.entry + ((size_t)unit[4] * p.H + h) * D * D
+                                         : la_entry(p, q, unit[3], h, D, skip);
       if (!src) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) s[e] = make_float2(0.f, 0.f);
@@ -527,7 +542,9 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       tc_fence_before();
       warp_arrive(&bars[GO], lane);
     }
-    float* dst = !ok ? nullptr : kState ? q.seg_state + uoff : last ? la_exit(p, q, n, h, D) : nullptr;
+    float* dst = !ok ? nullptr
+                 : kState ? q.sums + ((size_t)unit[4] * p.H + h) * D * D
+                 : unit[5] ? la_exit(p, q, unit[3], h, D) : nullptr;
     if (dst) {
       if (q.s_t && !kState) {
 #pragma unroll
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       for (int c = 0; c < nc; ++c) {
         const bool end = c + 1 == nc;
         const int L = end ? tail : C;
-        const int64_t r0 = rev ? s1 - (int64_t)c * C - L : s0 + (int64_t)c * C;
+        const int r0 = rev ? s1 - c * C - L : s0 + c * C;
         const float2* f2 = reinterpret_cast<const float2*>(rd + (end ? 64 : 0)) + (lane & 3);
         if (!warp_wait(&bars[ODONE], c & 1, cx)) break;
         tc_fence_after();
@@ -645,7 +662,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 }  // namespace
 
 cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
-  const int64_t grid = (int64_t)p.units * p.H * p.npass;
+  const int64_t grid = (int64_t)(state_only ? p.pre_units : p.units) * p.H * p.npass;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   Maps maps;

@@ -413,12 +413,12 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     } else {
       // -------------------------------------------------------------- P
       if (warp == 3) {
-        // lam^64 and lam^tail as sums of two floats: a state carried over thousands of chunks
-        // must not drift by the rounding of one factor
+        // lam^64 and lam^tail, each as a float and what that float lacks, relative to it: a state
+        // carried over thousands of chunks must not drift by the rounding of one factor
         if (lane < 2) {
           const double f = la_pow(d, lane ? tail : C);
           carry[2 * lane] = (float)f;
-          carry[2 * lane + 1] = (float)(f - (double)(float)f);
+          carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)(float)f - 1.0) : 0.f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[TBL]);
@@ -511,13 +511,22 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       warp_arrive(&bars[GO], lane);
     }
     bool ok = nc == 0 || warp_wait(&bars[TBL], 0, cx);
+    int since = 0;                                      // chunks since the factors were made good
 #pragma unroll 1
     for (int c = 0; c < nc && ok; ++c) {
       const bool end = c + 1 == nc;
       if (!(ok = warp_wait(&bars[EDONE + c % NE], (c / NE) & 1, cx))) break;
       tc_fence_after();
-      const float2 fh = make_float2(carry[end ? 2 : 0], carry[end ? 2 : 0]);
-      const float2 fl = make_float2(carry[end ? 3 : 1], carry[end ? 3 : 1]);
+      // every 16 chunks, and before the last, the state gets back what the factors lacked
+      if (since == 16 || end) {
+        const float lack = (float)since * carry[1] + (end ? carry[3] : 0.f);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = fma2(s[e], make_float2(lack, lack), s[e]);
+        since = 0;
+      }
+      ++since;
+      const float f = carry[end ? 2 : 0];
+      const float2 fh = make_float2(f, f);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x[32];
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2& v = s[16 * k + e];
-          v = fma2(fh, v, fma2(fl, v, make_float2(x[2 * e], x[2 * e + 1])));
+          v = fma2(fh, v, make_float2(x[2 * e], x[2 * e + 1]));
         }
       }
       if (kState || end) continue;

@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
             ++qn;
           }
         }
-        if (c > 0 && !(ok = warp_wait(&bars[OFREE], (c - 1) & 1, cx))) break;
         if (!(ok = warp_wait(&bars[GO], c & 1, cx))) break;
         if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
+        if (c > 0 && !(ok = warp_wait(&bars[OFREE], (c - 1) & 1, cx))) break;   // the last to come
         tc_fence_after();
         const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
         const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);

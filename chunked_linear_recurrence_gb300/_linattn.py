@@ -8,6 +8,7 @@ library, and a call that the library cannot take raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -67,10 +68,17 @@ def _tokens(q, k, v, decay, cu_seqlens):
     return B, T, H, HK, K, N
 
 
+@functools.lru_cache(maxsize=256)
+def _shape_of(B, T, H, K, V, N, dtype, scale, HK):
+    """The shape struct of these sizes (the library only reads it), and a reference to it."""
+    s = sf_gdn_shape(B, T, H, K, V, N, _dtype_code(dtype), float(scale) if scale is not None else 0.0,
+                     HK)
+    return s, ctypes.byref(s)
+
+
 def _shape(q, v, cu_seqlens, scale, dims=None):
     B, T, H, HK, K, N = dims or _tokens(q, None, v, None, cu_seqlens)
-    return sf_gdn_shape(B, T, H, K, v.shape[-1], N, _dtype_code(q.dtype),
-                        float(scale) if scale is not None else 0.0, HK)
+    return _shape_of(B, T, H, K, v.shape[3], N, q.dtype, scale, HK)[1]
 
 
 def _ws(ws):
@@ -83,14 +91,14 @@ def sf_linattn_fwd_workspace(q, v, cu_seqlens=None):
     """A workspace for sf_linattn_chunk_fwd and sf_linattn_paged_chunk_fwd on these shapes, to
     be kept and passed as ``ws`` (a call without one allocates its own)."""
     shape = _shape(q, v, cu_seqlens, None)
-    need = load().sf_linattn_fwd_workspace(ctypes.byref(shape), int(cu_seqlens is not None))
+    need = load().sf_linattn_fwd_workspace(shape, int(cu_seqlens is not None))
     return workspace(need, q.device)
 
 
 def sf_linattn_bwd_workspace(q, v, cu_seqlens=None):
     """The same for sf_linattn_chunk_bwd."""
     shape = _shape(q, v, cu_seqlens, None)
-    need = load().sf_linattn_bwd_workspace(ctypes.byref(shape), int(cu_seqlens is not None))
+    need = load().sf_linattn_bwd_workspace(shape, int(cu_seqlens is not None))
     return workspace(need, q.device)
 
 
@@ -110,17 +118,23 @@ def sf_linattn_chunk_fwd(q, k, v, decay, initial_state=None, cu_seqlens=None, sc
             _addr("cu_seqlens", cu_seqlens, (N + 1,), torch.int32))
     if out is None:
         out = torch.empty_like(v)
-    if output_final_state and final_state is None:
+    else:
+        _addr("out", out, v.shape, dt)
+    if not output_final_state:
+        final_state = None
+    elif final_state is None:
         final_state = torch.empty(st, dtype=_F32, device=q.device)
+    else:
+        _addr("final_state", final_state, st, _F32)
     if ws is None:
-        ws = workspace(lib.sf_linattn_fwd_workspace(ctypes.byref(shape), int(cu_seqlens is not None)),
+        ws = workspace(lib.sf_linattn_fwd_workspace(shape, int(cu_seqlens is not None)),
                        q.device)
     ws = _ws(ws)
     _check(lib.sf_linattn_chunk_fwd(
-        ctypes.byref(shape), *args, int(bool(output_final_state)), _addr("out", out, v.shape, dt),
-        _addr("final_state", final_state, st, _F32) if output_final_state else None,
-        ws.data_ptr(), ws.numel(), _stream(stream, q.device)))
-    return out, (final_state if output_final_state else None)
+        shape, *args, int(bool(output_final_state)), out.data_ptr(),
+        None if final_state is None else final_state.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(stream, q.device)))
+    return out, final_state
 
 
 def sf_linattn_paged_chunk_fwd(q, k, v, decay, state_cache, state_indices, cu_seqlens=None,
@@ -145,10 +159,10 @@ def sf_linattn_paged_chunk_fwd(q, k, v, decay, state_cache, state_indices, cu_se
     if out is None:
         out = torch.empty_like(v)
     if ws is None:
-        ws = workspace(lib.sf_linattn_fwd_workspace(ctypes.byref(shape), int(cu_seqlens is not None)),
+        ws = workspace(lib.sf_linattn_fwd_workspace(shape, int(cu_seqlens is not None)),
                        q.device)
     ws = _ws(ws)
-    _check(lib.sf_linattn_paged_chunk_fwd(ctypes.byref(shape), *args, _addr("out", out, v.shape, dt),
+    _check(lib.sf_linattn_paged_chunk_fwd(shape, *args, _addr("out", out, v.shape, dt),
                                           ws.data_ptr(), ws.numel(), _stream(stream, q.device)))
     return out
 
@@ -172,11 +186,11 @@ def sf_linattn_chunk_bwd(q, k, v, decay, initial_state, d_out, d_final_state=Non
                      d_initial_state=(torch.empty(st, dtype=_F32, device=q.device)
                                       if want_d_initial_state else None))
     if ws is None:
-        ws = workspace(lib.sf_linattn_bwd_workspace(ctypes.byref(shape), int(cu_seqlens is not None)),
+        ws = workspace(lib.sf_linattn_bwd_workspace(shape, int(cu_seqlens is not None)),
                        q.device)
     ws = _ws(ws)
     _check(lib.sf_linattn_chunk_bwd(
-        ctypes.byref(shape), *args, _addr("dq", grads["dq"], q.shape, dt),
+        shape, *args, _addr("dq", grads["dq"], q.shape, dt),
         _addr("dk", grads["dk"], q.shape, dt), _addr("dv", grads["dv"], v.shape, dt),
         _addr("d_initial_state", grads.get("d_initial_state"), st, _F32), ws.data_ptr(), ws.numel(),
         _stream(stream, q.device)))
@@ -189,13 +203,16 @@ def _step_args(q, k, v, state_cache, state_indices, scale, out):
     N, HK, K = q.shape
     H, V = v.shape[1], v.shape[2]
     dt, slots = q.dtype, state_cache.shape[0]
-    shape = sf_gdn_shape(1, 1, H, K, V, N, _dtype_code(dt),
-                         float(scale) if scale is not None else 0.0, HK)
+    shape = _shape_of(1, 1, H, K, V, N, dt, scale, HK)[1]
     head = (_addr("q", q, (N, HK, K), dt), _addr("k", k, (N, HK, K), dt), _addr("v", v, (N, H, V), dt))
     if out is None:
         out = torch.empty_like(v)
+        to = out.data_ptr()
+    else:
+        to = _addr("out", out, (N, H, V), dt)
     tail = (_addr("state_cache", state_cache, (slots, H, V, K), _F32), slots,
-            _addr("state_indices", state_indices, (N,), torch.int32), _addr("out", out, (N, H, V), dt))
+            None if state_indices is None else _addr("state_indices", state_indices, (N,), torch.int32),
+            to)
     return shape, N, H, head, tail, out
 
 
@@ -205,7 +222,7 @@ def sf_linattn_step(q, k, v, decay, state_cache, state_indices=None, scale=None,
     [num_slots,H,V,K] in place at the slots state_indices (int32 [N]; <= 0: padding, zero
     output; None: sequence n owns slot n).  Returns out [N,H,V]."""
     shape, N, H, head, tail, out = _step_args(q, k, v, state_cache, state_indices, scale, out)
-    _check(load().sf_linattn_step(ctypes.byref(shape), *head, _addr("decay", decay, (H,), _F32),
+    _check(load().sf_linattn_step(shape, *head, _addr("decay", decay, (H,), _F32),
                                   *tail, _stream(stream, q.device)))
     return out
 
@@ -214,7 +231,7 @@ def sf_gdn_step(q, k, v, gate, beta, state_cache, state_indices=None, scale=None
                 stream=None):
     """sf_linattn_step for the gated delta rule: gate, beta [N,H] FP32."""
     shape, N, H, head, tail, out = _step_args(q, k, v, state_cache, state_indices, scale, out)
-    _check(load().sf_gdn_step(ctypes.byref(shape), *head, _addr("gate", gate, (N, H), _F32),
+    _check(load().sf_gdn_step(shape, *head, _addr("gate", gate, (N, H), _F32),
                               _addr("beta", beta, (N, H), _F32), *tail, _stream(stream, q.device)))
     return out
 
@@ -278,10 +295,13 @@ def sf_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos_sin=None, positi
     s, args = _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps, interleaved)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _addr("q_out", q_out, q.shape, q.dtype)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _check(load().sf_qk_norm_rope_fwd(ctypes.byref(s), *args, _addr("q_out", q_out, q.shape, q.dtype),
-                                      _addr("k_out", k_out, k.shape, k.dtype),
+    else:
+        _addr("k_out", k_out, k.shape, k.dtype)
+    _check(load().sf_qk_norm_rope_fwd(ctypes.byref(s), *args, q_out.data_ptr(), k_out.data_ptr(),
                                       _stream(stream, q.device)))
     return q_out, k_out
 
@@ -301,7 +321,7 @@ def sf_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, d_q_out, d
     s, args = _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps, interleaved)
     lib, D, dev = load(), q.shape[3], q.device
     if grads is None:
-        w = torch.empty(2, D, dtype=_F32, device=dev) if want_weight_grads else (None, None)
+        w = torch.empty(2, D, dtype=_F32, device=dev).unbind() if want_weight_grads else (None, None)
         grads = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev),
                      dk=torch.empty(k.shape, dtype=k.dtype, device=dev), dq_weight=w[0],
                      dk_weight=w[1])

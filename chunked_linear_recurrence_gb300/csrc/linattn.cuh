@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/sf_linattn.h"
 
 namespace sfg {
@@ -239,6 +241,28 @@ cudaError_t launch_la_simt(const LaParams& p, bool bf16, int D, bool state_only,
 cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st);
 // sums -> entry: the entry state of every segment.
 cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st);
+
+// Lets `kern` take `bytes` of dynamic shared memory: once for each device and kernel (the call
+// costs a microsecond; a small problem's whole launch takes a few).
+template <typename K>
+inline cudaError_t allow_smem(K kern, size_t bytes) {
+  constexpr int DEVICES = 64;
+  static std::atomic<const void*> done[DEVICES][8];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void* id = reinterpret_cast<const void*>(kern);
+  if (dev < DEVICES)
+    for (auto& d : done[dev])
+      if (d.load(std::memory_order_relaxed) == id) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess || dev >= DEVICES) return e;
+  for (auto& d : done[dev]) {
+    const void* none = nullptr;
+    if (d.compare_exchange_strong(none, id, std::memory_order_relaxed)) break;
+  }
+  return cudaSuccess;
+}
 
 struct StepParams {
   const void* q;

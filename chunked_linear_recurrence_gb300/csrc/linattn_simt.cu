@@ -323,8 +323,7 @@ cudaError_t go(const LaParams& p, cudaStream_t st) {
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   auto kern = la_simt_kernel<T, D, kState>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Smem<D>));
+  const cudaError_t e = allow_smem(kern, sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)grid, 256, sizeof(Smem<D>), st>>>(p);
   return cudaGetLastError();

@@ -412,17 +412,6 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       __syncwarp();
     } else {
       // -------------------------------------------------------------- P
-      if (warp == 3) {
-        // lam^64 and lam^tail, each as a float and what that float lacks, relative to it: a state
-        // carried over thousands of chunks must not drift by the rounding of one factor
-        if (lane < 2) {
-          const double f = la_pow(d, lane ? tail : C);
-          carry[2 * lane] = (float)f;
-          carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)(float)f - 1.0) : 0.f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[TBL]);
-      }
       if (!kState) {
         // row r of P.  The half on the far side of the diagonal (32 columns of one warp) is never
         // touched: it stays zero.
@@ -572,6 +561,17 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     split_rows(0, NE);
   } else {
     // (as launched: 96 registers)
+    if (warp == 16) {
+      // lam^64 and lam^tail, each as a float and what that float lacks, relative to it: a state
+      // carried over thousands of chunks must not drift by the rounding of one factor
+      if (lane < 2) {
+        const double f = la_pow(d, lane ? tail : C);
+        carry[2 * lane] = (float)f;
+        carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)(float)f - 1.0) : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[TBL]);
+    }
     // ---------------------------------------------------------------- results
     // A warp takes the 32 columns z of its TMEM lanes, 32 rows at a time, as 8 x 8 tiles: of the
     // row pairs 8 g + 2 (lane % 4), + 1, columns 8 k + lane / 4.
@@ -686,7 +686,7 @@ cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
   }
   auto kern = state_only ? (returns ? la_tc_kernel<true, 3> : la_tc_kernel<true, 2>)
                          : (returns ? la_tc_kernel<false, 3> : la_tc_kernel<false, 2>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+  const cudaError_t e = allow_smem(kern, SMEM);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)grid, NT, SMEM, st>>>(maps, p);
   return cudaGetLastError();

@@ -234,11 +234,11 @@ __device__ __forceinline__ float* la_exit(const LaParams& p, const LaPass& q, in
 }
 #endif
 
-// The CUDA-core kernel (FP32 or BF16 tokens, D 64 or 128): state_only computes the pieces' sums,
+// The CUDA-core kernel (FP32 tokens, D 64 or 128): state_only computes the pieces' sums,
 // otherwise the outputs.
-cudaError_t launch_la_simt(const LaParams& p, bool bf16, int D, bool state_only, cudaStream_t st);
-// The tcgen05 kernel (BF16 tokens, D = 128; needs tc_fwd_available()).
-cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st);
+cudaError_t launch_la_simt(const LaParams& p, int D, bool state_only, cudaStream_t st);
+// The tcgen05 kernel (BF16 tokens, D 64 or 128; needs tc_fwd_available()).
+cudaError_t launch_la_tc(const LaParams& p, int D, bool state_only, cudaStream_t st);
 // sums -> entry: the entry state of every segment.
 cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st);
 

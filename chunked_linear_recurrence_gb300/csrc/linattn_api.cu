@@ -63,11 +63,11 @@ sf_status check_tokens(const sf_gdn_shape* s, bool packed, const char* fn) {
   return SF_OK;
 }
 
-// BF16 with K = V = 128 runs on the tensor-core kernel alone, which needs TMA descriptors.
+// BF16 runs on the tensor-core kernel alone, which needs TMA descriptors.
 sf_status check_encoder(const sf_gdn_shape* s, const char* fn) {
-  if (s->dtype == SF_BF16 && s->K == 128 && s->T > 0 && !sfg::tc_fwd_available())
+  if (s->dtype == SF_BF16 && s->T > 0 && !sfg::tc_fwd_available())
     return report(SF_ERR_UNSUPPORTED,
-                  "%s: BF16 with K = V = 128 needs the tensor-core kernels, but the driver entry "
+                  "%s: BF16 needs the tensor-core kernel, but the driver entry "
                   "point cuTensorMapEncodeTiled is unavailable (or disabled by "
                   "SF_GDN_DISABLE_TMA_ENCODER)", fn);
   return SF_OK;
@@ -86,7 +86,8 @@ struct Cost {
   double slots, t0, walk, walk1, state, state1;
   int least;
 };
-constexpr Cost kTc = {kSms, 4.5, 1.55, 1.35, 0.92, 0.80, 4};
+constexpr Cost kTc128 = {kSms, 4.5, 1.55, 1.35, 0.92, 0.80, 4};
+constexpr Cost kTc64 = {kSms, 4.5, 1.20, 1.10, 0.70, 0.65, 4};
 // The CUDA-core kernel (one CTA an SM at D = 128, two at 64).
 constexpr Cost kSimt128 = {kSms, 4.0, 19.0, 19.0, 8.0, 8.0, 2};
 constexpr Cost kSimt64 = {2 * kSms, 4.0, 14.0, 11.0, 7.0, 5.0, 2};
@@ -103,8 +104,8 @@ struct Cut {
 };
 
 Cut cut_walks(const sf_gdn_shape* s, bool packed, int npass) {
-  const bool tc = s->dtype == SF_BF16 && s->K == 128;
-  const Cost c = tc ? kTc : s->K == 128 ? kSimt128 : kSimt64;
+  const bool tc = s->dtype == SF_BF16;
+  const Cost c = tc ? (s->K == 128 ? kTc128 : kTc64) : s->K == 128 ? kSimt128 : kSimt64;
   const int lanes = npass * (tc ? 1 : s->K / 64);            // CTAs of a (sequence, head) walk
   const int64_t chunks = (s->T + 63) / 64;
   const Cut whole = {(int)((chunks > 0 ? chunks : 1) * 64), (int)((chunks > 0 ? chunks : 1) * 64)};
@@ -174,10 +175,10 @@ cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, i
     p.pass[i].entry = reinterpret_cast<float*>(ws + kStatusBytes + i * (l.entry + l.sums));
     p.pass[i].sums = p.pass[i].entry + l.entry / sizeof(float);
   }
-  // (T = 0: no token is read or written, only the states move; either kernel does)
-  const bool tc = bf16 && D == 128 && p.T > 0;
+  // (T = 0: no token is read or written, only the states move; the FP32 kernel does)
+  const bool tc = bf16 && p.T > 0;
   auto walk = [&](bool state_only) {
-    return tc ? sfg::launch_la_tc(p, state_only, cs) : sfg::launch_la_simt(p, bf16, D, state_only, cs);
+    return tc ? sfg::launch_la_tc(p, D, state_only, cs) : sfg::launch_la_simt(p, D, state_only, cs);
   };
   cudaError_t e = cudaSuccess;
   if (l.pre_units > 0) {

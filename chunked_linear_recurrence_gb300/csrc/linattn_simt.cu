@@ -1,5 +1,5 @@
-// linattn_simt.cu -- the decayed linear attention's product (linattn.cuh) on the CUDA cores:
-// FP32 tokens, and BF16 tokens with head size 64.  FP32 multiply-adds throughout.
+// linattn_simt.cu -- the decayed linear attention's product (linattn.cuh) on the CUDA cores, for
+// FP32 tokens: FP32 multiply-adds throughout.
 //
 // One CTA of 256 threads walks one (segment, head, 64-column slice of z).  Per 64-row chunk
 //     P  = a (X Y^T) o lam^|r-s|       64 x 64, each thread 4 x 4
@@ -11,8 +11,6 @@
 // thousands of chunks does not drift by the rounding of one factor.
 // Bound by the FP32 rate: about 5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, two
 // thirds of it in S and O, against 2 KB of tokens.
-#include <cuda_bf16.h>
-
 #include "common.cuh"
 #include "linattn.cuh"
 
@@ -23,21 +21,7 @@ constexpr int ZT = 64;   // columns of z per CTA
 constexpr int C = LA_CHUNK;
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
 __device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 u;
-  u.x = *reinterpret_cast<uint32_t*>(&a);
-  u.y = *reinterpret_cast<uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
-
 template <int D>
 struct Smem {
   float X[C][D + 4], Y[C][D + 4], Z[C][ZT + 4], P[C][ZT + 4], S[D][ZT + 4], tab[C + 4], carry[4];
@@ -45,8 +29,8 @@ struct Smem {
 
 // Rows [r0, r0 + L) of one head's columns [c0, c0 + W) into dst (leading dimension ld); the
 // other rows of the 64 become zero.
-template <typename T, int W>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t r0, int L,
+template <int W>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const float* src, int64_t r0, int L,
                                           int heads, int head, int D, int c0, int tid) {
   for (int idx = tid; idx < C * (W / 4); idx += 256) {
     const int r = idx / (W / 4), c = (idx % (W / 4)) * 4;
@@ -56,7 +40,7 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int6
   }
 }
 
-template <typename T, int D, bool kState>
+template <int D, bool kState>
 __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
@@ -78,7 +62,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
   const int zc = zt * ZT;
   if (skip) {                                     // padding of the paged pool
     if (kState) return;
-    T* o = reinterpret_cast<T*>(q.out);
+    float* o = static_cast<float*>(q.out);
     for (int64_t idx = tid; idx < rows * (ZT / 4); idx += 256)
       st4(o + ((size_t)(sb + idx / (ZT / 4)) * p.H + h) * D + zc + (int)(idx % (ZT / 4)) * 4,
           make_float4(0.f, 0.f, 0.f, 0.f));
@@ -114,9 +98,9 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
     const int64_t r0 = q.reverse ? se - done - L : sb + done;
     __syncthreads();                              // the last chunk's readers; the table
     if (!kState)
-      load_rows<T, D>(&sm.X[0][0], D + 4, reinterpret_cast<const T*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
-    load_rows<T, D>(&sm.Y[0][0], D + 4, reinterpret_cast<const T*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
-    load_rows<T, ZT>(&sm.Z[0][0], ZT + 4, reinterpret_cast<const T*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
+      load_rows<D>(&sm.X[0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
+    load_rows<D>(&sm.Y[0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
+    load_rows<ZT>(&sm.Z[0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
     if (!kState) {
 #pragma unroll
       for (int e = 0; e < YR; ++e) st4(&sm.S[ty * YR + e][4 * tx], s[e]);
@@ -190,8 +174,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
         const int r = 4 * ty + i;
         if (r >= L) continue;
         const size_t at = ((size_t)(r0 + r) * p.H + h) * D + zc + 4 * tx;
-        if (q.out_f32) st4(reinterpret_cast<float*>(q.out) + at, o[i]);
-        else st4(reinterpret_cast<T*>(q.out) + at, o[i]);
+        st4(static_cast<float*>(q.out) + at, o[i]);
       }
     }
     // S = lam^L S + c sum_r lam^f(r) y_r z_r
@@ -317,12 +300,12 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   }
 }
 
-template <typename T, int D, bool kState>
+template <int D, bool kState>
 cudaError_t go(const LaParams& p, cudaStream_t st) {
   const int64_t grid = (int64_t)(kState ? p.pre_units : p.units) * p.H * p.npass * (D / ZT);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  auto kern = la_simt_kernel<T, D, kState>;
+  auto kern = la_simt_kernel<D, kState>;
   const cudaError_t e = allow_smem(kern, sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)grid, 256, sizeof(Smem<D>), st>>>(p);
@@ -331,13 +314,9 @@ cudaError_t go(const LaParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_la_simt(const LaParams& p, bool bf16, int D, bool state_only, cudaStream_t st) {
-  if (bf16) {
-    if (D == 64) return state_only ? go<__nv_bfloat16, 64, true>(p, st) : go<__nv_bfloat16, 64, false>(p, st);
-    return state_only ? go<__nv_bfloat16, 128, true>(p, st) : go<__nv_bfloat16, 128, false>(p, st);
-  }
-  if (D == 64) return state_only ? go<float, 64, true>(p, st) : go<float, 64, false>(p, st);
-  return state_only ? go<float, 128, true>(p, st) : go<float, 128, false>(p, st);
+cudaError_t launch_la_simt(const LaParams& p, int D, bool state_only, cudaStream_t st) {
+  if (D == 64) return state_only ? go<64, true>(p, st) : go<64, false>(p, st);
+  return state_only ? go<128, true>(p, st) : go<128, false>(p, st);
 }
 
 cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st) {

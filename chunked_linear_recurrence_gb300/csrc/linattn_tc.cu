@@ -1,5 +1,5 @@
-// linattn_tc.cu -- the decayed linear attention's product (linattn.cuh) on tcgen05: BF16 tokens
-// with head size 128.
+// linattn_tc.cu -- the decayed linear attention's product (linattn.cuh) on tcgen05: BF16 tokens,
+// head sizes D = 128 and 64.
 //
 // One CTA walks one (segment, head) in 64-row chunks.  Rows r, s of a chunk, the state S [z][y]:
 //     QK  = [Y; X] Y^T           M = 128, N = 64, K = 128   (rows 64-127: X Y^T)
@@ -43,20 +43,26 @@ namespace {
 
 using namespace tc;
 
-constexpr int D = 128, C = LA_CHUNK, NT = 640, NS = 4;
+constexpr int C = LA_CHUNK, NT = 640, NS = 4;
 constexpr uint32_t PANEL = 8192;                 // 64 rows x 128 bytes
-constexpr uint32_t B_Y = 0, B_X = PANEL;         // panel 0 of Y and X; panel 1 two panels on
-constexpr uint32_t B_Z = 4 * PANEL, STAGE = 6 * PANEL;
-constexpr uint32_t O_P = NS * STAGE;             // P [64][64], two buffers
-constexpr uint32_t O_OUT = O_P + 2 * PANEL;      // results, [32 rows][32 columns] of each of four warps
-// b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4] (padded), the
-// weights of P by 64 + s - r in four copies, each a word further on, 8 banks apart
-constexpr uint32_t O_TAB = O_OUT + 8192;
 constexpr int PQ_LD = 136;
-constexpr uint32_t O_BAR = O_TAB + 3328;
-constexpr uint32_t SMEM = O_BAR + 320 + 1024;
-static_assert(256 * 4 + 64 + 4 * PQ_LD * 4 <= 3328 && O_BAR % 256 == 0, "tables");
-static_assert(SMEM <= 232448, "shared memory");
+// Shared memory for head size D (one or two panels a tile).
+template <int D>
+struct Mem {
+  static constexpr uint32_t NP = D / 64;
+  static constexpr uint32_t Y = 0, X = PANEL;      // panel 0 of Y and X; panel 1 two panels on
+  static constexpr uint32_t Z = 2 * NP * PANEL, STAGE = 3 * NP * PANEL;
+  static constexpr uint32_t P = NS * STAGE;        // P [64][64], two buffers
+  static constexpr uint32_t OUT = P + 2 * PANEL;   // results, [32 rows][32 columns] of each of four warps
+  // b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4] (padded), the
+  // weights of P by 64 + s - r in four copies, each a word further on, 8 banks apart
+  static constexpr uint32_t TAB = OUT + 8192;
+  static constexpr uint32_t BAR = TAB + 3328;
+  static constexpr uint32_t SIZE = BAR + 320 + 1024;
+};
+static_assert(Mem<128>::SIZE <= 232448, "shared memory");
+static_assert(256 * 4 + 64 + 4 * PQ_LD * 4 <= 3328 && Mem<128>::BAR % 256 == 0 && Mem<64>::BAR % 256 == 0,
+              "tables");
 
 // TMEM columns: E, the state's BF16 copy, QK, O1, O2, the weighted rows' parts (32 columns
 // each); a launch that computes states alone has two buffers of E and of the parts.
@@ -65,7 +71,6 @@ template <bool kState>
 __device__ __forceinline__ uint32_t tm_w(int buf) { return kState ? 256 + 96 * buf : 384; }
 
 constexpr uint32_t ID_QK = idesc_bf16(128, 64, false, false);
-constexpr uint32_t ID_E = idesc_bf16(128, 128, false, true);   // A in TMEM
 constexpr uint32_t ID_O1 = idesc_bf16(128, 64, false, false);   // A in TMEM
 constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 
@@ -109,19 +114,22 @@ __device__ __forceinline__ uint64_t kstep_k(int kk) {   // panels 16 KB apart
 }
 __device__ __forceinline__ uint64_t kstep_mn(int kk) { return (uint64_t)(kk * 2048 >> 4); }
 
-template <bool kState, int NSP>
+template <int D, bool kState, int NSP>
 __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Maps maps,
                                                       const LaParams p) {
+  using M = Mem<D>;
+  constexpr int NP = D / 64, KD = D / 16, WL = D / 32;   // panels, K steps over D, warps of D lanes
+  constexpr uint32_t ID_E = idesc_bf16(128, D, false, true);   // A in TMEM
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(sm);
-  float* rd = reinterpret_cast<float*>(sm + O_TAB);   // [2][64]
+  float* rd = reinterpret_cast<float*>(sm + M::TAB);   // [2][64]
   float* wr = rd + 128;                               // [2][64]
   float* carry = rd + 256;
   float* pq = rd + 272;                               // [4][PQ_LD]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + O_BAR);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR);
-  volatile uint32_t* cx = reinterpret_cast<uint32_t*>(sm + O_BAR + 8 * NBAR + 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::BAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + M::BAR + 8 * NBAR);
+  volatile uint32_t* cx = reinterpret_cast<uint32_t*>(sm + M::BAR + 8 * NBAR + 4);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   int id = blockIdx.x;
@@ -132,7 +140,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   constexpr int NE = kState ? 2 : 1;              // buffers of E and of the weighted rows
   // The unit, found by one warp: whether there is one (2: padding of the paged pool), its rows
   // [s0, s1), its sequence, its place, whether the walk ends with it.
-  int* unit = reinterpret_cast<int*>(sm + O_BAR + 8 * NBAR + 8);
+  int* unit = reinterpret_cast<int*>(sm + M::BAR + 8 * NBAR + 8);
   if (warp == 0) {
     LaUnit t;
     int code = la_locate<kState>(u, p, t);
@@ -152,8 +160,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     if (lane == 0) unit[0] = code, *cx = 0;
     if (lane < NBAR) {
       const int i = lane;
-      mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? 4
-                          : i == GO || i == EFREE || i == EFREE + 1 ? 8 : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
+      mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? WL
+                          : i == GO || i == EFREE || i == EFREE + 1 ? 2 * WL : i >= FREE && i < FREE + NS && !kState ? 2 : 1);
     }
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -170,15 +178,15 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   auto load = [&](int c) {
     const int b = c % NS, L = c + 1 == nc ? tail : C;
     const int r0 = rev ? s1 - c * C - L : s0 + c * C;
-    uint8_t* st = sm + b * STAGE;
+    uint8_t* st = sm + b * M::STAGE;
     uint64_t* bar = L < C ? &bars[LANDED] : &bars[FULL + b];   // (the last chunk only)
     if (elect_one()) {
-      mbar_arrive_expect_tx(bar, (kState ? 4 : 6) * PANEL);
+      mbar_arrive_expect_tx(bar, (kState ? 2 : 3) * NP * PANEL);
 #pragma unroll
-      for (int pp = 0; pp < 2; ++pp) {
-        tma_load_3d(st + B_Y + 2 * pp * PANEL, &maps.m[pi][1], bar, 64 * pp, hy, r0);
-        tma_load_3d(st + B_Z + pp * PANEL, &maps.m[pi][2], bar, 64 * pp, hz, r0);
-        if (!kState) tma_load_3d(st + B_X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
+      for (int pp = 0; pp < NP; ++pp) {
+        tma_load_3d(st + M::Y + 2 * pp * PANEL, &maps.m[pi][1], bar, 64 * pp, hy, r0);
+        tma_load_3d(st + M::Z + pp * PANEL, &maps.m[pi][2], bar, 64 * pp, hz, r0);
+        if (!kState) tma_load_3d(st + M::X + 2 * pp * PANEL, &maps.m[pi][0], bar, 64 * pp, hx, r0);
       }
     }
     __syncwarp();
@@ -202,8 +210,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     if (kState || unit[0] == 0) return;
     uint4* o = reinterpret_cast<uint4*>(q.out);   // padding: zero rows
 #pragma unroll 1
-    for (int i = tid; i < (s1 - s0) * 16; i += NT)
-      o[((size_t)(s0 + (i >> 4)) * p.H + h) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < (s1 - s0) * (D / 8); i += NT)
+      o[((size_t)(s0 + i / (D / 8)) * p.H + h) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
     return;
   }
   const float d = p.decay[h];
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   if (!kState)   // P on the far side of the diagonal stays zero
 #pragma unroll 1
     for (int i = tid; i < 2 * (int)PANEL / 16; i += NT)
-      *reinterpret_cast<uint4*>(sm + O_P + 16 * i) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(sm + M::P + 16 * i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -238,14 +246,14 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     // lane's source row of K step 0: j = 8 (m / 2) + i, columns z0 + 8 (m % 2) ..; z0 of either
     // half differs in bit 1 of the 16-byte chunk
     const uint32_t ch = (uint32_t)(4 * (warp & 1) + (m & 1));
-    const uint32_t src = sb + B_Z + (uint32_t)((warp & 3) >> 1) * PANEL + (uint32_t)(8 * (m >> 1) + i) * 128u;
+    const uint32_t src = sb + M::Z + (uint32_t)((warp & 3) >> 1) * PANEL + (uint32_t)(8 * (m >> 1) + i) * 128u;
     const uint32_t c0 = (ch ^ (uint32_t)i) << 4, c1 = ((ch + 2) ^ (uint32_t)i) << 4;
 #pragma unroll 1
     for (int c = first; c < nc; c += step) {
       const int b = c % NS, eb = c % NE;
       if (!warp_wait(&bars[FULL + b], (c / NS) & 1, cx)) break;
       const float2* wt = reinterpret_cast<const float2*>(wr + (c + 1 == nc ? 64 : 0)) + (lane & 3);
-      uint32_t from = src + b * STAGE, to = tl + tm_w<kState>(eb);
+      uint32_t from = src + b * M::STAGE, to = tl + tm_w<kState>(eb);
       bool ok = true;
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
@@ -295,12 +303,12 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       auto trim = [&]() {
         const int b = (nc - 1) % NS;
         if (!warp_wait(&bars[LANDED], 0, cx)) return false;
-        uint8_t* st = sm + b * STAGE;
+        uint8_t* st = sm + b * M::STAGE;
         const int per = (C - tail) * 8;                // 16-byte pieces of a panel
 #pragma unroll 1
-        for (int i = lane; i < 4 * per; i += 32) {
+        for (int i = lane; i < 2 * NP * per; i += 32) {
           const int t = i / per, rr = i % per;
-          uint8_t* base = st + (t < 2 ? B_Y + 2 * t * PANEL : B_Z + (t - 2) * PANEL);
+          uint8_t* base = st + (t < NP ? M::Y + 2 * t * PANEL : M::Z + (t - NP) * PANEL);
           *reinterpret_cast<uint4*>(base + (tail + rr / 8) * 128 + (rr % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       for (int c = 0; c < nc && ok; ++c) {
         const int b = c % NS;
         const int eb = c % NE, ph = (c / NE) & 1;
-        const uint64_t dy = sdesc_sw128(sb + b * STAGE + B_Y, 2 * PANEL, 1024);
+        const uint64_t dy = sdesc_sw128(sb + b * M::STAGE + M::Y, 2 * PANEL, 1024);
         if (c >= NE && !(ok = warp_wait(&bars[EFREE + eb], ph ^ 1, cx))) break;
         // E in two halves of 32 rows: the split warps refill the first under the second.  (They
         // have waited for the rows themselves.)
@@ -351,9 +359,9 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       // as long as the rest of a step), else in its own turn.
       int qn = 0;                                      // chunks whose QK is issued
       auto put_qk = [&]() {                            // by the elected lane
-        const uint64_t dy = sdesc_sw128(sb + (qn % NS) * STAGE + B_Y, 0, 1024);
+        const uint64_t dy = sdesc_sw128(sb + (qn % NS) * M::STAGE + M::Y, 0, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int kk = 0; kk < KD; ++kk)
           mma_bf16(tm + TM_P, dy + kstep_k(kk), dy + kstep_k(kk), ID_QK, kk > 0);
         mma_commit(&bars[QKDONE]);
       };
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 #pragma unroll 1
       for (int c = 0; !kState && c < nc && ok; ++c) {
         const int b = c % NS;
-        const uint32_t st = sb + b * STAGE;
+        const uint32_t st = sb + b * M::STAGE;
         if (qn == c) {                                 // its own turn
           if (!(ok = warp_wait(&bars[FULL + b], (c / NS) & 1, cx))) break;
           tc_fence_after();
@@ -391,12 +399,12 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         if (!(ok = warp_wait(&bars[PREADY + (c & 1)], (c >> 1) & 1, cx))) break;
         if (c > 0 && !(ok = warp_wait(&bars[OFREE], (c - 1) & 1, cx))) break;   // the last to come
         tc_fence_after();
-        const uint64_t dx = sdesc_sw128(st + B_X, 0, 1024);
-        const uint64_t dz = sdesc_sw128(st + B_Z, PANEL, 1024);
-        const uint64_t dp = sdesc_sw128(sb + O_P + (c & 1) * PANEL, 0, 1024);
+        const uint64_t dx = sdesc_sw128(st + M::X, 0, 1024);
+        const uint64_t dz = sdesc_sw128(st + M::Z, PANEL, 1024);
+        const uint64_t dp = sdesc_sw128(sb + M::P + (c & 1) * PANEL, 0, 1024);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < KD; ++kk)
             mma_bf16_ta(tm + TM_O1, tm + TM_SB + kk * 8, dx + kstep_k(kk), ID_O1, kk > 0);
           mma_commit(&bars[O1DONE]);
 #pragma unroll
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         for (int c = 0; c < nc; ++c) {
           if (!warp_wait(&bars[QKDONE], c & 1, cx)) break;
           tc_fence_after();
-          uint8_t* row = sm + O_P + (c & 1) * PANEL + r * 128;
+          uint8_t* row = sm + M::P + (c & 1) * PANEL + r * 128;
 #pragma unroll 1
           for (int s = s0; s < s1; s += 16) {
             float x[16];
@@ -457,11 +465,12 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     }
   } else if (warp < 12) {
     reg_alloc<128>();
+    if ((warp & 3) < WL) {                              // (the others have no lanes)
     // ---------------------------------------------------------------- state
     const int wg = (warp - 4) >> 2;
     const int z = ((warp & 3) << 5) + lane;
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    float2 s[32];                                       // columns 64 wg + 2 e, + 1 of row z
+    float2 s[D / 4];                                    // columns D / 2 wg + 2 e, + 1 of row z
     {
       bool skip;
       const bool split = p.seg < p.T;
@@ -469,15 +478,15 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
                                          : la_entry(p, q, unit[3], h, D, skip);
       if (!src) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] = make_float2(0.f, 0.f);
+        for (int e = 0; e < D / 4; ++e) s[e] = make_float2(0.f, 0.f);
       } else if (q.s_t && !split) {                   // stored [y][z]
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          s[e] = make_float2(src[(size_t)(64 * wg + 2 * e) * D + z], src[(size_t)(64 * wg + 2 * e + 1) * D + z]);
+        for (int e = 0; e < D / 4; ++e)
+          s[e] = make_float2(src[(size_t)(D / 2 * wg + 2 * e) * D + z], src[(size_t)(D / 2 * wg + 2 * e + 1) * D + z]);
       } else {
-        const float4* v = reinterpret_cast<const float4*>(src + (size_t)z * D + 64 * wg);
+        const float4* v = reinterpret_cast<const float4*>(src + (size_t)z * D + D / 2 * wg);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < D / 8; ++e) {
           const float4 f = v[e];
           s[2 * e] = make_float2(f.x, f.y);
           s[2 * e + 1] = make_float2(f.z, f.w);
@@ -486,11 +495,11 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     }
     auto put_state = [&]() {                          // BF16 copy, the A operand of S X^T
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NP; ++k) {
         uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(s[16 * k + e].x, s[16 * k + e].y);
-        tmem_st16(tl + TM_SB + 32 * wg + 16 * k, v);
+        tmem_st16(tl + TM_SB + D / 4 * wg + 16 * k, v);
       }
     };
     if (!kState && nc > 0) {
@@ -510,18 +519,18 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       if (since == 16 || end) {
         const float lack = (float)since * carry[1] + (end ? carry[3] : 0.f);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] = fma2(s[e], make_float2(lack, lack), s[e]);
+        for (int e = 0; e < D / 4; ++e) s[e] = fma2(s[e], make_float2(lack, lack), s[e]);
         since = 0;
       }
       ++since;
       const float f = carry[end ? 2 : 0];
       const float2 fh = make_float2(f, f);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NP; ++k) {
         float x[32];
-        tmem_ld32(tl + TM_E + 128 * (c % NE) + 64 * wg + 32 * k, x);
+        tmem_ld32(tl + TM_E + 128 * (c % NE) + D / 2 * wg + 32 * k, x);
         tmem_ld_wait();
-        if (k == 1) {
+        if (k == NP - 1) {
           tc_fence_before();
           warp_arrive(&bars[EFREE + c % NE], lane);
         }
@@ -546,19 +555,20 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     if (dst) {
       if (q.s_t && !kState) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          dst[(size_t)(64 * wg + 2 * e) * D + z] = s[e].x;
-          dst[(size_t)(64 * wg + 2 * e + 1) * D + z] = s[e].y;
+        for (int e = 0; e < D / 4; ++e) {
+          dst[(size_t)(D / 2 * wg + 2 * e) * D + z] = s[e].x;
+          dst[(size_t)(D / 2 * wg + 2 * e + 1) * D + z] = s[e].y;
         }
       } else {
-        float4* v = reinterpret_cast<float4*>(dst + (size_t)z * D + 64 * wg);
+        float4* v = reinterpret_cast<float4*>(dst + (size_t)z * D + D / 2 * wg);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
+        for (int e = 0; e < D / 8; ++e) v[e] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
       }
+    }
     }
   } else if (warp < 16) {
     reg_dealloc<72>();
-    split_rows(0, NE);
+    if ((warp & 3) < WL) split_rows(0, NE);
   } else {
     // (as launched: 96 registers)
     if (warp == 16) {
@@ -576,7 +586,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     // A warp takes the 32 columns z of its TMEM lanes, 32 rows at a time, as 8 x 8 tiles: of the
     // row pairs 8 g + 2 (lane % 4), + 1, columns 8 k + lane / 4.
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t stage = sb + O_OUT + (warp & 3) * 2048;
+    const uint32_t stage = sb + M::OUT + (warp & 3) * 2048;
     const int H = p.H;
     // the lane's row and 16 bytes of a store (eight rows a store)
     const int rr = lane >> 2;
@@ -648,7 +658,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         }
       }
     };
-    if (kState) {
+    if ((warp & 3) >= WL) {
+    } else if (kState) {
       split_rows(1, 2);                               // no results: the other buffer's chunks
     } else {
       if (q.out_f32) walk(std::true_type());
@@ -668,9 +679,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   }
 }
 
-}  // namespace
-
-cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
+template <int D>
+cudaError_t go(const LaParams& p, bool state_only, cudaStream_t st) {
   const int64_t grid = (int64_t)(state_only ? p.pre_units : p.units) * p.H * p.npass;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
@@ -680,16 +690,23 @@ cudaError_t launch_la_tc(const LaParams& p, bool state_only, cudaStream_t st) {
   for (int i = 0; i < p.npass; ++i) {
     const LaPass& q = p.pass[i];
     returns = returns || q.s_out;
-    if (!make_bf16_map(&maps.m[i][0], q.x, rows, q.hx) || !make_bf16_map(&maps.m[i][1], q.y, rows, q.hy) ||
-        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz))
+    if (!make_bf16_map(&maps.m[i][0], q.x, rows, q.hx, D) ||
+        !make_bf16_map(&maps.m[i][1], q.y, rows, q.hy, D) ||
+        !make_bf16_map(&maps.m[i][2], q.z, rows, q.hz, D))
       return cudaErrorInvalidValue;
   }
-  auto kern = state_only ? (returns ? la_tc_kernel<true, 3> : la_tc_kernel<true, 2>)
-                         : (returns ? la_tc_kernel<false, 3> : la_tc_kernel<false, 2>);
-  const cudaError_t e = allow_smem(kern, SMEM);
+  auto kern = state_only ? (returns ? la_tc_kernel<D, true, 3> : la_tc_kernel<D, true, 2>)
+                         : (returns ? la_tc_kernel<D, false, 3> : la_tc_kernel<D, false, 2>);
+  const cudaError_t e = allow_smem(kern, Mem<D>::SIZE);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)grid, NT, SMEM, st>>>(maps, p);
+  kern<<<(unsigned)grid, NT, Mem<D>::SIZE, st>>>(maps, p);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_la_tc(const LaParams& p, int D, bool state_only, cudaStream_t st) {
+  return D == 64 ? go<64>(p, state_only, st) : go<128>(p, state_only, st);
 }
 
 }  // namespace sfg

@@ -34,7 +34,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 bool tc_fwd_available() { return encode_fn() != nullptr; }
 
-bool make_bf16_map(CUtensorMap* m, const void* base, int rows, int H) {
+bool make_bf16_map(CUtensorMap* m, const void* base, int rows, int H, int D) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};

@@ -80,10 +80,10 @@ enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + 1, QKDONE = FREE + NS, PREA
 static_assert(8 * NBAR + 32 <= 320 && NBAR <= 32, "barriers");
 
 // Tries of a wait before it gives up: each may suspend the thread for up to 20 us (at the least
-// it takes the ~50 ns of the instruction), so between 0.2 and 80 s, where a wait that ends takes
+// it takes the ~50 ns of the instruction), so between 50 ms and 20 s, where a wait that ends takes
 // microseconds.  (A count and not a clock: the waits are inlined into every role's loop, and
 // the loops run at the speed of instruction fetch.)
-constexpr int WAIT_TRIES = 4000000;
+constexpr int WAIT_TRIES = 1000000;
 
 struct Maps {
   CUtensorMap m[3][3];   // x, y, z of each pass

@@ -22,26 +22,38 @@ constexpr int C = LA_CHUNK;
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+// Chunks in flight: at D = 128 one CTA fills an SM, so the next chunk's rows travel under the
+// present one's products; at D = 64 two CTAs share an SM and cover for one another.
+template <int D>
+constexpr int kStages = D == 128 ? 2 : 1;
+
 template <int D>
 struct Smem {
-  float X[C][D + 4], Y[C][D + 4], Z[C][ZT + 4], P[C][ZT + 4], S[D][ZT + 4], tab[C + 4], carry[4];
+  float X[kStages<D>][C][D + 4], Y[kStages<D>][C][D + 4], Z[kStages<D>][C][ZT + 4];
+  float P[C][ZT + 4], S[D][ZT + 4], tab[C + 4], wr[2][C], carry[4];
 };
 
-// Rows [r0, r0 + L) of one head's columns [c0, c0 + W) into dst (leading dimension ld); the
-// other rows of the 64 become zero.
+// Copies rows [r0, r0 + L) of one head's columns [c0, c0 + W) to dst (leading dimension ld); the
+// other rows of the 64 become zero.  Asynchronous: part of the thread's next commit.
 template <int W>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const float* src, int64_t r0, int L,
+__device__ __forceinline__ void copy_rows(float* dst, int ld, const float* src, int64_t r0, int L,
                                           int heads, int head, int D, int c0, int tid) {
   for (int idx = tid; idx < C * (W / 4); idx += 256) {
     const int r = idx / (W / 4), c = (idx % (W / 4)) * 4;
-    const float4 v = r < L ? ld4(src + ((size_t)(r0 + r) * heads + head) * D + c0 + c)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(dst + r * ld + c) = v;
+    const float* from = src + ((size_t)(r0 + (r < L ? r : 0)) * heads + head) * D + c0 + c;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * ld + c));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(r < L ? 16 : 0)
+                 : "memory");
   }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D, bool kState>
-__global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
+__global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const LaParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NZ = D / ZT, YR = D / 16;
@@ -71,11 +83,16 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
   const float d = p.decay[h];
   const int nc = (int)((rows + C - 1) / C);
   const int tail = (int)(rows - (int64_t)(nc - 1) * C);
-  if (tid <= C) sm.tab[tid] = tid == 0 ? 1.f : expf(d * (float)tid);
-  if (tid >= 128 && tid < 130) {                  // lam^64 and lam^tail as sums of two floats
-    const double f = la_pow(d, tid == 128 ? C : tail);
-    sm.carry[2 * (tid - 128)] = (float)f;
-    sm.carry[2 * (tid - 128) + 1] = (float)(f - (double)(float)f);
+  auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
+  if (tid <= C) sm.tab[tid] = pw(tid);
+  if (tid >= 128) {                               // weights of a full chunk's rows, and of the last's
+    const int r = tid & 63, at = (tid - 128) >> 6, n = at ? tail : C;
+    sm.wr[at][r] = r < n ? q.c * pw(q.reverse ? r + 1 : n - 1 - r) : 0.f;
+  }
+  if (tid == 96 || tid == 97) {                  // lam^64 and lam^tail as sums of two floats
+    const double f = la_pow(d, tid == 96 ? C : tail);
+    sm.carry[2 * (tid - 96)] = (float)f;
+    sm.carry[2 * (tid - 96) + 1] = (float)(f - (double)(float)f);
   }
 
   // S[y = ty YR + e][z = zc + 4 tx ..]: zeros, the caller's state, or the segment's entry
@@ -92,20 +109,37 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
                             src[(size_t)(z + 2) * D + y], src[(size_t)(z + 3) * D + y]);
   }
   const int G_x = p.H / q.hx, G_y = p.H / q.hy, G_z = p.H / q.hz;
-  for (int ci = 0; ci < nc; ++ci) {
+  constexpr int NB = kStages<D>;
+  auto fetch = [&](int ci) {
     const int64_t done = (int64_t)ci * C;
     const int L = (int)(rows - done < C ? rows - done : C);
     const int64_t r0 = q.reverse ? se - done - L : sb + done;
-    __syncthreads();                              // the last chunk's readers; the table
+    const int b = ci % NB;
     if (!kState)
-      load_rows<D>(&sm.X[0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
-    load_rows<D>(&sm.Y[0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
-    load_rows<ZT>(&sm.Z[0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
+      copy_rows<D>(&sm.X[b][0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
+    copy_rows<D>(&sm.Y[b][0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
+    copy_rows<ZT>(&sm.Z[b][0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
+    copies_commit();
+  };
+  if (NB > 1 && nc > 0) fetch(0);
+  for (int ci = 0; ci < nc; ++ci) {
+    const int64_t done = (int64_t)ci * C;
+    const bool end = ci + 1 == nc;
+    const int L = end ? tail : C;
+    const int64_t r0 = q.reverse ? se - done - L : sb + done;
+    __syncthreads();                              // the last chunk's readers; the tables
+    if (NB == 1) fetch(ci);
+    else if (!end) fetch(ci + 1);
     if (!kState) {
 #pragma unroll
       for (int e = 0; e < YR; ++e) st4(&sm.S[ty * YR + e][4 * tx], s[e]);
     }
+    if (NB > 1 && !end) copies_wait<1>();
+    else copies_wait<0>();
     __syncthreads();
+    const auto& X = sm.X[ci % NB];
+    const auto& Y = sm.Y[ci % NB];
+    const auto& Z = sm.Z[ci % NB];
     if (!kState) {
       // P rows 4 ty + i, columns tx + 16 j
       float acc[4][4] = {};
@@ -113,9 +147,9 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
       for (int c = 0; c < D; c += 4) {
         float4 xv[4], yv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xv[i] = ld4(&sm.X[4 * ty + i][c]);
+        for (int i = 0; i < 4; ++i) xv[i] = ld4(&X[4 * ty + i][c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) yv[j] = ld4(&sm.Y[tx + 16 * j][c]);
+        for (int j = 0; j < 4; ++j) yv[j] = ld4(&Y[tx + 16 * j][c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -142,7 +176,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
         for (int e = 0; e < 4; ++e) sv[e] = ld4(&sm.S[c + e][4 * tx]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 xv = ld4(&sm.X[4 * ty + i][c]);
+          const float4 xv = ld4(&X[4 * ty + i][c]);
           o[i].x = fmaf(xv.x, sv[0].x, fmaf(xv.y, sv[1].x, fmaf(xv.z, sv[2].x, fmaf(xv.w, sv[3].x, o[i].x))));
           o[i].y = fmaf(xv.x, sv[0].y, fmaf(xv.y, sv[1].y, fmaf(xv.z, sv[2].y, fmaf(xv.w, sv[3].y, o[i].y))));
           o[i].z = fmaf(xv.x, sv[0].z, fmaf(xv.y, sv[1].z, fmaf(xv.z, sv[2].z, fmaf(xv.w, sv[3].z, o[i].z))));
@@ -159,7 +193,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
       for (int c = 0; c < C; c += 4) {
         float4 zv[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) zv[e] = ld4(&sm.Z[c + e][4 * tx]);
+        for (int e = 0; e < 4; ++e) zv[e] = ld4(&Z[c + e][4 * tx]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 pv = ld4(&sm.P[4 * ty + i][c]);
@@ -178,21 +212,25 @@ __global__ void __launch_bounds__(256) la_simt_kernel(const LaParams p) {
       }
     }
     // S = lam^L S + c sum_r lam^f(r) y_r z_r
-    const float hi = sm.carry[ci + 1 == nc ? 2 : 0], lo = sm.carry[ci + 1 == nc ? 3 : 1];
+    const float hi = sm.carry[end ? 2 : 0], lo = sm.carry[end ? 3 : 1];
+    const float* wr = sm.wr[end];
     float4 acc[YR];
 #pragma unroll
     for (int e = 0; e < YR; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < L; ++r) {
-      const float wgt = q.c * sm.tab[q.reverse ? r + 1 : L - 1 - r];
-      float4 zv = ld4(&sm.Z[r][4 * tx]);
+#pragma unroll 4
+    for (int r = 0; r < C; ++r) {                 // (rows past L are zero)
+      const float wgt = wr[r];
+      float4 zv = ld4(&Z[r][4 * tx]);
       zv.x *= wgt; zv.y *= wgt; zv.z *= wgt; zv.w *= wgt;
+      float yv[YR];
+#pragma unroll
+      for (int e = 0; e < YR; e += 4) *reinterpret_cast<float4*>(&yv[e]) = ld4(&Y[r][ty * YR + e]);
 #pragma unroll
       for (int e = 0; e < YR; ++e) {
-        const float yv = sm.Y[r][ty * YR + e];
-        acc[e].x = fmaf(yv, zv.x, acc[e].x);
-        acc[e].y = fmaf(yv, zv.y, acc[e].y);
-        acc[e].z = fmaf(yv, zv.z, acc[e].z);
-        acc[e].w = fmaf(yv, zv.w, acc[e].w);
+        acc[e].x = fmaf(yv[e], zv.x, acc[e].x);
+        acc[e].y = fmaf(yv[e], zv.y, acc[e].y);
+        acc[e].z = fmaf(yv[e], zv.z, acc[e].z);
+        acc[e].w = fmaf(yv[e], zv.w, acc[e].w);
       }
     }
 #pragma unroll

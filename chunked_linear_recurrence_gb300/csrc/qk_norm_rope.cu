@@ -25,7 +25,7 @@
 namespace sfg {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 128;   // four CTAs an SM: persistent, 512 threads with 64 KB on the way
 
 // VEC consecutive elements as they come from memory, and as VEC / 2 pairs of floats.
 template <typename T, int VEC>
@@ -373,7 +373,7 @@ constexpr int FWD_U = 4, BWD_U = 2;
 template <typename T, int D, int VEC>
 cudaError_t fwd(QkParams p, cudaStream_t st) {
   unsigned blocks;
-  share<FWD_U>(p, NT / (D / (2 * VEC)), 152 * 6, blocks);
+  share<FWD_U>(p, NT / (D / (2 * VEC)), 152 * 4, blocks);
   qk_fwd_kernel<T, D, VEC, FWD_U><<<blocks, NT, 0, st>>>(p);
   return cudaGetLastError();
 }

@@ -264,6 +264,29 @@ inline cudaError_t allow_smem(K kern, size_t bytes) {
   return cudaSuccess;
 }
 
+// The launches of one call follow one another closely: each may start while the one before it
+// ends (its start needs none of that one's results), and waits for them (launch_wait) where it
+// does.  Only launches after a call's first do so: `early`.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(bool early, void (*kern)(P...), unsigned grid, unsigned threads,
+                                size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 struct StepParams {
   const void* q;
   const void* k;

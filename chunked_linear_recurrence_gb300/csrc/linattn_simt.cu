@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NZ = D / ZT, YR = D / 16;
+  if (kState) launch_next();
+  else if (p.seg < p.T) launch_wait();            // the entry states
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   int id = blockIdx.x;
   const int zt = id % NZ; id /= NZ;
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
 // float4 of the state; the sums of eight pieces are in flight together.
 template <int D>
 __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
+  launch_next();
   const int tid = threadIdx.x;
   int id = blockIdx.x;
   constexpr int PARTS = D * D / 1024, AHEAD = 8;
@@ -293,10 +296,12 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
     len = e - b;
   }
   const int S = la_segments(len, p.seg), pieces = (S - 1) * k;
-  if (u0 + S > p.units || s0 + pieces > p.pre_units) return;   // malformed offsets
   bool skip;
   const float* s_in = la_entry(p, q, n, h, D, skip);
-  if (skip) return;
+  if (skip || u0 + S > p.units || s0 + pieces > p.pre_units) {   // padding; malformed offsets
+    launch_wait();
+    return;
+  }
   const int at = (part * 256 + tid) * 4, z = at / D, y = at % D;
   float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
   if (s_in) {
@@ -313,6 +318,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   const size_t step = (size_t)p.H * D * D;
   float* out = q.entry + ((size_t)u0 * p.H + h) * D * D + at;
   const float* in = q.sums + ((size_t)s0 * p.H + h) * D * D + at;
+  launch_wait();                                       // the sums
   st4(out, e);
   __syncthreads();
   const float hi = pow_s[0], lo = pow_s[1];
@@ -346,8 +352,7 @@ cudaError_t go(const LaParams& p, cudaStream_t st) {
   auto kern = la_simt_kernel<D, kState>;
   const cudaError_t e = allow_smem(kern, sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)grid, 256, sizeof(Smem<D>), st>>>(p);
-  return cudaGetLastError();
+  return launch_after(!kState && p.pre_units > 0, kern, (unsigned)grid, 256, sizeof(Smem<D>), st, p);
 }
 
 }  // namespace
@@ -361,9 +366,7 @@ cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st) {
   const int64_t grid = (int64_t)p.N * p.H * p.npass * (D * D / 1024);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  if (D == 64) la_carry_kernel<64><<<(unsigned)grid, 256, 0, st>>>(p);
-  else la_carry_kernel<128><<<(unsigned)grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_after(true, D == 64 ? la_carry_kernel<64> : la_carry_kernel<128>, (unsigned)grid, 256, 0, st, p);
 }
 
 }  // namespace sfg

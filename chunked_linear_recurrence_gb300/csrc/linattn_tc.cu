@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + M::BAR + 8 * NBAR);
   volatile uint32_t* cx = reinterpret_cast<uint32_t*>(sm + M::BAR + 8 * NBAR + 4);
+  if (kState) launch_next();
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   int id = blockIdx.x;
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     __syncthreads();
   }
   if (unit[0] != 1) {
+    if (!kState && p.seg < p.T) launch_wait();
     if (kState || unit[0] == 0) return;
     uint4* o = reinterpret_cast<uint4*>(q.out);   // padding: zero rows
 #pragma unroll 1
@@ -470,6 +472,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     const int wg = (warp - 4) >> 2;
     const int z = ((warp & 3) << 5) + lane;
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    if (!kState && p.seg < p.T) launch_wait();          // the entry states
     float2 s[D / 4];                                    // columns D / 2 wg + 2 e, + 1 of row z
     {
       bool skip;
@@ -699,8 +702,7 @@ cudaError_t go(const LaParams& p, bool state_only, cudaStream_t st) {
                          : (returns ? la_tc_kernel<D, false, 3> : la_tc_kernel<D, false, 2>);
   const cudaError_t e = allow_smem(kern, Mem<D>::SIZE);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)grid, NT, Mem<D>::SIZE, st>>>(maps, p);
-  return cudaGetLastError();
+  return launch_after(!state_only && p.pre_units > 0, kern, (unsigned)grid, NT, Mem<D>::SIZE, st, maps, p);
 }
 
 }  // namespace

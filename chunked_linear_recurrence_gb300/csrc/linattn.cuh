@@ -33,8 +33,8 @@ struct LaPass {
   void* out;            // [rows, H, D]: the token type, or FP32 (out_f32)
   const float* s_in;    // [N,H,D,D] or NULL (zeros)
   float* s_out;         // [N,H,D,D] or NULL
-  float* entry;         // [units,H,D,D] (z rows): entry states of the segments
-  float* sums;          // [pre_units,H,D,D] (z rows): what each piece adds to the state
+  float* entry;         // [units,H,D/4,D,4] (y / 4, z, y % 4): entry states of the segments
+  float* sums;          // [pre_units,H,D/4,D,4]: what each piece adds to the state
   int hx, hy, hz;       // heads of x, y, z (each divides H)
   int s_t;              // the state is stored as [y][z] (s_in, s_out)
   int out_f32;

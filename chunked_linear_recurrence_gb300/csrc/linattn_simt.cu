@@ -58,7 +58,6 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NZ = D / ZT, YR = D / 16;
   if (kState) launch_next();
-  else if (p.seg < p.T) launch_wait();            // the entry states
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   int id = blockIdx.x;
   const int zt = id % NZ; id /= NZ;
@@ -101,12 +100,22 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   float4 s[YR];
   const size_t uoff = ((size_t)t.at * p.H + h) * D * D;
   const float* src = kState ? nullptr : split ? q.entry + uoff : s_in;
-  const bool st = q.s_t && !split;                // segment states are stored [z][y]
+  if (split && src) {
+#pragma unroll
+    for (int e = 0; e < YR; e += 4) {
+      const float* v = src + (size_t)(ty * YR + e) * D + 4 * (zc + 4 * tx);
+      const float4 c0 = ld4(v), c1 = ld4(v + 4), c2 = ld4(v + 8), c3 = ld4(v + 12);
+      s[e] = make_float4(c0.x, c1.x, c2.x, c3.x);
+      s[e + 1] = make_float4(c0.y, c1.y, c2.y, c3.y);
+      s[e + 2] = make_float4(c0.z, c1.z, c2.z, c3.z);
+      s[e + 3] = make_float4(c0.w, c1.w, c2.w, c3.w);
+    }
+  } else
 #pragma unroll
   for (int e = 0; e < YR; ++e) {
     const int y = ty * YR + e, z = zc + 4 * tx;
     if (!src) s[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    else if (st) s[e] = ld4(src + (size_t)y * D + z);
+    else if (q.s_t) s[e] = ld4(src + (size_t)y * D + z);
     else s[e] = make_float4(src[(size_t)z * D + y], src[(size_t)(z + 1) * D + y],
                             src[(size_t)(z + 2) * D + y], src[(size_t)(z + 3) * D + y]);
   }
@@ -245,11 +254,21 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   }
   float* dst = kState ? q.sums + uoff : t.last ? la_exit(p, q, n, h, D) : nullptr;
   if (!dst) return;
-  const bool dt = q.s_t && !kState;
+  if (kState) {
+#pragma unroll
+    for (int e = 0; e < YR; e += 4) {
+      float* v = dst + (size_t)(ty * YR + e) * D + 4 * (zc + 4 * tx);
+      st4(v, make_float4(s[e].x, s[e + 1].x, s[e + 2].x, s[e + 3].x));
+      st4(v + 4, make_float4(s[e].y, s[e + 1].y, s[e + 2].y, s[e + 3].y));
+      st4(v + 8, make_float4(s[e].z, s[e + 1].z, s[e + 2].z, s[e + 3].z));
+      st4(v + 12, make_float4(s[e].w, s[e + 1].w, s[e + 2].w, s[e + 3].w));
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < YR; ++e) {
     const int y = ty * YR + e, z = zc + 4 * tx;
-    if (dt) {
+    if (q.s_t) {
       st4(dst + (size_t)y * D + z, s[e]);
     } else {
       dst[(size_t)z * D + y] = s[e].x;
@@ -302,12 +321,12 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
     launch_wait();
     return;
   }
-  const int at = (part * 256 + tid) * 4, z = at / D, y = at % D;
+  const int at = (part * 256 + tid) * 4, z = at / 4 % D, y = at / (4 * D) * 4;
   float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
   if (s_in) {
     if (q.s_t) e = make_float4(s_in[(size_t)y * D + z], s_in[(size_t)(y + 1) * D + z],
                                s_in[(size_t)(y + 2) * D + z], s_in[(size_t)(y + 3) * D + z]);
-    else e = ld4(s_in + at);
+    else e = ld4(s_in + (size_t)z * D + y);
   }
   __shared__ float pow_s[2];
   if (tid == 0) {
@@ -352,7 +371,8 @@ cudaError_t go(const LaParams& p, cudaStream_t st) {
   auto kern = la_simt_kernel<D, kState>;
   const cudaError_t e = allow_smem(kern, sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
-  return launch_after(!kState && p.pre_units > 0, kern, (unsigned)grid, 256, sizeof(Smem<D>), st, p);
+  // (not early: CTAs placed beside the last ones of the launch before would share their SMs)
+  return launch_after(false, kern, (unsigned)grid, 256, sizeof(Smem<D>), st, p);
 }
 
 }  // namespace

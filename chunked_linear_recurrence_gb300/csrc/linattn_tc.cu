@@ -168,7 +168,28 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     fence_proxy_async_smem();
     __syncwarp();
   }
-  if (warp != 0) __syncthreads();                 // warp 0: once the first chunks are on their way
+  auto pw = [&](int e) { return e <= 0 ? 1.f : expf(p.decay[h] * (float)e); };
+  if (warp != 0) {                                // what does not depend on the unit
+    if (warp == 1) tmem_alloc(tslot, 512);
+    if (tid >= 128 && tid < 256) {
+      const int j = tid - 128;
+      if (j < C) {
+        rd[j] = q.b * pw(rev ? C - 1 - j : j + 1);
+        wr[j] = q.c * pw(rev ? j + 1 : C - 1 - j);
+      }
+      const int gap = rev ? j - 64 : 64 - j;          // |r - s| where s may contribute to r
+      const float f = gap >= 0 ? q.a * pw(gap) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pq[k * PQ_LD + j + k] = f;
+    }
+    if (!kState && tid >= 256)   // P on the far side of the diagonal stays zero
+#pragma unroll 1
+      for (int i = tid - 256; i < 2 * (int)PANEL / 16; i += NT - 256)
+        *reinterpret_cast<uint4*>(sm + M::P + 16 * i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();                              // warp 0: once the first chunk is on its way
+  }
   // (the shuffles tell the compiler that these are the same in every lane: they stay out of the
   // roles' registers)
   const int s0 = __shfl_sync(0xffffffffu, unit[1], 0), s1 = __shfl_sync(0xffffffffu, unit[2], 0);
@@ -201,13 +222,16 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     }
   };
   if (warp == 0) {
-    if (unit[0] == 1) {
-#pragma unroll 1
-      for (int c = 0; c < NS && c < nc; ++c) load(c);
-    }
+    if (unit[0] == 1 && nc > 0) load(0);
     __syncthreads();
   }
+  tc_fence_after();
+  const uint32_t tm = *tslot;
   if (unit[0] != 1) {
+    if (warp == 1) {
+      tmem_relinquish();
+      tmem_dealloc(tm, 512);
+    }
     if (!kState && p.seg < p.T) launch_wait();
     if (kState || unit[0] == 0) return;
     uint4* o = reinterpret_cast<uint4*>(q.out);   // padding: zero rows
@@ -216,27 +240,12 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       o[((size_t)(s0 + i / (D / 8)) * p.H + h) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const float d = p.decay[h];
-  if (warp == 1) tmem_alloc(tslot, 512);
-  auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
-  if (tid >= 128 && tid < 256) {
-    const int i = tid & 63, L = tid < 192 ? C : tail, j = tid - 128;
-    rd[j] = i < L ? q.b * pw(rev ? L - 1 - i : i + 1) : 0.f;
-    wr[j] = i < L ? q.c * pw(rev ? i + 1 : L - 1 - i) : 0.f;
-    const int gap = rev ? j - 64 : 64 - j;          // |r - s| where s may contribute to r
-    const float f = gap >= 0 ? q.a * pw(gap) : 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) pq[k * PQ_LD + j + k] = f;
+  if (tid >= 512 && tid < 576) {                  // the last chunk's weights
+    const int i = tid - 512;
+    rd[64 + i] = i < tail ? q.b * pw(rev ? tail - 1 - i : i + 1) : 0.f;
+    wr[64 + i] = i < tail ? q.c * pw(rev ? i + 1 : tail - 1 - i) : 0.f;
   }
-  if (!kState)   // P on the far side of the diagonal stays zero
-#pragma unroll 1
-    for (int i = tid; i < 2 * (int)PANEL / 16; i += NT)
-      *reinterpret_cast<uint4*>(sm + M::P + 16 * i) = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = *tslot;
 
   // ------------------------------------------------------------------ weighted rows in BF16 parts
   // (four warps; chunks first, first + step, ..)
@@ -306,17 +315,19 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         const int b = (nc - 1) % NS;
         if (!warp_wait(&bars[LANDED], 0, cx)) return false;
         uint8_t* st = sm + b * M::STAGE;
-        const int per = (C - tail) * 8;                // 16-byte pieces of a panel
 #pragma unroll 1
-        for (int i = lane; i < 2 * NP * per; i += 32) {
-          const int t = i / per, rr = i % per;
-          uint8_t* base = st + (t < NP ? M::Y + 2 * t * PANEL : M::Z + (t - NP) * PANEL);
-          *reinterpret_cast<uint4*>(base + (tail + rr / 8) * 128 + (rr % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        for (int at = tail * 128 + lane * 16; at < (int)PANEL; at += 512)
+#pragma unroll
+          for (int pp = 0; pp < NP; ++pp) {
+            *reinterpret_cast<uint4*>(st + M::Y + 2 * pp * PANEL + at) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(st + M::Z + pp * PANEL + at) = make_uint4(0, 0, 0, 0);
+          }
         fence_proxy_async_smem();
         warp_arrive(&bars[FULL + b], lane);
         return true;
       };
+#pragma unroll 1
+      for (int c = 1; !kState && c < NS && c < nc; ++c) load(c);
       bool ok = kState || nc != 1 || tail == C || trim();
 #pragma unroll 1
       for (int c = 0; c < nc && ok; ++c) {
@@ -369,10 +380,10 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       };
       bool ok = true;
       if (kState) {                                    // the loader, where E is the only product
-        issued = nc < NS ? nc : NS;
+        issued = 1;                                    // (by warp 0)
 #pragma unroll 1
-        for (int c = NS; c < nc; ++c) {
-          if (!(ok = warp_wait(&bars[FREE + c % NS], ((c - NS) / NS) & 1, cx))) break;
+        for (int c = 1; c < nc; ++c) {
+          if (c >= NS && !(ok = warp_wait(&bars[FREE + c % NS], ((c - NS) / NS) & 1, cx))) break;
           load(c);
         }
         if (!ok) land();
@@ -482,7 +493,15 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       if (!src) {
 #pragma unroll
         for (int e = 0; e < D / 4; ++e) s[e] = make_float2(0.f, 0.f);
-      } else if (q.s_t && !split) {                   // stored [y][z]
+      } else if (split) {
+        const float4* v = reinterpret_cast<const float4*>(src) + D / 8 * wg * D + z;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          const float4 f = v[e * D];
+          s[2 * e] = make_float2(f.x, f.y);
+          s[2 * e + 1] = make_float2(f.z, f.w);
+        }
+      } else if (q.s_t) {                             // stored [y][z]
 #pragma unroll
         for (int e = 0; e < D / 4; ++e)
           s[e] = make_float2(src[(size_t)(D / 2 * wg + 2 * e) * D + z], src[(size_t)(D / 2 * wg + 2 * e + 1) * D + z]);
@@ -556,16 +575,37 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
                  : kState ? q.sums + ((size_t)unit[4] * p.H + h) * D * D
                  : unit[5] ? la_exit(p, q, unit[3], h, D) : nullptr;
     if (dst) {
-      if (q.s_t && !kState) {
+      if (kState) {
+        float4* v = reinterpret_cast<float4*>(dst) + D / 8 * wg * D + z;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e)
+          v[e * D] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
+      } else if (q.s_t) {
 #pragma unroll
         for (int e = 0; e < D / 4; ++e) {
           dst[(size_t)(D / 2 * wg + 2 * e) * D + z] = s[e].x;
           dst[(size_t)(D / 2 * wg + 2 * e + 1) * D + z] = s[e].y;
         }
       } else {
-        float4* v = reinterpret_cast<float4*>(dst + (size_t)z * D + D / 2 * wg);
+        // By way of shared memory, so that a store covers whole rows: 16-byte pieces, those of
+        // eight rows on different banks.  The stages after the last chunk's (two at head size
+        // 128) are free: what they held has been read (O1 of the chunk before the last came
+        // after it), and no copy follows.
+        constexpr int PW = D / 8;                       // pieces of a warp's row
+        uint8_t* mine = sm + (wg ? (nc + 1) % NS : nc % NS) * M::STAGE + (warp & 3) * 32 * PW * 16;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) v[e] = make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
+        for (int e = 0; e < PW; ++e)
+          *reinterpret_cast<float4*>(mine + (lane * PW + (e ^ (lane & 7))) * 16) =
+              make_float4(s[2 * e].x, s[2 * e].y, s[2 * e + 1].x, s[2 * e + 1].y);
+        __syncwarp();
+        float* o = dst + (size_t)(z - lane + lane / PW) * D + D / 2 * wg + lane % PW * 4;
+#pragma unroll
+        for (int e = 0; e < PW; ++e) {
+          const int row = e * (32 / PW) + lane / PW;
+          *reinterpret_cast<float4*>(o) =
+              *reinterpret_cast<const float4*>(mine + (row * PW + (lane % PW ^ (row & 7))) * 16);
+          o += (size_t)(32 / PW) * D;
+        }
       }
     }
     }
@@ -578,7 +618,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       // lam^64 and lam^tail, each as a float and what that float lacks, relative to it: a state
       // carried over thousands of chunks must not drift by the rounding of one factor
       if (lane < 2) {
-        const double f = la_pow(d, lane ? tail : C);
+        const double f = la_pow(p.decay[h], lane ? tail : C);
         carry[2 * lane] = (float)f;
         carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)(float)f - 1.0) : 0.f;
       }

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   LaUnit t;
   if (!la_locate<kState>(u, p, t)) return;
   const int n = t.n;
-  const bool split = p.seg < p.T;
+  const bool split = p.seg < p.T && !(t.last && t.off == 0);
   const int64_t rows = t.rows;
   const int64_t sb = q.reverse ? t.eos - t.off - rows : t.bos + t.off, se = sb + rows;
   bool skip;
@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   constexpr int PARTS = D * D / 1024, AHEAD = 8;
   const int part = id % PARTS; id /= PARTS;
   const int pi = id % p.npass; id /= p.npass;
-  const int h = id % p.H, n = id / p.H;
+  const int h = id % p.H;
+  int n = id / p.H;                                    // packed: the n-th walk that is cut
   const LaPass& q = p.pass[pi];
   const int k = p.seg / p.pre;
   int64_t len = p.T;
@@ -301,23 +302,37 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
     s0 = n * (S - 1) * k;
   } else {
     const int lane = tid & 31;
-    int sum = 0;
-    int64_t b, e;
-    for (int m = lane; m < n; m += 32) {
-      seq_span(m, p.B, p.T, p.cu, b, e);
-      sum += la_segments(e - b, p.seg);
+    int found = -1, sum = 0;                           // its sequence; segments before it
+    for (int m0 = 0; m0 < p.N && found < 0; m0 += 32) {
+      const int m = m0 + lane;
+      int64_t b = 0, e = 0;
+      if (m < p.N) seq_span(m, p.B, p.T, p.cu, b, e);
+      unsigned hit = __ballot_sync(0xffffffffu, e - b > p.seg);
+      int upto = 32;
+      if (n < __popc(hit)) {
+        for (; n > 0; --n) hit &= hit - 1;
+        upto = __ffs(hit) - 1;
+        found = m0 + upto;
+        len = __shfl_sync(0xffffffffu, e - b, upto);
+      } else {
+        n -= __popc(hit);
+      }
+      if (lane < upto && m < p.N) sum += la_segments(e - b, p.seg);
     }
+    // Fewer walks are cut.  (Not even the launch before is waited for: a walk that is not cut
+    // reads the caller's state, and where none is cut that launch does nothing.)
+    if (found < 0) return;
+    n = found;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     u0 = sum;
     s0 = (sum - n) * k;
-    seq_span(n, p.B, p.T, p.cu, b, e);
-    len = e - b;
   }
   const int S = la_segments(len, p.seg), pieces = (S - 1) * k;
   bool skip;
   const float* s_in = la_entry(p, q, n, h, D, skip);
-  if (skip || u0 + S > p.units || s0 + pieces > p.pre_units) {   // padding; malformed offsets
+  // padding; malformed offsets
+  if (skip || u0 + S > p.units || s0 + pieces > p.pre_units) {
     launch_wait();
     return;
   }
@@ -383,7 +398,9 @@ cudaError_t launch_la_simt(const LaParams& p, int D, bool state_only, cudaStream
 }
 
 cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st) {
-  const int64_t grid = (int64_t)p.N * p.H * p.npass * (D * D / 1024);
+  // (a walk that is cut has more than `seg` rows: of packed ones there are T / seg at most)
+  const int walks = p.cu && p.T / p.seg < p.N ? p.T / p.seg : p.N;
+  const int64_t grid = (int64_t)walks * p.H * p.npass * (D * D / 1024);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_after(true, D == 64 ? la_carry_kernel<64> : la_carry_kernel<128>, (unsigned)grid, 256, 0, st, p);

@@ -77,7 +77,7 @@ constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + 1, QKDONE = FREE + NS, PREADY,
        PFREE = PREADY + 2, SPLIT, EHALF = SPLIT + 4, EDONE = EHALF + 2, EFREE = EDONE + 2,
        O1DONE = EFREE + 2, ODONE, OFREE, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
-static_assert(8 * NBAR + 32 <= 320 && NBAR <= 32, "barriers");
+static_assert(8 * NBAR + 36 <= 320 && NBAR <= 32, "barriers");
 
 // Tries of a wait before it gives up: each may suspend the thread for up to 20 us (at the least
 // it takes the ~50 ns of the instruction), so between 50 ms and 20 s, where a wait that ends takes
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const bool rev = q.reverse != 0;
   constexpr int NE = kState ? 2 : 1;              // buffers of E and of the weighted rows
   // The unit, found by one warp: whether there is one (2: padding of the paged pool), its rows
-  // [s0, s1), its sequence, its place, whether the walk ends with it.
+  // [s0, s1), its sequence, its place, whether the walk ends with it, whether it is cut.
   int* unit = reinterpret_cast<int*>(sm + M::BAR + 8 * NBAR + 8);
   if (warp == 0) {
     LaUnit t;
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         unit[3] = t.n;
         unit[4] = t.at;
         unit[5] = t.last;
+        unit[6] = p.seg < p.T && !(t.last && t.off == 0);
       }
     }
     if (lane == 0) unit[0] = code, *cx = 0;
@@ -423,6 +424,10 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)(kk * 2), ID_O2, kk > 0);
+          if (__builtin_expect(nc == 1, 0))
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(tm + TM_O2, dz + kstep_mn(kk), dp + (uint64_t)((PANEL >> 4) + kk * 2), ID_O2, true);
           mma_commit(&bars[ODONE]);
           mma_commit(&bars[FREE + b]);
         }
@@ -434,43 +439,51 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     } else {
       // -------------------------------------------------------------- P
       if (!kState) {
-        // row r of P.  The half on the far side of the diagonal (32 columns of one warp) is never
+        // row r of P.  A walk of one chunk has its rounding's rest in the second buffer: there a
+        // result may come from one or two elements, whose rounding to BF16 would show as much as
+        // the result's own (over more rows the roundings average out).  The half on the far side of the diagonal (32 columns of one warp) is never
         // touched: it stays zero.
         const int r = (warp - 2) * 32 + lane;          // TMEM lane 64 + r
         // a lam^|r-s|, or 0, at f[s] (the copy in which that is 16-byte aligned)
         const float* f = pq + (r & 3) * (PQ_LD + 1) + 64 - r;
         const uint32_t tl = tm + TM_P + ((uint32_t)(warp * 32) << 16);
         const int s0 = rev && warp == 3 ? 32 : 0, s1 = !rev && warp == 2 ? 32 : 64;
+        auto weigh = [&](int s, uint8_t* row, bool last, auto rest) {   // 16 columns
+          float x[16];
+          tmem_ld16(tl + s, x);
+          float4 g[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = *reinterpret_cast<const float4*>(f + s + 4 * e);
+          tmem_ld_wait();
+          if (last) {
+            tc_fence_before();
+            warp_arrive(&bars[PFREE], lane);
+          }
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 w = g[2 * ch + (e >> 1)];
+              const float2 t = mul2(make_float2(x[8 * ch + 2 * e], x[8 * ch + 2 * e + 1]),
+                                    e & 1 ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
+              v[e] = pack2(t);
+              if (rest.value) v[e] = pack2(sub2(t, unpack2(v[e])));
+            }
+            *reinterpret_cast<uint4*>(row + ((((s >> 3) + ch) ^ (r & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        };
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
           if (!warp_wait(&bars[QKDONE], c & 1, cx)) break;
           tc_fence_after();
           uint8_t* row = sm + M::P + (c & 1) * PANEL + r * 128;
 #pragma unroll 1
-          for (int s = s0; s < s1; s += 16) {
-            float x[16];
-            tmem_ld16(tl + s, x);
-            float4 g[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) g[e] = *reinterpret_cast<const float4*>(f + s + 4 * e);
-            tmem_ld_wait();
-            if (s + 16 >= s1) {
-              tc_fence_before();
-              warp_arrive(&bars[PFREE], lane);
-            }
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 w = g[2 * ch + (e >> 1)];
-                v[e] = pack2(mul2(make_float2(x[8 * ch + 2 * e], x[8 * ch + 2 * e + 1]),
-                                  e & 1 ? make_float2(w.z, w.w) : make_float2(w.x, w.y)));
-              }
-              *reinterpret_cast<uint4*>(row + ((((s >> 3) + ch) ^ (r & 7)) << 4)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
+          for (int s = s0; s < s1; s += 16) weigh(s, row, s + 16 >= s1, std::false_type());
+          if (__builtin_expect(nc == 1, 0))
+#pragma unroll 1
+            for (int s = s0; s < s1; s += 16) weigh(s, row + PANEL, false, std::true_type());
           fence_proxy_async_smem();
           warp_arrive(&bars[PREADY + (c & 1)], lane);
         }
@@ -483,11 +496,11 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
     const int wg = (warp - 4) >> 2;
     const int z = ((warp & 3) << 5) + lane;
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    if (!kState && p.seg < p.T) launch_wait();          // the entry states
+    if (!kState && unit[6]) launch_wait();              // the entry states
     float2 s[D / 4];                                    // columns D / 2 wg + 2 e, + 1 of row z
     {
       bool skip;
-      const bool split = p.seg < p.T;
+      const bool split = unit[6];
       const float* src = kState ? nullptr : split ? q.entry + ((size_t)unit[4] * p.H + h) * D * D
                                          : la_entry(p, q, unit[3], h, D, skip);
       if (!src) {
@@ -713,6 +726,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   __syncthreads();
   tc_fence_after();
   if (warp == 1) {
+    if (!kState) launch_wait();                       // no launch ends before the ones ahead of it
     tmem_relinquish();
     tmem_dealloc(tm, 512);
     if (lane == 0 && *cx && p.status) {

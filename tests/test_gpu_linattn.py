@@ -76,6 +76,24 @@ def test_dense_forward_and_backward(B, T, H, HK, dtype, D):
     assert err(g["d_initial_state"], rg["d_initial_state"]) <= STATE
 
 
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("B,T,H,HK", [(1, 1, 1, 1), (5, 1, 1, 1), (2, 5, 2, 1), (1, 33, 4, 2), (1, 64, 1, 1)])
+def test_a_single_chunk_is_rounded_once(B, T, H, HK, D):
+    """Up to 64 BF16 tokens with no state: every output is a sum kept in FP32 and rounded to BF16
+    once.  Each element is within half a unit in its last place (8 significant bits: 2^(e - 8)
+    for a value in [2^e, 2^(e+1))), and 1e-5 of the largest for the sums and for products of 16 bits."""
+    x = inputs(B, T, H, HK, D, BF16, seed=900 + T + D, s0=False)
+
+    def once(got, ref):
+        half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 8)
+        return (np.abs(f64(got) - ref) <= half + 1e-5 * np.abs(ref).max()).all()
+    assert once(run_fwd(x)[0], ref_fwd(x)[0])
+    g = _sf().sf_linattn_chunk_bwd(x["q"], x["k"], x["v"], x["decay"], None, x["do"])
+    rg = ref_bwd(x, df=False)
+    for n in ("dq", "dk", "dv"):
+        assert once(g[n], rg[n]), n
+
+
 @pytest.mark.parametrize("dtype,D,H,HK", [(BF16, 128, 4, 2), (BF16, 64, 3, 1), (F32, 64, 2, 2), (F32, 128, 2, 1)])
 def test_packed_sequences(dtype, D, H, HK):
     """Ragged lengths with empty and one-token sequences; rows past the last sequence hold NaN

@@ -240,6 +240,8 @@ def _token_stride(name, t):
     """Elements between consecutive tokens of [B,T,heads,D]: a token's heads are contiguous,
     and the batch rows follow one another at the same stride."""
     B, T, h, D = t.shape
+    if t.is_contiguous():
+        return h * D
     sb, st, sh, sd = t.stride()
     if t.numel() == 0:
         return h * D
@@ -252,6 +254,17 @@ def _token_stride(name, t):
     return st
 
 
+@functools.lru_cache(maxsize=256)
+def _qk_shape_of(rows, H, HK, D, dtype, norm, eps, interleaved, q_stride, k_stride, half, P, sections):
+    """The shape struct of these sizes (the library only reads it), and a reference to it."""
+    if len(sections) > 4:
+        raise ValueError("at most 4 position axes")
+    s = sf_qk_shape(rows, H, HK, D, _dtype_code(dtype), _NORMS[norm], float(eps), 2 * half,
+                    int(bool(interleaved)), P, len(sections), (ctypes.c_int * 4)(*map(int, sections)),
+                    q_stride, k_stride)
+    return s, ctypes.byref(s)
+
+
 def _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps, interleaved):
     if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
         raise ValueError("q must be [B,T,H,D] and k [B,T,HK,D]")
@@ -262,27 +275,24 @@ def _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps,
     if not q.is_cuda or not k.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
     B, T, H, D = q.shape
-    s = sf_qk_shape(B * T, H, k.shape[2], D, _dtype_code(q.dtype), _NORMS[norm], float(eps), 0,
-                    int(bool(interleaved)), 0, 0, (ctypes.c_int * 4)(),
-                    _token_stride("q", q), _token_stride("k", k))
-    args = [q.data_ptr(), k.data_ptr(), _addr("q_weight", q_weight, (D,), _F32),
-            _addr("k_weight", k_weight, (D,), _F32), None, None]
-    if cos_sin is not None:
+    table = at = None
+    P = half = 0
+    if cos_sin is None:
+        sections = ()
+    else:
         if cos_sin.dim() != 3 or cos_sin.shape[2] != 2:
             raise ValueError("cos_sin must be [table_rows, rotary_dim / 2, 2] FP32")
         P, half, _ = cos_sin.shape
         sections = (half,) if sections is None else tuple(sections)
-        if len(sections) > 4:
-            raise ValueError("at most 4 position axes")
-        positions = _need("positions", positions)
-        if positions.dim() == 1 or tuple(positions.shape) == (B, T):   # one axis
-            positions = positions.reshape(1, -1)
-        s.rotary_dim, s.table_rows, s.axes = 2 * half, P, len(sections)
-        for a, n in enumerate(sections):
-            s.sections[a] = int(n)
-        args[4] = _addr("cos_sin", cos_sin, (P, half, 2), _F32)
-        args[5] = _addr("positions", positions, (len(sections), B * T), torch.int32)
-    return s, args
+        shape = _need("positions", positions).shape
+        if len(sections) != 1 or (shape != (B * T,) and shape != (B, T)):
+            shape = (len(sections), B * T)
+        table = _addr("cos_sin", cos_sin, (P, half, 2), _F32)
+        at = _addr("positions", positions, shape, torch.int32)
+    s = _qk_shape_of(B * T, H, k.shape[2], D, q.dtype, norm, eps, interleaved, _token_stride("q", q),
+                     _token_stride("k", k), half, P, sections)[1]
+    return s, (q.data_ptr(), k.data_ptr(), _addr("q_weight", q_weight, (D,), _F32),
+               _addr("k_weight", k_weight, (D,), _F32), table, at)
 
 
 def sf_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos_sin=None, positions=None,
@@ -294,14 +304,14 @@ def sf_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos_sin=None, positi
     axis.  q and k may be slices of one fused projection.  Returns (q_out, k_out)."""
     s, args = _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps, interleaved)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _addr("q_out", q_out, q.shape, q.dtype)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         _addr("k_out", k_out, k.shape, k.dtype)
-    _check(load().sf_qk_norm_rope_fwd(ctypes.byref(s), *args, q_out.data_ptr(), k_out.data_ptr(),
+    _check(load().sf_qk_norm_rope_fwd(s, *args, q_out.data_ptr(), k_out.data_ptr(),
                                       _stream(stream, q.device)))
     return q_out, k_out
 
@@ -322,16 +332,15 @@ def sf_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, d_q_out, d
     lib, D, dev = load(), q.shape[3], q.device
     if grads is None:
         w = torch.empty(2, D, dtype=_F32, device=dev).unbind() if want_weight_grads else (None, None)
-        grads = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev),
-                     dk=torch.empty(k.shape, dtype=k.dtype, device=dev), dq_weight=w[0],
-                     dk_weight=w[1])
+        grads = dict(dq=torch.empty_like(q, memory_format=torch.contiguous_format),
+                     dk=torch.empty_like(k, memory_format=torch.contiguous_format),
+                     dq_weight=w[0], dk_weight=w[1])
     dqw, dkw = grads.get("dq_weight"), grads.get("dk_weight")
     if ws is None and (dqw is not None or dkw is not None):
-        ws = torch.empty(lib.sf_qk_norm_rope_bwd_workspace(ctypes.byref(s)), dtype=torch.uint8,
-                         device=dev)
+        ws = torch.empty(lib.sf_qk_norm_rope_bwd_workspace(s), dtype=torch.uint8, device=dev)
     ws = _ws(ws) if ws is not None else None
     _check(lib.sf_qk_norm_rope_bwd(
-        ctypes.byref(s), *args, _addr("d_q_out", d_q_out, q.shape, q.dtype),
+        s, *args, _addr("d_q_out", d_q_out, q.shape, q.dtype),
         _addr("d_k_out", d_k_out, k.shape, k.dtype), _addr("dq", grads["dq"], q.shape, q.dtype),
         _addr("dk", grads["dk"], k.shape, k.dtype), _addr("dq_weight", dqw, (D,), _F32),
         _addr("dk_weight", dkw, (D,), _F32), None if ws is None else ws.data_ptr(),

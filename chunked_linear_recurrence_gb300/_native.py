@@ -62,6 +62,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load the library (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -428,9 +428,7 @@ sf_status sf_gdn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const void*
   if (e != cudaSuccess) return cuda_fail(e, fn);
   if (lay.gqa) {
     const int64_t rows = (int64_t)shape->B * shape->T;
-    e = sfg::launch_group_sum(gq, dq, bf16, rows, shape->H, p.HK, D, cu_seqlens, shape->N, cs);
-    if (e == cudaSuccess)
-      e = sfg::launch_group_sum(gk, dk, bf16, rows, shape->H, p.HK, D, cu_seqlens, shape->N, cs);
+    e = sfg::launch_group_sum(gq, gk, dq, dk, bf16, rows, shape->H, p.HK, D, cu_seqlens, shape->N, cs);
     if (e != cudaSuccess) return cuda_fail(e, fn);
   }
   return SF_OK;

@@ -5,7 +5,8 @@
 // gradient of a shared query or key head is the sum of what its block of H / HK value
 // heads pushes back into it.  The gradient kernels leave those per-value-head parts in
 // FP32 [rows, H, D]; this kernel adds each block in a fixed order (the result does not
-// depend on scheduling) and writes [rows, HK, D] in the q/k dtype, active rows only.
+// depend on scheduling) and writes [rows, HK, D] in the q/k dtype, active rows only; the
+// query's and the key's gradients in one launch.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -15,10 +16,14 @@ namespace sfg {
 namespace {
 
 template <typename Tout>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict__ acc,
-                                                        Tout* __restrict__ out, int64_t rows,
+__global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict__ acc_q,
+                                                        const float* __restrict__ acc_k,
+                                                        Tout* __restrict__ out_q,
+                                                        Tout* __restrict__ out_k, int64_t rows,
                                                         int H, int HK, int D,
                                                         const int32_t* __restrict__ cu, int N) {
+  const float* acc = blockIdx.y ? acc_k : acc_q;
+  Tout* out = blockIdx.y ? out_k : out_q;
   // active rows: [0, cu[N]) for packed sequences (clamped into [0, rows]), else all
   int64_t active = rows;
   if (cu) {
@@ -49,19 +54,21 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict_
 
 }  // namespace
 
-cudaError_t launch_group_sum(const float* acc, void* out, bool bf16, int64_t rows, int H, int HK,
-                             int D, const int32_t* cu, int N, cudaStream_t st) {
+cudaError_t launch_group_sum(const float* acc_q, const float* acc_k, void* dq, void* dk, bool bf16,
+                             int64_t rows, int H, int HK, int D, const int32_t* cu, int N,
+                             cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   if (HK < 1 || H % HK || D % 4) return cudaErrorInvalidValue;
   const int64_t total = rows * HK * (D / 4);
   const int64_t want = (total + 255) / 256;
-  const unsigned grid = (unsigned)(want < 152 * 16 ? want : 152 * 16);
+  const dim3 grid((unsigned)(want < 152 * 16 ? want : 152 * 16), 2);
   if (bf16)
     group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
-        acc, reinterpret_cast<__nv_bfloat16*>(out), rows, H, HK, D, cu, N);
+        acc_q, acc_k, reinterpret_cast<__nv_bfloat16*>(dq), reinterpret_cast<__nv_bfloat16*>(dk),
+        rows, H, HK, D, cu, N);
   else
-    group_sum_kernel<float><<<grid, 256, 0, st>>>(acc, reinterpret_cast<float*>(out), rows, H, HK,
-                                                  D, cu, N);
+    group_sum_kernel<float><<<grid, 256, 0, st>>>(acc_q, acc_k, reinterpret_cast<float*>(dq),
+                                                  reinterpret_cast<float*>(dk), rows, H, HK, D, cu, N);
   return cudaGetLastError();
 }
 

@@ -89,8 +89,8 @@ struct Cost {
 constexpr Cost kTc128 = {kSms, 4.5, 1.55, 1.35, 0.92, 0.80, 4};
 constexpr Cost kTc64 = {kSms, 4.5, 1.20, 1.10, 0.70, 0.65, 4};
 // The CUDA-core kernel (one CTA an SM at D = 128, two at 64).
-constexpr Cost kSimt128 = {kSms, 4.0, 17.0, 17.0, 6.0, 6.0, 2};
-constexpr Cost kSimt64 = {2 * kSms, 4.0, 12.0, 9.0, 5.0, 4.0, 2};
+constexpr Cost kSimt128 = {kSms, 4.0, 17.0, 17.0, 6.0, 6.0, 1};
+constexpr Cost kSimt64 = {2 * kSms, 4.0, 12.0, 9.0, 5.0, 4.0, 1};
 
 double launch_time(const Cost& c, double ctas, double chunks, bool state) {
   const double busy = ctas < c.slots ? ctas / c.slots : 1.0;

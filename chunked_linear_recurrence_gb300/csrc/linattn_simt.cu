@@ -133,6 +133,10 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     copies_commit();
   };
   if (NB > 1 && nc > 0) fetch(0);
+  // A thread's four rows (and columns) of P and O lie in the chunk's four 16-row blocks, taken
+  // in walk order: row block i meets column blocks 0 .. i alone.
+  const int turn = q.reverse ? -16 : 16, first = q.reverse ? 48 : 0;
+  const int row0 = ty + first, col0 = tx + first;
   for (int ci = 0; ci < nc; ++ci) {
     const int64_t done = (int64_t)ci * C;
     const bool end = ci + 1 == nc;
@@ -152,31 +156,31 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     const auto& Y = sm.Y[ci % NB];
     const auto& Z = sm.Z[ci % NB];
     if (!kState) {
-      // P rows 4 ty + i, columns tx + 16 j
+      // P rows row0 + turn i, columns col0 + turn j
       float acc[4][4] = {};
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
         float4 xv[4], yv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xv[i] = ld4(&X[4 * ty + i][c]);
+        for (int i = 0; i < 4; ++i) xv[i] = ld4(&X[row0 + turn * i][c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) yv[j] = ld4(&Y[tx + 16 * j][c]);
+        for (int j = 0; j < 4; ++j) yv[j] = ld4(&Y[col0 + turn * j][c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j <= i; ++j)
             acc[i][j] = fmaf(xv[i].x, yv[j].x, fmaf(xv[i].y, yv[j].y,
                         fmaf(xv[i].z, yv[j].z, fmaf(xv[i].w, yv[j].w, acc[i][j]))));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * ty + i, c = tx + 16 * j, gap = q.reverse ? c - r : r - c;
+        for (int j = 0; j <= i; ++j) {
+          const int r = row0 + turn * i, c = col0 + turn * j, gap = q.reverse ? c - r : r - c;
           sm.P[r][c] = gap >= 0 ? acc[i][j] * (q.a * sm.tab[gap]) : 0.f;
         }
       __syncthreads();
-      // O rows 4 ty + i, columns 4 tx ..
+      // O rows row0 + turn i, columns 4 tx ..
       float4 o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
         for (int e = 0; e < 4; ++e) sv[e] = ld4(&sm.S[c + e][4 * tx]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 xv = ld4(&X[4 * ty + i][c]);
+          const float4 xv = ld4(&X[row0 + turn * i][c]);
           o[i].x = fmaf(xv.x, sv[0].x, fmaf(xv.y, sv[1].x, fmaf(xv.z, sv[2].x, fmaf(xv.w, sv[3].x, o[i].x))));
           o[i].y = fmaf(xv.x, sv[0].y, fmaf(xv.y, sv[1].y, fmaf(xv.z, sv[2].y, fmaf(xv.w, sv[3].y, o[i].y))));
           o[i].z = fmaf(xv.x, sv[0].z, fmaf(xv.y, sv[1].z, fmaf(xv.z, sv[2].z, fmaf(xv.w, sv[3].z, o[i].z))));
@@ -196,18 +200,21 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+        const int r = row0 + turn * i;
         const float f = r < L ? q.b * sm.tab[q.reverse ? L - 1 - r : r + 1] : 0.f;
         o[i].x *= f; o[i].y *= f; o[i].z *= f; o[i].w *= f;
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
 #pragma unroll 2
-      for (int c = 0; c < C; c += 4) {
+      for (int c4 = 0; c4 < 16; c4 += 4) {
+        const int c = col0 - tx + turn * j + c4;
         float4 zv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) zv[e] = ld4(&Z[c + e][4 * tx]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 pv = ld4(&sm.P[4 * ty + i][c]);
+        for (int i = j; i < 4; ++i) {
+          const float4 pv = ld4(&sm.P[row0 + turn * i][c]);
           o[i].x = fmaf(pv.x, zv[0].x, fmaf(pv.y, zv[1].x, fmaf(pv.z, zv[2].x, fmaf(pv.w, zv[3].x, o[i].x))));
           o[i].y = fmaf(pv.x, zv[0].y, fmaf(pv.y, zv[1].y, fmaf(pv.z, zv[2].y, fmaf(pv.w, zv[3].y, o[i].y))));
           o[i].z = fmaf(pv.x, zv[0].z, fmaf(pv.y, zv[1].z, fmaf(pv.z, zv[2].z, fmaf(pv.w, zv[3].z, o[i].z))));
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+        const int r = row0 + turn * i;
         if (r >= L) continue;
         const size_t at = ((size_t)(r0 + r) * p.H + h) * D + zc + 4 * tx;
         st4(static_cast<float*>(q.out) + at, o[i]);

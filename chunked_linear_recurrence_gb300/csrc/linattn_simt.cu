@@ -12,6 +12,7 @@
 // Bound by the FP32 rate: about 5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, two
 // thirds of it in S and O, against 2 KB of tokens.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "linattn.cuh"
 
 namespace sfg {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     const auto& Z = sm.Z[ci % NB];
     if (!kState) {
       // P rows row0 + turn i, columns col0 + turn j
-      float acc[4][4] = {};
+      float2 acc[4][4] = {};                      // sums over even and odd c
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
         float4 xv[4], yv[4];
@@ -169,21 +170,23 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j <= i; ++j)
-            acc[i][j] = fmaf(xv[i].x, yv[j].x, fmaf(xv[i].y, yv[j].y,
-                        fmaf(xv[i].z, yv[j].z, fmaf(xv[i].w, yv[j].w, acc[i][j]))));
+            acc[i][j] = fma2(make_float2(xv[i].x, xv[i].y), make_float2(yv[j].x, yv[j].y),
+                             fma2(make_float2(xv[i].z, xv[i].w), make_float2(yv[j].z, yv[j].w), acc[i][j]));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j <= i; ++j) {
           const int r = row0 + turn * i, c = col0 + turn * j, gap = q.reverse ? c - r : r - c;
-          sm.P[r][c] = gap >= 0 ? acc[i][j] * (q.a * sm.tab[gap]) : 0.f;
+          sm.P[r][c] = gap >= 0 ? (acc[i][j].x + acc[i][j].y) * (q.a * sm.tab[gap]) : 0.f;
         }
       __syncthreads();
       // O rows row0 + turn i, columns 4 tx ..
-      float4 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      float2 o[4][2] = {};
+      auto add = [](float2 (&o)[2], float x, float4 v) {   // o += x v
+        o[0] = fma2(make_float2(x, x), make_float2(v.x, v.y), o[0]);
+        o[1] = fma2(make_float2(x, x), make_float2(v.z, v.w), o[1]);
+      };
 #pragma unroll 2
       for (int c = 0; c < D; c += 4) {
         float4 sv[4];
@@ -192,17 +195,18 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 xv = ld4(&X[row0 + turn * i][c]);
-          o[i].x = fmaf(xv.x, sv[0].x, fmaf(xv.y, sv[1].x, fmaf(xv.z, sv[2].x, fmaf(xv.w, sv[3].x, o[i].x))));
-          o[i].y = fmaf(xv.x, sv[0].y, fmaf(xv.y, sv[1].y, fmaf(xv.z, sv[2].y, fmaf(xv.w, sv[3].y, o[i].y))));
-          o[i].z = fmaf(xv.x, sv[0].z, fmaf(xv.y, sv[1].z, fmaf(xv.z, sv[2].z, fmaf(xv.w, sv[3].z, o[i].z))));
-          o[i].w = fmaf(xv.x, sv[0].w, fmaf(xv.y, sv[1].w, fmaf(xv.z, sv[2].w, fmaf(xv.w, sv[3].w, o[i].w))));
+          add(o[i], xv.x, sv[0]);
+          add(o[i], xv.y, sv[1]);
+          add(o[i], xv.z, sv[2]);
+          add(o[i], xv.w, sv[3]);
         }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = row0 + turn * i;
         const float f = r < L ? q.b * sm.tab[q.reverse ? L - 1 - r : r + 1] : 0.f;
-        o[i].x *= f; o[i].y *= f; o[i].z *= f; o[i].w *= f;
+        o[i][0] = mul2(o[i][0], make_float2(f, f));
+        o[i][1] = mul2(o[i][1], make_float2(f, f));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -215,10 +219,10 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
 #pragma unroll
         for (int i = j; i < 4; ++i) {
           const float4 pv = ld4(&sm.P[row0 + turn * i][c]);
-          o[i].x = fmaf(pv.x, zv[0].x, fmaf(pv.y, zv[1].x, fmaf(pv.z, zv[2].x, fmaf(pv.w, zv[3].x, o[i].x))));
-          o[i].y = fmaf(pv.x, zv[0].y, fmaf(pv.y, zv[1].y, fmaf(pv.z, zv[2].y, fmaf(pv.w, zv[3].y, o[i].y))));
-          o[i].z = fmaf(pv.x, zv[0].z, fmaf(pv.y, zv[1].z, fmaf(pv.z, zv[2].z, fmaf(pv.w, zv[3].z, o[i].z))));
-          o[i].w = fmaf(pv.x, zv[0].w, fmaf(pv.y, zv[1].w, fmaf(pv.z, zv[2].w, fmaf(pv.w, zv[3].w, o[i].w))));
+          add(o[i], pv.x, zv[0]);
+          add(o[i], pv.y, zv[1]);
+          add(o[i], pv.z, zv[2]);
+          add(o[i], pv.w, zv[3]);
         }
       }
 #pragma unroll
@@ -226,37 +230,32 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
         const int r = row0 + turn * i;
         if (r >= L) continue;
         const size_t at = ((size_t)(r0 + r) * p.H + h) * D + zc + 4 * tx;
-        st4(static_cast<float*>(q.out) + at, o[i]);
+        st4(static_cast<float*>(q.out) + at, make_float4(o[i][0].x, o[i][0].y, o[i][1].x, o[i][1].y));
       }
     }
     // S = lam^L S + c sum_r lam^f(r) y_r z_r
     const float hi = sm.carry[end ? 2 : 0], lo = sm.carry[end ? 3 : 1];
     const float* wr = sm.wr[end];
-    float4 acc[YR];
-#pragma unroll
-    for (int e = 0; e < YR; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float2 acc[YR / 2][4] = {};                   // rows 2 e, 2 e + 1 of the state, columns 4 tx + j
 #pragma unroll 4
     for (int r = 0; r < C; ++r) {                 // (rows past L are zero)
       const float wgt = wr[r];
-      float4 zv = ld4(&Z[r][4 * tx]);
-      zv.x *= wgt; zv.y *= wgt; zv.z *= wgt; zv.w *= wgt;
-      float yv[YR];
+      const float4 z4 = ld4(&Z[r][4 * tx]);
+      const float zv[4] = {z4.x * wgt, z4.y * wgt, z4.z * wgt, z4.w * wgt};
+      float2 yv[YR / 2];
 #pragma unroll
-      for (int e = 0; e < YR; e += 4) *reinterpret_cast<float4*>(&yv[e]) = ld4(&Y[r][ty * YR + e]);
+      for (int e = 0; e < YR / 2; e += 2) *reinterpret_cast<float4*>(&yv[e]) = ld4(&Y[r][ty * YR + 2 * e]);
 #pragma unroll
-      for (int e = 0; e < YR; ++e) {
-        acc[e].x = fmaf(yv[e], zv.x, acc[e].x);
-        acc[e].y = fmaf(yv[e], zv.y, acc[e].y);
-        acc[e].z = fmaf(yv[e], zv.z, acc[e].z);
-        acc[e].w = fmaf(yv[e], zv.w, acc[e].w);
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < YR / 2; ++e) acc[e][j] = fma2(yv[e], make_float2(zv[j], zv[j]), acc[e][j]);
     }
 #pragma unroll
     for (int e = 0; e < YR; ++e) {
-      s[e].x = fmaf(hi, s[e].x, fmaf(lo, s[e].x, acc[e].x));
-      s[e].y = fmaf(hi, s[e].y, fmaf(lo, s[e].y, acc[e].y));
-      s[e].z = fmaf(hi, s[e].z, fmaf(lo, s[e].z, acc[e].z));
-      s[e].w = fmaf(hi, s[e].w, fmaf(lo, s[e].w, acc[e].w));
+      s[e].x = fmaf(hi, s[e].x, fmaf(lo, s[e].x, e & 1 ? acc[e / 2][0].y : acc[e / 2][0].x));
+      s[e].y = fmaf(hi, s[e].y, fmaf(lo, s[e].y, e & 1 ? acc[e / 2][1].y : acc[e / 2][1].x));
+      s[e].z = fmaf(hi, s[e].z, fmaf(lo, s[e].z, e & 1 ? acc[e / 2][2].y : acc[e / 2][2].x));
+      s[e].w = fmaf(hi, s[e].w, fmaf(lo, s[e].w, e & 1 ? acc[e / 2][3].y : acc[e / 2][3].x));
     }
   }
   float* dst = kState ? q.sums + uoff : t.last ? la_exit(p, q, n, h, D) : nullptr;

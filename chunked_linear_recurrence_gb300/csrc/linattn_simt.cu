@@ -6,11 +6,16 @@
 //     O  = b lam^e diag (X S^T) + P Z  64 x 64, each thread 4 x 4
 //     S' = lam^L S + c (lam^f Y)^T Z   D x 64, each thread D/16 x 4, kept in registers
 // Every product reads one operand as rows that sixteen threads share (a broadcast) and the
-// other as consecutive float4 of the row that the sixteen divide among them.  The state is
-// copied to shared memory once a chunk for the second product.  lam^64 is formed in FP64 and carried as a sum of two floats, so that a state kept over
-// thousands of chunks does not drift by the rounding of one factor.
-// Bound by the FP32 rate: about 5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, two
-// thirds of it in S and O, against 2 KB of tokens.
+// other as consecutive float4 of the row that the sixteen divide among them.  P is computed
+// and used up to the diagonal's 16 x 16 blocks alone.  The state is copied to shared memory
+// once a chunk for the second product.  lam^64 is formed in FP64 and carried as a sum of two
+// floats, so that a state kept over thousands of chunks does not drift by the rounding of one
+// factor.
+// Bound by multiply-adds and the shared-memory loads that feed them (8 warps an SM, half of the
+// FP32 rate): about 3.5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, against 2 KB of
+// tokens.  Measured, FP32, 2 x 2048 tokens of 16 heads: D = 128 35 us of pieces' states and 212
+// us (87 us at the full FP32 rate), D = 64 24 us and 65 us; 200
+// tokens of 2 heads, where every chunk is a segment: 26 us (D = 64), 36 us (128).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "linattn.cuh"
@@ -85,6 +90,20 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   const float d = p.decay[h];
   const int nc = (int)((rows + C - 1) / C);
   const int tail = (int)(rows - (int64_t)(nc - 1) * C);
+  const int G_x = p.H / q.hx, G_y = p.H / q.hy, G_z = p.H / q.hz;
+  constexpr int NB = kStages<D>;
+  auto fetch = [&](int ci) {
+    const int64_t done = (int64_t)ci * C;
+    const int L = (int)(rows - done < C ? rows - done : C);
+    const int64_t r0 = q.reverse ? se - done - L : sb + done;
+    const int b = ci % NB;
+    if (!kState)
+      copy_rows<D>(&sm.X[b][0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
+    copy_rows<D>(&sm.Y[b][0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
+    copy_rows<ZT>(&sm.Z[b][0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
+    copies_commit();
+  };
+  if (nc > 0) fetch(0);
   auto pw = [&](int e) { return e <= 0 ? 1.f : expf(d * (float)e); };
   if (tid <= C) sm.tab[tid] = pw(tid);
   if (tid >= 128) {                               // weights of a full chunk's rows, and of the last's
@@ -101,39 +120,24 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   float4 s[YR];
   const size_t uoff = ((size_t)t.at * p.H + h) * D * D;
   const float* src = kState ? nullptr : split ? q.entry + uoff : s_in;
-  if (split && src) {
+  if (!src) {
+#pragma unroll
+    for (int e = 0; e < YR; ++e) s[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  } else if (q.s_t && !split) {
+#pragma unroll
+    for (int e = 0; e < YR; ++e) s[e] = ld4(src + (size_t)(ty * YR + e) * D + zc + 4 * tx);
+  } else {                                        // four y of one z at a time
+    const int zs = split ? 4 : D, ys = split ? D : 1;
 #pragma unroll
     for (int e = 0; e < YR; e += 4) {
-      const float* v = src + (size_t)(ty * YR + e) * D + 4 * (zc + 4 * tx);
-      const float4 c0 = ld4(v), c1 = ld4(v + 4), c2 = ld4(v + 8), c3 = ld4(v + 12);
+      const float* v = src + (ty * YR + e) * ys + (zc + 4 * tx) * zs;
+      const float4 c0 = ld4(v), c1 = ld4(v + zs), c2 = ld4(v + 2 * zs), c3 = ld4(v + 3 * zs);
       s[e] = make_float4(c0.x, c1.x, c2.x, c3.x);
       s[e + 1] = make_float4(c0.y, c1.y, c2.y, c3.y);
       s[e + 2] = make_float4(c0.z, c1.z, c2.z, c3.z);
       s[e + 3] = make_float4(c0.w, c1.w, c2.w, c3.w);
     }
-  } else
-#pragma unroll
-  for (int e = 0; e < YR; ++e) {
-    const int y = ty * YR + e, z = zc + 4 * tx;
-    if (!src) s[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    else if (q.s_t) s[e] = ld4(src + (size_t)y * D + z);
-    else s[e] = make_float4(src[(size_t)z * D + y], src[(size_t)(z + 1) * D + y],
-                            src[(size_t)(z + 2) * D + y], src[(size_t)(z + 3) * D + y]);
   }
-  const int G_x = p.H / q.hx, G_y = p.H / q.hy, G_z = p.H / q.hz;
-  constexpr int NB = kStages<D>;
-  auto fetch = [&](int ci) {
-    const int64_t done = (int64_t)ci * C;
-    const int L = (int)(rows - done < C ? rows - done : C);
-    const int64_t r0 = q.reverse ? se - done - L : sb + done;
-    const int b = ci % NB;
-    if (!kState)
-      copy_rows<D>(&sm.X[b][0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
-    copy_rows<D>(&sm.Y[b][0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
-    copy_rows<ZT>(&sm.Z[b][0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
-    copies_commit();
-  };
-  if (NB > 1 && nc > 0) fetch(0);
   // A thread's four rows (and columns) of P and O lie in the chunk's four 16-row blocks, taken
   // in walk order: row block i meets column blocks 0 .. i alone.
   const int turn = q.reverse ? -16 : 16, first = q.reverse ? 48 : 0;
@@ -144,8 +148,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     const int L = end ? tail : C;
     const int64_t r0 = q.reverse ? se - done - L : sb + done;
     __syncthreads();                              // the last chunk's readers; the tables
-    if (NB == 1) fetch(ci);
-    else if (!end) fetch(ci + 1);
+    if (NB == 1 ? ci > 0 : !end) fetch(NB == 1 ? ci : ci + 1);
     if (!kState) {
 #pragma unroll
       for (int e = 0; e < YR; ++e) st4(&sm.S[ty * YR + e][4 * tx], s[e]);
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     if (!kState) {
       // P rows row0 + turn i, columns col0 + turn j
       float2 acc[4][4] = {};                      // sums over even and odd c
-#pragma unroll 4
+#pragma unroll 8
       for (int c = 0; c < D; c += 4) {
         float4 xv[4], yv[4];
 #pragma unroll
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
         o[0] = fma2(make_float2(x, x), make_float2(v.x, v.y), o[0]);
         o[1] = fma2(make_float2(x, x), make_float2(v.z, v.w), o[1]);
       };
-#pragma unroll 2
+#pragma unroll 4
       for (int c = 0; c < D; c += 4) {
         float4 sv[4];
 #pragma unroll
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-#pragma unroll 2
+#pragma unroll 4
       for (int c4 = 0; c4 < 16; c4 += 4) {
         const int c = col0 - tx + turn * j + c4;
         float4 zv[4];
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     const float hi = sm.carry[end ? 2 : 0], lo = sm.carry[end ? 3 : 1];
     const float* wr = sm.wr[end];
     float2 acc[YR / 2][4] = {};                   // rows 2 e, 2 e + 1 of the state, columns 4 tx + j
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < C; ++r) {                 // (rows past L are zero)
       const float wgt = wr[r];
       const float4 z4 = ld4(&Z[r][4 * tx]);
@@ -260,28 +263,19 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   }
   float* dst = kState ? q.sums + uoff : t.last ? la_exit(p, q, n, h, D) : nullptr;
   if (!dst) return;
-  if (kState) {
+  if (q.s_t && !kState) {
 #pragma unroll
-    for (int e = 0; e < YR; e += 4) {
-      float* v = dst + (size_t)(ty * YR + e) * D + 4 * (zc + 4 * tx);
-      st4(v, make_float4(s[e].x, s[e + 1].x, s[e + 2].x, s[e + 3].x));
-      st4(v + 4, make_float4(s[e].y, s[e + 1].y, s[e + 2].y, s[e + 3].y));
-      st4(v + 8, make_float4(s[e].z, s[e + 1].z, s[e + 2].z, s[e + 3].z));
-      st4(v + 12, make_float4(s[e].w, s[e + 1].w, s[e + 2].w, s[e + 3].w));
-    }
+    for (int e = 0; e < YR; ++e) st4(dst + (size_t)(ty * YR + e) * D + zc + 4 * tx, s[e]);
     return;
   }
+  const int zs = kState ? 4 : D, ys = kState ? D : 1;
 #pragma unroll
-  for (int e = 0; e < YR; ++e) {
-    const int y = ty * YR + e, z = zc + 4 * tx;
-    if (q.s_t) {
-      st4(dst + (size_t)y * D + z, s[e]);
-    } else {
-      dst[(size_t)z * D + y] = s[e].x;
-      dst[(size_t)(z + 1) * D + y] = s[e].y;
-      dst[(size_t)(z + 2) * D + y] = s[e].z;
-      dst[(size_t)(z + 3) * D + y] = s[e].w;
-    }
+  for (int e = 0; e < YR; e += 4) {
+    float* v = dst + (ty * YR + e) * ys + (zc + 4 * tx) * zs;
+    st4(v, make_float4(s[e].x, s[e + 1].x, s[e + 2].x, s[e + 3].x));
+    st4(v + zs, make_float4(s[e].y, s[e + 1].y, s[e + 2].y, s[e + 3].y));
+    st4(v + 2 * zs, make_float4(s[e].z, s[e + 1].z, s[e + 2].z, s[e + 3].z));
+    st4(v + 3 * zs, make_float4(s[e].w, s[e + 1].w, s[e + 2].w, s[e + 3].w));
   }
 }
 

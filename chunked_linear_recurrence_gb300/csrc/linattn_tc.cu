@@ -2,31 +2,46 @@
 // head sizes D = 128 and 64.
 //
 // One CTA walks one (segment, head) in 64-row chunks.  Rows r, s of a chunk, the state S [z][y]:
-//     QK  = [Y; X] Y^T           M = 128, N = 64, K = 128   (rows 64-127: X Y^T)
+//     QK  = [Y; X] Y^T           M = 128, N = 64, K = D     (rows 64-127: X Y^T)
 //     P   = a QK o lam^|r-s|     BF16, by two warps, to shared memory
-//     E   = (lam^f c Z)^T Y      M = 128, N = 128, K = 64   three times (below)
-//     O1^T = S X^T               M = 128, N = 64,  K = 128  (S as BF16 in TMEM)
-//     O2^T = Z^T P^T             M = 128, N = 64,  K = 64
+//     E   = (lam^f c Z)^T Y      M = 128, N = D,  K = 64    three times (below)
+//     O1^T = S X^T               M = 128, N = 64, K = D     (S as BF16 in TMEM)
+//     O2^T = Z^T P^T             M = 128, N = 64, K = 64
 //     out = b lam^e O1 + O2,     S <- lam^L S + E           (FP32)
-// Everything is laid out as the TMA brings it: [rows][128] BF16 tiles of two swizzled 64-column
-// panels, read K-major or MN-major as each product needs.
+// Everything is laid out as the TMA brings it: [rows][D] BF16 tiles of swizzled 64-column panels,
+// read K-major or MN-major as each product needs.  (At D = 64 the products' M = 128 is half
+// empty; the warps of the empty lanes have no work.)
 //
-// The state stays in the registers of eight warps (64 floats a thread), not in TMEM: every
+// The state stays in the registers of eight warps (D / 2 floats a thread), not in TMEM: every
 // chunk's E is a product of its own, so E of the next chunks never waits for S, no FP32 state
 // is read and written back around the products, and the sum over the chunks is rounded in
 // FP32 to nearest.  E's left operand is exact enough to keep FP32 accuracy of the state: the
-// weighted rows are split into three BF16 summands (8 bits each, 24 together), each multiplied
-// with the exact Y.  A launch that returns no state takes two of them (16 bits): its state
-// only ever reaches BF16 results.
+// weighted rows are split into three BF16 summands (8 bits each, 24 together) in TMEM, each
+// multiplied with the exact Y.  A launch that returns no state takes two of them (16 bits): its
+// state only ever reaches BF16 results.  (The parts as an MN-major operand in shared memory
+// needed 48 KB of stores and loads a chunk more: slower.)  BF16 roundings: S before O1 and P
+// before O2 (the results are BF16), P to 16 bits in walks of one chunk.
 //
-// Warps: 0 loads (three chunks in flight), 1 issues, 2-3 form P, 4-11 hold the state and write
-// the results (two warpgroups: columns y 0-63 and 64-127 of the state, rows 0-31 and 32-63 of
-// the results), 12-15 split the weighted rows.  Per chunk the issuer queues QK, E, then O1 (once
-// the state is there), then O2 (once P is there): while the state warps turn E into the next
-// entry state, the tensor pipe works on the next chunk's QK and E.  Warps meet through
-// mbarriers alone; every wait is bounded, and a thread that gives up writes SF_ERR_TIMEOUT to
-// the status word and raises the CTA's abort flag; copies and products in flight land before
-// the CTA leaves.
+// Twenty warps: 0 loads (four stages) and issues E, in two halves of 32 rows so that the split
+// refills one under the other; 1 issues QK, O1 and O2; 2-3 form P; 4-11 hold the state (two
+// warpgroups: columns y of either half); 12-15 split the weighted rows; 16-19 write the
+// results, turned in shared memory into 16-byte stores.  A batch of products costs ~170 cycles
+// beyond the pipe's own time, so O1 and O2 go together, and the next chunk's QK goes while the
+// last results are read.  A launch that computes pieces' states alone has E only: warp 1 loads,
+// two buffers of E and of the parts, and warps 16-19 split every other chunk.
+// Products are issued behind elect.sync in warp-uniform code (a lane test costs 62 cycles a
+// product instead of 32-64), and the loops are kept from unrolling: the roles run at the speed
+// of instruction fetch.  Register shares of the five warpgroups: 56, 128, 128, 72, 96.
+//
+// Warps meet through mbarriers alone; every wait is bounded, and a thread that gives up writes
+// SF_ERR_TIMEOUT to the status word and raises the CTA's abort flag; copies and products in
+// flight land before the CTA leaves.
+//
+// Bound by the tensor pipe, active 91 % of a CTA's time at D = 128: QK 8 products of 48 cycles,
+// E 12 of 64, O1 8 of 32, O2 4 of 48, and four batches' starts, ~2400 of the ~2500 cycles a
+// chunk.  Measured, D = 128: 96 walks of 128 chunks 166 us (3.6 TB/s on 96 SMs), 256 walks of 32
+// chunks 106 us (5.4 TB/s), 4 x 4096 tokens of 16 heads 21 us of pieces' states (0.9 us a chunk)
+// and 51 us; D = 64: 96 walks of 128 chunks 130 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -78,10 +78,13 @@ sf_status check_encoder(const sf_gdn_shape* s, const char* fn) {
 //
 // The times are a model of the kernels in microseconds for a 64-row chunk: `t0` a CTA's start
 // and end, `walk` and `state` a chunk of the two launches with every SM busy, `walk1` and
-// `state1` the same with few CTAs (bound by the chunk's own chain of steps instead of memory).
-// `least`: chunks of the shortest piece.  Measured: tcgen05 kernel, 152 walks of 64 chunks 103 us,
-// 128 of 32 chunks 54 us, state-only 54 us for 54 chunks on every SM; CUDA-core kernel, head
-// size 64, 4 chunks 48 us and 22 us (state-only) with few CTAs.
+// `state1` the same with few CTAs (bound by the chunk's own chain of steps).  `least`: chunks of
+// the shortest piece.  The constants only have to order the cuts.  Measured, chunks of a segment
+// / of a piece, tcgen05 kernel at D = 128: 24 walks of 300 chunks 50/50 128 us (chosen), 60/60
+// 140, 43/43 173, whole 378; 64 walks of 64 chunks 32/16 79 us (chosen), 32/32 85, 16/16 103,
+// whole 94; 96 walks of 128 chunks whole 169 us (chosen), 64/64 228.  CUDA-core kernel: 32 walks
+// of 32 chunks at D = 128 16/8 245 us (chosen), 8/8 284, 16/16 276; at 64 4/4 95 us (chosen), 8/8
+// 110.
 struct Cost {
   double slots, t0, walk, walk1, state, state1;
   int least;

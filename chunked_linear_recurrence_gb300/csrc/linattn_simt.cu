@@ -12,10 +12,10 @@
 // floats, so that a state kept over thousands of chunks does not drift by the rounding of one
 // factor.
 // Bound by multiply-adds and the shared-memory loads that feed them (8 warps an SM, half of the
-// FP32 rate): about 3.5 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, against 2 KB of
-// tokens.  Measured, FP32, 2 x 2048 tokens of 16 heads: D = 128 35 us of pieces' states and 212
-// us (87 us at the full FP32 rate), D = 64 24 us and 65 us; 200
-// tokens of 2 heads, where every chunk is a segment: 26 us (D = 64), 36 us (128).
+// FP32 rate): about 1.9 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, against 2 KB of
+// tokens.  Measured, one CTA on every SM, a chunk: D = 128 12.4 us and 4.0 us (states alone), D =
+// 64 8.1 us and 2.7 us.  2 x 2048 tokens of 16 heads: 247 us (86 us at the full FP32 rate) and 93
+// us; 200 tokens of 2 heads, where every chunk is a segment: 32 us and 24 us.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "linattn.cuh"

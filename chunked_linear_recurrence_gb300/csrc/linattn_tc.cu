@@ -38,7 +38,7 @@
 // flight land before the CTA leaves.
 //
 // Bound by the tensor pipe, active 91 % of a CTA's time at D = 128: QK 8 products of 48 cycles,
-// E 12 of 64, O1 8 of 32, O2 4 of 48, and four batches' starts, ~2400 of the ~2500 cycles a
+// E 12 of 64, O1 8 of 32, O2 4 of 48, and four batches' starts: ~2280 of the ~2500 cycles a
 // chunk.  Measured, D = 128: 96 walks of 128 chunks 166 us (3.6 TB/s on 96 SMs), 256 walks of 32
 // chunks 106 us (5.4 TB/s), 4 x 4096 tokens of 16 heads 21 us of pieces' states (0.9 us a chunk)
 // and 51 us; D = 64: 96 walks of 128 chunks 130 us.

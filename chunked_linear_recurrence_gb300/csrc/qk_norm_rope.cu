@@ -15,7 +15,11 @@
 // keys, not both (the grid is shared in proportion), so it keeps one weight and one gradient of
 // it.  Arithmetic goes two elements an instruction.  The weights' gradients are summed per lane
 // over everything a CTA takes, then over its lanes, then (a second kernel) over the CTAs, each
-// in a fixed order.
+// in a fixed order.  Everything is FP32 until the results are rounded to the tokens' type.
+// Measured, BF16, D = 128: forward of 32769 tokens of 16 + 16 heads with three axes 88.7 us (92 %
+// of the copy rate; one head at a time 109 us, eight 112-117), backward of 16384 tokens of 16 + 16
+// heads 70.0 us and 3.3 us for the weights (87 %; one head at a time 96 us, three 101-106).  Two
+// CTAs of 256 threads an SM instead of four of 128 are level in the forward (88.8 us).
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -11,7 +11,10 @@
 // the rows of a state are independent, so a CTA takes 64 of them: even one sequence of 16
 // heads gives 32 CTAs at K = 128.  Sums over a row's lanes are
 // butterflies that halve the number of values with every exchange (9 shuffles for 8 rows
-// instead of 40).
+// instead of 40).  Outputs are rounded once, to the token type; the state stays FP32.
+// Measured, BF16, K = 128: 256 sequences of 16 heads 82 us, 6.5 TB/s (537 MB; 96 % of the copy
+// rate), the delta rule on 128 of 32 heads the same; one sequence of 16 heads 2.8 us, the
+// latency of a launch.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

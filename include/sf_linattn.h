@@ -34,11 +34,15 @@ extern "C" {
  *                  is given.
  * An empty sequence hands its initial state through.  Rows past cu_seqlens[N]
  * are never written, and nothing in them (NaN, infinities) reaches a result.
+ * A NaN or infinity inside a sequence reaches that head's results from the
+ * start of its block of 64 tokens on (the products run over whole blocks; in the
+ * backward also down to the block's end), never another sequence or head.
  *
  * FP32 outputs and states carry FP32 accuracy.  With BF16 tokens, out is
  * rounded once from FP32 sums whose operands (the masked products of q and k,
- * and the state as the query reads it) are rounded to BF16; the state itself is
- * carried and returned with FP32 accuracy.
+ * and the state as the query reads it) are rounded to BF16 (the products to 16
+ * bits in sequences of up to 64 tokens); the state itself is carried and
+ * returned with FP32 accuracy.
  * ---------------------------------------------------------------------- */
 size_t sf_linattn_fwd_workspace(const sf_gdn_shape *shape, int packed);
 sf_status sf_linattn_chunk_fwd(const sf_gdn_shape *shape, const void *q, const void *k,

@@ -139,6 +139,32 @@ def test_a_long_walk_is_cut_into_segments(dtype, D):
         assert err(g["d_initial_state"], rg["d_initial_state"]) <= STATE
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_one_long_sequence_among_many_walks(dtype, D):
+    """More walks than SMs and one far above the even share: it alone is cut, the others (one of
+    them empty) read and write the caller's states next to it; also in place on a pool."""
+    lengths = [77, 1601, 0, 64, 1, 300]
+    x = inputs(1, sum(lengths) + 3, 32, 8, D, dtype, seed=77, lengths=lengths)
+    rows = np.arange(sum(lengths))
+    ro, rf = ref_fwd(x)
+    out, fin = run_fwd(x)
+    assert err(out, ro, rows) <= TOL[dtype]
+    for n in range(len(lengths)):
+        assert err(fin[n], rf[n]) <= STATE, n
+    cache = torch.full((8, 32, D, D), float("nan"), device="cuda")
+    idx = torch.tensor([3, 1, 7, 2, 6, 4], dtype=torch.int32, device="cuda")
+    cache[idx.long()] = x["s0"]
+    paged = _sf().sf_linattn_paged_chunk_fwd(x["q"], x["k"], x["v"], x["decay"], cache, idx, cu_seqlens=x["cu"])
+    assert torch.equal(paged[:, :len(rows)], out[:, :len(rows)]) and torch.equal(cache[idx.long()], fin)
+    rg = ref_bwd(x)
+    g = _sf().sf_linattn_chunk_bwd(x["q"], x["k"], x["v"], x["decay"], x["s0"], x["do"], x["df"],
+                                   cu_seqlens=x["cu"])
+    for n in ("dq", "dk", "dv"):
+        assert err(g[n], rg[n], rows) <= TOL[dtype], n
+    for n in range(len(lengths)):
+        assert err(g["d_initial_state"][n], rg["d_initial_state"][n]) <= STATE, n
+
+
 @pytest.mark.parametrize("dtype,D", [(BF16, 128), (F32, 64)])
 def test_decays_at_their_ends(dtype, D):
     """No decay, hardly any, one that underflows within a chunk, and no memory at all."""

@@ -166,3 +166,34 @@ def test_token_strides_of_a_fused_projection():
     for bad in (q.transpose(1, 2), q[:, ::2], q[..., ::2], q[:, :4]):
         with pytest.raises(ValueError):
             _token_stride("q", bad)
+
+
+_NO_ENCODER_SCRIPT = r'''
+import ctypes, sys
+sys.path.insert(0, sys.argv[1])
+from chunked_linear_recurrence_gb300 import _native
+lib = _native.load()
+F, big, r = ctypes.c_void_p(1 << 20), 1 << 40, []
+for D in (64, 128):
+    s = ctypes.byref(_native.sf_gdn_shape(B=1, T=64, H=1, K=D, V=D, N=1, dtype=1, scale=0.0, HK=0))
+    r.append((lib.sf_linattn_chunk_fwd(s, F, F, F, F, None, None, 0, F, None, F, big, None), lib.sf_last_error()))
+    r.append((lib.sf_linattn_paged_chunk_fwd(s, F, F, F, F, F, 4, F, None, None, F, F, big, None),
+              lib.sf_last_error()))
+    r.append((lib.sf_linattn_chunk_bwd(s, F, F, F, F, None, None, F, None, F, F, F, None, F, big, None),
+              lib.sf_last_error()))
+print(repr(r))
+'''
+
+
+def test_bf16_without_tensor_map_encoder_is_unsupported(lib):
+    """BF16 linear attention runs on the tensor-core kernel alone: with the driver's TMA descriptor
+    encoder reported absent (in a child process) its entry points refuse and launch nothing."""
+    import ast
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", _NO_ENCODER_SCRIPT, root], capture_output=True, text=True,
+                         env=dict(os.environ, SF_GDN_DISABLE_TMA_ENCODER="1"), timeout=300)
+    assert res.returncode == 0, res.stderr
+    for status, msg in ast.literal_eval(res.stdout.strip().splitlines()[-1]):
+        assert status == 2 and b"cuTensorMapEncodeTiled" in msg, (status, msg)

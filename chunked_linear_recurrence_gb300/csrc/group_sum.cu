@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "linattn.cuh"
 #include "simt_chunk.cuh"
 
 namespace sfg {
@@ -22,6 +23,7 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict_
                                                         Tout* __restrict__ out_k, int64_t rows,
                                                         int H, int HK, int D,
                                                         const int32_t* __restrict__ cu, int N) {
+  launch_wait();                                  // the parts
   const float* acc = blockIdx.y ? acc_k : acc_q;
   Tout* out = blockIdx.y ? out_k : out_q;
   // active rows: [0, cu[N]) for packed sequences (clamped into [0, rows]), else all
@@ -56,20 +58,18 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict_
 
 cudaError_t launch_group_sum(const float* acc_q, const float* acc_k, void* dq, void* dk, bool bf16,
                              int64_t rows, int H, int HK, int D, const int32_t* cu, int N,
-                             cudaStream_t st) {
+                             cudaStream_t st, bool early) {
   if (rows <= 0) return cudaSuccess;
   if (HK < 1 || H % HK || D % 4) return cudaErrorInvalidValue;
   const int64_t total = rows * HK * (D / 4);
   const int64_t want = (total + 255) / 256;
   const dim3 grid((unsigned)(want < 152 * 16 ? want : 152 * 16), 2);
   if (bf16)
-    group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
-        acc_q, acc_k, reinterpret_cast<__nv_bfloat16*>(dq), reinterpret_cast<__nv_bfloat16*>(dk),
-        rows, H, HK, D, cu, N);
-  else
-    group_sum_kernel<float><<<grid, 256, 0, st>>>(acc_q, acc_k, reinterpret_cast<float*>(dq),
-                                                  reinterpret_cast<float*>(dk), rows, H, HK, D, cu, N);
-  return cudaGetLastError();
+    return launch_after(early, group_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, acc_q, acc_k,
+                        reinterpret_cast<__nv_bfloat16*>(dq), reinterpret_cast<__nv_bfloat16*>(dk), rows,
+                        H, HK, D, cu, N);
+  return launch_after(early, group_sum_kernel<float>, grid, 256, 0, st, acc_q, acc_k,
+                      reinterpret_cast<float*>(dq), reinterpret_cast<float*>(dk), rows, H, HK, D, cu, N);
 }
 
 }  // namespace sfg

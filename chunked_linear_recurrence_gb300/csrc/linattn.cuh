@@ -80,7 +80,7 @@ struct LaUnit {
 };
 
 __device__ __forceinline__ int la_segments(int64_t len, int seg) {
-  return len > seg ? (int)((len + seg - 1) / seg) : 1;
+  return len > seg ? (int)(((unsigned)len + (unsigned)seg - 1) / (unsigned)seg) : 1;   // (len < 2^31)
 }
 
 // Unit u of a launch; a warp calls it together.  False when the unit holds nothing.  Whole
@@ -268,10 +268,10 @@ inline cudaError_t allow_smem(K kern, size_t bytes) {
 // ends (its start needs none of that one's results), and waits for them (launch_wait) where it
 // does.  Only launches after a call's first do so: `early`.
 template <typename... P, typename... A>
-inline cudaError_t launch_after(bool early, void (*kern)(P...), unsigned grid, unsigned threads,
+inline cudaError_t launch_after(bool early, void (*kern)(P...), dim3 grid, unsigned threads,
                                 size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

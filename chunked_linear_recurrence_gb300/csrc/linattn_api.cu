@@ -396,7 +396,8 @@ sf_status sf_linattn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const v
   cudaError_t e = run_passes(p, l, ws, bf16, shape->K, cs);
   if (e == cudaSuccess && f32) {
     const int64_t rows = (int64_t)shape->B * shape->T;
-    e = sfg::launch_group_sum(gq, gk, dq, dk, bf16, rows, H, hk, shape->K, cu_seqlens, shape->N, cs);
+    e = sfg::launch_group_sum(gq, gk, dq, dk, bf16, rows, H, hk, shape->K, cu_seqlens, shape->N, cs,
+                              true);
   }
   return cuda_status(e, fn);
 }

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NZ = D / ZT, YR = D / 16;
-  if (kState) launch_next();
+  launch_next();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   int id = blockIdx.x;
   const int zt = id % NZ; id /= NZ;

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + M::BAR + 8 * NBAR);
   volatile uint32_t* cx = reinterpret_cast<uint32_t*>(sm + M::BAR + 8 * NBAR + 4);
-  if (kState) launch_next();
+  launch_next();
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   int id = blockIdx.x;

@@ -18,7 +18,8 @@
 // in a fixed order.  Everything is FP32 until the results are rounded to the tokens' type.
 // Measured, BF16, D = 128: forward of 32769 tokens of 16 + 16 heads with three axes 88.7 us (92 %
 // of the copy rate; one head at a time 109 us, eight 112-117), backward of 16384 tokens of 16 + 16
-// heads 70.0 us and 3.3 us for the weights (87 %; one head at a time 96 us, three 101-106).  Two
+// heads 70.0 us (87 %), 74.3 with the weights, whose launch waits for the first one's end (77.5 when
+// it started after it; one head at a time 96 us, three 101-106).  Two
 // CTAs of 256 threads an SM instead of four of 128 are level in the forward (88.8 us).
 #include <cuda_bf16.h>
 
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(NT) qk_fwd_kernel(const QkParams p) {
 
 template <typename T, int D, int VEC, int U>
 __global__ void __launch_bounds__(NT) qk_bwd_kernel(const QkParams p) {
+  launch_next();
   constexpr int LPR = D / (2 * VEC), GROUPS = NT / LPR, NP = VEC / 2;
   __shared__ float red[GROUPS][D];
   const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(1024) qk_weight_kernel(const float* part, int 
   const int col = (blockIdx.x % (D / 32)) * 32;
   const int lo = is_q ? 0 : q_blocks, hi = is_q ? q_blocks : blocks;
   float* dst = is_q ? dqw : dkw;
+  launch_wait();                                  // the partial sums
   if (!dst) return;
   float s = 0.f;
 #pragma unroll 4
@@ -384,14 +387,16 @@ cudaError_t fwd(QkParams p, cudaStream_t st) {
 template <typename T, int D, int VEC>
 cudaError_t bwd(QkParams p, float* dqw, float* dkw, cudaStream_t st) {
   unsigned blocks = 0;
+  cudaError_t e = cudaSuccess;
   if (p.rows > 0) {
     share<BWD_U>(p, NT / (D / (2 * VEC)), QK_PARTS, blocks);
     qk_bwd_kernel<T, D, VEC, BWD_U><<<blocks, NT, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    e = cudaGetLastError();
   }
-  if (dqw || dkw) qk_weight_kernel<<<2 * D / 32, 1024, 0, st>>>(p.part, p.q_blocks, (int)blocks, D, dqw, dkw);
-  return cudaGetLastError();
+  if (e == cudaSuccess && (dqw || dkw))
+    e = launch_after(p.rows > 0, qk_weight_kernel, 2 * D / 32, 1024, 0, st, (const float*)p.part, p.q_blocks,
+                     (int)blocks, D, dqw, dkw);
+  return e;
 }
 
 }  // namespace

@@ -80,9 +80,10 @@ cudaError_t launch_simt_bwd(const ChainParams& p, bool bf16, int D, int64_t slot
                             cudaStream_t st, bool chain_only = false);
 // Grouped heads: out[r, hk, c] = sum over j < H / HK of acc[r, hk (H / HK) + j, c] for the
 // active rows r (r < cu[N] when cu != NULL, else all B*T), in the q/k/v dtype; dq and dk.
+// `early`: the launch before lets this one start while it ends.
 cudaError_t launch_group_sum(const float* acc_q, const float* acc_k, void* dq, void* dk, bool bf16,
                              int64_t rows, int H, int HK, int D, const int32_t* cu, int N,
-                             cudaStream_t st);
+                             cudaStream_t st, bool early = false);
 // BF16 backward's reverse cotangent chain on the warp-level tensor cores
 // (bwd_chain_mma.cu): per-chunk factors into p.fac, then the chain (tape, ds0).
 size_t mma_bwd_fac_bytes(int D);

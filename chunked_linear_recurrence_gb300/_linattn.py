@@ -259,14 +259,15 @@ def _qk_shape_of(rows, H, HK, D, dtype, norm, eps, interleaved, q_stride, k_stri
     """The shape struct of these sizes (the library only reads it), and a reference to it."""
     if len(sections) > 4:
         raise ValueError("at most 4 position axes")
-    s = sf_qk_shape(rows, H, HK, D, _dtype_code(dtype), _NORMS[norm], float(eps), 2 * half,
-                    int(bool(interleaved)), P, len(sections), (ctypes.c_int * 4)(*map(int, sections)),
+    s = sf_qk_shape(rows, H, HK, D, _dtype_code(dtype), _NORMS[norm], eps, 2 * half,
+                    int(bool(interleaved)), P, len(sections), (ctypes.c_int * 4)(*sections),
                     q_stride, k_stride)
     return s, ctypes.byref(s)
 
 
 def _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps, interleaved):
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[1] != ks[1] or qs[3] != ks[3]:
         raise ValueError("q must be [B,T,H,D] and k [B,T,HK,D]")
     if q.dtype != k.dtype:
         raise ValueError("q and k must share one dtype")
@@ -274,7 +275,8 @@ def _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps,
         raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
     if not q.is_cuda or not k.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
-    B, T, H, D = q.shape
+    B, T, H, D = qs
+    HK = ks[2]
     table = at = None
     P = half = 0
     if cos_sin is None:
@@ -283,14 +285,15 @@ def _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps,
         if cos_sin.dim() != 3 or cos_sin.shape[2] != 2:
             raise ValueError("cos_sin must be [table_rows, rotary_dim / 2, 2] FP32")
         P, half, _ = cos_sin.shape
-        sections = (half,) if sections is None else tuple(sections)
+        sections = (half,) if sections is None else tuple(map(int, sections))
         shape = _need("positions", positions).shape
         if len(sections) != 1 or (shape != (B * T,) and shape != (B, T)):
             shape = (len(sections), B * T)
         table = _addr("cos_sin", cos_sin, (P, half, 2), _F32)
         at = _addr("positions", positions, shape, torch.int32)
-    s = _qk_shape_of(B * T, H, k.shape[2], D, q.dtype, norm, eps, interleaved, _token_stride("q", q),
-                     _token_stride("k", k), half, P, sections)[1]
+    s = _qk_shape_of(B * T, H, HK, D, q.dtype, norm, float(eps), interleaved,
+                     H * D if q.is_contiguous() else _token_stride("q", q),
+                     HK * D if k.is_contiguous() else _token_stride("k", k), half, P, sections)[1]
     return s, (q.data_ptr(), k.data_ptr(), _addr("q_weight", q_weight, (D,), _F32),
                _addr("k_weight", k_weight, (D,), _F32), table, at)
 

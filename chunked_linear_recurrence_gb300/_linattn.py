@@ -27,6 +27,17 @@ def _stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _at(name, t):
+    """Device address of a contiguous tensor."""
+    if t is None:
+        raise ValueError(f"{name} is needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must be on a CUDA device")
+    return t.data_ptr()
+
+
 def _addr(name, t, shape, dtype):
     """Device address of a contiguous tensor of this shape and type (None for None)."""
     if t is None:
@@ -48,17 +59,18 @@ def _need(name, t):
 
 def _tokens(q, k, v, decay, cu_seqlens):
     """Shape checks of a token stream: (B, T, H, HK, D, N)."""
-    if q.dim() != 4 or v.dim() != 4:
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q/k and v must be 4-D: [B,T,HK,K] and [B,T,H,V]")
-    B, T, HK, K = q.shape
-    H = v.shape[2]
-    if v.shape[0] != B or v.shape[1] != T:
-        raise ValueError(f"v {tuple(v.shape)} does not match q {tuple(q.shape)} in [B,T]")
-    if k is not None and k.shape != q.shape:
-        raise ValueError(f"k {tuple(k.shape)} must match q {tuple(q.shape)} in shape and dtype")
-    if v.dtype != q.dtype or (k is not None and k.dtype != q.dtype):
+    B, T, HK, K = qs
+    H = vs[2]
+    if vs[0] != B or vs[1] != T:
+        raise ValueError(f"v {tuple(vs)} does not match q {tuple(qs)} in [B,T]")
+    if k is not None and k.shape != qs:
+        raise ValueError(f"k {tuple(k.shape)} must match q {tuple(qs)} in shape and dtype")
+    if v.dtype != dt or (k is not None and k.dtype != dt):
         raise ValueError("q, k and v must share one dtype")
-    if decay is not None and tuple(decay.shape) != (H,):
+    if decay is not None and decay.shape != (H,):
         raise ValueError(f"decay must be [H] = {(H,)}, got {tuple(decay.shape)}")
     N = B
     if cu_seqlens is not None:
@@ -113,7 +125,7 @@ def sf_linattn_chunk_fwd(q, k, v, decay, initial_state=None, cu_seqlens=None, sc
     B, T, H, HK, K, N = dims
     shape = _shape(q, v, cu_seqlens, scale, dims)
     dt, st = q.dtype, (N, H, v.shape[3], K)
-    args = (_addr("q", q, q.shape, dt), _addr("k", k, q.shape, dt), _addr("v", v, v.shape, dt),
+    args = (_at("q", q), _at("k", k), _at("v", v),
             _addr("decay", decay, (H,), _F32), _addr("initial_state", initial_state, st, _F32),
             _addr("cu_seqlens", cu_seqlens, (N + 1,), torch.int32))
     if out is None:
@@ -150,7 +162,7 @@ def sf_linattn_paged_chunk_fwd(q, k, v, decay, state_cache, state_indices, cu_se
     if state_cache.dim() != 4:
         raise ValueError("state_cache must be [num_slots,H,V,K]")
     slots = state_cache.shape[0]
-    args = (_addr("q", q, q.shape, dt), _addr("k", k, q.shape, dt), _addr("v", v, v.shape, dt),
+    args = (_at("q", q), _at("k", k), _at("v", v),
             _addr("decay", decay, (H,), _F32),
             _addr("state_cache", state_cache, (slots, H, v.shape[3], K), _F32), slots,
             _addr("state_indices", state_indices, (N,), torch.int32),
@@ -176,7 +188,7 @@ def sf_linattn_chunk_bwd(q, k, v, decay, initial_state, d_out, d_final_state=Non
     B, T, H, HK, K, N = dims
     shape = _shape(q, v, cu_seqlens, scale, dims)
     dt, st = q.dtype, (N, H, v.shape[3], K)
-    args = (_addr("q", q, q.shape, dt), _addr("k", k, q.shape, dt), _addr("v", v, v.shape, dt),
+    args = (_at("q", q), _at("k", k), _at("v", v),
             _addr("decay", decay, (H,), _F32), _addr("initial_state", initial_state, st, _F32),
             _addr("cu_seqlens", cu_seqlens, (N + 1,), torch.int32),
             _addr("d_out", _need("d_out", d_out), v.shape, dt),
@@ -198,13 +210,14 @@ def sf_linattn_chunk_bwd(q, k, v, decay, initial_state, d_out, d_final_state=Non
 
 
 def _step_args(q, k, v, state_cache, state_indices, scale, out):
-    if q.dim() != 3 or v.dim() != 3 or state_cache.dim() != 4:
+    qs, vs, cs, dt = q.shape, v.shape, state_cache.shape, q.dtype
+    if len(qs) != 3 or len(vs) != 3 or len(cs) != 4:
         raise ValueError("q/k must be [N,HK,K], v [N,H,V] and state_cache [num_slots,H,V,K]")
-    N, HK, K = q.shape
-    H, V = v.shape[1], v.shape[2]
-    dt, slots = q.dtype, state_cache.shape[0]
+    N, HK, K = qs
+    _, H, V = vs
+    slots = cs[0]
     shape = _shape_of(1, 1, H, K, V, N, dt, scale, HK)[1]
-    head = (_addr("q", q, (N, HK, K), dt), _addr("k", k, (N, HK, K), dt), _addr("v", v, (N, H, V), dt))
+    head = (_at("q", q), _addr("k", k, qs, dt), _addr("v", v, (N, H, V), dt))
     if out is None:
         out = torch.empty_like(v)
         to = out.data_ptr()

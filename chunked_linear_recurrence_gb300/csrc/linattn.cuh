@@ -26,6 +26,24 @@
 
 namespace sfg {
 
+// Division of 0 <= n < 2^31 by a constant of the launch, d >= 1 (Granlund and Montgomery 1994): with
+// 2^(sh-1) < d <= 2^sh and mul = floor(2^32 (2^sh - d) / d) + 1, n / d = (n mul / 2^32 + n) / 2^sh.
+// A unit's place takes six divisions in a row before its first copy can start, and one by a
+// variable costs ~150 cycles.
+struct FastDiv {
+  uint32_t mul, sh;
+  static FastDiv of(uint32_t d) {
+    uint32_t sh = 0;
+    while ((1ull << sh) < d) ++sh;
+    return {(uint32_t)((((1ull << sh) - d) << 32) / d + 1), sh};
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> sh);
+  }
+#endif
+};
+
 struct LaPass {
   const void* x;
   const void* y;
@@ -53,6 +71,8 @@ struct LaParams {
   int num_slots;
   int B, T, H, N;
   int seg, pre;         // rows of a segment and of a piece, multiples of 64; pre divides seg
+  int per_seg, cuts;    // pieces of a segment; segments of a walk (not packed)
+  FastDiv by_pass, by_head, by_group, by_n, by_seg, by_pieces;   // npass, H, H / HK, N, seg, pieces of a walk
   int units, pre_units; // launched (sequence, segment) and (sequence, piece) units; packed: bounds
   int* status;
 };
@@ -79,8 +99,19 @@ struct LaUnit {
   bool last;            // the walk ends with it
 };
 
-__device__ __forceinline__ int la_segments(int64_t len, int seg) {
-  return len > seg ? (int)(((unsigned)len + (unsigned)seg - 1) / (unsigned)seg) : 1;   // (len < 2^31)
+__device__ __forceinline__ int la_segments(int64_t len, const LaParams& p) {
+  return len > p.seg ? p.by_seg((int)len + p.seg - 1) : 1;   // (fewer than 2^26 rows)
+}
+// A CTA's pass, head and unit.
+__device__ __forceinline__ void la_place(int id, const LaParams& p, int& pass, int& h, int& u) {
+  const int a = p.by_pass(id), b = p.by_head(a);
+  pass = id - a * p.npass;
+  h = a - b * p.H;
+  u = b;
+}
+// The head that value head h reads of a tensor with `heads` of them (H or HK).
+__device__ __forceinline__ int la_head(int h, int heads, const LaParams& p) {
+  return heads == p.H ? h : p.by_group(h);
 }
 
 // Unit u of a launch; a warp calls it together.  False when the unit holds nothing.  Whole
@@ -89,19 +120,17 @@ __device__ __forceinline__ int la_segments(int64_t len, int seg) {
 template <bool kPieces>
 __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
   const int64_t total = (int64_t)p.B * p.T;
-  const int k = p.seg / p.pre;
+  const int k = p.per_seg;
   if (!p.cu) {
-    const int S = la_segments(p.T, p.seg);
+    const int S = p.cuts;
     int w;
     if (kPieces) {
-      const int per = (S - 1) * k;
-      if (per == 0) return false;
-      t.n = u / per;
-      w = u % per;
+      t.n = p.by_pieces(u);
+      w = u - t.n * (S - 1) * k;
       t.at = u;
     } else {
-      w = u / p.N;
-      t.n = u % p.N;
+      w = p.by_n(u);
+      t.n = u - w * p.N;
       t.at = t.n * S + w;
       if (w >= S) return false;
     }
@@ -129,7 +158,7 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
     int S = 0;
     if (m < p.N) {
       span(m, b, e);
-      S = la_segments(e - b, p.seg);
+      S = la_segments(e - b, p);
     }
     const int cnt = S > 0 ? (kPieces ? (S - 1) * k : S - 1) : 0;
     int incl = cnt, slots = kPieces ? cnt : S;         // before the walk's last segment; stored
@@ -168,7 +197,7 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
       auto rem = [&](int m) {
         int64_t b, e;
         span(m, b, e);
-        return e - b - (int64_t)(la_segments(e - b, p.seg) - 1) * p.seg;
+        return e - b - (int64_t)(la_segments(e - b, p) - 1) * p.seg;
       };
 #pragma unroll 1
       for (int m0 = 0; m0 < p.N; m0 += 32) {
@@ -188,14 +217,14 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
       }
     }
     span(found, t.bos, t.eos);
-    const int S = la_segments(t.eos - t.bos, p.seg);
+    const int S = la_segments(t.eos - t.bos, p);
     w = S - 1;
     at = 0;                                            // segments of the sequences before it
 #pragma unroll 1
     for (int m = lane; m < found; m += 32) {
       int64_t b, e;
       span(m, b, e);
-      at += la_segments(e - b, p.seg);
+      at += la_segments(e - b, p);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) at += __shfl_xor_sync(0xffffffffu, at, o);

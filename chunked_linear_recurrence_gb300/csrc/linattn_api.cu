@@ -1,6 +1,7 @@
 // linattn_api.cu -- the C ABI of include/sf_linattn.h: argument checks, workspace layout and
 // dispatch.  No entry point allocates memory or synchronises the host.
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/sf_linattn.h"
 #include "api_internal.cuh"
@@ -178,6 +179,17 @@ cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, i
                        cudaStream_t cs) {
   p.seg = l.cut.seg;
   p.pre = l.cut.pre;
+  p.per_seg = p.seg / p.pre;
+  p.cuts = p.T > p.seg ? (p.T + p.seg - 1) / p.seg : 1;
+  int hk = p.H;
+  for (int i = 0; i < p.npass; ++i)
+    for (const int n : {p.pass[i].hx, p.pass[i].hy, p.pass[i].hz}) hk = n < hk ? n : hk;
+  p.by_pass = sfg::FastDiv::of(p.npass);
+  p.by_head = sfg::FastDiv::of(p.H);
+  p.by_group = sfg::FastDiv::of(p.H / hk);
+  p.by_n = sfg::FastDiv::of(p.N);
+  p.by_seg = sfg::FastDiv::of(p.seg);
+  p.by_pieces = sfg::FastDiv::of(p.cuts > 1 ? (p.cuts - 1) * p.per_seg : 1);
   p.units = (int)l.units;
   p.pre_units = (int)l.pre_units;
   p.status = reinterpret_cast<int*>(ws);

@@ -65,10 +65,9 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   constexpr int NZ = D / ZT, YR = D / 16;
   launch_next();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  int id = blockIdx.x;
-  const int zt = id % NZ; id /= NZ;
-  const int pi = id % p.npass; id /= p.npass;
-  const int h = id % p.H, u = id / p.H;
+  const int zt = blockIdx.x % NZ;
+  int pi, h, u;
+  la_place(blockIdx.x / NZ, p, pi, h, u);
   const LaPass& q = p.pass[pi];
   LaUnit t;
   if (!la_locate<kState>(u, p, t)) return;
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
   const float d = p.decay[h];
   const int nc = (int)((rows + C - 1) / C);
   const int tail = (int)(rows - (int64_t)(nc - 1) * C);
-  const int G_x = p.H / q.hx, G_y = p.H / q.hy, G_z = p.H / q.hz;
+  const int hx = la_head(h, q.hx, p), hy = la_head(h, q.hy, p), hz = la_head(h, q.hz, p);
   constexpr int NB = kStages<D>;
   auto fetch = [&](int ci) {
     const int64_t done = (int64_t)ci * C;
@@ -98,9 +97,9 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
     const int64_t r0 = q.reverse ? se - done - L : sb + done;
     const int b = ci % NB;
     if (!kState)
-      copy_rows<D>(&sm.X[b][0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, h / G_x, D, 0, tid);
-    copy_rows<D>(&sm.Y[b][0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, h / G_y, D, 0, tid);
-    copy_rows<ZT>(&sm.Z[b][0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, h / G_z, D, zc, tid);
+      copy_rows<D>(&sm.X[b][0][0], D + 4, static_cast<const float*>(q.x), r0, L, q.hx, hx, D, 0, tid);
+    copy_rows<D>(&sm.Y[b][0][0], D + 4, static_cast<const float*>(q.y), r0, L, q.hy, hy, D, 0, tid);
+    copy_rows<ZT>(&sm.Z[b][0][0], ZT + 4, static_cast<const float*>(q.z), r0, L, q.hz, hz, D, zc, tid);
     copies_commit();
   };
   if (nc > 0) fetch(0);
@@ -289,18 +288,16 @@ template <int D>
 __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   launch_next();
   const int tid = threadIdx.x;
-  int id = blockIdx.x;
   constexpr int PARTS = D * D / 1024, AHEAD = 8;
-  const int part = id % PARTS; id /= PARTS;
-  const int pi = id % p.npass; id /= p.npass;
-  const int h = id % p.H;
-  int n = id / p.H;                                    // packed: the n-th walk that is cut
+  const int part = blockIdx.x % PARTS;
+  int pi, h, n;                                        // packed: the n-th walk that is cut
+  la_place(blockIdx.x / PARTS, p, pi, h, n);
   const LaPass& q = p.pass[pi];
-  const int k = p.seg / p.pre;
+  const int k = p.per_seg;
   int64_t len = p.T;
   int u0, s0;
   if (!p.cu) {
-    const int S = la_segments(p.T, p.seg);
+    const int S = p.cuts;
     u0 = n * S;
     s0 = n * (S - 1) * k;
   } else {
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
       } else {
         n -= __popc(hit);
       }
-      if (lane < upto && m < p.N) sum += la_segments(e - b, p.seg);
+      if (lane < upto && m < p.N) sum += la_segments(e - b, p);
     }
     // Fewer walks are cut.  (Not even the launch before is waited for: a walk that is not cut
     // reads the caller's state, and where none is cut that launch does nothing.)
@@ -331,7 +328,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
     u0 = sum;
     s0 = (sum - n) * k;
   }
-  const int S = la_segments(len, p.seg), pieces = (S - 1) * k;
+  const int S = la_segments(len, p), pieces = (S - 1) * k;
   bool skip;
   const float* s_in = la_entry(p, q, n, h, D, skip);
   // padding; malformed offsets

@@ -148,9 +148,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   launch_next();
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  int id = blockIdx.x;
-  const int pi = id % p.npass; id /= p.npass;
-  const int h = id % p.H, u = id / p.H;
+  int pi, h, u;
+  la_place(blockIdx.x, p, pi, h, u);
   const LaPass& q = p.pass[pi];
   const bool rev = q.reverse != 0;
   constexpr int NE = kState ? 2 : 1;              // buffers of E and of the weighted rows
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   const int s0 = __shfl_sync(0xffffffffu, unit[1], 0), s1 = __shfl_sync(0xffffffffu, unit[2], 0);
   const int nc = (s1 - s0 + C - 1) / C;
   const int tail = s1 - s0 - (nc - 1) * C;        // rows of the walk's last chunk
-  const int hx = h / (p.H / q.hx), hy = h / (p.H / q.hy), hz = h / (p.H / q.hz);
+  const int hx = la_head(h, q.hx, p), hy = la_head(h, q.hy, p), hz = la_head(h, q.hz, p);
   int issued = 0;
   auto load = [&](int c) {
     const int b = c % NS, L = c + 1 == nc ? tail : C;

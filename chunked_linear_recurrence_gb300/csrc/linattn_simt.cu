@@ -14,8 +14,8 @@
 // Bound by multiply-adds and the shared-memory loads that feed them (8 warps an SM, half of the
 // FP32 rate): about 1.9 C D + 2 D^2 multiply-adds a row at C = 64, D = 128, against 2 KB of
 // tokens.  Measured, one CTA on every SM, a chunk: D = 128 12.4 us and 4.0 us (states alone), D =
-// 64 8.1 us and 2.7 us.  2 x 2048 tokens of 16 heads: 247 us (86 us at the full FP32 rate) and 93
-// us; 200 tokens of 2 heads, where every chunk is a segment: 32 us and 24 us.
+// 64 8.1 us and 2.7 us.  2 x 2048 tokens of 16 heads: 35 + 199 us (86 us at the full FP32 rate) and
+// 23 + 60 us; 200 tokens of 2 heads, where every chunk is a segment: 32 us and 24 us a call.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "linattn.cuh"

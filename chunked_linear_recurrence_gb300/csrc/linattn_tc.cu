@@ -39,9 +39,10 @@
 //
 // Bound by the tensor pipe, active 91 % of a CTA's time at D = 128: QK 8 products of 48 cycles,
 // E 12 of 64, O1 8 of 32, O2 4 of 48, and four batches' starts: ~2280 of the ~2500 cycles a
-// chunk.  Measured, D = 128: 96 walks of 128 chunks 166 us (3.6 TB/s on 96 SMs), 256 walks of 32
-// chunks 106 us (5.4 TB/s), 4 x 4096 tokens of 16 heads 21 us of pieces' states (0.9 us a chunk)
-// and 51 us; D = 64: 96 walks of 128 chunks 130 us.
+// chunk.  Measured, D = 128: 96 walks of 128 chunks 165 us (3.7 TB/s on 96 SMs), 256 walks of 32
+// chunks 106 us (5.4 TB/s), 4 x 4096 tokens of 16 heads 19 us of pieces' states and 49 us, one
+// prompt of 130 tokens 9 us; a chunk takes 1.2 us (0.58 us of a piece's states) with few CTAs, 1.5
+// (0.88) with one on every SM.  D = 64: 96 walks of 128 chunks 129 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

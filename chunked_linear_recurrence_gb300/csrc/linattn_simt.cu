@@ -280,15 +280,17 @@ __global__ void __launch_bounds__(256, D == 128 ? 1 : 2) la_simt_kernel(const La
 
 // Entry states of the segments of one (sequence, head, pass): e = the caller's state, then
 // e = lam^pre e + sum over the pieces, kept at every segment's start.  Each thread carries one
-// float4 of the state; the sums of eight pieces are in flight together, and sixteen CTAs share a
-// state at D = 128, so that a single walk does not wait for one SM's loads.  Bound by memory and by
-// two launches' latency: 4 us behind the pieces for 4 x 4096 tokens of 16 heads, 10 us for the 140
-// pieces (9 MB) of 131072 tokens of 4 heads.  Both kernels' walks use it.
-template <int D>
+// float4 of the state, and sixteen CTAs share a state at D = 128.  Bound by the latency of L2, which
+// the early copies of the launch behind it stretch to microseconds: AHEAD pieces' sums are in
+// flight together, 32 where the walks leave each CTA an SM, else 8, whose registers leave room for
+// more CTAs.  Measured, all three launches (8, 32 ahead): 4 walks of 35 pieces 156.6, 146.4 us, 6 of
+// 24 68.6, 62.5 us; 16 walks 82.9, 85.0 us, 64 walks of 2 pieces 76.8, 91.2 us.  (Loading a piece as
+// another is used: 37.8 -> 58.4 us for one walk of 127.)  Both kernels' walks use it.
+template <int D, int AHEAD>
 __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
   launch_next();
   const int tid = threadIdx.x;
-  constexpr int PARTS = D * D / 1024, AHEAD = 8;
+  constexpr int PARTS = D * D / 1024;
   const int part = blockIdx.x % PARTS;
   int pi, h, n;                                        // packed: the n-th walk that is cut
   la_place(blockIdx.x / PARTS, p, pi, h, n);
@@ -403,7 +405,12 @@ cudaError_t launch_la_carry(const LaParams& p, int D, cudaStream_t st) {
   const int64_t grid = (int64_t)walks * p.H * p.npass * (D * D / 1024);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_after(true, D == 64 ? la_carry_kernel<64> : la_carry_kernel<128>, (unsigned)grid, 256, 0, st, p);
+  // pieces of a walk (of packed ones that are cut: of an average one)
+  const int pieces = p.cu ? p.pre_units / walks : (p.cuts - 1) * p.per_seg;
+  const bool deep = pieces > 8 && grid <= 152;
+  auto kern = D == 64 ? (deep ? la_carry_kernel<64, 32> : la_carry_kernel<64, 8>)
+                      : (deep ? la_carry_kernel<128, 32> : la_carry_kernel<128, 8>);
+  return launch_after(true, kern, (unsigned)grid, 256, 0, st, p);
 }
 
 }  // namespace sfg

@@ -83,15 +83,15 @@ sf_status check_encoder(const sf_gdn_shape* s, const char* fn) {
 // the shortest piece.  The constants only have to order the cuts.  Measured, chunks of a segment
 // / of a piece, tcgen05 kernel at D = 128: 24 walks of 300 chunks 50/50 128 us (chosen), 60/60
 // 140, 43/43 173, whole 378; 64 walks of 64 chunks 32/16 79 us (chosen), 32/32 85, 16/16 103,
-// whole 94; 96 walks of 128 chunks whole 169 us (chosen), 64/64 228.  CUDA-core kernel: 32 walks
-// of 32 chunks at D = 128 16/8 245 us (chosen), 8/8 284, 16/16 276; at 64 4/4 95 us (chosen), 8/8
-// 110.
+// whole 94; 96 walks of 128 chunks whole 169 us (chosen), 64/64 228; 2 walks of 21 chunks 2/2
+// 19.5 us (chosen), 4/4 21.5, whole 38.9.  CUDA-core kernel: 32 walks of 32 chunks at D = 128 16/8
+// 245 us (chosen), 8/8 284, 16/16 276; at D = 64 4/4 95 us (chosen), 8/8 110.
 struct Cost {
   double slots, t0, walk, walk1, state, state1;
   int least;
 };
-constexpr Cost kTc128 = {kSms, 4.5, 1.55, 1.35, 0.92, 0.80, 4};
-constexpr Cost kTc64 = {kSms, 4.5, 1.20, 1.10, 0.70, 0.65, 4};
+constexpr Cost kTc128 = {kSms, 4.5, 1.55, 1.35, 0.92, 0.80, 2};
+constexpr Cost kTc64 = {kSms, 4.5, 1.20, 1.10, 0.70, 0.65, 2};
 // The CUDA-core kernel (one CTA an SM at D = 128, two at 64).
 constexpr Cost kSimt128 = {kSms, 4.0, 17.0, 17.0, 6.0, 6.0, 1};
 constexpr Cost kSimt64 = {2 * kSms, 4.0, 12.0, 9.0, 5.0, 4.0, 1};
@@ -122,11 +122,15 @@ Cut cut_walks(const sf_gdn_shape* s, bool packed, int npass) {
     // 266, 309, 508 us; 8 of 32 heads 415, 375, 383 us, with half of the tokens in one of them
     // 480, 390, 635 us.
     const double share = (double)chunks * s->H * lanes / c.slots;
-    const bool many = (double)s->N * s->H * lanes >= c.slots;
+    const double walks = (double)s->N * s->H * lanes;
+    const bool many = walks >= c.slots;
     const int k = many ? 3 : 1;
     int64_t seg = (int64_t)std::ceil(share * (many ? 1.2 : 1.1));
-    if (seg < 2 * c.least - 2) seg = 2 * c.least - 2;
-    if (seg < k * c.least) seg = k * c.least;
+    // Short segments only where few walks leave most SMs idle.  Measured, segments of at least 2,
+    // 3, 6 chunks: 700 tokens in 2 of 2 heads 17.4, 19.5, 23.6 us, in 5 of 4 23.6, 19.6, 21.5, in
+    // 5 of 16 27.6, 27.6, 23.6.
+    const int64_t least = !tc ? k : many ? 12 : walks > 32 ? 6 : walks > 16 ? 3 : 2;
+    if (seg < least) seg = least;
     seg = (seg + k - 1) / k * k;
     if (seg >= chunks) return whole;
     return {(int)seg * 64, (int)(seg / k) * 64};
@@ -141,7 +145,7 @@ Cut cut_walks(const sf_gdn_shape* s, bool packed, int npass) {
       if (seg / k < c.least || (S - 1) * seg >= chunks) continue;
       const double units = walks * S, pieces = walks * (S - 1) * k;
       const double t = launch_time(c, units, (double)seg, false) +
-                       launch_time(c, pieces, (double)(seg / k), true) + 5.0 +
+                       launch_time(c, pieces, (double)(seg / k), true) + 2.0 +
                        (units + pieces) * s->K * s->K * 4.0 / 5e6;
       if (t < best) {
         best = t;

@@ -347,10 +347,10 @@ def sf_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, d_q_out, d
     s, args = _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps, interleaved)
     lib, D, dev = load(), q.shape[3], q.device
     if grads is None:
-        w = torch.empty(2, D, dtype=_F32, device=dev).unbind() if want_weight_grads else (None, None)
         grads = dict(dq=torch.empty_like(q, memory_format=torch.contiguous_format),
                      dk=torch.empty_like(k, memory_format=torch.contiguous_format),
-                     dq_weight=w[0], dk_weight=w[1])
+                     dq_weight=torch.empty(D, dtype=_F32, device=dev) if want_weight_grads else None,
+                     dk_weight=torch.empty(D, dtype=_F32, device=dev) if want_weight_grads else None)
     dqw, dkw = grads.get("dq_weight"), grads.get("dk_weight")
     if ws is None and (dqw is not None or dkw is not None):
         ws = torch.empty(lib.sf_qk_norm_rope_bwd_workspace(s), dtype=torch.uint8, device=dev)

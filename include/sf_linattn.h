@@ -32,6 +32,7 @@ extern "C" {
  *   workspace      sf_linattn_fwd_workspace(shape, packed) bytes, its first 256
  *                  bytes zero before the first use; packed != 0 when cu_seqlens
  *                  is given.
+ * Outputs overlap no input and no workspace; final_state may be initial_state.
  * An empty sequence hands its initial state through.  Rows past cu_seqlens[N]
  * are never written, and nothing in them (NaN, infinities) reaches a result.
  * A NaN or infinity inside a sequence reaches that head's results from the
@@ -70,7 +71,8 @@ sf_status sf_linattn_paged_chunk_fwd(const sf_gdn_shape *shape, const void *q, c
  *   d_out [B,T,H,V]; d_final_state [N,H,V,K] or NULL (zeros); dq, dk [B,T,HK,K]
  *   (sums over each block of H / HK value heads), dv [B,T,H,V];
  *   d_initial_state [N,H,V,K] or NULL (not computed).  Inactive rows of the
- *   gradients are not written.  K == V, either 64 or 128, BF16 or FP32.
+ *   gradients are not written.  Outputs overlap no input.  K == V, either 64 or
+ *   128, BF16 or FP32.
  * ---------------------------------------------------------------------- */
 size_t sf_linattn_bwd_workspace(const sf_gdn_shape *shape, int packed);
 sf_status sf_linattn_chunk_bwd(const sf_gdn_shape *shape, const void *q, const void *k,

@@ -207,6 +207,19 @@ def test_scale_missing_states_and_missing_cotangent(dtype, D):
         assert err(g[n], rg[n]) <= TOL[dtype], n
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_final_state_in_place_of_the_initial_state(dtype, D):
+    """One walk, cut into segments, and packed ones of which one is not cut."""
+    for lengths in (None, [1900, 60, 0]):
+        x = inputs(1, 2000, 2, 1, D, dtype, seed=96, lengths=lengths)
+        end = 2000 if lengths is None else sum(lengths)
+        out, fin = run_fwd(x)
+        state = x["s0"].clone()
+        again, same = _sf().sf_linattn_chunk_fwd(x["q"], x["k"], x["v"], x["decay"], state, cu_seqlens=x["cu"],
+                                                 output_final_state=True, final_state=state)
+        assert same is state and torch.equal(state, fin) and torch.equal(again[:, :end], out[:, :end])
+
+
 def test_no_tokens_hand_the_state_through():
     for D, dtype in ((128, BF16), (64, F32)):
         x = inputs(2, 0, 2, 1, D, dtype, seed=1)

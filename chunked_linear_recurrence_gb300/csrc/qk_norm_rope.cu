@@ -164,6 +164,10 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// max(x, least), NaN where x is NaN (fmaxf would give `least`, and a head that holds a NaN finite
+// results).
+__device__ __forceinline__ float at_least(float x, float least) { return x < least ? least : x; }
+
 template <int VEC>
 __device__ __forceinline__ void load_weight(const float* w, const Lane& t, float2* x) {
 #pragma unroll
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(NT) qk_fwd_kernel(const QkParams p) {
 #pragma unroll
       for (int e = 1; e < VEC; ++e) q = fma2(x[e], x[e], q);
       const float ss = row_sum<LPR>(q.x + q.y);
-      const float r = p.l2 ? 1.f / fmaxf(sqrtf(ss), p.eps) : rsqrtf(ss * (1.f / D) + p.eps);
+      const float r = p.l2 ? 1.f / at_least(sqrtf(ss), p.eps) : rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[e] = mul2(x[e], mul2(wt[e], make_float2(r, r)));
       turn<VEC, false>(x, x + NP, t, p.inter, c, s);
@@ -302,8 +306,8 @@ __global__ void __launch_bounds__(NT) qk_bwd_kernel(const QkParams p) {
       float r, f;
       if (p.l2) {
         const float nrm = sqrtf(ss);
-        r = 1.f / fmaxf(nrm, p.eps);
-        f = nrm > p.eps ? r * r * gx : 0.f;
+        r = 1.f / at_least(nrm, p.eps);
+        f = nrm <= p.eps ? 0.f : r * r * gx;
       } else {
         r = rsqrtf(ss * (1.f / D) + p.eps);
         f = r * r * (1.f / D) * gx;

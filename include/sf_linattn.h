@@ -130,7 +130,8 @@ sf_status sf_gdn_step(const sf_gdn_shape *shape, const void *q, const void *k, c
  *                       clamped into it
  *   D 64 or 128; rotary_dim a multiple of 8, at most D (0: no rotation, then
  *   cos_sin, positions and sections are not used); 1 to 4 axes whose sections
- *   sum to rotary_dim / 2.  All arithmetic is FP32, rounded once.
+ *   sum to rotary_dim / 2.  All arithmetic is FP32, rounded once.  A NaN in a head
+ *   gives NaN in all of that head (both norms, forward and backward), no other.
  * ---------------------------------------------------------------------- */
 typedef enum { SF_NORM_RMS = 0, SF_NORM_L2 = 1 } sf_norm;
 

@@ -12,7 +12,7 @@ import functools
 
 import torch
 
-from ._native import _check, _dtype_code, load, sf_gdn_shape, sf_qk_shape, workspace
+from ._native import _check, _dtype_code, load, on_its_stream, sf_gdn_shape, sf_qk_shape, workspace
 
 _NORMS = {"rms": 0, "l2": 1}
 _F32 = torch.float32
@@ -114,6 +114,7 @@ def sf_linattn_bwd_workspace(q, v, cu_seqlens=None):
     return workspace(need, q.device)
 
 
+@on_its_stream
 def sf_linattn_chunk_fwd(q, k, v, decay, initial_state=None, cu_seqlens=None, scale=None,
                          output_final_state=False, out=None, final_state=None, ws=None,
                          stream=None):
@@ -149,6 +150,7 @@ def sf_linattn_chunk_fwd(q, k, v, decay, initial_state=None, cu_seqlens=None, sc
     return out, final_state
 
 
+@on_its_stream
 def sf_linattn_paged_chunk_fwd(q, k, v, decay, state_cache, state_indices, cu_seqlens=None,
                                has_initial_state=None, scale=None, out=None, ws=None, stream=None):
     """sf_linattn_chunk_fwd advancing state_cache [num_slots,H,V,K] in place at the slots
@@ -179,6 +181,7 @@ def sf_linattn_paged_chunk_fwd(q, k, v, decay, state_cache, state_indices, cu_se
     return out
 
 
+@on_its_stream
 def sf_linattn_chunk_bwd(q, k, v, decay, initial_state, d_out, d_final_state=None, cu_seqlens=None,
                          scale=None, want_d_initial_state=True, grads=None, ws=None, stream=None):
     """Backward of sf_linattn_chunk_fwd.  Returns dict dq, dk, dv, d_initial_state (the decay
@@ -229,6 +232,7 @@ def _step_args(q, k, v, state_cache, state_indices, scale, out):
     return shape, N, H, head, tail, out
 
 
+@on_its_stream
 def sf_linattn_step(q, k, v, decay, state_cache, state_indices=None, scale=None, out=None,
                     stream=None):
     """One token of every sequence: q, k [N,HK,K], v [N,H,V], decay [H]; advances state_cache
@@ -240,6 +244,7 @@ def sf_linattn_step(q, k, v, decay, state_cache, state_indices=None, scale=None,
     return out
 
 
+@on_its_stream
 def sf_gdn_step(q, k, v, gate, beta, state_cache, state_indices=None, scale=None, out=None,
                 stream=None):
     """sf_linattn_step for the gated delta rule: gate, beta [N,H] FP32."""
@@ -311,6 +316,7 @@ def _qk_shape(q, k, q_weight, k_weight, cos_sin, positions, sections, norm, eps,
                _addr("k_weight", k_weight, (D,), _F32), table, at)
 
 
+@on_its_stream
 def sf_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos_sin=None, positions=None,
                         sections=None, norm="rms", eps=1e-6, interleaved=False, q_out=None,
                         k_out=None, stream=None):
@@ -339,6 +345,7 @@ def sf_qk_norm_rope_bwd_workspace(q, k):
     return torch.empty(need, dtype=torch.uint8, device=q.device)
 
 
+@on_its_stream
 def sf_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, d_q_out, d_k_out,
                         sections=None, norm="rms", eps=1e-6, interleaved=False,
                         want_weight_grads=True, grads=None, ws=None, stream=None):

@@ -7,6 +7,8 @@ library is missing or fails to load, every call raises -- nothing falls back.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -149,6 +151,23 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def on_its_stream(fn):
+    """Makes a call that is given a ``stream`` run with that stream as the current one, so that
+    the buffers it makes for itself (a workspace, outputs) are cleared, written and handed back to
+    the allocator in the order of the kernels that use them.  Outputs of such a call belong to
+    ``stream``: another stream waits for it before it reads them."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 def _dtype_code(dt):
     if dt == torch.bfloat16:
         return SF_BF16
@@ -212,6 +231,7 @@ def _f32(t):
     return t
 
 
+@on_its_stream
 def sf_gdn_chunk_fwd(q, k, v, gate, beta, initial_state=None, cu_seqlens=None, scale=None,
                      output_final_state=False, out=None, final_state=None, ws=None, stream=None):
     """chunk_gdn forward.  Returns (out [B,T,H,V], final_state [N,H,V,K] or None)."""
@@ -238,6 +258,7 @@ def sf_gdn_chunk_fwd(q, k, v, gate, beta, initial_state=None, cu_seqlens=None, s
     return out, (final_state if output_final_state else None)
 
 
+@on_its_stream
 def sf_gdn_paged_chunk_fwd(q, k, v, gate, beta, state_cache, state_indices, cu_seqlens=None,
                            has_initial_state=None, scale=None, out=None, ws=None, stream=None):
     """paged_chunk_gdn: the forward advancing state_cache [num_slots,H,V,K] in place at the
@@ -268,6 +289,7 @@ def sf_gdn_paged_chunk_fwd(q, k, v, gate, beta, state_cache, state_indices, cu_s
     return out
 
 
+@on_its_stream
 def sf_gdn_segment_summary(k, v, gate, beta, bounds, P=None, S_ext=None, ws=None, stream=None):
     """Affine map of each token range: returns (P [R,H,K,K], S_ext [R,H,V,K])."""
     lib = load()
@@ -291,6 +313,7 @@ def sf_gdn_segment_summary(k, v, gate, beta, bounds, P=None, S_ext=None, ws=None
     return P, S_ext
 
 
+@on_its_stream
 def sf_state_scan(P, S_ext, S0=None, entry_states=None, final_state=None, stream=None,
                   want_final=True):
     """Exclusive scan of segment maps: returns (entry_states [R,H,V,K], final [H,V,K])."""
@@ -306,6 +329,7 @@ def sf_state_scan(P, S_ext, S0=None, entry_states=None, final_state=None, stream
     return entry_states, final_state
 
 
+@on_its_stream
 def sf_gdn_segment_reverse_summary(q, k, gate, beta, d_out, seg_offsets, scale=None, C=None,
                                    ws=None, stream=None):
     """Cotangent map of consecutive segments (offsets [R+1], cu_seqlens convention) of one
@@ -328,6 +352,7 @@ def sf_gdn_segment_reverse_summary(q, k, gate, beta, d_out, seg_offsets, scale=N
     return C
 
 
+@on_its_stream
 def sf_state_scan_reverse(P, C, dS_final=None, exit_cotangents=None, d_initial=None,
                           stream=None, want_initial=True):
     """Reverse scan of cotangent maps: returns (exit cotangents [R,H,V,K], d_initial [H,V,K])."""
@@ -358,6 +383,7 @@ def _validate_bwd(q, k, v, gate, beta, initial_state, d_out, d_final_state, cu_s
                       ("d_initial_state", g.get("d_initial_state"))])
 
 
+@on_its_stream
 def sf_gdn_chunk_bwd(q, k, v, gate, beta, initial_state, d_out, d_final_state=None,
                      cu_seqlens=None, scale=None, want_d_initial_state=True, grads=None, ws=None,
                      stream=None):
@@ -384,6 +410,7 @@ def sf_gdn_chunk_bwd(q, k, v, gate, beta, initial_state, d_out, d_final_state=No
     return grads
 
 
+@on_its_stream
 def sf_gdn_chunk_bwd_noalloc(q, k, v, gate, beta, initial_state, d_out, d_final_state=None,
                              cu_seqlens=None, scale=None, want_d_initial_state=True, grads=None,
                              stream=None):

@@ -12,7 +12,7 @@ import functools
 
 import torch
 
-from ._native import _check, _dtype_code, load, on_its_stream, sf_gdn_shape, sf_qk_shape, workspace
+from ._native import _check, _dtype_code, load, on_its_stream, sf_gdn_shape, sf_qk_shape
 
 _NORMS = {"rms": 0, "l2": 1}
 _F32 = torch.float32
@@ -96,6 +96,14 @@ def _shape(q, v, cu_seqlens, scale, dims=None):
 def _ws(ws):
     if not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on a CUDA device")
+    return ws
+
+
+def workspace(nbytes, device):
+    """Uninitialised bytes behind a cleared status word: the kernels write what else they read (it
+    can be gigabytes, and clearing it would take a good part of a call's time)."""
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
     return ws
 
 

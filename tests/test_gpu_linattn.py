@@ -298,3 +298,21 @@ def test_repeats_bitwise_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, o3) and torch.equal(fin, f3)
         sf.sf_workspace_status(ws)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F32, 64)])
+def test_nothing_but_the_status_word_is_read_before_it_is_written(dtype, D):
+    """Walks that are cut and shared heads, in a workspace of NaN bit patterns."""
+    sf = _sf()
+    for lengths in (None, [1700, 0, 300]):
+        x = inputs(1, 2000, 4, 2, D, dtype, seed=103, lengths=lengths)
+        args = (x["q"], x["k"], x["v"], x["decay"], x["s0"])
+        for call, need in ((lambda ws: run_fwd(x, ws=ws), sf.sf_linattn_fwd_workspace),
+                           (lambda ws: tuple(sf.sf_linattn_chunk_bwd(*args, x["do"], x["df"], cu_seqlens=x["cu"],
+                                                                     ws=ws).values()), sf.sf_linattn_bwd_workspace)):
+            ws = need(x["q"], x["v"], x["cu"])
+            assert ws.numel() > 256
+            clean = call(torch.zeros_like(ws))
+            ws[256:] = 255
+            assert all(torch.equal(a, b) for a, b in zip(call(ws), clean))
+            sf.sf_workspace_status(ws)

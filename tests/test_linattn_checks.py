@@ -168,6 +168,14 @@ def test_token_strides_of_a_fused_projection():
             _token_stride("q", bad)
 
 
+def test_only_the_status_word_of_a_workspace_is_cleared(monkeypatch):
+    from chunked_linear_recurrence_gb300 import _linattn
+    monkeypatch.setattr(torch, "empty", lambda n, **kw: torch.full((n,), 255, **kw))
+    ws = _linattn.workspace(4096, "cpu")
+    assert ws.numel() == 4096 and not ws[:256].any() and (ws[256:] == 255).all()
+    assert _linattn.workspace(8, "cpu").numel() == 256
+
+
 _NO_ENCODER_SCRIPT = r'''
 import ctypes, sys
 sys.path.insert(0, sys.argv[1])

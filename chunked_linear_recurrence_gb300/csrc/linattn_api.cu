@@ -230,8 +230,8 @@ sf_status chunk_fwd(const char* fn, const sf_gdn_shape* shape, const void* q, co
       !aligned16(initial_state) || !aligned16(final_state))
     return report(SF_ERR_INVALID_ARG, "%s: q, k, v, out and states must be 16-byte aligned", fn);
   const Layout l = layout(shape, packed, 1);
-  if (!workspace || ws_bytes < l.total)
-    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, l.total);
+  if (!workspace || !aligned16(workspace) || ws_bytes < l.total)
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn, l.total);
   const sf_status enc = check_encoder(shape, fn);
   if (enc != SF_OK) return enc;
   sfg::LaParams p{};
@@ -382,8 +382,8 @@ sf_status sf_linattn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const v
     if (!aligned16(a))
       return report(SF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
   const Layout l = layout(shape, packed, 3);
-  if (!workspace || ws_bytes < l.total)
-    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn, l.total);
+  if (!workspace || !aligned16(workspace) || ws_bytes < l.total)
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn, l.total);
   const sf_status enc = check_encoder(shape, fn);
   if (enc != SF_OK) return enc;
   char* ws = static_cast<char*>(workspace);
@@ -480,7 +480,7 @@ sf_status sf_qk_norm_rope_bwd(const sf_qk_shape* shape, const void* q, const voi
     return report(SF_ERR_INVALID_ARG, "%s: cotangents and gradients must be 16-byte aligned", fn);
   const bool weights = dq_weight || dk_weight;
   if (weights && (!workspace || !aligned16(workspace) || ws_bytes < sf_qk_norm_rope_bwd_workspace(shape)))
-    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes", fn,
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn,
                   sf_qk_norm_rope_bwd_workspace(shape));
   p.q_out = dq;
   p.k_out = dk;

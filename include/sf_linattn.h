@@ -29,9 +29,9 @@ extern "C" {
  *                  fixed property of the head: no gradient of it is formed.
  *   shape, q, k, v, initial_state, cu_seqlens, out, final_state: as
  *                  sf_gdn_chunk_fwd.  K == V, either 64 or 128, BF16 or FP32.
- *   workspace      sf_linattn_fwd_workspace(shape, packed) bytes, its first 256
- *                  bytes zero before the first use; packed != 0 when cu_seqlens
- *                  is given.
+ *   workspace      sf_linattn_fwd_workspace(shape, packed) bytes, 16-byte aligned,
+ *                  its first 256 bytes zero before the first use; packed != 0
+ *                  when cu_seqlens is given.
  * Outputs overlap no input and no workspace; final_state may be initial_state.
  * An empty sequence hands its initial state through.  Rows past cu_seqlens[N]
  * are never written, and nothing in them (NaN, infinities) reaches a result.
@@ -153,7 +153,8 @@ sf_status sf_qk_norm_rope_fwd(const sf_qk_shape *shape, const void *q, const voi
 
 /* Its backward: d_q_out, d_k_out contiguous -> dq, dk contiguous, dq_weight, dk_weight [D]
  * FP32 or NULL (each is computed only if given).  The weights' gradients are summed in a
- * fixed order.  workspace: sf_qk_norm_rope_bwd_workspace bytes, no initial contents. */
+ * fixed order.  workspace: sf_qk_norm_rope_bwd_workspace bytes, 16-byte aligned, no
+ * initial contents. */
 size_t sf_qk_norm_rope_bwd_workspace(const sf_qk_shape *shape);
 sf_status sf_qk_norm_rope_bwd(const sf_qk_shape *shape, const void *q, const void *k,
                               const float *q_weight, const float *k_weight, const float *cos_sin,

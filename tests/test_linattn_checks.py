@@ -60,6 +60,17 @@ def test_chunked_entry_points_reject_bad_pointers_and_workspaces(lib):
     assert bwd(do=None) == 1 and bwd(dq=None) == 1 and bwd(dq=ODD) == 1 and bwd(ws=64) == 3
 
 
+def test_workspaces_that_are_not_16_byte_aligned_are_refused(lib):
+    """The kernels read and write the segments' states in it 16 bytes at a time."""
+    s = _shape(T=1 << 16)
+    assert _fwd(lib, s, ws=ODD) == 3
+    assert lib.sf_linattn_paged_chunk_fwd(s, FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, None, None, FAKE, ODD, 1 << 40,
+                                          None) == 3
+    assert lib.sf_linattn_chunk_bwd(s, *([FAKE] * 4), None, None, FAKE, None, FAKE, FAKE, FAKE, None, ODD,
+                                    1 << 40, None) == 3
+    assert lib.sf_qk_norm_rope_bwd(_qk(), *([FAKE] * 12), ODD, 1 << 40, None) == 3
+
+
 def test_workspace_grows_with_segments_and_shared_heads(lib):
     """A walk of one segment needs the status word alone; a long one the states of its
     segments; grouped heads the per-value-head parts of dq and dk."""

@@ -70,6 +70,8 @@ def _tokens(q, k, v, decay, cu_seqlens):
         raise ValueError(f"k {tuple(k.shape)} must match q {tuple(qs)} in shape and dtype")
     if v.dtype != dt or (k is not None and k.dtype != dt):
         raise ValueError("q, k and v must share one dtype")
+    if HK < 1:          # (to the library 0 means H, and it would read that many)
+        raise ValueError("q and k need at least one head")
     if decay is not None and decay.shape != (H,):
         raise ValueError(f"decay must be [H] = {(H,)}, got {tuple(decay.shape)}")
     N = B
@@ -226,6 +228,8 @@ def _step_args(q, k, v, state_cache, state_indices, scale, out):
         raise ValueError("q/k must be [N,HK,K], v [N,H,V] and state_cache [num_slots,H,V,K]")
     N, HK, K = qs
     _, H, V = vs
+    if HK < 1:
+        raise ValueError("q and k need at least one head")
     slots = cs[0]
     shape = _shape_of(1, 1, H, K, V, N, dt, scale, HK)[1]
     head = (_at("q", q), _addr("k", k, qs, dt), _addr("v", v, (N, H, V), dt))

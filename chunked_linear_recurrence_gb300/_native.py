@@ -202,6 +202,8 @@ def _validate(q, v, k=None, gate=None, beta=None, cu_seqlens=None, tensors=(), s
         raise ValueError("q, k and v must share one dtype")
     if k is not None and (k.shape != q.shape or k.dtype != q.dtype):
         raise ValueError(f"k {tuple(k.shape)} must match q {tuple(q.shape)} in shape and dtype")
+    if HK < 1:          # (to the library 0 means H, and it would read that many)
+        raise ValueError("q and k need at least one head")
     for name, t in (("gate", gate), ("beta", beta)):
         if t is not None and tuple(t.shape) != (B, T, H):
             raise ValueError(f"{name} must be [B,T,H] = {(B, T, H)}, got {tuple(t.shape)}")

@@ -167,6 +167,25 @@ def test_binding_checks_shapes_types_and_strides():
         sf.sf_qk_norm_rope_fwd(q, q)
 
 
+def test_no_query_heads_are_refused():
+    """In the shape struct HK = 0 stands for H heads: a slice without any would be read as H."""
+    import chunked_linear_recurrence_gb300 as sf
+    z = torch.zeros
+    q, v, dec, g = z(1, 64, 2, 64), z(1, 64, 2, 64), z(2), z(1, 64, 2)
+    none, cache, idx = q[:, :, :0], z(4, 2, 64, 64), z(1, dtype=torch.int32)
+    t = v[0]
+    for call in (lambda: sf.sf_linattn_chunk_fwd(none, none, v, dec),
+                 lambda: sf.sf_linattn_paged_chunk_fwd(none, none, v, dec, cache, idx),
+                 lambda: sf.sf_linattn_chunk_bwd(none, none, v, dec, None, v),
+                 lambda: sf.sf_linattn_fwd_workspace(none, v),
+                 lambda: sf.sf_linattn_step(t[:, :0], t[:, :0], t, dec, cache),
+                 lambda: sf.sf_gdn_step(t[:, :0], t[:, :0], t, z(64, 2), z(64, 2), cache),
+                 lambda: sf.sf_gdn_chunk_fwd(none, none, v, g, g),
+                 lambda: sf.sf_gdn_chunk_bwd(none, none, v, g, g, None, v)):
+        with pytest.raises(ValueError, match="at least one head"):
+            call()
+
+
 def test_token_strides_of_a_fused_projection():
     from chunked_linear_recurrence_gb300._linattn import _token_stride
     x = torch.zeros(2, 5, (4 + 2 + 2) * 64)

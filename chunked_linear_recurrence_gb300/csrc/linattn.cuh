@@ -51,7 +51,7 @@ struct LaPass {
   void* out;            // [rows, H, D]: the token type, or FP32 (out_f32)
   const float* s_in;    // [N,H,D,D] or NULL (zeros)
   float* s_out;         // [N,H,D,D] or NULL
-  float* entry;         // [units,H,D/4,D,4] (y / 4, z, y % 4): entry states of the segments
+  float* entry;         // [entries,H,D/4,D,4] (y / 4, z, y % 4): entry states of cut walks' segments
   float* sums;          // [pre_units,H,D/4,D,4]: what each piece adds to the state
   int hx, hy, hz;       // heads of x, y, z (each divides H)
   int s_t;              // the state is stored as [y][z] (s_in, s_out)
@@ -74,6 +74,7 @@ struct LaParams {
   int per_seg, cuts;    // pieces of a segment; segments of a walk (not packed)
   FastDiv by_pass, by_head, by_group, by_n, by_seg, by_pieces;   // npass, H, H / HK, N, seg, pieces of a walk
   int units, pre_units; // launched (sequence, segment) and (sequence, piece) units; packed: bounds
+  int entries;          // segments of walks that are cut; packed: a bound
   int* status;
 };
 
@@ -89,19 +90,28 @@ inline int64_t la_pre_units(int64_t T, int64_t N, bool packed, int64_t seg, int6
   const int64_t cuts = packed ? T / seg : N * ((T > seg ? (T + seg - 1) / seg : 1) - 1);
   return cuts * (seg / pre);
 }
+// Segments of the walks that are cut (the others take their states from the caller).  Packed: such
+// a walk's S segments but the last are whole, T / seg of them in all, and S <= 2 (S - 1).
+inline int64_t la_entries(int64_t T, int64_t N, bool packed, int64_t seg) {
+  if (T <= seg) return 0;
+  const int64_t whole = T / seg;
+  return packed ? whole + (whole < N ? whole : N) : N * ((T + seg - 1) / seg);
+}
 
 #ifdef __CUDACC__
 struct LaUnit {
   int n;                // sequence
   int64_t bos, eos;     // its rows, clamped into [0, B T]
   int64_t off, rows;    // the unit's rows in walk order
-  int at;               // its place in `entry` (segments) or `sums` (pieces)
+  int at;               // its place in `entry` (segments of a cut walk) or `sums` (pieces)
   bool last;            // the walk ends with it
 };
 
 __device__ __forceinline__ int la_segments(int64_t len, const LaParams& p) {
   return len > p.seg ? p.by_seg((int)len + p.seg - 1) : 1;   // (fewer than 2^26 rows)
 }
+// Entry states of a walk of S segments.
+__device__ __forceinline__ int la_kept(int S) { return S > 1 ? S : 0; }
 // A CTA's pass, head and unit.
 __device__ __forceinline__ void la_place(int id, const LaParams& p, int& pass, int& h, int& u) {
   const int a = p.by_pass(id), b = p.by_head(a);
@@ -161,7 +171,7 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
       S = la_segments(e - b, p);
     }
     const int cnt = S > 0 ? (kPieces ? (S - 1) * k : S - 1) : 0;
-    int incl = cnt, slots = kPieces ? cnt : S;         // before the walk's last segment; stored
+    int incl = cnt, slots = kPieces ? cnt : la_kept(S);   // before the walk's last segment; stored
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o), y = __shfl_up_sync(0xffffffffu, slots, o);
@@ -172,7 +182,7 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
       const int src = __ffs(hit) - 1;
       found = m0 + src;
       w = u - __shfl_sync(0xffffffffu, base + incl - cnt, src);
-      at += __shfl_sync(0xffffffffu, slots - (kPieces ? cnt : S), src) + w;
+      at += __shfl_sync(0xffffffffu, slots - (kPieces ? cnt : la_kept(S)), src) + w;
       break;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -219,12 +229,12 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
     span(found, t.bos, t.eos);
     const int S = la_segments(t.eos - t.bos, p);
     w = S - 1;
-    at = 0;                                            // segments of the sequences before it
+    at = 0;                                            // entry states of the sequences before it
 #pragma unroll 1
     for (int m = lane; m < found; m += 32) {
       int64_t b, e;
       span(m, b, e);
-      at += la_segments(e - b, p);
+      at += la_kept(la_segments(e - b, p));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
@@ -235,7 +245,7 @@ __device__ __forceinline__ bool la_locate(int u, const LaParams& p, LaUnit& t) {
   t.off = (int64_t)w * p.seg;
   t.rows = t.last ? t.eos - t.bos - t.off : p.seg;
   t.at = at;
-  return t.at < p.units;
+  return (t.last && w == 0) || at < p.entries;         // (malformed offsets could ask for more)
 }
 
 // lam^n for a natural-log decay d (n = 0: 1 even for d = -inf).

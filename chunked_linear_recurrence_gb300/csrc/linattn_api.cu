@@ -158,19 +158,20 @@ Cut cut_walks(const sf_gdn_shape* s, bool packed, int npass) {
 
 struct Layout {
   Cut cut;
-  int64_t units, pre_units;
+  int64_t units, pre_units, entries;
   size_t entry, sums, gqa, total;   // segment states of one pass; one FP32 [B,T,H,K] area
 };
 
 Layout layout(const sf_gdn_shape* s, bool packed, int npass) {
-  Layout l{{64, 64}, 0, 0, 0, 0, 0, kStatusBytes};
+  Layout l{{64, 64}, 0, 0, 0, 0, 0, 0, kStatusBytes};
   if (!s || s->K < 1 || s->V < 1 || s->H < 1 || s->T < 0 || s->N < 1) return l;
   l.cut = cut_walks(s, packed, npass);
   l.units = sfg::la_units(s->T, s->N, packed, l.cut.seg);
   if (l.cut.seg < s->T) {
     l.pre_units = sfg::la_pre_units(s->T, s->N, packed, l.cut.seg, l.cut.pre);
     const size_t state = (size_t)s->H * s->K * s->V * sizeof(float);
-    l.entry = round_up(l.units * state);
+    l.entries = sfg::la_entries(s->T, s->N, packed, l.cut.seg);
+    l.entry = round_up(l.entries * state);
     l.sums = round_up(l.pre_units * state);
   }
   if (npass > 1 && eff_hk(s) < s->H)
@@ -196,6 +197,7 @@ cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, i
   p.by_pieces = sfg::FastDiv::of(p.cuts > 1 ? (p.cuts - 1) * p.per_seg : 1);
   p.units = (int)l.units;
   p.pre_units = (int)l.pre_units;
+  p.entries = (int)l.entries;
   p.status = reinterpret_cast<int*>(ws);
   for (int i = 0; i < p.npass; ++i) {
     p.pass[i].entry = reinterpret_cast<float*>(ws + kStatusBytes + i * (l.entry + l.sums));

@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
     s0 = n * (S - 1) * k;
   } else {
     const int lane = tid & 31;
-    int found = -1, sum = 0;                           // its sequence; segments before it
+    const int nth = n;
+    int found = -1, sum = 0;                           // its sequence; segments of the ones before it
     for (int m0 = 0; m0 < p.N && found < 0; m0 += 32) {
       const int m = m0 + lane;
       int64_t b = 0, e = 0;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
       } else {
         n -= __popc(hit);
       }
-      if (lane < upto && m < p.N) sum += la_segments(e - b, p);
+      if (lane < upto && e - b > p.seg) sum += la_segments(e - b, p);
     }
     // Fewer walks are cut.  (Not even the launch before is waited for: a walk that is not cut
     // reads the caller's state, and where none is cut that launch does nothing.)
@@ -328,13 +329,13 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     u0 = sum;
-    s0 = (sum - n) * k;
+    s0 = (sum - nth) * k;
   }
   const int S = la_segments(len, p), pieces = (S - 1) * k;
   bool skip;
   const float* s_in = la_entry(p, q, n, h, D, skip);
   // padding; malformed offsets
-  if (skip || u0 + S > p.units || s0 + pieces > p.pre_units) {
+  if (skip || u0 + S > p.entries || s0 + pieces > p.pre_units) {
     launch_wait();
     return;
   }

@@ -81,6 +81,16 @@ def test_workspace_grows_with_segments_and_shared_heads(lib):
     assert grouped == plain + 2 * 200 * 4 * 128 * 4
 
 
+def test_workspace_of_many_short_sequences(lib):
+    """Only walks that are cut need entry states: T / seg whole segments and as many remainders at
+    the most, whatever the number of sequences (a state of 32 heads is 2 MB; a forward's cut makes
+    three pieces to a segment)."""
+    state = 32 * 128 * 128 * 4
+    fwd = lib.sf_linattn_fwd_workspace(_shape(T=65536, H=32, N=1024), 1)
+    bwd = lib.sf_linattn_bwd_workspace(_shape(T=32768, H=32, N=512), 1)
+    assert 256 < fwd <= 256 + 5 * 8 * state and 256 < bwd <= 256 + 3 * 5 * 8 * state
+
+
 @pytest.mark.parametrize("delta", [False, True])
 def test_steps_reject_bad_arguments(lib, delta):
     def call(shape, q=FAKE, gate=FAKE, cache=FAKE, slots=4, idx=FAKE, out=FAKE):

@@ -322,9 +322,10 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const LaParams p) {
       }
       if (lane < upto && e - b > p.seg) sum += la_segments(e - b, p);
     }
-    // Fewer walks are cut.  (Not even the launch before is waited for: a walk that is not cut
-    // reads the caller's state, and where none is cut that launch does nothing.)
-    if (found < 0) return;
+    if (found < 0) {                                   // fewer walks are cut
+      launch_wait();                                   // (the launch before may still read the offsets)
+      return;
+    }
     n = found;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

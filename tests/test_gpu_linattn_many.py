@@ -61,3 +61,23 @@ def test_many_sequences_of_which_none_is_cut(dtype, D):
             assert err(cache[int(idx[n])], rf[n]) <= STATE, n
         else:
             assert not out[:, cu[n]:cu[n + 1]].any()
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F32, 64)])
+def test_offsets_are_free_for_reuse_when_a_call_is_over(dtype, D):
+    """No walk of the first call is cut, all of the second's offsets are written over the first's
+    right behind it, and one walk of those is: neither launch of the first may still read them."""
+    import chunked_linear_recurrence_gb300 as sf
+    T = 1536
+    even, ragged = [48] * 32, [3] * 31 + [T - 93]
+    x = inputs(1, T, 1, 1, D, dtype, seed=3, lengths=even, decay=[-0.01])
+    y = dict(x, cu=torch.tensor([0] + list(np.cumsum(ragged)), dtype=torch.int32, device="cuda"))
+    a, b = run_fwd(x), run_fwd(y)
+    ws = sf.sf_linattn_fwd_workspace(x["q"], x["v"], x["cu"])
+    cu = x["cu"].clone()
+    for _ in range(20):
+        cu.copy_(x["cu"])
+        first = run_fwd(dict(x, cu=cu), ws=ws)
+        cu.copy_(y["cu"])
+        second = run_fwd(dict(x, cu=cu), ws=ws)
+        assert all(map(torch.equal, first, a)) and all(map(torch.equal, second, b))

@@ -70,7 +70,7 @@ struct Mem {
   static constexpr uint32_t Z = 2 * NP * PANEL, STAGE = 3 * NP * PANEL;
   static constexpr uint32_t P = NS * STAGE;        // P [64][64], two buffers
   static constexpr uint32_t OUT = P + 2 * PANEL;   // results, [32 rows][32 columns] of each of four warps
-  // b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [4] (padded), the
+  // b lam^e and c lam^f of a full chunk and of the walk's last one [64] each, carry [6] (padded to 16), the
   // weights of P by 64 + s - r in four copies, each a word further on, 8 banks apart
   static constexpr uint32_t TAB = OUT + 8192;
   static constexpr uint32_t BAR = TAB + 3328;
@@ -559,22 +559,22 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       warp_arrive(&bars[GO], lane);
     }
     bool ok = nc == 0 || warp_wait(&bars[TBL], 0, cx);
-    int since = 0;                                      // chunks since the factors were made good
+    // lam^64 lies between two floats.  Each chunk takes the one of them that keeps the product of
+    // the factors nearest to the power (error diffusion): rows of any age are off by an ulp of the
+    // factor at most and by nothing on average, at no cost to the elements.  The last chunk makes
+    // good what is left.  (One float alone, with its lack given back every 16 chunks, left younger
+    // rows up to 1e-6 off.)
+    float lack = 0.f;                                   // of the factors so far, relative
 #pragma unroll 1
     for (int c = 0; c < nc && ok; ++c) {
       const bool end = c + 1 == nc;
       if (!(ok = warp_wait(&bars[EDONE + c % NE], (c / NE) & 1, cx))) break;
       tc_fence_after();
-      // every 16 chunks, and before the last, the state gets back what the factors lacked
-      if (since == 16 || end) {
-        const float lack = (float)since * carry[1] + (end ? carry[3] : 0.f);
-#pragma unroll
-        for (int e = 0; e < D / 4; ++e) s[e] = fma2(s[e], make_float2(lack, lack), s[e]);
-        since = 0;
-      }
-      ++since;
-      const float f = carry[end ? 2 : 0];
-      const float2 fh = make_float2(f, f);
+      const bool other = fabsf(lack + carry[5]) < fabsf(lack + carry[1]);
+      const int at = end ? 2 : other ? 4 : 0;
+      lack += carry[at + 1];
+      const float f = carry[at];
+      const float2 fh = make_float2(f, f), fl = make_float2(f * lack, f * lack);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         float x[32];
@@ -583,6 +583,14 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         if (k == NP - 1) {
           tc_fence_before();
           warp_arrive(&bars[EFREE + c % NE], lane);
+        }
+        if (end) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 t = fma2(fl, s[16 * k + e], make_float2(x[2 * e], x[2 * e + 1]));
+            x[2 * e] = t.x;
+            x[2 * e + 1] = t.y;
+          }
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -643,12 +651,15 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
   } else {
     // (as launched: 96 registers)
     if (warp == 16) {
-      // lam^64 and lam^tail, each as a float and what that float lacks, relative to it: a state
-      // carried over thousands of chunks must not drift by the rounding of one factor
-      if (lane < 2) {
-        const double f = la_pow(p.decay[h], lane ? tail : C);
-        carry[2 * lane] = (float)f;
-        carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)(float)f - 1.0) : 0.f;
+      // lam^64, lam^tail and the float on the other side of lam^64, each with what it lacks,
+      // relative to it: a state carried over thousands of chunks must not drift by the rounding of
+      // one factor
+      if (lane < 3) {
+        const double f = la_pow(p.decay[h], lane == 1 ? tail : C);
+        float g = (float)f;
+        if (lane == 2) g = nextafterf(g, f > (double)g ? INFINITY : 0.f);
+        carry[2 * lane] = g;
+        carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)g - 1.0) : 0.f;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[TBL]);

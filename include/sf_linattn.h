@@ -36,8 +36,10 @@ extern "C" {
  * An empty sequence hands its initial state through.  Rows past cu_seqlens[N]
  * are never written, and nothing in them (NaN, infinities) reaches a result.
  * A NaN or infinity inside a sequence reaches that head's results from the
- * start of its block of 64 tokens on (the products run over whole blocks; in the
- * backward also down to the block's end), never another sequence or head.
+ * start of its block of 64 tokens on, counted from the sequence's start (the
+ * products run over whole blocks); what the backward walks from the end (dk, dv,
+ * d_initial_state) from the end of its block, counted from the sequence's end.
+ * It reaches no other sequence or head.
  *
  * FP32 outputs and states carry FP32 accuracy.  With BF16 tokens, out is
  * rounded once from FP32 sums whose operands (the masked products of q and k,

@@ -134,3 +134,33 @@ def test_gradient_against_differences_and_repeats_bitwise():
         exact = (g[grad].double() * u.double()).sum()
         size = (g[grad].double().norm() * u.double().norm())
         assert abs(d - exact) <= 1e-3 * size, name
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("rot,axes", [(8, 1), (24, 2), (40, 3), (56, 4)])
+def test_partial_rotation_of_bf16_that_ends_inside_a_group_of_eight(D, rot, axes):
+    """rotary_dim / 2 is no multiple of 8: groups of four elements, 8-byte accesses."""
+    for norm, interleaved in (("rms", False), ("rms", True), ("l2", False), ("l2", True)):
+        check(make(2, 19, 5, 3, D, BF16, rot + D, rot, axes), BF16, norm, interleaved=interleaved)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_and_backward_in_a_graph(dtype):
+    """Replayed on new inputs in the same buffers: bitwise the calls' results."""
+    import chunked_linear_recurrence_gb300 as sf
+    x, y = (make(2, 33, 4, 2, 128, dtype, s, 128, 3, fused=False) for s in (21, 22))
+    ws = sf.sf_qk_norm_rope_bwd_workspace(x["q"], x["k"])
+
+    def run(z, ws=None):
+        a = (z["q"], z["k"], z["qw"], z["kw"], z["cs"], z["pos"])
+        f = sf.sf_qk_norm_rope_fwd(*a, sections=z["sections"])
+        return list(f) + list(sf.sf_qk_norm_rope_bwd(*a, z["dq"], z["dk"], sections=z["sections"], ws=ws).values())
+    run(x, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(x, ws)
+    for n in ("q", "k", "qw", "kw", "cs", "pos", "dq", "dk"):
+        x[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(map(torch.equal, got, run(y)))

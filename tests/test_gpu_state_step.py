@@ -145,3 +145,20 @@ def test_prefill_then_steps_equal_one_prefill(delta):
         ro, rf = la.fwd(f64(q), f64(k), f64(v), f64(decay))
         tol = 5e-3
     assert err(out, ro) <= tol and err(cache[idx.long()], rf) <= (tol if delta else 1e-5)
+
+
+@pytest.mark.parametrize("delta", [False, True])
+def test_steps_replayed_in_a_graph(delta):
+    """Three replays advance the pool as three calls do."""
+    x = inputs(5, 4, 2, 128, BF16, 41, 8)
+    idx = torch.tensor([3, 1, -1, 7, 2], dtype=torch.int32, device="cuda")
+    y = dict(x, cache=x["cache"].clone())
+    call(dict(x, cache=x["cache"].clone()), delta, idx)                 # loaded before the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(y, delta, idx)
+    for _ in range(3):
+        ref = call(x, delta, idx)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(x["cache"], y["cache"])

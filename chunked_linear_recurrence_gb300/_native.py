@@ -33,7 +33,8 @@ EXPORTS = ("sf_last_error", "sf_version", "sf_gdn_fwd_workspace", "sf_gdn_chunk_
            "sf_testing_inject_timeout",
            "sf_linattn_fwd_workspace", "sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd",
            "sf_linattn_bwd_workspace", "sf_linattn_chunk_bwd", "sf_linattn_step", "sf_gdn_step",
-           "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd_workspace", "sf_qk_norm_rope_bwd")
+           "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd_workspace", "sf_qk_norm_rope_bwd",
+           "sf_testing_inject_linattn_timeout")
 
 
 class SfError(RuntimeError):
@@ -100,6 +101,7 @@ def load(path: str = LIB_PATH):
         lib.sf_workspace_status.argtypes = [vp, vp]
         lib.sf_gdn_chunk_bwd_noalloc_status.argtypes = [vp]
         lib.sf_testing_inject_timeout.argtypes = [ctypes.c_longlong, ctypes.c_longlong]
+        lib.sf_testing_inject_linattn_timeout.argtypes = [I]
         qp = ctypes.POINTER(sf_qk_shape)
         lib.sf_linattn_fwd_workspace.argtypes = [sp, I]
         lib.sf_linattn_fwd_workspace.restype = sz
@@ -123,6 +125,7 @@ def load(path: str = LIB_PATH):
                   "sf_state_scan",
                   "sf_gdn_chunk_bwd", "sf_gdn_chunk_bwd_noalloc",
                   "sf_gdn_chunk_bwd_noalloc_status", "sf_testing_inject_timeout",
+                  "sf_testing_inject_linattn_timeout",
                   "sf_validate_cu_seqlens",
                   "sf_workspace_status", "sf_gdn_segment_reverse_summary",
                   "sf_state_scan_reverse"):

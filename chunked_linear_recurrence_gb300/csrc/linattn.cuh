@@ -76,6 +76,7 @@ struct LaParams {
   int units, pre_units; // launched (sequence, segment) and (sequence, piece) units; packed: bounds
   int entries;          // segments of walks that are cut; packed: a bound
   int* status;
+  int tries;            // of a wait in a launch that a test makes give up (linattn_tc.cu), else 0
 };
 
 constexpr int LA_CHUNK = 64;

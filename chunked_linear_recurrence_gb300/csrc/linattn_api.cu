@@ -14,6 +14,7 @@ using sfg::report;
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+thread_local int g_tries = 0;   // sf_testing_inject_linattn_timeout
 constexpr int kSms = 152;   // the segment rule's machine: workspace sizes do not ask the device
 
 size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -205,6 +206,10 @@ cudaError_t run_passes(sfg::LaParams& p, const Layout& l, char* ws, bool bf16, i
   }
   // (T = 0: no token is read or written, only the states move; the FP32 kernel does)
   const bool tc = bf16 && p.T > 0;
+  if (tc) {
+    p.tries = g_tries;
+    g_tries = 0;
+  }
   auto walk = [&](bool state_only) {
     return tc ? sfg::launch_la_tc(p, D, state_only, cs) : sfg::launch_la_simt(p, D, state_only, cs);
   };
@@ -418,6 +423,13 @@ sf_status sf_linattn_chunk_bwd(const sf_gdn_shape* shape, const void* q, const v
                               true);
   }
   return cuda_status(e, fn);
+}
+
+sf_status sf_testing_inject_linattn_timeout(int tries) {
+  if (tries < 1 || tries > 10000)
+    return report(SF_ERR_INVALID_ARG, "sf_testing_inject_linattn_timeout: need 1 <= tries <= 10000");
+  g_tries = tries;
+  return SF_OK;
 }
 
 sf_status sf_linattn_step(const sf_gdn_shape* shape, const void* q, const void* k, const void* v,

@@ -93,13 +93,14 @@ constexpr uint32_t ID_O2 = idesc_bf16(128, 64, true, false);
 enum { FULL = 0, LANDED = FULL + NS, FREE = LANDED + 1, QKDONE = FREE + NS, PREADY,
        PFREE = PREADY + 2, SPLIT, EHALF = SPLIT + 4, EDONE = EHALF + 2, EFREE = EDONE + 2,
        O1DONE = EFREE + 2, ODONE, OFREE, GO, TBL, DRAIN, NBAR = DRAIN + 2 };
-static_assert(8 * NBAR + 36 <= 320 && NBAR <= 32, "barriers");
+static_assert(8 * NBAR + 40 <= 320 && NBAR <= 32, "barriers");
 
 // Tries of a wait before it gives up: each may suspend the thread for up to 20 us (at the least
 // it takes the ~50 ns of the instruction), so between 50 ms and 20 s, where a wait that ends takes
 // microseconds.  (A count and not a clock: the waits are inlined into every role's loop, and
-// the loops run at the speed of instruction fetch.)
-constexpr int WAIT_TRIES = 1000000;
+// the loops run at the speed of instruction fetch.  It lies in shared memory, TRIES words behind
+// the abort flag, so that a test can shorten it.)
+constexpr int WAIT_TRIES = 1000000, TRIES = 8;
 
 struct Maps {
   CUtensorMap m[3][3];   // x, y, z of each pass
@@ -108,11 +109,12 @@ struct Maps {
 // False when the wait gave up, or another thread of the CTA did (`abort`: where, once).
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
   if (mbar_try_wait(bar, parity)) return true;
+  int i = 0;
 #pragma unroll 1
-  for (int i = 0; i < WAIT_TRIES; ++i) {
+  do {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
     if (*abort) return false;
-  }
+  } while (++i < (int)abort[TRIES]);
   *abort = 0x40000000u | ((threadIdx.x >> 5) << 6) | ((smem_u32(bar) & 255u) >> 3);
   return false;
 }
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         unit[6] = p.seg < p.T && !(t.last && t.off == 0);
       }
     }
-    if (lane == 0) unit[0] = code, *cx = 0;
+    if (lane == 0) unit[0] = code, *cx = 0, cx[TRIES] = p.tries > 0 ? p.tries : WAIT_TRIES;
     if (lane < NBAR) {
       const int i = lane;
       mbar_init(&bars[i], i >= PREADY && i <= PFREE ? 2 : (i >= SPLIT && i < SPLIT + 4) || i == OFREE ? WL
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
           if (c >= NS && !(ok = warp_wait(&bars[FREE + c % NS], ((c - NS) / NS) & 1, cx))) break;
           load(c);
         }
-        if (!ok) land();
+        land();                                        // also where other warps give up on them
       }
 #pragma unroll 1
       for (int c = 0; !kState && c < nc && ok; ++c) {
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
         carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)g - 1.0) : 0.f;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[TBL]);
+      if (lane == 0 && p.tries == 0) mbar_arrive(&bars[TBL]);   // (a test leaves it out)
     }
     // ---------------------------------------------------------------- results
     // A warp takes the 32 columns z of its TMEM lanes, 32 rows at a time, as 8 x 8 tiles: of the

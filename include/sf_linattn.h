@@ -164,6 +164,13 @@ sf_status sf_qk_norm_rope_bwd(const sf_qk_shape *shape, const void *q, const voi
                               void *dq, void *dk, float *dq_weight, float *dk_weight,
                               void *workspace, size_t ws_bytes, sf_stream_t stream);
 
+/* Failure-detection testing only, as sf_testing_inject_timeout: in the next BF16 call of
+ * sf_linattn_chunk_fwd, sf_linattn_paged_chunk_fwd or sf_linattn_chunk_bwd on the calling
+ * host thread no CTA's table of factors is ever announced, and every internal wait gives up
+ * after `tries` (1 .. 10000) tries of 20 us at the most each.  The status word then reads
+ * SF_ERR_TIMEOUT, and the call's outputs are undefined; later calls are normal. */
+sf_status sf_testing_inject_linattn_timeout(int tries);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,14 +19,19 @@
 // weighted rows are split into three BF16 summands (8 bits each, 24 together) in TMEM, each
 // multiplied with the exact Y.  A launch that returns no state takes two of them (16 bits): its
 // state only ever reaches BF16 results.  (The parts as an MN-major operand in shared memory
-// needed 48 KB of stores and loads a chunk more: slower.)  BF16 roundings: S before O1 and P
-// before O2 (the results are BF16), P to 16 bits in walks of one chunk.
+// needed 48 KB of stores and loads a chunk more: slower.)
+//
+// Roundings to BF16: S before O1 and P before O2, where the results are BF16 themselves.  Their
+// error against FP64 is 2.35e-3 (2-norm) with them, 1.66e-3, the result's own rounding, without;
+// both in two parts, 16 bits, took 223 us for 167 (backward of 2 x 8192 tokens of 16 heads) and 500
+// for 378 (65536 packed tokens of 32 heads), measured with the work alone.  P keeps 16 bits in walks
+// of one chunk, whose results may come from one or two elements.
 //
 // Twenty warps: 0 loads (four stages) and issues E, in two halves of 32 rows so that the split
 // refills one under the other; 1 issues QK, O1 and O2; 2-3 form P; 4-11 hold the state (two
 // warpgroups: columns y of either half); 12-15 split the weighted rows; 16-19 write the
 // results, turned in shared memory into 16-byte stores.  A batch of products costs ~170 cycles
-// beyond the pipe's own time, so O1 and O2 go together, and the next chunk's QK goes while the
+// beyond its products' own time, so O1 and O2 go together, and the next chunk's QK goes while the
 // last results are read.  A launch that computes pieces' states alone has E only: warp 1 loads,
 // two buffers of E and of the parts, and warps 16-19 split every other chunk.
 // Products are issued behind elect.sync in warp-uniform code (a lane test costs 62 cycles a
@@ -37,12 +42,16 @@
 // SF_ERR_TIMEOUT to the status word and raises the CTA's abort flag; copies and products in
 // flight land before the CTA leaves.
 //
-// Bound by the tensor pipe, active 91 % of a CTA's time at D = 128: QK 8 products of 48 cycles,
-// E 12 of 64, O1 8 of 32, O2 4 of 48, and four batches' starts: ~2280 of the ~2500 cycles a
-// chunk.  Measured, D = 128: 96 walks of 128 chunks 165 us (3.7 TB/s on 96 SMs), 256 walks of 32
-// chunks 106 us (5.4 TB/s), 4 x 4096 tokens of 16 heads 19 us of pieces' states and 49 us, one
+// Bound by the chain of roles that a chunk passes through, not by one unit: at D = 128 the tensor
+// pipe is active 54 % of a CTA's time (1410 of ~2500 cycles a chunk; QK 8 products, E 12, O1 8, O2
+// 4, four batches' starts between them), and the same backward takes 190-194 us for 167 with
+// the products of O1 and O2, those of QK or P's work done twice, 218 with the state's copy (where
+// it spills).  At D = 64 the pipe is active 39 %.  With a CTA on every SM and no state to wait for
+// memory is near: 131072 tokens of 4 heads read and write 5.9 TB/s in the walks, 5.5 in the pieces'
+// states.  Measured, D = 128: 96 walks of 128 chunks 167 us (3.6 TB/s on 96 SMs), 256 walks of 32
+// chunks 110 us (5.2 TB/s), 4 x 4096 tokens of 16 heads 19 us of pieces' states and 50 us, one
 // prompt of 130 tokens 9 us; a chunk takes 1.2 us (0.58 us of a piece's states) with few CTAs, 1.5
-// (0.88) with one on every SM.  D = 64: 96 walks of 128 chunks 129 us.
+// (0.88) with one on every SM.  D = 64: 96 walks of 128 chunks 131 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -384,8 +393,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------------- issuer of QK, O1, O2
-      // (the whole warp waits; one elected lane issues).  A batch of products costs ~200 cycles
-      // beyond the tensor pipe's own time, so O1 and O2 go together.  The next chunk's QK goes
+      // (the whole warp waits; one elected lane issues).  A batch of products costs ~170 cycles
+      // beyond its products' own time, so O1 and O2 go together.  The next chunk's QK goes
       // first, while the results of the last chunk are being read, if its rows are there (P takes
       // as long as the rest of a step), else in its own turn.
       int qn = 0;                                      // chunks whose QK is issued
@@ -458,8 +467,8 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       if (!kState) {
         // row r of P.  A walk of one chunk has its rounding's rest in the second buffer: there a
         // result may come from one or two elements, whose rounding to BF16 would show as much as
-        // the result's own (over more rows the roundings average out).  The half on the far side of the diagonal (32 columns of one warp) is never
-        // touched: it stays zero.
+        // the result's own.  The half on the far side of the diagonal (32 columns of one warp) is
+        // never touched: it stays zero.
         const int r = (warp - 2) * 32 + lane;          // TMEM lane 64 + r
         // a lam^|r-s|, or 0, at f[s] (the copy in which that is 16-byte aligned)
         const float* f = pq + (r & 3) * (PQ_LD + 1) + 64 - r;

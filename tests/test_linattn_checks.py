@@ -208,12 +208,15 @@ def test_token_strides_of_a_fused_projection():
             _token_stride("q", bad)
 
 
-def test_only_the_status_word_of_a_workspace_is_cleared(monkeypatch):
+def test_only_the_status_word_of_a_large_workspace_is_cleared(monkeypatch):
     from chunked_linear_recurrence_gb300 import _linattn
     monkeypatch.setattr(torch, "empty", lambda n, **kw: torch.full((n,), 255, **kw))
-    ws = _linattn.workspace(4096, "cpu")
-    assert ws.numel() == 4096 and not ws[:256].any() and (ws[256:] == 255).all()
-    assert _linattn.workspace(8, "cpu").numel() == 256
+    n = (1 << 24) + 256
+    ws = _linattn.workspace(n, "cpu")
+    assert ws.numel() == n and not ws[:256].any() and (ws[256:] == 255).all()
+    for n, size in ((8, 256), (4096, 4096), (1 << 24, 1 << 24)):
+        ws = _linattn.workspace(n, "cpu")
+        assert ws.numel() == size and not ws.any()
 
 
 _NO_ENCODER_SCRIPT = r'''

@@ -665,12 +665,17 @@ __global__ void __launch_bounds__(NT, 1) la_tc_kernel(const __grid_constant__ Ma
       // lam^64, lam^tail and the float on the other side of lam^64, each with what it lacks,
       // relative to it: a state carried over thousands of chunks must not drift by the rounding of
       // one factor
-      if (lane < 3) {
-        const double f = la_pow(p.decay[h], lane == 1 ? tail : C);
-        float g = (float)f;
-        if (lane == 2) g = nextafterf(g, f > (double)g ? INFINITY : 0.f);
-        carry[2 * lane] = g;
-        carry[2 * lane + 1] = f > 1e-30 ? (float)(f / (double)g - 1.0) : 0.f;
+      if (lane < 2) {
+        const double v = la_pow(p.decay[h], lane ? tail : C);
+        const float f = (float)v, less = (float)(v - (double)f);
+        const float g = __int_as_float(__float_as_int(f) + (less < 0.f ? -1 : 1));
+        const bool live = v > 1e-30;
+        carry[2 * lane] = f;
+        carry[2 * lane + 1] = live ? less / f : 0.f;
+        if (lane == 0) {
+          carry[4] = g;
+          carry[5] = live ? (less - (g - f)) / g : 0.f;
+        }
       }
       __syncwarp();
       if (lane == 0 && p.tries == 0) mbar_arrive(&bars[TBL]);   // (a test leaves it out)

@@ -34,7 +34,10 @@ EXPORTS = ("sf_last_error", "sf_version", "sf_gdn_fwd_workspace", "sf_gdn_chunk_
            "sf_linattn_fwd_workspace", "sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd",
            "sf_linattn_bwd_workspace", "sf_linattn_chunk_bwd", "sf_linattn_step", "sf_gdn_step",
            "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd_workspace", "sf_qk_norm_rope_bwd",
-           "sf_testing_inject_linattn_timeout")
+           "sf_testing_inject_linattn_timeout",
+           "sf_gdn_draft_step", "sf_linattn_draft_step", "sf_gdn_commit", "sf_linattn_commit",
+           "sf_draft_verify", "sf_state_workspace", "sf_state_copy", "sf_state_fork",
+           "sf_state_compact")
 
 
 class SfError(RuntimeError):
@@ -56,6 +59,24 @@ class sf_qk_shape(ctypes.Structure):
                 ("interleaved", ctypes.c_int), ("table_rows", ctypes.c_int),
                 ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4),
                 ("rows_stride_q", ctypes.c_int64), ("rows_stride_k", ctypes.c_int64)]
+
+
+class sf_pending(ctypes.Structure):
+    _fields_ = [("P", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("count", ctypes.c_void_p)]
+
+
+class sf_verify_shape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("T", ctypes.c_int), ("V", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("target_seq", ctypes.c_int64),
+                ("target_row", ctypes.c_int64), ("draft_seq", ctypes.c_int64),
+                ("draft_row", ctypes.c_int64)]
+
+
+class sf_state_pool(ctypes.Structure):
+    _fields_ = [("num_slots", ctypes.c_int), ("num_caches", ctypes.c_int),
+                ("caches", ctypes.POINTER(ctypes.c_void_p)),
+                ("slot_bytes", ctypes.POINTER(ctypes.c_size_t))]
 
 
 _lock = threading.Lock()
@@ -119,7 +140,21 @@ def load(path: str = LIB_PATH):
         lib.sf_qk_norm_rope_bwd_workspace.restype = sz
         lib.sf_qk_norm_rope_bwd.argtypes = [qp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                             sz, vp]
-        for f in ("sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd", "sf_linattn_chunk_bwd",
+        pp, vs = ctypes.POINTER(sf_state_pool), ctypes.POINTER(sf_verify_shape)
+        pd = ctypes.POINTER(sf_pending)
+        lib.sf_gdn_draft_step.argtypes = [sp, vp, vp, vp, vp, vp, vp, pd, vp, I, vp, vp, vp]
+        lib.sf_linattn_draft_step.argtypes = [sp, vp, vp, vp, vp, vp, pd, vp, I, vp, vp, vp]
+        lib.sf_gdn_commit.argtypes = [sp, vp, vp, vp, vp, vp, vp, I, vp, vp]
+        lib.sf_linattn_commit.argtypes = [sp, vp, vp, vp, vp, vp, I, vp, vp]
+        lib.sf_draft_verify.argtypes = [vs, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.sf_state_workspace.argtypes = [I, I]
+        lib.sf_state_workspace.restype = sz
+        lib.sf_state_copy.argtypes = [pp, vp, vp, I, vp]
+        lib.sf_state_fork.argtypes = [pp, vp, I, vp, I, vp, vp, vp, sz, vp]
+        lib.sf_state_compact.argtypes = [pp, vp, I, vp, vp, vp, sz, vp]
+        for f in ("sf_gdn_draft_step", "sf_linattn_draft_step", "sf_gdn_commit",
+                  "sf_linattn_commit", "sf_draft_verify", "sf_state_copy", "sf_state_fork",
+                  "sf_state_compact", "sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd", "sf_linattn_chunk_bwd",
                   "sf_linattn_step", "sf_gdn_step", "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd",
                   "sf_gdn_chunk_fwd", "sf_gdn_paged_chunk_fwd", "sf_gdn_segment_summary",
                   "sf_state_scan",

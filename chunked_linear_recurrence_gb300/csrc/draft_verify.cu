@@ -1,61 +1,198 @@
 // draft_verify.cu -- drafted tokens against the target's probabilities (include/sf_decode.h).
 //
 // A cluster of CTAs takes a sequence: every CTA finds the first rejected draft a (a gather of two
-// values a draft), then sums its slice of the weights w = max(p_a - q_a, 0); the slices' sums meet
-// in shared memory, and the warp whose slice crosses u * total reads it again (from L2) to find
-// the token.  Bound by memory: one row of p and one of q.
+// values a draft), then each warp sums its slice of the weights w = max(p_a - q_a, 0); the slices'
+// sums meet in the shared memory of all CTAs, and the CTA of the slice that crosses u * total reads
+// it again (from L2) to find the token.  Bound by memory: one row of p and one of q.
 //
 // The comparison and the search have to give what exact arithmetic gives, however the sums are
-// split: the test is one product in FP64 (exact for FP32 factors); a thread sums in two floats
-// (the rounding error of every difference and sum is kept: FP64 at a fraction of its cost on this
-// machine), and the threads' sums are joined in FP64 in a fixed order.
-#include <cooperative_groups.h>
+// split: the test is one product in FP64 (exact for FP32 factors), and sums are two floats, a sum
+// and the rounding errors of all its additions and differences (48 bits; FP64 would be exact
+// enough, but this machine does two FP64 operations a clock and SM, and a warp's scan in it takes
+// 1.5 us).
+//
+// Measured, 128 sequences, 7 drafts, 100003 tokens, FP32: 27 us (floor 12.9: one row of p, most of q)
+// of which the test 1.5, the stream 13 for the median CTA and 19 for the last one, the pick among
+// the warps 0.9, the search 3.5.  Copies of 16 bytes to shared memory against 4-byte loads to
+// registers (rows start at any multiple of an element): stream 22 -> 13-19.  Sums sent with st.async to a
+// barrier against a cluster barrier with release and acquire: 28.3 -> 26.9 us.  Five CTAs an SM:
+// 26.9; 3, 4, 6: 32.0, 27.5, 31-35 (six leave clusters for a second wave).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "decode.cuh"
+#include "tc_ptx.cuh"
 
 namespace sfg {
 namespace {
 
-namespace cg = cooperative_groups;
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
+constexpr int CTAS = 5;           // of an SM
+constexpr int STAGES = 2;         // chunks of a warp's slice in flight
+constexpr int CHUNK_BYTES = 1024; // of a row
+constexpr int kSlice = 1024;      // elements that are worth a CTA
+
+constexpr int kNone = -1, kAgain = -2, kLate = -3;     // in place of the picked warp
 
 enum Weight { kTarget, kLess, kOthers };   // p, max(p - q, 0), p but for the drafted token
 
-// w as two floats (the second one the rounding error of the difference); not positive: zero.
-template <typename T>
-__device__ __forceinline__ float2 weight(const T* p, const T* q, int y, int skip, Weight how) {
-  const float a = to_f(p[y]);
+// w as two floats (the second one the rounding error of the difference, exact where the first is
+// positive and the draft's value is not negative); not positive: zero.
+template <Weight how>
+__device__ __forceinline__ float2 weight(float a, float b, bool skip) {
   if (how == kLess) {
-    const float b = to_f(q[y]);
-    const float d = __fsub_rn(a, b), t = __fsub_rn(d, a);
-    const float e = __fsub_rn(__fsub_rn(a, __fsub_rn(d, t)), __fadd_rn(b, t));
-    return d > 0.f ? make_float2(d, e) : make_float2(0.f, 0.f);
+    const float d = __fsub_rn(a, b);
+    return d > 0.f ? make_float2(d, __fsub_rn(__fsub_rn(a, d), b)) : make_float2(0.f, 0.f);
   }
-  return make_float2(a > 0.f && !(how == kOthers && y == skip) ? a : 0.f, 0.f);
+  return make_float2(a > 0.f && !(how == kOthers && skip) ? a : 0.f, 0.f);
 }
 
 __device__ __forceinline__ void add(float2& s, float2 w) {
   const float n = __fadd_rn(s.x, w.x), t = __fsub_rn(n, s.x);
-  s.y += __fadd_rn(__fsub_rn(s.x, __fsub_rn(n, t)), __fsub_rn(w.x, t)) + w.y;
+  s.y = __fadd_rn(s.y, __fadd_rn(__fadd_rn(__fsub_rn(s.x, __fsub_rn(n, t)), __fsub_rn(w.x, t)), w.y));
   s.x = n;
 }
+__device__ __forceinline__ float2 sum(float2 a, float2 b) {
+  add(a, b);
+  return a;
+}
+// a > b, of sums of non-negative weights; false with a NaN.
+__device__ __forceinline__ bool more(float2 a, float2 b) {
+  const float ah = __fadd_rn(a.x, a.y), al = __fadd_rn(__fsub_rn(a.x, ah), a.y);
+  const float bh = __fadd_rn(b.x, b.y), bl = __fadd_rn(__fsub_rn(b.x, bh), b.y);
+  return ah > bh || (ah == bh && al > bl);
+}
+__device__ __forceinline__ float2 shfl(float2 s, int lane) {
+  return make_float2(__shfl_sync(0xffffffffu, s.x, lane), __shfl_sync(0xffffffffu, s.y, lane));
+}
+// (Behind the stream, once: kept out of the stream's registers.)
+__device__ __noinline__ float2 warp_sum(float2 s) {
+#pragma unroll 1
+  for (int o = 16; o >= 1; o >>= 1)
+    add(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+  return shfl(s, 0);     // (the lanes' low parts may differ)
+}
 
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// A warp's sum of the weights [lo, hi).  Rows start anywhere: whole chunks are copied in
+// 16-byte units from the unit that holds their first element to the one behind their last, which lie
+// within the slice because 16 bytes at least of it are left at either end; those ends are loaded.
+template <typename T, Weight how>
+__device__ __forceinline__ float2 sum_slice(const T* p, const T* q, int lo, int hi, int skip, char* buf) {
+  constexpr int E = 16 / sizeof(T), C = CHUNK_BYTES / sizeof(T);
+  constexpr int ROW = CHUNK_BYTES + 16, UNITS = ROW / 16;
+  const int lane = threadIdx.x & 31;
+  const int chunks = hi - lo >= C + 2 * E ? (hi - lo - 2 * E) / C : 0;
+  const char* pa = reinterpret_cast<const char*>(p + lo + E);
+  const char* qa = reinterpret_cast<const char*>(q + lo + E);
+  const int ps = (int)(reinterpret_cast<uintptr_t>(pa) & 15), qs = (int)(reinterpret_cast<uintptr_t>(qa) & 15);
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(buf);
+  auto fetch = [&](int c) {
+    if (c < chunks) {
+      const uint32_t s = to + (c % STAGES) * 2 * ROW;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+      for (int i = 0; i < (UNITS + 31) / 32; ++i) {
+        const int j = lane + i * 32;
+        if (j < UNITS) {
+          copy16(s + j * 16, pa - ps + (size_t)c * CHUNK_BYTES + j * 16);
+          if (how == kLess) copy16(s + ROW + j * 16, qa - qs + (size_t)c * CHUNK_BYTES + j * 16);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int c = 0; c < STAGES; ++c) fetch(c);
+  float2 s = make_float2(0.f, 0.f);
+  const int ends = hi - lo - chunks * C;
+#pragma unroll 4
+  for (int t = lane; t < ends; t += 32) {
+    const int y = lo + t + (t >= E ? chunks * C : 0);
+    add(s, weight<how>(to_f(p[y]), how == kLess ? to_f(q[y]) : 0.f, y == skip));
+  }
+  for (int c = 0; c < chunks; ++c) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    __syncwarp();
+    const char* at = buf + (c % STAGES) * 2 * ROW;
+    const T* a = reinterpret_cast<const T*>(at + ps) + lane;
+    const T* b = reinterpret_cast<const T*>(at + ROW + qs) + lane;
+    const int y = lo + E + c * C + lane;
+#pragma unroll
+    for (int i = 0; i < C / 32; ++i)
+      add(s, weight<how>(to_f(a[i * 32]), how == kLess ? to_f(b[i * 32]) : 0.f, y + i * 32 == skip));
+    __syncwarp();
+    fetch(c + STAGES);
+  }
+  return s;
+}
+
+// The CTAs of a cluster.  Arrivals order nothing by themselves: a release would wait for every store
+// in flight (1.3 to 6 thousand cycles here).
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ int cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Eight bytes to the same place of another CTA of the cluster, counted by its barrier.
+__device__ __forceinline__ void send(float2* to, uint64_t* bar, int rank, float2 v) {
+  asm volatile(
+      "{\n .reg .b32 a, b;\n mapa.shared::cluster.u32 a, %0, %2;\n mapa.shared::cluster.u32 b, %1, %2;\n"
+      " st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [a], %3, [b];\n}"
+      ::"r"(tc::smem_u32(to)), "r"(tc::smem_u32(bar)), "r"(rank), "l"(*reinterpret_cast<uint64_t*>(&v)) : "memory");
+}
+
+// One weight, in a search.
+template <typename T>
+__device__ __forceinline__ float2 one(const T* p, const T* q, int y, int skip, Weight how) {
+  const float a = to_f(p[y]), b = how == kLess ? to_f(q[y]) : 0.f;
+  return how == kLess ? weight<kLess>(a, b, false) : weight<kOthers>(a, b, how == kOthers && y == skip);
+}
+
+// The first lane whose sum (in the lanes' order, behind `before`) passes the aim, and what lies
+// before it; the last lane with any weight where rounding, or a u outside [0,1), leaves none (lane 0
+// if there is none).
+struct Pick {
+  float2 before;
+  int who;
+};
+__device__ __noinline__ Pick pick_lane(float2 mine, float2 before, float2 aim) {
+  const int lane = threadIdx.x & 31;
+  float2 incl = mine;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const float2 t = make_float2(__shfl_up_sync(0xffffffffu, incl.x, o), __shfl_up_sync(0xffffffffu, incl.y, o));
+    if (lane >= o) incl = sum(t, incl);
+  }
+  float2 excl = make_float2(__shfl_up_sync(0xffffffffu, incl.x, 1), __shfl_up_sync(0xffffffffu, incl.y, 1));
+  if (lane == 0) excl = make_float2(0.f, 0.f);
+  const unsigned over = __ballot_sync(0xffffffffu, mine.x > 0.f && more(sum(before, incl), aim));
+  const unsigned some = __ballot_sync(0xffffffffu, mine.x > 0.f);
+  const int who = over ? __ffs(over) - 1 : max(31 - __clz(some), 0);
+  return {sum(before, shfl(excl, who)), who};
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) draft_verify_kernel(const VerifyParams p) {
-  __shared__ double sums[2][MAX_CLUSTER * WARPS];    // of every warp of the cluster, in order
-  __shared__ int accepted;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+__global__ void __launch_bounds__(THREADS, CTAS) draft_verify_kernel(const VerifyParams p) {
+  constexpr int EACH = MAX_CLUSTER * WARPS / 32;     // warps of a cluster to a lane
+  __shared__ __align__(16) char stages[WARPS][STAGES * 2 * (CHUNK_BYTES + 16)];
+  __shared__ float2 sums[2][MAX_CLUSTER * WARPS];    // of every warp of the cluster, in order
+  __shared__ float2 runs[WARPS];                     // of the picked slice
+  __shared__ float2 found[2];                        // what lies before the picked warp, and the aim
+  __shared__ int accepted, rejected, picked, range[2];
+  __shared__ uint64_t arrived[2];                    // the sums of a pass
+  const int rank = cluster_rank(), ranks = cluster_size();
   const int n = blockIdx.x / ranks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* target = reinterpret_cast<const T*>(p.target) + n * p.target_seq;
@@ -71,21 +208,37 @@ __global__ void __launch_bounds__(THREADS) draft_verify_kernel(const VerifyParam
     }
     return;
   }
-  cluster.barrier_arrive();   // waited for before the first store into another CTA
+  const int64_t workers = (int64_t)ranks * WARPS, me = (int64_t)rank * WARPS + warp;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&arrived[i], 1);
+    tc::fence_mbar_init();
+    for (int i = 0; i < 2; ++i) tc::mbar_arrive_expect_tx(&arrived[i], (uint32_t)(workers * sizeof(float2)));
+  }
+  __syncwarp();
+  cluster_arrive();   // the barriers are there; waited for before the first sum is sent
+  float final_u = 0.f;
   if (warp == 0) {
+    final_u = u[p.T];
     int a = 0;
     while (a < nd) {
+      // (loaded for all T drafts: nothing waits for num)
       const int i = a + lane;
+      int y = -1;
       bool ok = false;
-      if (i < nd) {
-        const int y = x[i];
+      if (i < p.T) {
+        y = x[i];
         if (y >= 0 && y < p.V) {
           const double q = p.draft ? (double)to_f(draft[i * p.draft_row + y]) : 1.0;
-          ok = (double)u[i] * q < (double)to_f(target[i * p.target_row + y]);
+          ok = i < nd && (double)u[i] * q < (double)to_f(target[i * p.target_row + y]);
         }
       }
       const unsigned no = ~__ballot_sync(0xffffffffu, ok);
-      if (no) { a += __ffs(no) - 1; break; }
+      if (no) {
+        const int f = __ffs(no) - 1;
+        if (lane == f) rejected = y;
+        a += f;
+        break;
+      }
       a += 32;
     }
     if (lane == 0) accepted = min(a, nd);
@@ -99,82 +252,112 @@ __global__ void __launch_bounds__(THREADS) draft_verify_kernel(const VerifyParam
   }
   const T* pr = target + a * p.target_row;
   const T* qr = a < nd && p.draft ? draft + a * p.draft_row : nullptr;
-  const int skip = a < nd ? x[a] : -1;
+  const int skip = a < nd ? rejected : -1;
   Weight how = a == nd ? kTarget : qr ? kLess : kOthers;
 
-  const int64_t workers = (int64_t)ranks * WARPS, me = (int64_t)rank * WARPS + warp;
   const int lo = (int)(p.V * me / workers), hi = (int)(p.V * (me + 1) / workers);
   for (int pass = 0;; ++pass) {
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int y = lo + lane; y < hi; y += 32) add(s, weight(pr, qr, y, skip, how));
-    const double mine = warp_sum((double)s.x + (double)s.y);
-    if (pass == 0) cluster.barrier_wait();
-    if (lane < ranks) cluster.map_shared_rank(&sums[pass][0], lane)[me] = mine;
-    cluster.sync();
-    double total = 0.0, before = 0.0;
-    for (int w = 0; w < workers; ++w) {
-      const double v = sums[pass][w];
-      if (w == me) before = total;
-      total += v;
+    float2 s = how == kLess     ? sum_slice<T, kLess>(pr, qr, lo, hi, skip, stages[warp])
+               : how == kOthers ? sum_slice<T, kOthers>(pr, pr, lo, hi, skip, stages[warp])
+                                : sum_slice<T, kTarget>(pr, pr, lo, hi, skip, stages[warp]);
+    s = warp_sum(s);
+    __syncwarp();
+    if (pass == 0) cluster_wait();
+    if (lane < ranks) send(&sums[pass][me], &arrived[pass], lane, s);
+    if (warp == 0) {
+      const bool late = !tc::mbar_wait(&arrived[pass], 0);
+      __syncwarp();
+      float2 v[EACH], all = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        const int w = lane * EACH + i;
+        v[i] = w < workers ? sums[pass][w] : make_float2(0.f, 0.f);
+        add(all, v[i]);
+      }
+      const float2 total = warp_sum(all);
+      int pick = kNone;
+      if (__any_sync(0xffffffffu, late)) pick = kLate;
+      else if (total.x == 0.f && how != kTarget) pick = kAgain;
+      else if (total.x > 0.f && isfinite(total.x) && isfinite(total.y)) {
+        const float hi_u = __fmul_rn(final_u, total.x);
+        const float2 aim = make_float2(hi_u, __fmaf_rn(final_u, total.y, __fmaf_rn(final_u, total.x, -hi_u)));
+        const Pick lanes = pick_lane(all, make_float2(0.f, 0.f), aim);
+        // the same rule over the lane's own
+        int at = -1;
+        float2 before = lanes.before, lower = before;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+          if (v[i].x > 0.f && (at < 0 || !more(before, aim))) {
+            at = lane * EACH + i;
+            lower = before;
+            add(before, v[i]);
+          }
+        pick = __shfl_sync(0xffffffffu, at, lanes.who);
+        lower = shfl(lower, lanes.who);
+        if (lane == 0) {
+          found[0] = lower;
+          found[1] = aim;
+        }
+      }
+      if (lane == 0) picked = pick;
     }
-    if (!(total > 0.0) && how != kTarget && total == 0.0) {   // nothing is left: draw from p
+    __syncthreads();
+    if (picked == kAgain) {     // nothing is left: draw from p
       how = kTarget;
       continue;
     }
-    if (!(total > 0.0) || isinf(total)) {
-      if (rank == 0 && threadIdx.x == 0) tokens[a] = -1;
+    if (picked == kNone || picked == kLate) {
+      if (threadIdx.x == 0 && (rank == 0 || picked == kLate)) tokens[a] = -1;
+      if (threadIdx.x == 0 && picked == kLate) p.count[n] = -1;
       return;
     }
-    const double aim = (double)u[p.T] * total;
-    // the first warp whose slice passes the aim; the last one with any weight if rounding or a u
-    // outside [0,1) leaves none
-    int pick = -1, any = -1;
-    double run = 0.0;
-    for (int w = 0; w < workers; ++w) {
-      const double v = sums[pass][w];
-      run += v;
-      if (v > 0.0) any = w;
-      if (v > 0.0 && run > aim) { pick = w; break; }
+    if (picked / WARPS != rank) return;
+    // that slice once more, by the whole CTA: a run of neighbours to a thread, until the run with
+    // the token has a lane for each
+    float2 before = found[0];
+    const float2 aim = found[1];
+    int from = (int)(p.V * (int64_t)picked / workers), to = (int)(p.V * (int64_t)(picked + 1) / workers);
+    for (;;) {
+      const int per = (to - from + THREADS - 1) / THREADS;
+      const int b = min(from + (int)threadIdx.x * per, to), e = min(b + per, to);
+      float2 mine = make_float2(0.f, 0.f);
+#pragma unroll 8
+      for (int y = b; y < e; ++y) add(mine, one(pr, qr, y, skip, how));
+      const float2 r = warp_sum(mine);
+      if (lane == 0) runs[warp] = r;
+      __syncthreads();
+      const Pick warps = pick_lane(lane < WARPS ? runs[lane] : make_float2(0.f, 0.f), before, aim);
+      if (warp == warps.who) {
+        const Pick lanes = pick_lane(mine, warps.before, aim);
+        from = __shfl_sync(0xffffffffu, b, lanes.who);
+        to = __shfl_sync(0xffffffffu, e, lanes.who);
+        if (per <= 32) {
+          mine = from + lane < to ? one(pr, qr, from + lane, skip, how) : make_float2(0.f, 0.f);
+          const Pick last = pick_lane(mine, lanes.before, aim);
+          if (lane == last.who) tokens[a] = from + lane;
+        } else if (lane == 0) {
+          range[0] = from;
+          range[1] = to;
+          found[0] = lanes.before;
+        }
+      }
+      if (per <= 32) return;
+      __syncthreads();
+      from = range[0];
+      to = range[1];
+      before = found[0];
     }
-    if (pick < 0) pick = any;
-    if (pick != me) return;
-    // this warp's slice once more, a run of neighbours to a lane
-    const int len = hi - lo, per = (len + 31) / 32;
-    const int b = min(lo + lane * per, hi), e = min(b + per, hi);
-    double sum = 0.0;
-    for (int y = b; y < e; ++y) {
-      const float2 w = weight(pr, qr, y, skip, how);
-      sum += (double)w.x + (double)w.y;
-    }
-    double incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    const unsigned over = __ballot_sync(0xffffffffu, sum > 0.0 && before + incl > aim);
-    const unsigned some = __ballot_sync(0xffffffffu, sum > 0.0);
-    const int who = over ? __ffs(over) - 1 : 31 - __clz(some);
-    if (lane != who) return;
-    double at = before + (incl - sum);
-    int y = -1;
-    for (int i = b; i < e; ++i) {
-      const float2 w = weight(pr, qr, i, skip, how);
-      const double v = (double)w.x + (double)w.y;
-      if (!(v > 0.0)) continue;
-      at += v;
-      y = i;
-      if (at > aim) break;
-    }
-    tokens[a] = y;
-    return;
   }
 }
 
 template <typename T>
 cudaError_t go(const VerifyParams& p, cudaStream_t st) {
+  // as many CTAs to a sequence as one wave holds, each with a slice worth its start
   int ranks = MAX_CLUSTER;
+  const int wave = 152 * CTAS;
+  if (ranks > wave / p.N) ranks = wave / p.N;
+  if (ranks > (p.V + kSlice - 1) / kSlice) ranks = (p.V + kSlice - 1) / kSlice;
+  if (ranks < 1) ranks = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.N * ranks));
   cfg.blockDim = dim3(THREADS);

@@ -95,8 +95,10 @@ sf_status sf_linattn_commit(const sf_gdn_shape *shape, const void *k, const void
  *   tokens         int32 [N,T+1]: the accepted drafts, the drawn token, then -1.  The
  *                  drawn token is -1 where the weights' sum is not positive and finite.
  *   num_tokens     int32 [N]: accepted drafts + 1 (0 for padding): the tokens gained, and
- *                  the number to commit of [last token, draft 0, draft 1, ...]
- * A negative weight or a NaN counts as zero.  Products and sums are exact to 2^-45 or
+ *                  the number to commit of [last token, draft 0, draft 1, ...].  -1: a
+ *                  kernel's bounded internal wait expired (2 s; there is no workspace to
+ *                  say so in)
+ * A negative weight or a NaN counts as zero.  Products and sums are exact to 2^-40 or
  * better, so that a result does not depend on how the sums are split.
  * N >= 0, T >= 0 (T = 0: one token is drawn from p_0), V >= 1.
  * ---------------------------------------------------------------------- */

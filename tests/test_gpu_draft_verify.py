@@ -1,7 +1,7 @@
 """Verification of drafted tokens on the GPU against the FP64 oracle.  Tokens are whole numbers
-and have to be equal: the tests and sums behind them are exact to 2^-45, the oracle's to 2^-49 or
+and have to be equal: the tests and sums behind them are exact to 2^-40, the oracle's to 2^-49 or
 so, and the inputs' uniforms are at random (a draw differs if its uniform lies within that of a
-border between two tokens: 1e-13 times the number of tokens)."""
+border between two tokens: 1e-12 times the number of tokens)."""
 import pytest
 import torch
 

@@ -42,42 +42,42 @@ def _pool(state_cache, state_indices, N, H, V, K):
             _addr("state_indices", state_indices, (N,), _I32))
 
 
-def _draft(entry, q, k, v, rule, rule_at, state_cache, state_indices, num_tokens, pending, num_pending,
-           scale, out, stream):
-    """`rule`: the rule's own inputs of the tokens and their names; rule_at(tensors, N, T, H, prefix)
-    gives their addresses."""
-    dims = _tokens(q, v, state_cache, "q")
-    N, T, H, HK, K, V = dims
+def _draft(q, k, v, gate, beta, delta, state_cache, state_indices, num_tokens, pending, num_pending, scale,
+           out):
+    """Checks and addresses of a draft step: (shape, tokens, gates, num_tokens, pending, the rest), out."""
+    N, T, H, HK, K, V = _tokens(q, v, state_cache, "q")
     dt = q.dtype
-    shape = _draft_shape(N, T, H, HK, K, V, dt, scale)[1]
-    args = (_at("q", q), _addr("k", k, q.shape, dt), _addr("v", v, (N, T, H, V), dt),
-            *rule_at(rule, N, T, H, ""), _addr("num_tokens", num_tokens, (N,), _I32))
+    vs = (N, T, H, V)
+    tokens = (_at("q", q), _addr("k", k, q.shape, dt), _addr("v", v, vs, dt))
+    gates = ()
+    if delta:
+        gates = (_addr("gate", _need("gate", gate), (N, T, H), _F32),
+                 _addr("beta", _need("beta", beta), (N, T, H), _F32))
+    num = _addr("num_tokens", num_tokens, (N,), _I32)
     pend = None
     if pending is not None:
-        pk, pv = pending[:2]
+        if len(pending) != (4 if delta else 2):
+            raise ValueError("pending must be (k, v, gate, beta)" if delta else "pending must be (k, v)")
+        pk = pending[0]
         if pk.dim() != 4:
             raise ValueError("pending k must be [N,P,HK,K]")
         P = pk.shape[1]
-        gates = rule_at(pending[2:], N, P, H, "pending ")
+        pg = pb = None
+        if delta:
+            pg = _addr("pending gate", _need("pending gate", pending[2]), (N, P, H), _F32)
+            pb = _addr("pending beta", _need("pending beta", pending[3]), (N, P, H), _F32)
         pend = sf_pending(P, _addr("pending k", pk, (N, P, HK, K), dt),
-                          _addr("pending v", pv, (N, P, H, V), dt),
-                          *(gates if len(pending) == 4 else (None, None)),
+                          _addr("pending v", pending[1], (N, P, H, V), dt), pg, pb,
                           _addr("num_pending", num_pending, (N,), _I32))
-        pend = ctypes.byref(pend)
     elif num_pending is not None:
         raise ValueError("num_pending needs pending tokens")
     pool = _pool(state_cache, state_indices, N, H, V, K)
     if out is None:
         out = torch.empty_like(v)
-    to = _addr("out", out, (N, T, H, V), dt)
-    _check(entry(shape, *args, pend, *pool, to, _stream(stream, q.device)))
-    return out
-
-
-def _gates(tensors, N, T, H, prefix):
-    gate, beta = tensors
-    return (_addr(prefix + "gate", _need(prefix + "gate", gate), (N, T, H), _F32),
-            _addr(prefix + "beta", _need(prefix + "beta", beta), (N, T, H), _F32))
+        to = out.data_ptr()
+    else:
+        to = _addr("out", out, vs, dt)
+    return (_draft_shape(N, T, H, HK, K, V, dt, scale)[1], tokens, gates, num, pend, (*pool, to)), out
 
 
 @on_its_stream
@@ -89,23 +89,21 @@ def sf_gdn_draft_step(q, k, v, gate, beta, state_cache, state_indices=None, num_
     state_indices (as sf_gdn_step), by the first num_pending (int32 [N]; None: all) of the
     ``pending`` tokens (k [N,P,HK,K], v [N,P,H,V], gate, beta [N,P,H]); the drafts leave it as
     it then is.  Returns out [N,T,H,V], zero behind num_tokens and in padding."""
-    if pending is not None and len(pending) != 4:
-        raise ValueError("pending must be (k, v, gate, beta)")
-    return _draft(load().sf_gdn_draft_step, q, k, v, (gate, beta), _gates, state_cache, state_indices,
-                  num_tokens, pending, num_pending, scale, out, stream)
+    (shape, tokens, gates, num, pend, rest), out = _draft(
+        q, k, v, gate, beta, True, state_cache, state_indices, num_tokens, pending, num_pending, scale, out)
+    _check(load().sf_gdn_draft_step(shape, *tokens, *gates, num, pend, *rest, _stream(stream, q.device)))
+    return out
 
 
 @on_its_stream
 def sf_linattn_draft_step(q, k, v, decay, state_cache, state_indices=None, num_tokens=None,
                           pending=None, num_pending=None, scale=None, out=None, stream=None):
     """sf_gdn_draft_step for linear attention: decay [H]; pending (k, v)."""
-    if pending is not None and len(pending) != 2:
-        raise ValueError("pending must be (k, v)")
-
-    def at(_, N, T, H, prefix):
-        return () if prefix else (_addr("decay", _need("decay", decay), (H,), _F32),)
-    return _draft(load().sf_linattn_draft_step, q, k, v, (), at, state_cache, state_indices,
-                  num_tokens, pending, num_pending, scale, out, stream)
+    (shape, tokens, _, num, pend, rest), out = _draft(
+        q, k, v, None, None, False, state_cache, state_indices, num_tokens, pending, num_pending, scale, out)
+    decay = _addr("decay", _need("decay", decay), (v.shape[2],), _F32)
+    _check(load().sf_linattn_draft_step(shape, *tokens, decay, num, pend, *rest, _stream(stream, q.device)))
+    return out
 
 
 @on_its_stream
@@ -115,7 +113,8 @@ def sf_gdn_commit(k, v, gate, beta, state_cache, state_indices=None, num_tokens=
     N, T, H, HK, K, V = _tokens(k, v, state_cache)
     shape = _draft_shape(N, T, H, HK, K, V, k.dtype, None)[1]
     _check(load().sf_gdn_commit(shape, _at("k", k), _addr("v", v, (N, T, H, V), k.dtype),
-                                *_gates((gate, beta), N, T, H, ""),
+                                _addr("gate", _need("gate", gate), (N, T, H), _F32),
+                                _addr("beta", _need("beta", beta), (N, T, H), _F32),
                                 _addr("num_tokens", num_tokens, (N,), _I32),
                                 *_pool(state_cache, state_indices, N, H, V, K),
                                 _stream(stream, k.device)))
@@ -182,26 +181,33 @@ def sf_draft_verify(target_probs, draft_tokens, uniforms, draft_probs=None, num_
 
 
 def _state_pool(caches):
-    """The pool struct of one cache or several, [num_slots, ...] each, and what it points to."""
-    caches = (caches,) if isinstance(caches, torch.Tensor) else tuple(caches)
-    if not caches:
-        raise ValueError("at least one cache is needed")
-    slots = caches[0].shape[0] if caches[0].dim() else 0
+    """The pool struct of one cache or several, [num_slots, ...] each, and their device."""
+    if isinstance(caches, torch.Tensor):
+        caches = (caches,)
     n = len(caches)
-    at, size = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)()
-    for i, c in enumerate(caches):
+    if n == 0:
+        raise ValueError("at least one cache is needed")
+    first = caches[0]
+    slots = first.shape[0] if first.dim() else 0
+    at, size = [], []
+    for c in caches:
         if c.dim() < 2 or c.shape[0] != slots or slots < 1:
             raise ValueError(f"caches must be [num_slots, ...] of one num_slots >= 1, got {tuple(c.shape)}")
-        at[i] = _at(f"caches[{i}]", c)
-        size[i] = c.numel() // slots * c.element_size()
-    return sf_state_pool(slots, n, at, size), caches[0].device
+        at.append(_at("caches", c))
+        size.append(c.nbytes // slots)
+    return sf_state_pool(slots, n, (ctypes.c_void_p * n)(*at), (ctypes.c_size_t * n)(*size)), first.device
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(slots, rows):
+    return load().sf_state_workspace(slots, rows)
 
 
 def sf_state_workspace(caches, rows):
     """A workspace for sf_state_fork (rows: the number of parents) and sf_state_compact (of
     indices) on a pool, to be kept and passed as ``ws``."""
     cache = caches if isinstance(caches, torch.Tensor) else caches[0]
-    return torch.empty(load().sf_state_workspace(cache.shape[0], rows), dtype=torch.uint8, device=cache.device)
+    return torch.empty(_workspace_bytes(cache.shape[0], rows), dtype=torch.uint8, device=cache.device)
 
 
 def _vector(name, t):
@@ -222,13 +228,17 @@ def sf_state_copy(caches, src, dst, stream=None):
 
 
 def _plan_args(pool, device, reserved, rows, out, ws):
+    slots = pool.num_slots
     if out is None:
-        out = torch.empty((rows,), dtype=_I32, device=device)
-    to = _addr("out", out, (rows,), _I32)
+        out = torch.empty(rows, dtype=_I32, device=device)
+        to = out.data_ptr()
+    else:
+        to = _addr("out", out, (rows,), _I32)
     if ws is None:
-        ws = torch.empty(load().sf_state_workspace(pool.num_slots, rows), dtype=torch.uint8, device=device)
-    ws = _ws(ws)
-    return out, (_addr("reserved", reserved, (pool.num_slots,), torch.bool), to, ws.data_ptr(), ws.numel())
+        ws = torch.empty(_workspace_bytes(slots, rows), dtype=torch.uint8, device=device)
+    else:
+        _ws(ws)
+    return out, ws, (_addr("reserved", reserved, (slots,), torch.bool), to, ws.data_ptr(), ws.numel())
 
 
 @on_its_stream
@@ -240,7 +250,7 @@ def sf_state_fork(caches, state_indices, parents, reserved=None, out=None, ws=No
     pool, device = _state_pool(caches)
     idx, N = _vector("state_indices", state_indices)
     par, M = _vector("parents", parents)
-    out, tail = _plan_args(pool, device, reserved, M, out, ws)
+    out, ws, tail = _plan_args(pool, device, reserved, M, out, ws)
     _check(load().sf_state_fork(ctypes.byref(pool), idx, N, par, M, *tail, _stream(stream, device)))
     return out
 
@@ -251,6 +261,6 @@ def sf_state_compact(caches, state_indices, reserved=None, out=None, ws=None, st
     for ``reserved`` slots (bool [num_slots]), which stay.  Returns where each is then, int32 [N]."""
     pool, device = _state_pool(caches)
     idx, N = _vector("state_indices", state_indices)
-    out, tail = _plan_args(pool, device, reserved, N, out, ws)
+    out, ws, tail = _plan_args(pool, device, reserved, N, out, ws)
     _check(load().sf_state_compact(ctypes.byref(pool), idx, N, *tail, _stream(stream, device)))
     return out

@@ -48,13 +48,15 @@ sf_status draft(const char* fn, const sf_gdn_shape* s, const sfg::DraftTokens& f
     if (!aligned4(t->gate) || !aligned4(t->beta) || !aligned4(t->num))
       return report(SF_ERR_INVALID_ARG, "%s: gates and counts must be 4-byte aligned", fn);
   }
-  if (!aligned16(out) || !aligned16(pool) || !aligned4(idx) || !aligned4(decay))
-    return report(SF_ERR_INVALID_ARG, "%s: out and state_cache must be 16-byte aligned", fn);
-  if ((long long)s->N * s->H * (s->K / 64) > 0x7fffffffLL)
+  if (!aligned16(out) || (reinterpret_cast<uintptr_t>(pool) & 31) || !aligned4(idx) || !aligned4(decay))
+    return report(SF_ERR_INVALID_ARG, "%s: out must be 16-byte aligned, state_cache 32-byte", fn);
+  if ((long long)s->N * s->H > 1LL << 27)
     return report(SF_ERR_UNSUPPORTED, "%s: N * H is too large for one launch", fn);
   sfg::DraftParams p{};
   p.fresh = fresh; p.pend = pend; p.decay = delta ? nullptr : decay; p.pool = pool; p.idx = idx; p.out = out;
-  p.N = s->N; p.H = s->H; p.HK = sfg::eff_hk(s); p.num_slots = num_slots; p.scale = sfg::eff_scale(s);
+  p.N = s->N; p.H = s->H; p.HK = sfg::eff_hk(s);
+  p.by_head = sfg::FastDiv::of(p.H); p.by_group = sfg::FastDiv::of(p.H / p.HK);
+  p.num_slots = num_slots; p.scale = sfg::eff_scale(s);
   return cuda_status(sfg::launch_draft_step(p, s->dtype == SF_BF16, s->K, reinterpret_cast<cudaStream_t>(stream)),
                      fn);
 }

@@ -1,0 +1,470 @@
+// draft_mma.cu -- several BF16 tokens of every sequence on the paged pool of FP32 states [V,K]
+// (include/sf_decode.h): accepted tokens advance the state, drafted ones read it.
+//
+// Tokens go in groups of up to 8, the chunk form over each (draft_step.cu), the state advanced
+// between them.  A warp holds 16 rows of a state in registers and needs no other warp: with
+// g = lane / 4, t = lane % 4 a lane holds of rows g and g + 8 the columns 32 j + 8 t .. + 7.  That is at
+// once
+//  * an accumulator of 16x8 products and the left operand of 16x8x16 products, if column pair e of
+//    every lane is taken as one tile of 8 columns (the sum's order is free);
+//  * for a token g in BF16, the right operand of those (S k, S q of 8 tokens), both operands of the
+//    tokens' own products, and through movmatrix the right operand of the update W K.
+// So nothing passes through shared memory but the tokens' 8x8 products and 16x8 results, for the
+// solve, one row to a lane, and the next strip's state, copied ahead by the lane that reads it.
+//
+// Precision: what reaches the state is FP32.  For accepted tokens the state that k reads and the
+// rows' weights W are split into three BF16 summands (24 bits), and the update's sum is formed apart
+// and added to the state by one FP32 multiply-add with rounding to nearest, so that the state has
+// no bias of the tensor core's sums.  Drafts read two summands (16 bits, 2^-17 of an element):
+// nothing of them is kept but outputs that are rounded to 2^-9.
+//
+// A warp takes four strips of a head in a row, with their tokens and what those are to each other in
+// shared memory, then four strips of the head that comes next in the whole grid's order: the grid moves
+// through the pool as one window.
+//
+// Bound by memory, 4 V K bytes read and as many written (if a token was accepted), and by the chain
+// of a strip's steps (1400 instructions with both kinds of tokens, two warps to a scheduler).  Measured,
+// K = 128: 128 sequences of 32 heads, 5 + 5 tokens 96 us (537 MB, 5.7 TB/s, 84 % of the copy rate),
+// 256 of 16 heads, 8 + 8 tokens by linear attention 98 us, a commit of 8 tokens 92 us; one sequence
+// of 16 heads 4.9 us.  The same movement without any tokens' work takes 88-95 us.  What it came
+// from: FP32 pipes with shared-memory tokens 156, 148, 120 us; states loaded where they are used
+// 164, 149, 113; copied ahead 158, 146, 121; factors and tokens of a run of strips kept 100, 114,
+// 102; whole rows to a copy and whole lines to a store, eight warps an SM and a window 96, 98, 92.
+// Twelve warps an SM (168 registers, some spilled) 98, 109, 95; runs of one strip 115, 102, 88.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "decode.cuh"
+#include "f32x2.cuh"
+
+namespace sfg {
+namespace {
+
+constexpr int GROUP = 8;      // tokens
+constexpr int STRIP = 16;     // rows of a state to a warp
+constexpr int CTAS = 8;       // of one warp each, on an SM
+constexpr int RUN = 4;        // strips of a head that a warp takes in a row
+constexpr int LD = 12;        // floats between rows of 8 in shared memory: 8 lanes' 16 bytes in distinct banks
+
+// A group's tokens in shared memory.  q and k as a lane reads them (token g, columns 32 j + 8 t .. + 7).
+template <int D>
+struct Tokens {
+  uint4 k[D / 32][32];
+  __nv_bfloat16 v[GROUP][STRIP];
+  float gate[GROUP], beta[GROUP];
+};
+// What a group's tokens are to each other.
+struct Factors {
+  float A[GROUP * GROUP];                     // R_ij (k_i . k_j), column j together
+  float c[GROUP], rest[GROUP];                // c_i, R_mi
+};
+template <int D>
+struct Scratch {                              // of a warp
+  float4 state[STRIP][D / 4];                 // the next strip's; in odd rows 16-byte units 2 i, 2 i + 1 swapped
+  Tokens<D> pend, fresh;
+  uint4 q[D / 32][32];
+  Factors fp, ff;
+  float B[GROUP * GROUP];                     // R_ij (q_i . k_j) of fresh tokens
+  float dk[STRIP * LD], dq[STRIP * LD];       // S k, then the rows' weights; S q
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// (from zero)
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <int BYTES>
+__device__ __forceinline__ void copy(void* to, const void* from) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(BYTES) : "memory");
+}
+// The same, or zeros in its place (`from` is not read then).
+template <int BYTES>
+__device__ __forceinline__ void copy_or_zero(void* to, const void* from, bool on) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(to), n = on ? BYTES : 0;
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(from), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(s), "l"(from), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the LEFT last groups of copies.
+template <int LEFT>
+__device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// 32 bytes of a lane: four lanes write a whole line.
+__device__ __forceinline__ void store32(float* to, float2 a, float2 b, float2 c, float2 d) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y),
+               "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y) : "memory");
+}
+
+// A strip: its number, its sequence's slot and accepted and drafted tokens (both 0: nothing to do).
+struct Strip {
+  unsigned at;
+  int slot, a, m;
+};
+struct Place {
+  int n, h, row0;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const DraftParams& p, unsigned at) {
+  const int nh = (int)(at / (D / STRIP)), n = p.by_head(nh);
+  return {n, nh - n * p.H, (int)(at % (D / STRIP)) * STRIP};
+}
+template <int D>
+__device__ __forceinline__ Strip strip_at(const DraftParams& p, unsigned at, unsigned strips) {
+  Strip s{at, 0, 0, 0};
+  if (at >= strips) return s;
+  const int n = p.by_head((int)(s.at / (D / STRIP)));
+  s.slot = p.idx ? p.idx[n] : n;
+  if (p.idx ? s.slot > 0 && s.slot < p.num_slots : s.slot < p.num_slots) {
+    s.a = p.pend.num ? min(max(p.pend.num[n], 0), p.pend.rows) : p.pend.rows;
+    s.m = p.fresh.num ? min(max(p.fresh.num[n], 0), p.fresh.rows) : p.fresh.rows;
+  }
+  return s;
+}
+template <int D>
+__device__ __forceinline__ float* state_of(const DraftParams& p, const Strip& s) {
+  const Place at = place_of<D>(p, s.at);
+  return p.pool + (((int64_t)s.slot * p.H + at.h) * D + at.row0) * D;
+}
+// (Whole rows to a copy.)
+template <int D>
+__device__ __forceinline__ void fetch_state(const DraftParams& p, const Strip& s, Scratch<D>& w) {
+  if (s.a | s.m) {
+    constexpr int U = D / 4, R = 32 / U > 0 ? 32 / U : 1;    // units of a row, rows of a copy
+    const int lane = threadIdx.x & 31, r = lane / U, c = lane % U;
+    const float* S = state_of<D>(p, s) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < STRIP / R; ++i) copy<16>(&w.state[i * R + r][c ^ ((i * R + r) & 1)], S + i * R * D);
+  }
+  commit();
+}
+// The group from token `first` of `count` on; what lies behind its last token is zero.  Where the
+// buffer has the head's tokens (`all` false) the strip's values alone.
+template <int D, bool kDelta, bool kFresh>
+__device__ __forceinline__ void fetch_tokens(const DraftParams& p, const DraftTokens& tok, Tokens<D>& to,
+                                             uint4 (*q)[32], unsigned strip, int first, int count, bool all = true) {
+  const int m = min(count - first, GROUP);
+  if (m > 0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const Place at = place_of<D>(p, strip);
+    const int64_t token0 = (int64_t)at.n * tok.rows + first;
+    if (all) {
+      // (a token behind the last one of the sequence is not read: any address of the tensor does)
+      const int64_t mine = ((token0 + (g < m ? g : 0)) * p.HK + p.by_group(at.h)) * D + 8 * t;
+      const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(tok.k) + mine;
+      const __nv_bfloat16* x = kFresh ? reinterpret_cast<const __nv_bfloat16*>(tok.q) + mine : nullptr;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        copy_or_zero<16>(&to.k[j][lane], k + j * 32, g < m);
+        if (kFresh) copy_or_zero<16>(&q[j][lane], x + j * 32, g < m);
+      }
+    }
+    if (lane < 2 * GROUP) {
+      const int i = lane & 7, i2 = lane >> 1, half = (lane & 1) * 8;
+      if (kDelta && all && i < m)
+        copy<4>(lane < GROUP ? &to.gate[i] : &to.beta[i],
+                (lane < GROUP ? tok.gate : tok.beta) + (token0 + i) * p.H + at.h);
+      copy_or_zero<16>(&to.v[i2][half],
+                       reinterpret_cast<const __nv_bfloat16*>(tok.v) +
+                           ((token0 + (i2 < m ? i2 : 0)) * p.H + at.h) * D + at.row0 + half, i2 < m);
+    }
+  }
+  commit();
+}
+
+// The factors of a group of m tokens.
+template <int D, bool kDelta, bool kFresh>
+__device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D>& tok, Factors& f, Scratch<D>& w,
+                                        unsigned strip, int m) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // the decay of token lane % 8
+  float lam = 1.f;
+  if ((lane & 7) < m) lam = expf(kDelta ? tok.gate[lane & 7] : p.decay[place_of<D>(p, strip).h]);
+  if (kDelta || kFresh) {
+    // k_i . k_j (rows g) and q_i . k_j (rows g + 8) for j = 2 t, 2 t + 1
+    float c[4] = {};
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const uint4 k = tok.k[j][lane], q = kFresh ? w.q[j][lane] : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {k.x, q.x, k.y, q.y}, y[4] = {k.z, q.z, k.w, q.w};
+      mma_bf16(c, x, k.x, k.y);
+      mma_bf16(c, y, k.z, k.w);
+    }
+    float R0 = 1.f, R1 = 1.f;
+#pragma unroll
+    for (int l = 1; l < GROUP; ++l) {
+      const float x = __shfl_sync(0xffffffffu, lam, l);
+      if (l <= g && l > 2 * t) R0 *= x;
+      if (l <= g && l > 2 * t + 1) R1 *= x;
+    }
+    if (kDelta) {
+      f.A[2 * t * GROUP + g] = R0 * c[0];
+      f.A[(2 * t + 1) * GROUP + g] = R1 * c[1];
+    }
+    if (kFresh) {
+      w.B[2 * t * GROUP + g] = R0 * c[2];
+      w.B[(2 * t + 1) * GROUP + g] = R1 * c[3];
+    }
+  }
+  // products of the decays up to a token and from behind it to the last one
+  float c = lam, rest = __shfl_down_sync(0xffffffffu, lam, 1, 8);
+  if ((lane & 7) == 7) rest = 1.f;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, c, o, 8), y = __shfl_down_sync(0xffffffffu, rest, o, 8);
+    if ((lane & 7) >= o) c *= x;
+    if ((lane & 7) + o < 8) rest *= y;
+  }
+  if (lane < GROUP) {
+    f.c[lane] = c;
+    f.rest[lane] = rest;
+  }
+  __syncwarp();
+}
+
+// One group of m tokens (1 .. 8) from row `first` of its tokens.  kFresh: outputs; update: the state
+// is advanced.  s[j][e][i]: row g + 8 i, columns 32 j + 8 t + 2 e, + 1.
+template <int D, bool kDelta, bool kFresh>
+__device__ __forceinline__ void group(const DraftParams& p, const Tokens<D>& tok, const Factors& f,
+                                      float2 (&s)[D / 32][4][2], Scratch<D>& w, const Strip& strip, int first,
+                                      int m, bool update) {
+  constexpr int J = D / 32;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r = lane & 15;
+  if (kDelta || kFresh) {
+    // S k and S q
+    constexpr int SUMMANDS = kFresh ? 2 : 3;
+    float ck[2][4] = {}, cq[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint4 k = tok.k[j][lane], q = kFresh ? w.q[j][lane] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float2 x[4] = {s[j][e][0], s[j][e][1], s[j][e + 1][0], s[j][e + 1][1]};
+#pragma unroll
+        for (int l = 0; l < SUMMANDS; ++l) {
+          uint32_t a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = pack2(x[i]);
+            if (l + 1 < SUMMANDS) x[i] = sub2(x[i], unpack2(a[i]));
+          }
+          if (kDelta) mma_bf16(ck[l & 1], a, e ? k.z : k.x, e ? k.w : k.y);
+          if (kFresh) mma_bf16(cq[l & 1], a, e ? q.z : q.x, e ? q.w : q.y);
+        }
+      }
+    }
+    if (kDelta) {
+      *reinterpret_cast<float2*>(&w.dk[g * LD + 2 * t]) = make_float2(ck[0][0] + ck[1][0], ck[0][1] + ck[1][1]);
+      *reinterpret_cast<float2*>(&w.dk[(g + 8) * LD + 2 * t]) = make_float2(ck[0][2] + ck[1][2], ck[0][3] + ck[1][3]);
+    }
+    if (kFresh) {
+      *reinterpret_cast<float2*>(&w.dq[g * LD + 2 * t]) = make_float2(cq[0][0] + cq[1][0], cq[0][1] + cq[1][1]);
+      *reinterpret_cast<float2*>(&w.dq[(g + 8) * LD + 2 * t]) = make_float2(cq[0][2] + cq[1][2], cq[0][3] + cq[1][3]);
+    }
+    __syncwarp();
+  }
+
+  // u of row r (both halves of the warp the same) and the outputs, column by column of A and B
+  auto load8 = [](float (&x)[GROUP], const float* from) {
+    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from);
+    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(from + 4);
+  };
+  float u[GROUP], o[GROUP], c[GROUP];
+  if (kDelta) load8(u, &w.dk[r * LD]);
+  if (kFresh) load8(o, &w.dq[r * LD]);
+  load8(c, f.c);
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) {
+    const float v = __bfloat162float(tok.v[i][r]);
+    u[i] = kDelta ? fmaf(-c[i], u[i], v) : v;
+    if (kFresh) o[i] *= c[i];
+  }
+  __nv_bfloat16* out = nullptr;
+  const int step = p.H * D;
+  if (kFresh) {
+    const Place at = place_of<D>(p, strip.at);
+    out = reinterpret_cast<__nv_bfloat16*>(p.out) +
+          (((int64_t)at.n * p.fresh.rows + first) * p.H + at.h) * D + at.row0 + r;
+  }
+#pragma unroll
+  for (int j = 0; j < GROUP; ++j) {
+    if (j >= m) break;
+    float x[GROUP];
+    if (kDelta) {
+      u[j] *= tok.beta[j];
+      load8(x, &f.A[j * GROUP]);
+#pragma unroll
+      for (int i = j + 1; i < GROUP; ++i) u[i] = fmaf(-x[i], u[j], u[i]);
+    }
+    if (kFresh) {
+      load8(x, &w.B[j * GROUP]);
+#pragma unroll
+      for (int i = j; i < GROUP; ++i) o[i] = fmaf(x[i], u[j], o[i]);
+      if (lane >> 4 == (j & 1)) *out = __float2bfloat16_rn(p.scale * o[j]);
+      out += step;
+    }
+  }
+  if (!update) {
+    __syncwarp();
+    return;
+  }
+
+  // S = c_m S + sum_j R_mj u_j k_j^T
+  const float ce = c[GROUP - 1];
+  load8(c, f.rest);
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) u[i] = i < m ? u[i] * c[i] : 0.f;
+  __syncwarp();
+  if (lane < STRIP) {
+    *reinterpret_cast<float4*>(&w.dk[r * LD]) = make_float4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<float4*>(&w.dk[r * LD + 4]) = make_float4(u[4], u[5], u[6], u[7]);
+  }
+  __syncwarp();
+  uint32_t a[4], last[2];     // rows g, g + 8: the first two summands as 16 columns, and the third
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float2 x = *reinterpret_cast<const float2*>(&w.dk[(g + 8 * i) * LD + 2 * t]);
+    a[i] = pack2(x);
+    x = sub2(x, unpack2(a[i]));
+    a[i + 2] = pack2(x);
+    last[i] = pack2(sub2(x, unpack2(a[i + 2])));
+  }
+  const float2 c2 = make_float2(ce, ce);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const uint4 k = tok.k[j][lane];
+    const uint32_t pairs[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float d[4];
+      const uint32_t x = transpose8(pairs[e]);
+      mma_bf16_k8(d, last[0], last[1], x);
+      mma_bf16(d, a, x, x);
+      s[j][e][0] = fma2(c2, s[j][e][0], make_float2(d[0], d[1]));
+      s[j][e][1] = fma2(c2, s[j][e][1], make_float2(d[2], d[3]));
+    }
+  }
+  __syncwarp();
+}
+
+template <int D, bool kDelta>
+__global__ void __launch_bounds__(32, CTAS) draft_mma_kernel(const DraftParams p) {
+  constexpr int J = D / 32;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x, g = lane >> 2, t = lane & 3;
+  Scratch<D>& w = *reinterpret_cast<Scratch<D>*>(smem);
+  // A warp takes `run` strips of a head in a row, then the run as many warps on: the tokens and their
+  // factors stay for a run.
+  const unsigned run = p.run;     // a power of two
+  const unsigned strips = (unsigned)p.N * p.H * (D / STRIP), ahead = gridDim.x * run;
+  unsigned where = blockIdx.x * run;
+  auto next_at = [&](unsigned x) { return (x + 1) & (run - 1) ? x + 1 : x + 1 - run + ahead; };
+  Strip at = strip_at<D>(p, where, strips), next = strip_at<D>(p, next_at(where), strips);
+  // Copies are committed in the order state and pending tokens of a strip, fresh tokens of it, state of
+  // the next one, ...: each where the buffer is free, a phase or two ahead of its use.
+  fetch_state(p, at, w);
+  fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, at.at, 0, at.a);
+  fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, at.at, 0, at.m);
+  bool new_pend = true, new_fresh = true;   // the buffers hold tokens whose factors are not formed yet
+#pragma unroll 1
+  for (; where < strips; where = next_at(where)) {
+    Strip after = next;
+    after.at = next_at(next.at);
+    if ((after.at & (run - 1)) == 0) after = strip_at<D>(p, after.at, strips);
+    if (at.m < p.fresh.rows) {
+      const Place pl = place_of<D>(p, where);
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) +
+                           ((int64_t)pl.n * p.fresh.rows * p.H + pl.h) * D + pl.row0;
+      for (int i = at.m * STRIP + lane; i < p.fresh.rows * STRIP; i += 32)
+        out[(int64_t)(i / STRIP) * p.H * D + i % STRIP] = __float2bfloat16_rn(0.f);
+    }
+    const bool last = ((where + 1) & (run - 1)) == 0;
+    float2 s[J][4][2];
+    wait<1>();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float4 x = w.state[g + 8 * i][(8 * j + 2 * t + e / 2) ^ (g & 1)];
+          s[j][e][i] = make_float2(x.x, x.y);
+          s[j][e + 1][i] = make_float2(x.z, x.w);
+        }
+    __syncwarp();
+    fetch_state(p, next, w);
+#pragma unroll 1
+    for (int first = 0; first < at.a; first += GROUP) {
+      if (first > 0) {
+        fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, at.at, first, at.a);
+        wait<0>();
+        __syncwarp();
+      }
+      const int m = min(at.a - first, GROUP);
+      if (first > 0 || new_pend) factors<D, kDelta, false>(p, w.pend, w.fp, w, at.at, m);
+      group<D, kDelta, false>(p, w.pend, w.fp, s, w, at, first, m, true);
+    }
+    new_pend = last || at.a > GROUP;
+    fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, next.at, 0, next.a, new_pend);
+    if (at.a > 0) {
+      float* S = state_of<D>(p, at) + g * D + 8 * t;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) store32(S + i * 8 * D + j * 32, s[j][0][i], s[j][1][i], s[j][2][i], s[j][3][i]);
+    }
+    wait<2>();
+    __syncwarp();
+#pragma unroll 1
+    for (int first = 0; first < at.m; first += GROUP) {
+      if (first > 0) {
+        fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, at.at, first, at.m);
+        wait<0>();
+        __syncwarp();
+      }
+      const int m = min(at.m - first, GROUP);
+      if (first > 0 || new_fresh) factors<D, kDelta, true>(p, w.fresh, w.ff, w, at.at, m);
+      group<D, kDelta, true>(p, w.fresh, w.ff, s, w, at, first, m, first + GROUP < at.m);
+    }
+    new_fresh = last || at.m > GROUP;
+    fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, next.at, 0, next.m, new_fresh);
+    at = next;
+    next = after;
+  }
+}
+
+template <int D, bool kDelta>
+cudaError_t go(DraftParams p, cudaStream_t st) {
+  const int strips = p.N * p.H * (D / STRIP);
+  p.run = strips <= 152 * CTAS ? 1 : RUN;
+  const int want = strips / p.run, grid = want < 152 * CTAS ? want : 152 * CTAS;
+  const int bytes = (int)sizeof(Scratch<D>);
+  auto kernel = draft_mma_kernel<D, kDelta>;
+  static_assert(sizeof(Scratch<D>) <= 48 * 1024, "no opt-in to more shared memory");
+  kernel<<<grid, 32, bytes, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_draft_mma(const DraftParams& p, int D, cudaStream_t st) {
+  if (D == 128) return p.decay ? go<128, false>(p, st) : go<128, true>(p, st);
+  return p.decay ? go<64, false>(p, st) : go<64, true>(p, st);
+}
+
+}  // namespace sfg

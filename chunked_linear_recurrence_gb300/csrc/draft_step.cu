@@ -1,4 +1,4 @@
-// draft_step.cu -- several tokens of every sequence on the paged pool of FP32 states [V,K]
+// draft_step.cu -- several FP32 tokens of every sequence on the paged pool of FP32 states [V,K]
 // (include/sf_decode.h): accepted tokens advance the state, drafted ones read it.
 //
 // Chunk form over m tokens from the state S0, with lam_i = e^{gate_i} (e^{decay_h}),
@@ -9,8 +9,6 @@
 // The R_ij are products, not exponentials of differences of sums, so that a gate of -inf gives 0
 // and not NaN.  The state is touched 2 m times for the drafts and 2 m + 1 for the accepted ones,
 // against 4 m for each by the rule itself.
-#include <cuda_bf16.h>
-
 #include "common.cuh"
 #include "decode.cuh"
 
@@ -22,12 +20,6 @@ constexpr int THREADS = 128;  // 4 warps of 16 rows; 8 lanes share a row
 constexpr int RL = 4;         // rows of a lane
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
@@ -74,20 +66,20 @@ __device__ __forceinline__ float* carve(float* s, Tok& t, int rows, int D, bool 
   return s;
 }
 
-template <typename T, int D, bool kDelta>
+template <int D, bool kDelta>
 __device__ __forceinline__ void load_tokens(const DraftTokens& g, const Tok& t, int m, int n, int h, int hk,
                                             int row0, const DraftParams& p) {
   constexpr int LK = D / 4;
   for (int i = threadIdx.x; i < m * LK; i += THREADS) {
     const int r = i / LK, c = (i % LK) * 4;
     const size_t at = (((size_t)n * g.rows + r) * p.HK + hk) * D + c;
-    *reinterpret_cast<float4*>(t.k + r * D + c) = ld4(reinterpret_cast<const T*>(g.k) + at);
-    if (t.q) *reinterpret_cast<float4*>(t.q + r * D + c) = ld4(reinterpret_cast<const T*>(g.q) + at);
+    *reinterpret_cast<float4*>(t.k + r * D + c) = ld4(static_cast<const float*>(g.k) + at);
+    if (t.q) *reinterpret_cast<float4*>(t.q + r * D + c) = ld4(static_cast<const float*>(g.q) + at);
   }
   for (int i = threadIdx.x; i < m * (ROWS / 4); i += THREADS) {
     const int r = i / (ROWS / 4), c = (i % (ROWS / 4)) * 4;
     const size_t at = (((size_t)n * g.rows + r) * p.H + h) * D + row0 + c;
-    *reinterpret_cast<float4*>(t.v + r * ROWS + c) = ld4(reinterpret_cast<const T*>(g.v) + at);
+    *reinterpret_cast<float4*>(t.v + r * ROWS + c) = ld4(static_cast<const float*>(g.v) + at);
   }
   for (int r = threadIdx.x; r < m; r += THREADS) {
     const size_t at = ((size_t)n * g.rows + r) * p.H + h;
@@ -168,7 +160,7 @@ __device__ __forceinline__ void solve(const Tok& t, int m, int rows) {
   }
 }
 
-template <typename T, int D, bool kDelta>
+template <int D, bool kDelta>
 __global__ void __launch_bounds__(THREADS) draft_step_kernel(const DraftParams p) {
   extern __shared__ __align__(16) float smem[];
   constexpr int CPS = D / ROWS;       // CTAs of a state
@@ -177,13 +169,13 @@ __global__ void __launch_bounds__(THREADS) draft_step_kernel(const DraftParams p
   const int nh = blockIdx.x / CPS, n = nh / p.H, h = nh % p.H, hk = h / (p.H / p.HK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row0 = part * ROWS;
   const int P = p.pend.rows, M = p.fresh.rows;
-  T* out = reinterpret_cast<T*>(p.out);
+  float* out = static_cast<float*>(p.out);
   const int slot = p.idx ? p.idx[n] : n;
   const bool live = p.idx ? slot > 0 && slot < p.num_slots : slot < p.num_slots;
   int a = !live ? 0 : p.pend.num ? min(max(p.pend.num[n], 0), P) : P;
   int m = !live ? 0 : p.fresh.num ? min(max(p.fresh.num[n], 0), M) : M;
   for (int i = m * ROWS + threadIdx.x; i < M * ROWS; i += THREADS)
-    out[(((size_t)n * M + i / ROWS) * p.H + h) * D + row0 + i % ROWS] = from_f<T>(0.f);
+    out[(((size_t)n * M + i / ROWS) * p.H + h) * D + row0 + i % ROWS] = 0.f;
   if (a == 0 && m == 0) return;
 
   const int r0 = warp * 16 + (lane >> 3) * RL, c = (lane & 7) * 4;
@@ -198,8 +190,8 @@ __global__ void __launch_bounds__(THREADS) draft_step_kernel(const DraftParams p
   float* next = carve(smem, tp, P, D, false, kDelta);
   next += -(next - smem) & 3;
   carve(next, tm, M, D, true, kDelta);
-  load_tokens<T, D, kDelta>(p.pend, tp, a, n, h, hk, row0, p);
-  load_tokens<T, D, kDelta>(p.fresh, tm, m, n, h, hk, row0, p);
+  load_tokens<D, kDelta>(p.pend, tp, a, n, h, hk, row0, p);
+  load_tokens<D, kDelta>(p.fresh, tm, m, n, h, hk, row0, p);
   __syncthreads();
   products<D, kDelta>(tp, a, P);
   products<D, kDelta>(tm, m, M);
@@ -245,35 +237,30 @@ __global__ void __launch_bounds__(THREADS) draft_step_kernel(const DraftParams p
     const int i = e / ROWS, r = e % ROWS;
     float o = tm.c[i] * tm.dq[i * ROWS + r];
     for (int j = 0; j <= i; ++j) o = fmaf(tm.B[i * M + j], tm.dk[j * ROWS + r], o);
-    out[(((size_t)n * M + i) * p.H + h) * D + row0 + r] = from_f<T>(p.scale * o);
+    out[(((size_t)n * M + i) * p.H + h) * D + row0 + r] = p.scale * o;
   }
 }
 
-template <typename T, int D, bool kDelta>
+template <int D, bool kDelta>
 cudaError_t go(const DraftParams& p, cudaStream_t st) {
-  const int64_t grid = (int64_t)p.N * p.H * (D / ROWS);
-  if (grid <= 0 || p.pend.rows + p.fresh.rows == 0) return cudaSuccess;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  const int grid = p.N * p.H * (D / ROWS);
   const size_t bytes = 4 * (tok_floats(p.pend.rows, D, false, kDelta) + tok_floats(p.fresh.rows, D, true, kDelta));
-  auto kernel = draft_step_kernel<T, D, kDelta>;
+  auto kernel = draft_step_kernel<D, kDelta>;
   if (bytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)grid, THREADS, bytes, st>>>(p);
+  kernel<<<grid, THREADS, bytes, st>>>(p);
   return cudaGetLastError();
-}
-
-template <typename T, int D>
-cudaError_t rule(const DraftParams& p, cudaStream_t st) {
-  return p.decay ? go<T, D, false>(p, st) : go<T, D, true>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_draft_step(const DraftParams& p, bool bf16, int D, cudaStream_t st) {
-  if (bf16) return D == 128 ? rule<__nv_bfloat16, 128>(p, st) : rule<__nv_bfloat16, 64>(p, st);
-  return D == 128 ? rule<float, 128>(p, st) : rule<float, 64>(p, st);
+  if (p.N < 1 || p.pend.rows + p.fresh.rows == 0) return cudaSuccess;
+  if (bf16) return launch_draft_mma(p, D, st);
+  if (D == 128) return p.decay ? go<128, false>(p, st) : go<128, true>(p, st);
+  return p.decay ? go<64, false>(p, st) : go<64, true>(p, st);
 }
 
 }  // namespace sfg

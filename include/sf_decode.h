@@ -52,9 +52,10 @@ typedef struct {
  *                  from num_tokens[n] on are zero, and nothing in the inputs' rows there
  *                  (NaN, infinities) reaches a result; the same for pending rows.
  *   state_cache, num_slots, state_indices: as sf_gdn_step.  Padding gives zero rows.
- * 16-byte aligned tensors; out overlaps no input.  All arithmetic is FP32: a token is
- * a row of the chunk form (dot products with the state before the tokens, and a
- * triangular solve over them), whatever other tokens the call holds.
+ * 16-byte aligned tensors, a 32-byte aligned state_cache; out overlaps no input.  The
+ * tokens go through the chunk form (dot products with the state before eight tokens, and a
+ * triangular solve over them).  States are computed in FP32; FP32 outputs too.  Outputs of
+ * BF16 tokens are rounded from FP32 sums over the state's first 16 bits.
  * ---------------------------------------------------------------------- */
 sf_status sf_gdn_draft_step(const sf_gdn_shape *shape, const void *q, const void *k, const void *v,
                             const float *gate, const float *beta, const int32_t *num_tokens,

@@ -9,6 +9,7 @@ import torch
 FAKE = ctypes.c_void_p(1 << 20)          # 16-byte aligned, never dereferenced
 ODD = ctypes.c_void_p((1 << 20) + 4)
 BYTE = ctypes.c_void_p((1 << 20) + 1)
+HALF = ctypes.c_void_p((1 << 20) + 16)   # (states are stored 32 bytes at a time)
 
 
 @pytest.fixture(scope="module")
@@ -61,7 +62,7 @@ def test_draft_steps_and_commits_reject_bad_pointers(lib, delta):
     assert _draft(lib, delta, None) == 1 and _commit(lib, delta, None) == 1
     for kw in (dict(q=None), dict(q=ODD), dict(k=None), dict(k=ODD), dict(v=None), dict(v=ODD), dict(rule=None),
                dict(rule=BYTE), dict(num=BYTE), dict(cache=None), dict(cache=ODD), dict(out=None), dict(out=ODD),
-               dict(idx=BYTE), dict(slots=-1), dict(idx=None, slots=2)):
+               dict(cache=HALF), dict(idx=BYTE), dict(slots=-1), dict(idx=None, slots=2)):
         assert _draft(lib, delta, s, **kw) == 1, kw
         if not set(kw) & {"q", "out"}:
             assert _commit(lib, delta, s, **kw) == 1, kw

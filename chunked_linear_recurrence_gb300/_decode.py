@@ -229,16 +229,19 @@ def sf_state_copy(caches, src, dst, stream=None):
 
 def _plan_args(pool, device, reserved, rows, out, ws):
     slots = pool.num_slots
+    reserved = _addr("reserved", reserved, (slots,), torch.bool)
     if out is None:
         out = torch.empty(rows, dtype=_I32, device=device)
         to = out.data_ptr()
+        if ws is None and slots <= 4096 and rows <= 1024 and pool.num_caches <= 64:
+            return out, None, (reserved, to, None, 0)        # (none is used)
     else:
         to = _addr("out", out, (rows,), _I32)
     if ws is None:
         ws = torch.empty(_workspace_bytes(slots, rows), dtype=torch.uint8, device=device)
     else:
         _ws(ws)
-    return out, ws, (_addr("reserved", reserved, (slots,), torch.bool), to, ws.data_ptr(), ws.numel())
+    return out, ws, (reserved, to, ws.data_ptr(), ws.numel())
 
 
 @on_its_stream

@@ -60,7 +60,10 @@ struct PoolPlan {
   int32_t* count;             // ... and how many
   int32_t* first;             // fork: [num_slots]
 };
-cudaError_t launch_pool_plan(const PoolPlan& p, cudaStream_t st);
+// The plan, and its copies in every cache: in one launch that needs no workspace, or in two.
+bool pool_move_needs_workspace(const PoolPlan& plan, int num_caches);
+cudaError_t launch_pool_move(const PoolPlan& plan, int num_caches, void* const* caches,
+                             const size_t* slot_bytes, cudaStream_t st);
 // Copies of src[i] to dst[i], i < *count (or rows where count is NULL), in every cache.
 cudaError_t launch_pool_copy(int num_slots, int num_caches, void* const* caches,
                              const size_t* slot_bytes, const int32_t* src, const int32_t* dst,

@@ -86,21 +86,19 @@ sf_status check_pool(const sf_state_pool* p, const char* fn) {
 // A plan over `rows` rows, then the copies it gives.
 sf_status planned(const char* fn, const sf_state_pool* pool, sfg::PoolPlan p, int rows, void* ws, size_t ws_bytes,
                   sf_stream_t stream) {
-  const size_t need = sf_state_workspace(pool->num_slots, rows);
-  if (!ws || !aligned16(ws) || ws_bytes < need)
-    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn, need);
-  char* at = static_cast<char*>(ws);
-  p.count = reinterpret_cast<int32_t*>(at);
-  p.src = reinterpret_cast<int32_t*>(at + 256);
-  p.dst = reinterpret_cast<int32_t*>(at + 256 + round_up((size_t)rows * 4));
-  p.first = reinterpret_cast<int32_t*>(at + 256 + 2 * round_up((size_t)rows * 4));
   p.num_slots = pool->num_slots;
-  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = sfg::launch_pool_plan(p, cs);
-  if (e == cudaSuccess)
-    e = sfg::launch_pool_copy(pool->num_slots, pool->num_caches, pool->caches, pool->slot_bytes, p.src, p.dst, p.count,
-                              rows, cs);
-  return cuda_status(e, fn);
+  if (sfg::pool_move_needs_workspace(p, pool->num_caches)) {
+    const size_t need = sf_state_workspace(pool->num_slots, rows);
+    if (!ws || !aligned16(ws) || ws_bytes < need)
+      return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn, need);
+    char* at = static_cast<char*>(ws);
+    p.count = reinterpret_cast<int32_t*>(at);
+    p.src = reinterpret_cast<int32_t*>(at + 256);
+    p.dst = reinterpret_cast<int32_t*>(at + 256 + round_up((size_t)rows * 4));
+    p.first = reinterpret_cast<int32_t*>(at + 256 + 2 * round_up((size_t)rows * 4));
+  }
+  return cuda_status(sfg::launch_pool_move(p, pool->num_caches, pool->caches, pool->slot_bytes,
+                                           reinterpret_cast<cudaStream_t>(stream)), fn);
 }
 
 }  // namespace

@@ -105,7 +105,7 @@ def _pool(slots=8, sizes=(1 << 16,), at=None):
 
 
 def test_pool_operators_reject_bad_arguments(lib):
-    need = lib.sf_state_workspace(8, 4)
+    need = lib.sf_state_workspace(8, 4)      # used here, because out and the indices are one
     copy = lambda p, src=FAKE, dst=FAKE, M=4: lib.sf_state_copy(p, src, dst, M, None)   # noqa: E731
     fork = lambda p, idx=FAKE, N=4, par=FAKE, M=4, res=None, out=FAKE, ws=FAKE, n=need: lib.sf_state_fork(   # noqa: E731
         p, idx, N, par, M, res, out, ws, n, None)

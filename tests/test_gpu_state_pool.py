@@ -197,3 +197,24 @@ def test_replayed_in_a_graph_and_on_another_stream():
     side.synchronize()
     new, copies = od.fork(idx.tolist(), parents.tolist(), 40)
     assert got.tolist() == new and torch.equal(x[0], moved(caches, copies)[0])
+
+
+def test_more_rows_than_a_plan_in_every_cta_takes():
+    """Both forms of the move, side by side: in place, and with the new indices apart, on either side
+    of the sizes where the plan is made once."""
+    import chunked_linear_recurrence_gb300 as sf
+    for slots, rows in ((4096, 1024), (4097, 1024), (4096, 1025), (4100, 1100)):
+        r = np.random.RandomState(slots + rows)
+        idx = i32(r.randint(-1, slots + 1, rows))
+        parents = i32(r.randint(-1, rows + 1, rows))
+        res = mask(slots, r.randint(1, slots, 50))
+        a = torch.arange(slots * 4, device="cuda").view(slots, 4)
+        b, at = a.clone(), idx.clone()
+        new, copies = od.fork(idx.tolist(), parents.tolist(), slots, set(res.nonzero()[:, 0].tolist()))
+        got = sf.sf_state_fork(a, idx, parents, reserved=res)
+        sf.sf_state_fork(b, at, parents, reserved=res, out=at)
+        assert got.tolist() == new and torch.equal(got, at) and torch.equal(a, b)
+        new, _ = od.compact(got.tolist(), slots, set(res.nonzero()[:, 0].tolist()))
+        got = sf.sf_state_compact(a, got, reserved=res)
+        sf.sf_state_compact(b, at, reserved=res, out=at)
+        assert got.tolist() == new and torch.equal(got, at) and torch.equal(a, b)

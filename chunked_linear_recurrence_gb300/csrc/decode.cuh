@@ -26,12 +26,11 @@ struct DraftParams {
   const int32_t* idx;   // [N] or NULL
   void* out;
   int N, H, HK, num_slots;
-  int run;                      // strips of a head that a warp takes in a row (BF16)
+  int run;                      // strips of a head that a warp takes in a row
   FastDiv by_head, by_group;    // of H, H / HK
   float scale;
 };
 cudaError_t launch_draft_step(const DraftParams& p, bool bf16, int D, cudaStream_t st);
-cudaError_t launch_draft_mma(const DraftParams& p, int D, cudaStream_t st);   // BF16 tokens
 
 struct VerifyParams {
   const void* target;

@@ -1,4 +1,4 @@
-// draft_step.cu -- several FP32 tokens of every sequence on the paged pool of FP32 states [V,K]
+// draft_step.cu -- several tokens of every sequence on the paged pool of FP32 states [V,K]
 // (include/sf_decode.h): accepted tokens advance the state, drafted ones read it.
 //
 // Chunk form over m tokens from the state S0, with lam_i = e^{gate_i} (e^{decay_h}),
@@ -7,260 +7,545 @@
 //     out_i = scale (c_i S0 q_i + sum_{j<=i} R_ij (q_i . k_j) u_j)
 //     S_m   = c_m S0 + sum_j R_mj u_j k_j^T
 // The R_ij are products, not exponentials of differences of sums, so that a gate of -inf gives 0
-// and not NaN.  The state is touched 2 m times for the drafts and 2 m + 1 for the accepted ones,
-// against 4 m for each by the rule itself.
+// and not NaN.  The state is touched twice a token by the drafts, and twice and once more by the
+// accepted ones, against four times each by the rule itself.
+//
+// Tokens go in groups of up to 8, the state advanced between them.  A warp holds 16 rows of a state in registers and needs no other warp: with
+// g = lane / 4, t = lane % 4 a lane holds of rows g and g + 8 the columns 32 j + 8 t .. + 7.  That is at
+// once
+//  * an accumulator of 16x8 products and the left operand of 16x8x16 products, if column pair e of
+//    every lane is taken as one tile of 8 columns (the sum's order is free);
+//  * for a token g in BF16, the right operand of those (S k, S q of 8 tokens), both operands of the
+//    tokens' own products, and through movmatrix the right operand of the update W K.
+// So nothing passes through shared memory but the tokens' 8x8 products and 16x8 results, for the
+// solve, one row to a lane, and the next strip's state, copied ahead by the lane that reads it.
+//
+// Precision: what reaches the state is FP32.  For accepted tokens the state that k reads and the
+// rows' weights W are split into three BF16 summands (24 bits), and the update's sum is formed apart
+// and added to the state by one FP32 multiply-add with rounding to nearest, so that the state has
+// no bias of the tensor core's sums.  BF16 drafts read two summands (16 bits, 2^-17 of an element):
+// nothing of them is kept but outputs that are rounded to 2^-9.  FP32 tokens are split into three
+// summands themselves, and the six products down to 2^-24 are formed everywhere.
+//
+// A warp takes four strips of a head in a row, with their tokens and what those are to each other in
+// shared memory, then four strips of the head that comes next in the whole grid's order: the grid moves
+// through the pool as one window.
+//
+// Bound by memory, 4 V K bytes read and as many written (if a token was accepted), and by the chain
+// of a strip's steps (1400 instructions with both kinds of tokens, two warps to a scheduler).  Measured,
+// K = 128: 128 sequences of 32 heads, 5 + 5 tokens 96 us (537 MB, 5.7 TB/s, 84 % of the copy rate),
+// 256 of 16 heads, 8 + 8 tokens by linear attention 98 us, a commit of 8 tokens 92 us; one sequence
+// of 16 heads 4.6 us.  The same movement without any tokens' work takes 88 us.  What it came
+// from: FP32 pipes with shared-memory tokens 156, 148, 120 us; states loaded where they are used
+// 164, 149, 113; copied ahead 158, 146, 121; factors and tokens of a run of strips kept 100, 114,
+// 102; whole rows to a copy and whole lines to a store, eight warps an SM and a window 96, 98, 92.
+// Twelve warps an SM (168 registers, some spilled) 98, 109, 95; runs of one strip 115, 102, 88;
+// summands by truncation and byte permutes instead of conversions: the same.  FP32 tokens, 64
+// sequences of 32 heads: 5 + 5 tokens 85 us, a commit of 8 53 us (on the FP32 pipes 85, 68; floor
+// 41); 16 + 16 tokens 253 us, BF16 90 (each strip loads the tokens of its later groups again).
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 #include "decode.cuh"
+#include "f32x2.cuh"
 
 namespace sfg {
 namespace {
 
-constexpr int ROWS = 64;      // rows of a state that a CTA holds
-constexpr int THREADS = 128;  // 4 warps of 16 rows; 8 lanes share a row
-constexpr int RL = 4;         // rows of a lane
+constexpr int GROUP = 8;      // tokens
+constexpr int STRIP = 16;     // rows of a state to a warp
+template <typename T>
+constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;     // BF16 summands of a token
+// CTAs of one warp each on an SM.
+template <int D, typename T>
+constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : 16) : (D == 128 ? 7 : 14);
+constexpr int RUN = 4;        // strips of a head that a warp takes in a row
+constexpr int LD = 12;        // floats between rows of 8 in shared memory: 8 lanes' 16 bytes in distinct banks
 
-__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
-}
-
-// Sums 4 values over 8 lanes; a lane ends with value (lane / 2) % 4.
-__device__ __forceinline__ float sum_rows(float (&x)[RL], int lane) {
-  const bool b4 = lane & 4, b2 = lane & 2;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float send = b4 ? x[i] : x[i + 2], keep = b4 ? x[i + 2] : x[i];
-    x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
-  }
-  const float send = b2 ? x[0] : x[1], keep = b2 ? x[1] : x[0];
-  const float y = keep + __shfl_xor_sync(0xffffffffu, send, 2);
-  return y + __shfl_xor_sync(0xffffffffu, y, 1);
-}
-
-// A CTA's tokens in shared memory, FP32.
-struct Tok {
-  float *k, *q, *v;          // [rows][D], [rows][D], [rows][ROWS]
-  float *A, *B;              // [rows][rows]: R_ij (k_i . k_j), R_ij (q_i . k_j)
-  float *lam, *beta, *c;     // [rows]
-  float *dk, *dq;            // [rows][ROWS]: S0 k_i (then u_i), S0 q_i
+// A group's tokens in shared memory.  q and k as a lane reads them (token g, columns 32 j + 8 t .. + 7).
+template <int D, typename T>
+struct Tokens {
+  uint4 k[PLANES<T>][D / 32][32];
+  T v[GROUP][STRIP];
+  float gate[GROUP], beta[GROUP];
 };
-constexpr size_t tok_floats(int rows, int D, bool reads, bool delta) {
-  const size_t n = (size_t)rows * (D + ROWS + 3 + ROWS) + (delta ? (size_t)rows * rows : 0) +
-                   (reads ? (size_t)rows * (D + ROWS + rows) : 0);
-  return (n + 3) / 4 * 4;
+// What a group's tokens are to each other.
+struct Factors {
+  float A[GROUP * GROUP];                     // R_ij (k_i . k_j), column j together
+  float c[GROUP], rest[GROUP];                // c_i, R_mi
+};
+template <int D, typename T>
+struct Scratch {                              // of a warp
+  float4 state[STRIP][D / 4];                 // the next strip's; in odd rows 16-byte units 2 i, 2 i + 1 swapped
+  Tokens<D, T> pend, fresh;
+  uint4 q[PLANES<T>][D / 32][32];
+  Factors fp, ff;
+  float B[GROUP * GROUP];                     // R_ij (q_i . k_j) of fresh tokens
+  float dk[STRIP * LD], dq[STRIP * LD];       // S k, then the rows' weights; S q
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float* carve(float* s, Tok& t, int rows, int D, bool reads, bool delta) {
-  t.k = s; s += rows * D;
-  t.v = s; s += rows * ROWS;
-  t.dk = s; s += rows * ROWS;
-  t.q = t.dq = t.A = t.B = nullptr;
-  if (reads) {
-    t.q = s; s += rows * D;
-    t.dq = s; s += rows * ROWS;
-    t.B = s; s += rows * rows;
+// (from zero)
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <int BYTES>
+__device__ __forceinline__ void copy(void* to, const void* from) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(BYTES) : "memory");
+}
+// The same, or zeros in its place (`from` is not read then).
+template <int BYTES>
+__device__ __forceinline__ void copy_or_zero(void* to, const void* from, bool on) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(to), n = on ? BYTES : 0;
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(from), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(s), "l"(from), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the LEFT last groups of copies.
+template <int LEFT>
+__device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// 32 bytes of a lane: four lanes write a whole line.
+__device__ __forceinline__ void store32(float* to, float2 a, float2 b, float2 c, float2 d) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y),
+               "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y) : "memory");
+}
+
+// A strip: its number, its sequence's slot and accepted and drafted tokens (both 0: nothing to do).
+struct Strip {
+  unsigned at;
+  int slot, a, m;
+};
+struct Place {
+  int n, h, row0;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const DraftParams& p, unsigned at) {
+  const int nh = (int)(at / (D / STRIP)), n = p.by_head(nh);
+  return {n, nh - n * p.H, (int)(at % (D / STRIP)) * STRIP};
+}
+template <int D>
+__device__ __forceinline__ Strip strip_at(const DraftParams& p, unsigned at, unsigned strips) {
+  Strip s{at, 0, 0, 0};
+  if (at >= strips) return s;
+  const int n = p.by_head((int)(s.at / (D / STRIP)));
+  s.slot = p.idx ? p.idx[n] : n;
+  if (p.idx ? s.slot > 0 && s.slot < p.num_slots : s.slot < p.num_slots) {
+    s.a = p.pend.num ? min(max(p.pend.num[n], 0), p.pend.rows) : p.pend.rows;
+    s.m = p.fresh.num ? min(max(p.fresh.num[n], 0), p.fresh.rows) : p.fresh.rows;
   }
-  if (delta) { t.A = s; s += rows * rows; }
-  t.lam = s; s += rows;
-  t.beta = s; s += rows;
-  t.c = s; s += rows;
   return s;
 }
-
-template <int D, bool kDelta>
-__device__ __forceinline__ void load_tokens(const DraftTokens& g, const Tok& t, int m, int n, int h, int hk,
-                                            int row0, const DraftParams& p) {
-  constexpr int LK = D / 4;
-  for (int i = threadIdx.x; i < m * LK; i += THREADS) {
-    const int r = i / LK, c = (i % LK) * 4;
-    const size_t at = (((size_t)n * g.rows + r) * p.HK + hk) * D + c;
-    *reinterpret_cast<float4*>(t.k + r * D + c) = ld4(static_cast<const float*>(g.k) + at);
-    if (t.q) *reinterpret_cast<float4*>(t.q + r * D + c) = ld4(static_cast<const float*>(g.q) + at);
+template <int D>
+__device__ __forceinline__ float* state_of(const DraftParams& p, const Strip& s) {
+  const Place at = place_of<D>(p, s.at);
+  return p.pool + (((int64_t)s.slot * p.H + at.h) * D + at.row0) * D;
+}
+// (Whole rows to a copy.)
+template <int D, typename T>
+__device__ __forceinline__ void fetch_state(const DraftParams& p, const Strip& s, Scratch<D, T>& w) {
+  if (s.a | s.m) {
+    constexpr int U = D / 4, R = 32 / U > 0 ? 32 / U : 1;    // units of a row, rows of a copy
+    const int lane = threadIdx.x & 31, r = lane / U, c = lane % U;
+    const float* S = state_of<D>(p, s) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < STRIP / R; ++i) copy<16>(&w.state[i * R + r][c ^ ((i * R + r) & 1)], S + i * R * D);
   }
-  for (int i = threadIdx.x; i < m * (ROWS / 4); i += THREADS) {
-    const int r = i / (ROWS / 4), c = (i % (ROWS / 4)) * 4;
-    const size_t at = (((size_t)n * g.rows + r) * p.H + h) * D + row0 + c;
-    *reinterpret_cast<float4*>(t.v + r * ROWS + c) = ld4(static_cast<const float*>(g.v) + at);
-  }
-  for (int r = threadIdx.x; r < m; r += THREADS) {
-    const size_t at = ((size_t)n * g.rows + r) * p.H + h;
-    t.lam[r] = expf(kDelta ? g.gate[at] : p.decay[h]);
-    t.beta[r] = kDelta ? g.beta[at] : 1.f;
+  commit();
+}
+// Eight FP32 values of a lane as three BF16 summands each (zeros if not `on`).
+template <int J>
+__device__ __forceinline__ void split_to(uint4 (*to)[J][32], int j, const float* from, bool on) {
+  const float4 a = on ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 b = on ? *reinterpret_cast<const float4*>(from + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 x[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+#pragma unroll
+  for (int l = 0; l < 3; ++l) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[i] = pack2(x[i]);
+      x[i] = sub2(x[i], unpack2(u[i]));
+    }
+    to[l][j][threadIdx.x & 31] = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
-
-// A, B and c.
-template <int D, bool kDelta>
-__device__ __forceinline__ void products(const Tok& t, int m, int rows) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = warp; e < m * m; e += THREADS / 32) {
-    const int i = e / m, j = e % m;
-    if (j > i || (!t.B && (j == i || !kDelta))) continue;
-    float kk = 0.f, qk = 0.f;
+// The group from token `first` of `count` on; what lies behind its last token is zero.  Where the
+// buffer has the head's tokens (`all` false) the strip's values alone.
+template <int D, bool kDelta, bool kFresh, typename T>
+__device__ __forceinline__ void fetch_tokens(const DraftParams& p, const DraftTokens& tok, Tokens<D, T>& to,
+                                             uint4 (*q)[D / 32][32], unsigned strip, int first, int count,
+                                             bool all = true) {
+  const int m = min(count - first, GROUP);
+  if (m > 0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const Place at = place_of<D>(p, strip);
+    const int64_t token0 = (int64_t)at.n * tok.rows + first;
+    if (all) {
+      // (a token behind the last one of the sequence is not read: any address of the tensor does)
+      const int64_t mine = ((token0 + (g < m ? g : 0)) * p.HK + p.by_group(at.h)) * D + 8 * t;
+      const T* k = reinterpret_cast<const T*>(tok.k) + mine;
+      const T* x = kFresh ? reinterpret_cast<const T*>(tok.q) + mine : nullptr;
 #pragma unroll
-    for (int c = lane; c < D; c += 32) {
-      const float b = t.k[j * D + c];
-      if (kDelta) kk = fmaf(t.k[i * D + c], b, kk);
-      if (t.B) qk = fmaf(t.q[i * D + c], b, qk);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      kk += __shfl_xor_sync(0xffffffffu, kk, o);
-      qk += __shfl_xor_sync(0xffffffffu, qk, o);
-    }
-    float R = 1.f;
-    for (int l = j + 1; l <= i; ++l) R *= t.lam[l];
-    if (lane == 0) {
-      if (kDelta) t.A[i * rows + j] = R * kk;
-      if (t.B) t.B[i * rows + j] = R * qk;
-    }
-  }
-  for (int i = threadIdx.x; i < m; i += THREADS) {
-    float c = 1.f;
-    for (int l = 0; l <= i; ++l) c *= t.lam[l];
-    t.c[i] = c;
-  }
-}
-
-// dk, dq: the dot products of the CTA's rows of S with the tokens.
-template <int D, bool kDelta>
-__device__ __forceinline__ void read_state(const float4 (&s)[RL][D / 32], const Tok& t, int m) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = (lane & 7) * 4, row = warp * 16 + (lane >> 3) * RL + ((lane >> 1) & 3);
-  for (int i = 0; i < m; ++i) {
-#pragma unroll
-    for (int what = 0; what < 2; ++what) {
-      const float* x = what ? t.q : t.k;
-      if (what ? !t.q : !kDelta) continue;
-      float a[RL] = {};
-#pragma unroll
-      for (int b = 0; b < D / 32; ++b) {
-        const float4 y = ld4(x + i * D + b * 32 + c);
-#pragma unroll
-        for (int r = 0; r < RL; ++r) a[r] = dot4(s[r][b], y, a[r]);
-      }
-      const float y = sum_rows(a, lane);
-      if (!(lane & 1)) (what ? t.dq : t.dk)[i * ROWS + row] = y;
-    }
-  }
-}
-
-// dk becomes u.
-template <bool kDelta>
-__device__ __forceinline__ void solve(const Tok& t, int m, int rows) {
-  const int r = threadIdx.x;
-  if (r >= ROWS) return;
-  for (int i = 0; i < m; ++i) {
-    float u = t.v[i * ROWS + r];
-    if (kDelta) {
-      u = fmaf(-t.c[i], t.dk[i * ROWS + r], u);
-      for (int j = 0; j < i; ++j) u = fmaf(-t.A[i * rows + j], t.dk[j * ROWS + r], u);
-      u *= t.beta[i];
-    }
-    t.dk[i * ROWS + r] = u;
-  }
-}
-
-template <int D, bool kDelta>
-__global__ void __launch_bounds__(THREADS) draft_step_kernel(const DraftParams p) {
-  extern __shared__ __align__(16) float smem[];
-  constexpr int CPS = D / ROWS;       // CTAs of a state
-  constexpr int CV = D / 32;
-  const int part = blockIdx.x % CPS;
-  const int nh = blockIdx.x / CPS, n = nh / p.H, h = nh % p.H, hk = h / (p.H / p.HK);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row0 = part * ROWS;
-  const int P = p.pend.rows, M = p.fresh.rows;
-  float* out = static_cast<float*>(p.out);
-  const int slot = p.idx ? p.idx[n] : n;
-  const bool live = p.idx ? slot > 0 && slot < p.num_slots : slot < p.num_slots;
-  int a = !live ? 0 : p.pend.num ? min(max(p.pend.num[n], 0), P) : P;
-  int m = !live ? 0 : p.fresh.num ? min(max(p.fresh.num[n], 0), M) : M;
-  for (int i = m * ROWS + threadIdx.x; i < M * ROWS; i += THREADS)
-    out[(((size_t)n * M + i / ROWS) * p.H + h) * D + row0 + i % ROWS] = 0.f;
-  if (a == 0 && m == 0) return;
-
-  const int r0 = warp * 16 + (lane >> 3) * RL, c = (lane & 7) * 4;
-  float* S = p.pool + (((size_t)slot * p.H + h) * D + row0 + r0) * D + c;
-  float4 s[RL][CV];
-#pragma unroll
-  for (int r = 0; r < RL; ++r)
-#pragma unroll
-    for (int b = 0; b < CV; ++b) s[r][b] = ld4(S + (size_t)r * D + b * 32);
-
-  Tok tp, tm;
-  float* next = carve(smem, tp, P, D, false, kDelta);
-  next += -(next - smem) & 3;
-  carve(next, tm, M, D, true, kDelta);
-  load_tokens<D, kDelta>(p.pend, tp, a, n, h, hk, row0, p);
-  load_tokens<D, kDelta>(p.fresh, tm, m, n, h, hk, row0, p);
-  __syncthreads();
-  products<D, kDelta>(tp, a, P);
-  products<D, kDelta>(tm, m, M);
-  if (a > 0) {
-    read_state<D, kDelta>(s, tp, a);
-    __syncthreads();
-    solve<kDelta>(tp, a, P);
-    __syncthreads();
-    const float ce = tp.c[a - 1];
-#pragma unroll
-    for (int r = 0; r < RL; ++r)
-#pragma unroll
-      for (int b = 0; b < CV; ++b) { s[r][b].x *= ce; s[r][b].y *= ce; s[r][b].z *= ce; s[r][b].w *= ce; }
-    float R = 1.f;
-    for (int i = a - 1; i >= 0; --i) {
-      float w[RL];
-#pragma unroll
-      for (int r = 0; r < RL; ++r) w[r] = R * tp.dk[i * ROWS + r0 + r];
-#pragma unroll
-      for (int b = 0; b < CV; ++b) {
-        const float4 y = ld4(tp.k + i * D + b * 32 + c);
-#pragma unroll
-        for (int r = 0; r < RL; ++r) {
-          s[r][b].x = fmaf(w[r], y.x, s[r][b].x);
-          s[r][b].y = fmaf(w[r], y.y, s[r][b].y);
-          s[r][b].z = fmaf(w[r], y.z, s[r][b].z);
-          s[r][b].w = fmaf(w[r], y.w, s[r][b].w);
+      for (int j = 0; j < D / 32; ++j) {
+        if constexpr (PLANES<T> == 1) {
+          copy_or_zero<16>(&to.k[0][j][lane], k + j * 32, g < m);
+          if (kFresh) copy_or_zero<16>(&q[0][j][lane], x + j * 32, g < m);
+        } else {
+          split_to(to.k, j, k + j * 32, g < m);
+          if (kFresh) split_to(q, j, x + j * 32, g < m);
         }
       }
-      R *= tp.lam[i];
+    }
+    constexpr int E = 16 / sizeof(T), UNITS = STRIP / E;      // units of a token's values
+    const int i = lane & 7, i2 = lane / UNITS, part = lane % UNITS * E;
+    if (kDelta && all && lane < 2 * GROUP && i < m)
+      copy<4>(lane < GROUP ? &to.gate[i] : &to.beta[i],
+              (lane < GROUP ? tok.gate : tok.beta) + (token0 + i) * p.H + at.h);
+    if (lane < GROUP * UNITS)
+      copy_or_zero<16>(&to.v[i2][part],
+                       reinterpret_cast<const T*>(tok.v) + ((token0 + (i2 < m ? i2 : 0)) * p.H + at.h) * D + at.row0 +
+                           part, i2 < m);
+  }
+  commit();
+}
+
+// The factors of a group of m tokens.
+template <int D, bool kDelta, bool kFresh, typename T>
+__device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>& tok, Factors& f, Scratch<D, T>& w,
+                                        unsigned strip, int m) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // the decay of token lane % 8
+  float lam = 1.f;
+  if ((lane & 7) < m) lam = expf(kDelta ? tok.gate[lane & 7] : p.decay[place_of<D>(p, strip).h]);
+  if (kDelta || kFresh) {
+    // k_i . k_j (rows g) and q_i . k_j (rows g + 8) for j = 2 t, 2 t + 1
+    float c[4] = {};
+#pragma unroll
+    for (int l = 0; l < PLANES<T>; ++l)
+#pragma unroll
+      for (int o = 0; o + l < PLANES<T>; ++o)
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 k = tok.k[l][j][lane], q = kFresh ? w.q[l][j][lane] : make_uint4(0, 0, 0, 0);
+          const uint4 z = tok.k[o][j][lane];
+          const uint32_t x[4] = {k.x, q.x, k.y, q.y}, y[4] = {k.z, q.z, k.w, q.w};
+          mma_bf16(c, x, z.x, z.y);
+          mma_bf16(c, y, z.z, z.w);
+        }
+    float R0 = 1.f, R1 = 1.f;
+#pragma unroll
+    for (int l = 1; l < GROUP; ++l) {
+      const float x = __shfl_sync(0xffffffffu, lam, l);
+      if (l <= g && l > 2 * t) R0 *= x;
+      if (l <= g && l > 2 * t + 1) R1 *= x;
+    }
+    if (kDelta) {
+      f.A[2 * t * GROUP + g] = R0 * c[0];
+      f.A[(2 * t + 1) * GROUP + g] = R1 * c[1];
+    }
+    if (kFresh) {
+      w.B[2 * t * GROUP + g] = R0 * c[2];
+      w.B[(2 * t + 1) * GROUP + g] = R1 * c[3];
+    }
+  }
+  // products of the decays up to a token and from behind it to the last one
+  float c = lam, rest = __shfl_down_sync(0xffffffffu, lam, 1, 8);
+  if ((lane & 7) == 7) rest = 1.f;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, c, o, 8), y = __shfl_down_sync(0xffffffffu, rest, o, 8);
+    if ((lane & 7) >= o) c *= x;
+    if ((lane & 7) + o < 8) rest *= y;
+  }
+  if (lane < GROUP) {
+    f.c[lane] = c;
+    f.rest[lane] = rest;
+  }
+  __syncwarp();
+}
+
+// One group of m tokens (1 .. 8) from row `first` of its tokens.  kFresh: outputs; update: the state
+// is advanced.  s[j][e][i]: row g + 8 i, columns 32 j + 8 t + 2 e, + 1.
+template <int D, bool kDelta, bool kFresh, typename T>
+__device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& tok, const Factors& f,
+                                      float2 (&s)[D / 32][4][2], Scratch<D, T>& w, const Strip& strip, int first,
+                                      int m, bool update) {
+  constexpr int J = D / 32, NP = PLANES<T>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r = lane & 15;
+  if (kDelta || kFresh) {
+    // S k and S q
+    constexpr int SUMMANDS = kFresh && NP == 1 ? 2 : 3;
+    float ck[2][4] = {}, cq[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      uint4 k[NP], q[NP];
+#pragma unroll
+      for (int o = 0; o < NP; ++o) {
+        k[o] = tok.k[o][j][lane];
+        q[o] = kFresh ? w.q[o][j][lane] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float2 x[4] = {s[j][e][0], s[j][e][1], s[j][e + 1][0], s[j][e + 1][1]};
+#pragma unroll
+        for (int l = 0; l < SUMMANDS; ++l) {
+          uint32_t a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = pack2(x[i]);
+            if (l + 1 < SUMMANDS) x[i] = sub2(x[i], unpack2(a[i]));
+          }
+          // (products of summands l and o below 2^-24 of the whole are left out)
+#pragma unroll
+          for (int o = 0; o < NP && o + l < 3; ++o) {
+            if (kDelta) mma_bf16(ck[(l + o) & 1], a, e ? k[o].z : k[o].x, e ? k[o].w : k[o].y);
+            if (kFresh) mma_bf16(cq[(l + o) & 1], a, e ? q[o].z : q[o].x, e ? q[o].w : q[o].y);
+          }
+        }
+      }
+    }
+    if (kDelta) {
+      *reinterpret_cast<float2*>(&w.dk[g * LD + 2 * t]) = make_float2(ck[0][0] + ck[1][0], ck[0][1] + ck[1][1]);
+      *reinterpret_cast<float2*>(&w.dk[(g + 8) * LD + 2 * t]) = make_float2(ck[0][2] + ck[1][2], ck[0][3] + ck[1][3]);
+    }
+    if (kFresh) {
+      *reinterpret_cast<float2*>(&w.dq[g * LD + 2 * t]) = make_float2(cq[0][0] + cq[1][0], cq[0][1] + cq[1][1]);
+      *reinterpret_cast<float2*>(&w.dq[(g + 8) * LD + 2 * t]) = make_float2(cq[0][2] + cq[1][2], cq[0][3] + cq[1][3]);
+    }
+    __syncwarp();
+  }
+
+  // u of row r (both halves of the warp the same) and the outputs, column by column of A and B
+  auto load8 = [](float (&x)[GROUP], const float* from) {
+    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from);
+    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(from + 4);
+  };
+  float u[GROUP], o[GROUP], c[GROUP];
+  if (kDelta) load8(u, &w.dk[r * LD]);
+  if (kFresh) load8(o, &w.dq[r * LD]);
+  load8(c, f.c);
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) {
+    const float v = to_f(tok.v[i][r]);
+    u[i] = kDelta ? fmaf(-c[i], u[i], v) : v;
+    if (kFresh) o[i] *= c[i];
+  }
+  T* out = nullptr;
+  const int step = p.H * D;
+  if (kFresh) {
+    const Place at = place_of<D>(p, strip.at);
+    out = reinterpret_cast<T*>(p.out) +
+          (((int64_t)at.n * p.fresh.rows + first) * p.H + at.h) * D + at.row0 + r;
+  }
+#pragma unroll
+  for (int j = 0; j < GROUP; ++j) {
+    if (j >= m) break;
+    float x[GROUP];
+    if (kDelta) {
+      u[j] *= tok.beta[j];
+      load8(x, &f.A[j * GROUP]);
+#pragma unroll
+      for (int i = j + 1; i < GROUP; ++i) u[i] = fmaf(-x[i], u[j], u[i]);
+    }
+    if (kFresh) {
+      load8(x, &w.B[j * GROUP]);
+#pragma unroll
+      for (int i = j; i < GROUP; ++i) o[i] = fmaf(x[i], u[j], o[i]);
+      if (lane >> 4 == (j & 1)) *out = from_f<T>(p.scale * o[j]);
+      out += step;
+    }
+  }
+  if (!update) {
+    __syncwarp();
+    return;
+  }
+
+  // S = c_m S + sum_j R_mj u_j k_j^T
+  const float ce = c[GROUP - 1];
+  load8(c, f.rest);
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) u[i] = i < m ? u[i] * c[i] : 0.f;
+  __syncwarp();
+  if (lane < STRIP) {
+    *reinterpret_cast<float4*>(&w.dk[r * LD]) = make_float4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<float4*>(&w.dk[r * LD + 4]) = make_float4(u[4], u[5], u[6], u[7]);
+  }
+  __syncwarp();
+  uint32_t a[4], last[2];     // rows g, g + 8: the first two summands as 16 columns, and the third
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float2 x = *reinterpret_cast<const float2*>(&w.dk[(g + 8 * i) * LD + 2 * t]);
+    a[i] = pack2(x);
+    x = sub2(x, unpack2(a[i]));
+    a[i + 2] = pack2(x);
+    last[i] = pack2(sub2(x, unpack2(a[i + 2])));
+  }
+  const float2 c2 = make_float2(ce, ce);
+  const uint32_t ends[4] = {last[0], last[1], a[0], a[1]};     // the third summand, and the first once more
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    uint32_t pairs[NP][4];
+#pragma unroll
+    for (int o = 0; o < NP; ++o) {
+      const uint4 k = tok.k[o][j][lane];
+      pairs[o][0] = k.x; pairs[o][1] = k.y; pairs[o][2] = k.z; pairs[o][3] = k.w;
     }
 #pragma unroll
-    for (int r = 0; r < RL; ++r)
-#pragma unroll
-      for (int b = 0; b < CV; ++b) *reinterpret_cast<float4*>(S + (size_t)r * D + b * 32) = s[r][b];
+    for (int e = 0; e < 4; ++e) {
+      float d[4];
+      const uint32_t x = transpose8(pairs[0][e]);
+      if constexpr (NP == 1) {
+        mma_bf16_k8(d, last[0], last[1], x);
+      } else {
+        const uint32_t y = transpose8(pairs[1][e]), z = transpose8(pairs[2][e]);
+        d[0] = d[1] = d[2] = d[3] = 0.f;
+        mma_bf16(d, ends, x, z);
+        mma_bf16(d, a, y, y);
+      }
+      mma_bf16(d, a, x, x);
+      s[j][e][0] = fma2(c2, s[j][e][0], make_float2(d[0], d[1]));
+      s[j][e][1] = fma2(c2, s[j][e][1], make_float2(d[2], d[3]));
+    }
   }
-  if (m == 0) return;
-  read_state<D, kDelta>(s, tm, m);
-  __syncthreads();
-  solve<kDelta>(tm, m, M);
-  __syncthreads();
-  for (int e = threadIdx.x; e < m * ROWS; e += THREADS) {
-    const int i = e / ROWS, r = e % ROWS;
-    float o = tm.c[i] * tm.dq[i * ROWS + r];
-    for (int j = 0; j <= i; ++j) o = fmaf(tm.B[i * M + j], tm.dk[j * ROWS + r], o);
-    out[(((size_t)n * M + i) * p.H + h) * D + row0 + r] = p.scale * o;
+  __syncwarp();
+}
+
+template <int D, bool kDelta, typename T>
+__global__ void __launch_bounds__(32, CTAS<D, T>) draft_kernel(const DraftParams p) {
+  constexpr int J = D / 32;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x, g = lane >> 2, t = lane & 3;
+  Scratch<D, T>& w = *reinterpret_cast<Scratch<D, T>*>(smem);
+  // A warp takes `run` strips of a head in a row, then the run as many warps on: the tokens and their
+  // factors stay for a run.
+  const unsigned run = p.run;     // a power of two
+  const unsigned strips = (unsigned)p.N * p.H * (D / STRIP), ahead = gridDim.x * run;
+  unsigned where = blockIdx.x * run;
+  auto next_at = [&](unsigned x) { return (x + 1) & (run - 1) ? x + 1 : x + 1 - run + ahead; };
+  Strip at = strip_at<D>(p, where, strips), next = strip_at<D>(p, next_at(where), strips);
+  // Copies are committed in the order state and pending tokens of a strip, fresh tokens of it, state of
+  // the next one, ...: each where the buffer is free, a phase or two ahead of its use.
+  fetch_state(p, at, w);
+  fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, at.at, 0, at.a);
+  fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, at.at, 0, at.m);
+  bool new_pend = true, new_fresh = true;   // the buffers hold tokens whose factors are not formed yet
+#pragma unroll 1
+  for (; where < strips; where = next_at(where)) {
+    Strip after = next;
+    after.at = next_at(next.at);
+    if ((after.at & (run - 1)) == 0) after = strip_at<D>(p, after.at, strips);
+    if (at.m < p.fresh.rows) {
+      const Place pl = place_of<D>(p, where);
+      T* out = reinterpret_cast<T*>(p.out) +
+                           ((int64_t)pl.n * p.fresh.rows * p.H + pl.h) * D + pl.row0;
+      for (int i = at.m * STRIP + lane; i < p.fresh.rows * STRIP; i += 32)
+        out[(int64_t)(i / STRIP) * p.H * D + i % STRIP] = from_f<T>(0.f);
+    }
+    const bool last = ((where + 1) & (run - 1)) == 0;
+    float2 s[J][4][2];
+    wait<1>();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float4 x = w.state[g + 8 * i][(8 * j + 2 * t + e / 2) ^ (g & 1)];
+          s[j][e][i] = make_float2(x.x, x.y);
+          s[j][e + 1][i] = make_float2(x.z, x.w);
+        }
+    __syncwarp();
+    fetch_state(p, next, w);
+#pragma unroll 1
+    for (int first = 0; first < at.a; first += GROUP) {
+      if (first > 0) {
+        fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, at.at, first, at.a);
+        wait<0>();
+        __syncwarp();
+      }
+      const int m = min(at.a - first, GROUP);
+      if (first > 0 || new_pend) factors<D, kDelta, false>(p, w.pend, w.fp, w, at.at, m);
+      group<D, kDelta, false>(p, w.pend, w.fp, s, w, at, first, m, true);
+    }
+    new_pend = last || at.a > GROUP;
+    fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, next.at, 0, next.a, new_pend);
+    if (at.a > 0) {
+      float* S = state_of<D>(p, at) + g * D + 8 * t;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) store32(S + i * 8 * D + j * 32, s[j][0][i], s[j][1][i], s[j][2][i], s[j][3][i]);
+    }
+    wait<2>();
+    __syncwarp();
+#pragma unroll 1
+    for (int first = 0; first < at.m; first += GROUP) {
+      if (first > 0) {
+        fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, at.at, first, at.m);
+        wait<0>();
+        __syncwarp();
+      }
+      const int m = min(at.m - first, GROUP);
+      if (first > 0 || new_fresh) factors<D, kDelta, true>(p, w.fresh, w.ff, w, at.at, m);
+      group<D, kDelta, true>(p, w.fresh, w.ff, s, w, at, first, m, first + GROUP < at.m);
+    }
+    new_fresh = last || at.m > GROUP;
+    fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, next.at, 0, next.m, new_fresh);
+    at = next;
+    next = after;
   }
 }
 
-template <int D, bool kDelta>
-cudaError_t go(const DraftParams& p, cudaStream_t st) {
-  const int grid = p.N * p.H * (D / ROWS);
-  const size_t bytes = 4 * (tok_floats(p.pend.rows, D, false, kDelta) + tok_floats(p.fresh.rows, D, true, kDelta));
-  auto kernel = draft_step_kernel<D, kDelta>;
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
+template <int D, bool kDelta, typename T>
+cudaError_t go(DraftParams p, cudaStream_t st) {
+  const int strips = p.N * p.H * (D / STRIP);
+  // Strips in a row save work (128 sequences of 32 heads, 5 + 5 tokens: runs of one 115 us, two 102,
+  // four 96), but the CTAs take whole runs in turns.
+  constexpr int kSlots = 152 * CTAS<D, T>;
+  double best = 0;
+  for (int run = 1; run <= RUN; run *= 2) {
+    const int turns = (strips / run + kSlots - 1) / kSlots;
+    const double time = turns * run * (run == 1 ? 1.18 : run == 2 ? 1.06 : 1.0);
+    if (run == 1 || time < best) {
+      best = time;
+      p.run = run;
+    }
   }
-  kernel<<<grid, THREADS, bytes, st>>>(p);
+  const int want = strips / p.run, grid = want < kSlots ? want : kSlots;
+  const int bytes = (int)sizeof(Scratch<D, T>);
+  static_assert(sizeof(Scratch<D, T>) <= 48 * 1024, "no opt-in to more shared memory");
+  draft_kernel<D, kDelta, T><<<grid, 32, bytes, st>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t rule(const DraftParams& p, cudaStream_t st) {
+  return p.decay ? go<D, false, T>(p, st) : go<D, true, T>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_draft_step(const DraftParams& p, bool bf16, int D, cudaStream_t st) {
   if (p.N < 1 || p.pend.rows + p.fresh.rows == 0) return cudaSuccess;
-  if (bf16) return launch_draft_mma(p, D, st);
-  if (D == 128) return p.decay ? go<128, false>(p, st) : go<128, true>(p, st);
-  return p.decay ? go<64, false>(p, st) : go<64, true>(p, st);
+  if (bf16) return D == 128 ? rule<128, __nv_bfloat16>(p, st) : rule<64, __nv_bfloat16>(p, st);
+  return D == 128 ? rule<128, float>(p, st) : rule<64, float>(p, st);
 }
 
 }  // namespace sfg

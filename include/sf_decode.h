@@ -101,7 +101,7 @@ sf_status sf_linattn_commit(const sf_gdn_shape *shape, const void *k, const void
  *                  say so in)
  * A negative weight or a NaN counts as zero.  Products and sums are exact to 2^-40 or
  * better, so that a result does not depend on how the sums are split.
- * N >= 0, T >= 0 (T = 0: one token is drawn from p_0), V >= 1.
+ * N >= 0, T >= 0 (T = 0: one token is drawn from p_0), V >= 1.  Outputs overlap no input.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int N, T, V;

@@ -90,6 +90,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same for FP32 results, added outside: the tensor core cuts its sums instead of rounding them,
+// and a row of them would add up to ten FP32 roundings.
+__device__ __forceinline__ void add_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  float x[4] = {};
+  mma_bf16(x, a, b0, b1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] += x[i];
+}
 // (from zero)
 __device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
   asm volatile(
@@ -235,7 +243,7 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
   if ((lane & 7) < m) lam = expf(kDelta ? tok.gate[lane & 7] : p.decay[place_of<D>(p, strip).h]);
   if (kDelta || kFresh) {
     // k_i . k_j (rows g) and q_i . k_j (rows g + 8) for j = 2 t, 2 t + 1
-    float c[4] = {};
+    float c[4] = {}, small[4] = {};
 #pragma unroll
     for (int l = 0; l < PLANES<T>; ++l)
 #pragma unroll
@@ -245,9 +253,19 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
           const uint4 k = tok.k[l][j][lane], q = kFresh ? w.q[l][j][lane] : make_uint4(0, 0, 0, 0);
           const uint4 z = tok.k[o][j][lane];
           const uint32_t x[4] = {k.x, q.x, k.y, q.y}, y[4] = {k.z, q.z, k.w, q.w};
-          mma_bf16(c, x, z.x, z.y);
-          mma_bf16(c, y, z.z, z.w);
+          if (PLANES<T> == 1) {
+            mma_bf16(c, x, z.x, z.y);
+            mma_bf16(c, y, z.z, z.w);
+          } else if (l + o == 0) {
+            add_mma(c, x, z.x, z.y);
+            add_mma(c, y, z.z, z.w);
+          } else {
+            mma_bf16(small, x, z.x, z.y);
+            mma_bf16(small, y, z.z, z.w);
+          }
         }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] += small[i];
     float R0 = 1.f, R1 = 1.f;
 #pragma unroll
     for (int l = 1; l < GROUP; ++l) {
@@ -314,8 +332,16 @@ __device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& 
           // (products of summands l and o below 2^-24 of the whole are left out)
 #pragma unroll
           for (int o = 0; o < NP && o + l < 3; ++o) {
-            if (kDelta) mma_bf16(ck[(l + o) & 1], a, e ? k[o].z : k[o].x, e ? k[o].w : k[o].y);
-            if (kFresh) mma_bf16(cq[(l + o) & 1], a, e ? q[o].z : q[o].x, e ? q[o].w : q[o].y);
+            const uint32_t k0 = e ? k[o].z : k[o].x, k1 = e ? k[o].w : k[o].y;
+            const uint32_t q0 = e ? q[o].z : q[o].x, q1 = e ? q[o].w : q[o].y;
+            if (NP > 1 && l + o == 0) {
+              if (kDelta) add_mma(ck[0], a, k0, k1);
+              if (kFresh) add_mma(cq[0], a, q0, q1);
+            } else {
+              constexpr bool kApart = NP > 1;     // the small products together
+              if (kDelta) mma_bf16(ck[kApart ? 1 : l & 1], a, k0, k1);
+              if (kFresh) mma_bf16(cq[kApart ? 1 : l & 1], a, q0, q1);
+            }
           }
         }
       }

@@ -9,9 +9,10 @@
 // the new indices go where the old ones are read, one CTA makes it in a launch before.
 //
 // The copies are bound by memory.  Measured: 59 slots in 8 caches of 1 MB (990 MB) 148 us, 99 % of
-// the copy rate; a compaction's 48 (805 MB) 129 us, 92 % (its 10.1 pieces a CTA take 11 turns); one
-// slot copied three times 4.7 us.  Pieces of 16 KB, 16 CTAs of 128 threads an SM; 8 KB 153, 133; 32 KB,
-// 8 CTAs of 256 threads 150, 130.  In two launches the smallest fork takes 6.5 us.
+// the copy rate; a compaction's 48 (805 MB) 129 us, 92 %; one slot copied three times 4.7 us.  Pieces of
+// 16 KB, 16 CTAs of 128 threads an SM; 8 KB 153, 133; 32 KB, 8 CTAs of 256 threads 150, 130; the last
+// turn's pieces cut for the CTAs that have none 150, 130.  In two launches the smallest fork takes
+// 6.5 us.
 #include "common.cuh"
 #include "decode.cuh"
 #include "linattn.cuh"

@@ -41,8 +41,8 @@
 // 102; whole rows to a copy and whole lines to a store, eight warps an SM and a window 96, 98, 92.
 // Twelve warps an SM (168 registers, some spilled) 98, 109, 95; runs of one strip 115, 102, 88;
 // summands by truncation and byte permutes instead of conversions: the same.  FP32 tokens, 64
-// sequences of 32 heads: 5 + 5 tokens 85 us, a commit of 8 53 us (on the FP32 pipes 85, 68; floor
-// 41); 16 + 16 tokens 253 us, BF16 90 (each strip loads the tokens of its later groups again).
+// sequences of 32 heads: 5 + 5 tokens 88 us, a commit of 8 52 us (on the FP32 pipes 85, 68; floor
+// 41).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -56,9 +56,10 @@ constexpr int GROUP = 8;      // tokens
 constexpr int STRIP = 16;     // rows of a state to a warp
 template <typename T>
 constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;     // BF16 summands of a token
-// CTAs of one warp each on an SM.
-template <int D, typename T>
-constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : 16) : (D == 128 ? 7 : 14);
+// CTAs of one warp each on an SM; G groups of tokens in their shared memory.
+template <int D, typename T, int G>
+constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : G == 1 ? 16 : 14)
+                                    : (D == 128 ? (G == 1 ? 7 : 4) : G == 1 ? 12 : 8);
 constexpr int RUN = 4;        // strips of a head that a warp takes in a row
 constexpr int LD = 12;        // floats between rows of 8 in shared memory: 8 lanes' 16 bytes in distinct banks
 
@@ -74,13 +75,13 @@ struct Factors {
   float A[GROUP * GROUP];                     // R_ij (k_i . k_j), column j together
   float c[GROUP], rest[GROUP];                // c_i, R_mi
 };
-template <int D, typename T>
+template <int D, typename T, int G>
 struct Scratch {                              // of a warp
   float4 state[STRIP][D / 4];                 // the next strip's; in odd rows 16-byte units 2 i, 2 i + 1 swapped
-  Tokens<D, T> pend, fresh;
-  uint4 q[PLANES<T>][D / 32][32];
-  Factors fp, ff;
-  float B[GROUP * GROUP];                     // R_ij (q_i . k_j) of fresh tokens
+  Tokens<D, T> pend[G], fresh[G];
+  uint4 q[G][PLANES<T>][D / 32][32];
+  Factors fp[G], ff[G];
+  float B[G][GROUP * GROUP];                  // R_ij (q_i . k_j) of fresh tokens
   float dk[STRIP * LD], dq[STRIP * LD];       // S k, then the rows' weights; S q
 };
 
@@ -165,8 +166,8 @@ __device__ __forceinline__ float* state_of(const DraftParams& p, const Strip& s)
   return p.pool + (((int64_t)s.slot * p.H + at.h) * D + at.row0) * D;
 }
 // (Whole rows to a copy.)
-template <int D, typename T>
-__device__ __forceinline__ void fetch_state(const DraftParams& p, const Strip& s, Scratch<D, T>& w) {
+template <int D, typename W>
+__device__ __forceinline__ void fetch_state(const DraftParams& p, const Strip& s, W& w) {
   if (s.a | s.m) {
     constexpr int U = D / 4, R = 32 / U > 0 ? 32 / U : 1;    // units of a row, rows of a copy
     const int lane = threadIdx.x & 31, r = lane / U, c = lane % U;
@@ -230,13 +231,23 @@ __device__ __forceinline__ void fetch_tokens(const DraftParams& p, const DraftTo
                        reinterpret_cast<const T*>(tok.v) + ((token0 + (i2 < m ? i2 : 0)) * p.H + at.h) * D + at.row0 +
                            part, i2 < m);
   }
+}
+// All the groups that the buffers hold.
+template <int D, bool kDelta, bool kFresh, typename W>
+__device__ __forceinline__ void fetch_groups(const DraftParams& p, W& w, unsigned strip, int count, bool all) {
+  constexpr int G = sizeof(w.fp) / sizeof(Factors);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    if (kFresh) fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh[i], w.q[i], strip, i * GROUP, count, all);
+    else fetch_tokens<D, kDelta, false>(p, p.pend, w.pend[i], w.q[0], strip, i * GROUP, count, all);
+  }
   commit();
 }
 
 // The factors of a group of m tokens.
 template <int D, bool kDelta, bool kFresh, typename T>
-__device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>& tok, Factors& f, Scratch<D, T>& w,
-                                        unsigned strip, int m) {
+__device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>& tok, const uint4 (*qs)[D / 32][32],
+                                        Factors& f, float* B, unsigned strip, int m) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the decay of token lane % 8
   float lam = 1.f;
@@ -250,7 +261,7 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
       for (int o = 0; o + l < PLANES<T>; ++o)
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint4 k = tok.k[l][j][lane], q = kFresh ? w.q[l][j][lane] : make_uint4(0, 0, 0, 0);
+          const uint4 k = tok.k[l][j][lane], q = kFresh ? qs[l][j][lane] : make_uint4(0, 0, 0, 0);
           const uint4 z = tok.k[o][j][lane];
           const uint32_t x[4] = {k.x, q.x, k.y, q.y}, y[4] = {k.z, q.z, k.w, q.w};
           if (PLANES<T> == 1) {
@@ -278,8 +289,8 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
       f.A[(2 * t + 1) * GROUP + g] = R1 * c[1];
     }
     if (kFresh) {
-      w.B[2 * t * GROUP + g] = R0 * c[2];
-      w.B[(2 * t + 1) * GROUP + g] = R1 * c[3];
+      B[2 * t * GROUP + g] = R0 * c[2];
+      B[(2 * t + 1) * GROUP + g] = R1 * c[3];
     }
   }
   // products of the decays up to a token and from behind it to the last one
@@ -300,10 +311,10 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
 
 // One group of m tokens (1 .. 8) from row `first` of its tokens.  kFresh: outputs; update: the state
 // is advanced.  s[j][e][i]: row g + 8 i, columns 32 j + 8 t + 2 e, + 1.
-template <int D, bool kDelta, bool kFresh, typename T>
-__device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& tok, const Factors& f,
-                                      float2 (&s)[D / 32][4][2], Scratch<D, T>& w, const Strip& strip, int first,
-                                      int m, bool update) {
+template <int D, bool kDelta, bool kFresh, typename T, typename W>
+__device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& tok, const uint4 (*qs)[D / 32][32],
+                                      const Factors& f, const float* B, float2 (&s)[D / 32][4][2], W& w,
+                                      const Strip& strip, int first, int m, bool update) {
   constexpr int J = D / 32, NP = PLANES<T>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r = lane & 15;
   if (kDelta || kFresh) {
@@ -316,7 +327,7 @@ __device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& 
 #pragma unroll
       for (int o = 0; o < NP; ++o) {
         k[o] = tok.k[o][j][lane];
-        q[o] = kFresh ? w.q[o][j][lane] : make_uint4(0, 0, 0, 0);
+        q[o] = kFresh ? qs[o][j][lane] : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
@@ -390,7 +401,7 @@ __device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& 
       for (int i = j + 1; i < GROUP; ++i) u[i] = fmaf(-x[i], u[j], u[i]);
     }
     if (kFresh) {
-      load8(x, &w.B[j * GROUP]);
+      load8(x, &B[j * GROUP]);
 #pragma unroll
       for (int i = j; i < GROUP; ++i) o[i] = fmaf(x[i], u[j], o[i]);
       if (lane >> 4 == (j & 1)) *out = from_f<T>(p.scale * o[j]);
@@ -452,12 +463,12 @@ __device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& 
   __syncwarp();
 }
 
-template <int D, bool kDelta, typename T>
-__global__ void __launch_bounds__(32, CTAS<D, T>) draft_kernel(const DraftParams p) {
+template <int D, bool kDelta, typename T, int G>
+__global__ void __launch_bounds__(32, CTAS<D, T, G>) draft_kernel(const DraftParams p) {
   constexpr int J = D / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x, g = lane >> 2, t = lane & 3;
-  Scratch<D, T>& w = *reinterpret_cast<Scratch<D, T>*>(smem);
+  Scratch<D, T, G>& w = *reinterpret_cast<Scratch<D, T, G>*>(smem);
   // A warp takes `run` strips of a head in a row, then the run as many warps on: the tokens and their
   // factors stay for a run.
   const unsigned run = p.run;     // a power of two
@@ -467,9 +478,9 @@ __global__ void __launch_bounds__(32, CTAS<D, T>) draft_kernel(const DraftParams
   Strip at = strip_at<D>(p, where, strips), next = strip_at<D>(p, next_at(where), strips);
   // Copies are committed in the order state and pending tokens of a strip, fresh tokens of it, state of
   // the next one, ...: each where the buffer is free, a phase or two ahead of its use.
-  fetch_state(p, at, w);
-  fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, at.at, 0, at.a);
-  fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, at.at, 0, at.m);
+  fetch_state<D>(p, at, w);
+  fetch_groups<D, kDelta, false>(p, w, at.at, at.a, true);
+  fetch_groups<D, kDelta, true>(p, w, at.at, at.m, true);
   bool new_pend = true, new_fresh = true;   // the buffers hold tokens whose factors are not formed yet
 #pragma unroll 1
   for (; where < strips; where = next_at(where)) {
@@ -498,20 +509,22 @@ __global__ void __launch_bounds__(32, CTAS<D, T>) draft_kernel(const DraftParams
           s[j][e + 1][i] = make_float2(x.z, x.w);
         }
     __syncwarp();
-    fetch_state(p, next, w);
+    fetch_state<D>(p, next, w);
 #pragma unroll 1
     for (int first = 0; first < at.a; first += GROUP) {
-      if (first > 0) {
-        fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, at.at, first, at.a);
+      const int i = first / GROUP % G, m = min(at.a - first, GROUP);
+      const bool late = first >= G * GROUP;        // a group that the buffers do not hold yet
+      if (late) {
+        fetch_tokens<D, kDelta, false>(p, p.pend, w.pend[i], w.q[0], at.at, first, at.a, true);
+        commit();
         wait<0>();
         __syncwarp();
       }
-      const int m = min(at.a - first, GROUP);
-      if (first > 0 || new_pend) factors<D, kDelta, false>(p, w.pend, w.fp, w, at.at, m);
-      group<D, kDelta, false>(p, w.pend, w.fp, s, w, at, first, m, true);
+      if (late || new_pend) factors<D, kDelta, false>(p, w.pend[i], w.q[0], w.fp[i], w.B[0], at.at, m);
+      group<D, kDelta, false>(p, w.pend[i], w.q[0], w.fp[i], w.B[0], s, w, at, first, m, true);
     }
-    new_pend = last || at.a > GROUP;
-    fetch_tokens<D, kDelta, false>(p, p.pend, w.pend, nullptr, next.at, 0, next.a, new_pend);
+    new_pend = last || at.a > G * GROUP;
+    fetch_groups<D, kDelta, false>(p, w, next.at, next.a, new_pend);
     if (at.a > 0) {
       float* S = state_of<D>(p, at) + g * D + 8 * t;
 #pragma unroll
@@ -523,28 +536,30 @@ __global__ void __launch_bounds__(32, CTAS<D, T>) draft_kernel(const DraftParams
     __syncwarp();
 #pragma unroll 1
     for (int first = 0; first < at.m; first += GROUP) {
-      if (first > 0) {
-        fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, at.at, first, at.m);
+      const int i = first / GROUP % G, m = min(at.m - first, GROUP);
+      const bool late = first >= G * GROUP;
+      if (late) {
+        fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh[i], w.q[i], at.at, first, at.m, true);
+        commit();
         wait<0>();
         __syncwarp();
       }
-      const int m = min(at.m - first, GROUP);
-      if (first > 0 || new_fresh) factors<D, kDelta, true>(p, w.fresh, w.ff, w, at.at, m);
-      group<D, kDelta, true>(p, w.fresh, w.ff, s, w, at, first, m, first + GROUP < at.m);
+      if (late || new_fresh) factors<D, kDelta, true>(p, w.fresh[i], w.q[i], w.ff[i], w.B[i], at.at, m);
+      group<D, kDelta, true>(p, w.fresh[i], w.q[i], w.ff[i], w.B[i], s, w, at, first, m, first + GROUP < at.m);
     }
-    new_fresh = last || at.m > GROUP;
-    fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh, w.q, next.at, 0, next.m, new_fresh);
+    new_fresh = last || at.m > G * GROUP;
+    fetch_groups<D, kDelta, true>(p, w, next.at, next.m, new_fresh);
     at = next;
     next = after;
   }
 }
 
-template <int D, bool kDelta, typename T>
+template <int D, bool kDelta, typename T, int G>
 cudaError_t go(DraftParams p, cudaStream_t st) {
   const int strips = p.N * p.H * (D / STRIP);
   // Strips in a row save work (128 sequences of 32 heads, 5 + 5 tokens: runs of one 115 us, two 102,
   // four 96), but the CTAs take whole runs in turns.
-  constexpr int kSlots = 152 * CTAS<D, T>;
+  constexpr int kSlots = 152 * CTAS<D, T, G>;
   double best = 0;
   for (int run = 1; run <= RUN; run *= 2) {
     const int turns = (strips / run + kSlots - 1) / kSlots;
@@ -555,23 +570,35 @@ cudaError_t go(DraftParams p, cudaStream_t st) {
     }
   }
   const int want = strips / p.run, grid = want < kSlots ? want : kSlots;
-  const int bytes = (int)sizeof(Scratch<D, T>);
-  static_assert(sizeof(Scratch<D, T>) <= 48 * 1024, "no opt-in to more shared memory");
-  draft_kernel<D, kDelta, T><<<grid, 32, bytes, st>>>(p);
+  constexpr int bytes = (int)sizeof(Scratch<D, T, G>);
+  static_assert(CTAS<D, T, G> * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
+  auto kernel = draft_kernel<D, kDelta, T, G>;
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, 32, bytes, st>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, typename T>
+template <int D, typename T, int G>
 cudaError_t rule(const DraftParams& p, cudaStream_t st) {
-  return p.decay ? go<D, false, T>(p, st) : go<D, true, T>(p, st);
+  return p.decay ? go<D, false, T, G>(p, st) : go<D, true, T, G>(p, st);
+}
+// Two groups in shared memory where a sequence may have them: otherwise each strip would load its
+// tokens again (64 sequences of 32 heads, 16 + 16 tokens, delta rule and linear attention, BF16 92 and
+// 77 us against 86 and 69, FP32 267 and 171 against 245 and 148).
+template <int D, typename T>
+cudaError_t groups(const DraftParams& p, cudaStream_t st) {
+  return p.pend.rows > GROUP || p.fresh.rows > GROUP ? rule<D, T, 2>(p, st) : rule<D, T, 1>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_draft_step(const DraftParams& p, bool bf16, int D, cudaStream_t st) {
   if (p.N < 1 || p.pend.rows + p.fresh.rows == 0) return cudaSuccess;
-  if (bf16) return D == 128 ? rule<128, __nv_bfloat16>(p, st) : rule<64, __nv_bfloat16>(p, st);
-  return D == 128 ? rule<128, float>(p, st) : rule<64, float>(p, st);
+  if (bf16) return D == 128 ? groups<128, __nv_bfloat16>(p, st) : groups<64, __nv_bfloat16>(p, st);
+  return D == 128 ? groups<128, float>(p, st) : groups<64, float>(p, st);
 }
 
 }  // namespace sfg

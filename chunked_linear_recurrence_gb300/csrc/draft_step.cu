@@ -10,15 +10,16 @@
 // and not NaN.  The state is touched twice a token by the drafts, and twice and once more by the
 // accepted ones, against four times each by the rule itself.
 //
-// Tokens go in groups of up to 8, the state advanced between them.  A warp holds 16 rows of a state in registers and needs no other warp: with
-// g = lane / 4, t = lane % 4 a lane holds of rows g and g + 8 the columns 32 j + 8 t .. + 7.  That is at
-// once
+// Tokens go in groups of up to 8, the state advanced between them; a group of accepted BF16 tokens and
+// one of drafts take one pass over the state before both (both()).  A warp holds 16 rows of a state
+// in registers and needs no other warp: with g = lane / 4, t = lane % 4 a lane holds of rows g and
+// g + 8 the columns 32 j + 8 t .. + 7.  That is at once
 //  * an accumulator of 16x8 products and the left operand of 16x8x16 products, if column pair e of
 //    every lane is taken as one tile of 8 columns (the sum's order is free);
 //  * for a token g in BF16, the right operand of those (S k, S q of 8 tokens), both operands of the
 //    tokens' own products, and through movmatrix the right operand of the update W K.
 // So nothing passes through shared memory but the tokens' 8x8 products and 16x8 results, for the
-// solve, one row to a lane, and the next strip's state, copied ahead by the lane that reads it.
+// solve, one row to a lane, and what is copied ahead: the tokens, and the next strip's state.
 //
 // Precision: what reaches the state is FP32.  For accepted tokens the state that k reads and the
 // rows' weights W are split into three BF16 summands (24 bits), and the update's sum is formed apart
@@ -32,17 +33,17 @@
 // through the pool as one window.
 //
 // Bound by memory, 4 V K bytes read and as many written (if a token was accepted), and by the chain
-// of a strip's steps (1400 instructions with both kinds of tokens, two warps to a scheduler).  Measured,
-// K = 128: 128 sequences of 32 heads, 5 + 5 tokens 96 us (537 MB, 5.7 TB/s, 84 % of the copy rate),
-// 256 of 16 heads, 8 + 8 tokens by linear attention 98 us, a commit of 8 tokens 92 us; one sequence
-// of 16 heads 4.6 us.  The same movement without any tokens' work takes 88 us.  What it came
+// of a strip's steps (1250 instructions with both kinds of tokens, two warps to a scheduler).  Measured,
+// K = 128: 128 sequences of 32 heads, 5 + 5 tokens 93.5 us (537 MB, 5.85 TB/s, 86 % of the copy rate),
+// 256 of 16 heads, 8 + 8 tokens by linear attention 96 us, a commit of 8 tokens 92 us; one sequence
+// of 16 heads 4.5 us.  The same movement without any tokens' work takes 88 us.  What it came
 // from: FP32 pipes with shared-memory tokens 156, 148, 120 us; states loaded where they are used
 // 164, 149, 113; copied ahead 158, 146, 121; factors and tokens of a run of strips kept 100, 114,
-// 102; whole rows to a copy and whole lines to a store, eight warps an SM and a window 96, 98, 92.
-// Twelve warps an SM (168 registers, some spilled) 98, 109, 95; runs of one strip 115, 102, 88;
-// summands by truncation and byte permutes instead of conversions: the same.  FP32 tokens, 64
-// sequences of 32 heads: 5 + 5 tokens 88 us, a commit of 8 52 us (on the FP32 pipes 85, 68; floor
-// 41).
+// 102; whole rows to a copy and whole lines to a store, eight warps an SM and a window 96-98, 98, 92;
+// one pass for both kinds of tokens 93.5, 96.  Twelve warps an SM (168 registers, some spilled) 98, 109,
+// 95; runs of one strip 115, 102, 88; summands by truncation and byte permutes instead of
+// conversions: the same.  FP32 tokens, 64 sequences of 32 heads: 5 + 5 tokens 88 us, a commit of
+// 8 52 us (on the FP32 pipes 85, 68; floor 41).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -58,8 +59,12 @@ template <typename T>
 constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;     // BF16 summands of a token
 // CTAs of one warp each on an SM; G groups of tokens in their shared memory.
 template <int D, typename T, int G>
-constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : G == 1 ? 16 : 14)
-                                    : (D == 128 ? (G == 1 ? 7 : 4) : G == 1 ? 12 : 8);
+constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : G == 1 ? 16 : 13)
+                                    : (D == 128 ? (G == 1 ? 7 : 4) : G == 1 ? 12 : 7);
+// Whether pending and fresh tokens take one pass over the state (both()): at the most 8 of each, BF16.
+// (FP32 tokens, whose pass would keep more than fits in registers and shared memory: 91 -> 128 us.)
+template <typename T, int G>
+constexpr bool ONE_PASS = sizeof(T) == 2 && G == 1;
 constexpr int RUN = 4;        // strips of a head that a warp takes in a row
 constexpr int LD = 12;        // floats between rows of 8 in shared memory: 8 lanes' 16 bytes in distinct banks
 
@@ -67,7 +72,6 @@ constexpr int LD = 12;        // floats between rows of 8 in shared memory: 8 la
 template <int D, typename T>
 struct Tokens {
   uint4 k[PLANES<T>][D / 32][32];
-  T v[GROUP][STRIP];
   float gate[GROUP], beta[GROUP];
 };
 // What a group's tokens are to each other.
@@ -81,8 +85,11 @@ struct Scratch {                              // of a warp
   Tokens<D, T> pend[G], fresh[G];
   uint4 q[G][PLANES<T>][D / 32][32];
   Factors fp[G], ff[G];
+  T v[2][2][G][GROUP][STRIP];                 // values of this strip and the next, pending and fresh
   float B[G][GROUP * GROUP];                  // R_ij (q_i . k_j) of fresh tokens
+  float X[ONE_PASS<T, G> ? 2 : 1][ONE_PASS<T, G> ? GROUP * GROUP : 4];     // k_i . k_j, q_i . k_j of fresh i and pending j (both())
   float dk[STRIP * LD], dq[STRIP * LD];       // S k, then the rows' weights; S q
+  float df[ONE_PASS<T, G> ? STRIP * LD : 4];          // S k of fresh tokens where dk is of pending ones
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -175,7 +182,6 @@ __device__ __forceinline__ void fetch_state(const DraftParams& p, const Strip& s
 #pragma unroll
     for (int i = 0; i < STRIP / R; ++i) copy<16>(&w.state[i * R + r][c ^ ((i * R + r) & 1)], S + i * R * D);
   }
-  commit();
 }
 // Eight FP32 values of a lane as three BF16 summands each (zeros if not `on`).
 template <int J>
@@ -194,54 +200,118 @@ __device__ __forceinline__ void split_to(uint4 (*to)[J][32], int j, const float*
     to[l][j][threadIdx.x & 31] = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
-// The group from token `first` of `count` on; what lies behind its last token is zero.  Where the
-// buffer has the head's tokens (`all` false) the strip's values alone.
+// The queries, keys and gates of the group from token `first` of `count` on; what lies behind its last
+// token is zero.
 template <int D, bool kDelta, bool kFresh, typename T>
 __device__ __forceinline__ void fetch_tokens(const DraftParams& p, const DraftTokens& tok, Tokens<D, T>& to,
-                                             uint4 (*q)[D / 32][32], unsigned strip, int first, int count,
-                                             bool all = true) {
+                                             uint4 (*q)[D / 32][32], unsigned strip, int first, int count) {
   const int m = min(count - first, GROUP);
   if (m > 0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const Place at = place_of<D>(p, strip);
     const int64_t token0 = (int64_t)at.n * tok.rows + first;
-    if (all) {
-      // (a token behind the last one of the sequence is not read: any address of the tensor does)
-      const int64_t mine = ((token0 + (g < m ? g : 0)) * p.HK + p.by_group(at.h)) * D + 8 * t;
-      const T* k = reinterpret_cast<const T*>(tok.k) + mine;
-      const T* x = kFresh ? reinterpret_cast<const T*>(tok.q) + mine : nullptr;
+    // (a token behind the last one of the sequence is not read: any address of the tensor does)
+    const int64_t mine = ((token0 + (g < m ? g : 0)) * p.HK + p.by_group(at.h)) * D + 8 * t;
+    const T* k = reinterpret_cast<const T*>(tok.k) + mine;
+    const T* x = kFresh ? reinterpret_cast<const T*>(tok.q) + mine : nullptr;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        if constexpr (PLANES<T> == 1) {
-          copy_or_zero<16>(&to.k[0][j][lane], k + j * 32, g < m);
-          if (kFresh) copy_or_zero<16>(&q[0][j][lane], x + j * 32, g < m);
-        } else {
-          split_to(to.k, j, k + j * 32, g < m);
-          if (kFresh) split_to(q, j, x + j * 32, g < m);
-        }
+    for (int j = 0; j < D / 32; ++j) {
+      if constexpr (PLANES<T> == 1) {
+        copy_or_zero<16>(&to.k[0][j][lane], k + j * 32, g < m);
+        if (kFresh) copy_or_zero<16>(&q[0][j][lane], x + j * 32, g < m);
+      } else {
+        split_to(to.k, j, k + j * 32, g < m);
+        if (kFresh) split_to(q, j, x + j * 32, g < m);
       }
     }
-    constexpr int E = 16 / sizeof(T), UNITS = STRIP / E;      // units of a token's values
-    const int i = lane & 7, i2 = lane / UNITS, part = lane % UNITS * E;
-    if (kDelta && all && lane < 2 * GROUP && i < m)
+    const int i = lane & 7;
+    if (kDelta && lane < 2 * GROUP && i < m)
       copy<4>(lane < GROUP ? &to.gate[i] : &to.beta[i],
               (lane < GROUP ? tok.gate : tok.beta) + (token0 + i) * p.H + at.h);
-    if (lane < GROUP * UNITS)
-      copy_or_zero<16>(&to.v[i2][part],
-                       reinterpret_cast<const T*>(tok.v) + ((token0 + (i2 < m ? i2 : 0)) * p.H + at.h) * D + at.row0 +
-                           part, i2 < m);
   }
 }
-// All the groups that the buffers hold.
+// The values of a group of the strip's rows.
+template <int D, typename T>
+__device__ __forceinline__ void fetch_values(const DraftParams& p, const DraftTokens& tok, T (*v)[STRIP],
+                                             unsigned strip, int first, int count) {
+  const int m = min(count - first, GROUP);
+  if (m > 0) {
+    constexpr int E = 16 / sizeof(T), UNITS = STRIP / E;      // units of a token's values
+    const int lane = threadIdx.x & 31, i = lane / UNITS, part = lane % UNITS * E;
+    const Place at = place_of<D>(p, strip);
+    const int64_t token = (int64_t)at.n * tok.rows + first + (i < m ? i : 0);
+    if (lane < GROUP * UNITS)
+      copy_or_zero<16>(&v[i][part],
+                       reinterpret_cast<const T*>(tok.v) + (token * p.H + at.h) * D + at.row0 + part, i < m);
+  }
+}
+// All the groups that the buffers hold, if they are to be loaded.
 template <int D, bool kDelta, bool kFresh, typename W>
-__device__ __forceinline__ void fetch_groups(const DraftParams& p, W& w, unsigned strip, int count, bool all) {
+__device__ __forceinline__ void fetch_groups(const DraftParams& p, W& w, unsigned strip, int count, bool on) {
   constexpr int G = sizeof(w.fp) / sizeof(Factors);
+  if (on) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    if (kFresh) fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh[i], w.q[i], strip, i * GROUP, count, all);
-    else fetch_tokens<D, kDelta, false>(p, p.pend, w.pend[i], w.q[0], strip, i * GROUP, count, all);
+    for (int i = 0; i < G; ++i) {
+      if (kFresh) fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh[i], w.q[i], strip, i * GROUP, count);
+      else fetch_tokens<D, kDelta, false>(p, p.pend, w.pend[i], w.q[0], strip, i * GROUP, count);
+    }
   }
   commit();
+}
+// A strip's state and values.
+template <int D, typename W>
+__device__ __forceinline__ void fetch_strip(const DraftParams& p, const Strip& s, W& w, int side) {
+  constexpr int G = sizeof(w.fp) / sizeof(Factors);
+  fetch_state<D>(p, s, w);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    fetch_values<D>(p, p.pend, w.v[side][0][i], s.at, i * GROUP, s.a);
+    fetch_values<D>(p, p.fresh, w.v[side][1][i], s.at, i * GROUP, s.m);
+  }
+  commit();
+}
+
+// k_i . x_j (rows g) and q_i . x_j (rows g + 8) for j = 2 t, 2 t + 1.
+template <int D, bool kQueries, typename T>
+__device__ __forceinline__ void token_products(float (&c)[4], const uint4 (*ks)[D / 32][32], const uint4 (*qs)[D / 32][32],
+                                               const uint4 (*xs)[D / 32][32]) {
+  const int lane = threadIdx.x & 31;
+  float small[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = 0.f;
+#pragma unroll
+  for (int l = 0; l < PLANES<T>; ++l)
+#pragma unroll
+    for (int o = 0; o + l < PLANES<T>; ++o)
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const uint4 k = ks[l][j][lane], q = kQueries ? qs[l][j][lane] : make_uint4(0, 0, 0, 0), z = xs[o][j][lane];
+        const uint32_t x[4] = {k.x, q.x, k.y, q.y}, y[4] = {k.z, q.z, k.w, q.w};
+        if (PLANES<T> == 1) {
+          mma_bf16(c, x, z.x, z.y);
+          mma_bf16(c, y, z.z, z.w);
+        } else if (l + o == 0) {
+          add_mma(c, x, z.x, z.y);
+          add_mma(c, y, z.z, z.w);
+        } else {
+          mma_bf16(small, x, z.x, z.y);
+          mma_bf16(small, y, z.z, z.w);
+        }
+      }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += small[i];
+}
+// The products of fresh tokens with pending keys.
+template <int D, typename T, typename W>
+__device__ __forceinline__ void cross_products(W& w) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float c[4];
+  token_products<D, true, T>(c, w.fresh[0].k, w.q[0], w.pend[0].k);
+  w.X[0][2 * t * GROUP + g] = c[0];
+  w.X[0][(2 * t + 1) * GROUP + g] = c[1];
+  w.X[1][2 * t * GROUP + g] = c[2];
+  w.X[1][(2 * t + 1) * GROUP + g] = c[3];
+  __syncwarp();
 }
 
 // The factors of a group of m tokens.
@@ -253,30 +323,8 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
   float lam = 1.f;
   if ((lane & 7) < m) lam = expf(kDelta ? tok.gate[lane & 7] : p.decay[place_of<D>(p, strip).h]);
   if (kDelta || kFresh) {
-    // k_i . k_j (rows g) and q_i . k_j (rows g + 8) for j = 2 t, 2 t + 1
-    float c[4] = {}, small[4] = {};
-#pragma unroll
-    for (int l = 0; l < PLANES<T>; ++l)
-#pragma unroll
-      for (int o = 0; o + l < PLANES<T>; ++o)
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint4 k = tok.k[l][j][lane], q = kFresh ? qs[l][j][lane] : make_uint4(0, 0, 0, 0);
-          const uint4 z = tok.k[o][j][lane];
-          const uint32_t x[4] = {k.x, q.x, k.y, q.y}, y[4] = {k.z, q.z, k.w, q.w};
-          if (PLANES<T> == 1) {
-            mma_bf16(c, x, z.x, z.y);
-            mma_bf16(c, y, z.z, z.w);
-          } else if (l + o == 0) {
-            add_mma(c, x, z.x, z.y);
-            add_mma(c, y, z.z, z.w);
-          } else {
-            mma_bf16(small, x, z.x, z.y);
-            mma_bf16(small, y, z.z, z.w);
-          }
-        }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] += small[i];
+    float c[4];
+    token_products<D, kFresh, T>(c, tok.k, qs, tok.k);
     float R0 = 1.f, R1 = 1.f;
 #pragma unroll
     for (int l = 1; l < GROUP; ++l) {
@@ -309,94 +357,90 @@ __device__ __forceinline__ void factors(const DraftParams& p, const Tokens<D, T>
   __syncwarp();
 }
 
-// One group of m tokens (1 .. 8) from row `first` of its tokens.  kFresh: outputs; update: the state
-// is advanced.  s[j][e][i]: row g + 8 i, columns 32 j + 8 t + 2 e, + 1.
-template <int D, bool kDelta, bool kFresh, typename T, typename W>
-__device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& tok, const uint4 (*qs)[D / 32][32],
-                                      const Factors& f, const float* B, float2 (&s)[D / 32][4][2], W& w,
-                                      const Strip& strip, int first, int m, bool update) {
-  constexpr int J = D / 32, NP = PLANES<T>;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r = lane & 15;
-  if (kDelta || kFresh) {
-    // S k and S q
-    constexpr int SUMMANDS = kFresh && NP == 1 ? 2 : 3;
-    float ck[2][4] = {}, cq[2][4] = {};
+// s[j][e][i]: row g + 8 i, columns 32 j + 8 t + 2 e, + 1 of a strip's state.
+template <int D>
+using State = float2[D / 32][4][2];
+
+// S k of up to 8 pending tokens (to dk) and S k, S q of up to 8 fresh ones (to df and dq).
+template <int D, bool kDelta, bool kPend, bool kFresh, typename T>
+__device__ __forceinline__ void read_state(const State<D>& s, const uint4 (*pk)[D / 32][32], const uint4 (*fk)[D / 32][32],
+                                           const uint4 (*fq)[D / 32][32], float* dk, float* df, float* dq) {
+  constexpr int NP = PLANES<T>;
+  constexpr bool kP = kPend && kDelta, kF = kFresh && kDelta;
+  constexpr int READ = NP == 1 ? 2 : 3, SUMMANDS = kP ? 3 : READ;     // of the state, for fresh tokens and at all
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float cp[2][4] = {}, cf[2][4] = {}, cq[2][4] = {};
+  const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      uint4 k[NP], q[NP];
+  for (int j = 0; j < D / 32; ++j) {
+    uint4 k[NP], f[NP], q[NP];
 #pragma unroll
-      for (int o = 0; o < NP; ++o) {
-        k[o] = tok.k[o][j][lane];
-        q[o] = kFresh ? qs[o][j][lane] : make_uint4(0, 0, 0, 0);
-      }
+    for (int o = 0; o < NP; ++o) {
+      k[o] = kP ? pk[o][j][lane] : none;
+      f[o] = kF ? fk[o][j][lane] : none;
+      q[o] = kFresh ? fq[o][j][lane] : none;
+    }
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float2 x[4] = {s[j][e][0], s[j][e][1], s[j][e + 1][0], s[j][e + 1][1]};
+    for (int e = 0; e < 4; e += 2) {
+      float2 x[4] = {s[j][e][0], s[j][e][1], s[j][e + 1][0], s[j][e + 1][1]};
 #pragma unroll
-        for (int l = 0; l < SUMMANDS; ++l) {
-          uint32_t a[4];
+      for (int l = 0; l < SUMMANDS; ++l) {
+        uint32_t a[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[i] = pack2(x[i]);
-            if (l + 1 < SUMMANDS) x[i] = sub2(x[i], unpack2(a[i]));
-          }
-          // (products of summands l and o below 2^-24 of the whole are left out)
+        for (int i = 0; i < 4; ++i) {
+          a[i] = pack2(x[i]);
+          if (l + 1 < SUMMANDS) x[i] = sub2(x[i], unpack2(a[i]));
+        }
+        // (products of summands l and o below 2^-24 of the whole are left out)
 #pragma unroll
-          for (int o = 0; o < NP && o + l < 3; ++o) {
-            const uint32_t k0 = e ? k[o].z : k[o].x, k1 = e ? k[o].w : k[o].y;
-            const uint32_t q0 = e ? q[o].z : q[o].x, q1 = e ? q[o].w : q[o].y;
-            if (NP > 1 && l + o == 0) {
-              if (kDelta) add_mma(ck[0], a, k0, k1);
-              if (kFresh) add_mma(cq[0], a, q0, q1);
-            } else {
-              constexpr bool kApart = NP > 1;     // the small products together
-              if (kDelta) mma_bf16(ck[kApart ? 1 : l & 1], a, k0, k1);
-              if (kFresh) mma_bf16(cq[kApart ? 1 : l & 1], a, q0, q1);
-            }
-          }
+        for (int o = 0; o < NP && o + l < 3; ++o) {
+          auto add = [&](float (&c)[2][4], const uint4& y) {
+            const uint32_t b0 = e ? y.z : y.x, b1 = e ? y.w : y.y;
+            if (NP > 1 && l + o == 0) add_mma(c[0], a, b0, b1);
+            else mma_bf16(c[NP > 1 ? 1 : l & 1], a, b0, b1);       // (FP32: the small products together)
+          };
+          if (kP) add(cp, k[o]);
+          if (kF && l < READ) add(cf, f[o]);
+          if (kFresh && l < READ) add(cq, q[o]);
         }
       }
     }
-    if (kDelta) {
-      *reinterpret_cast<float2*>(&w.dk[g * LD + 2 * t]) = make_float2(ck[0][0] + ck[1][0], ck[0][1] + ck[1][1]);
-      *reinterpret_cast<float2*>(&w.dk[(g + 8) * LD + 2 * t]) = make_float2(ck[0][2] + ck[1][2], ck[0][3] + ck[1][3]);
-    }
-    if (kFresh) {
-      *reinterpret_cast<float2*>(&w.dq[g * LD + 2 * t]) = make_float2(cq[0][0] + cq[1][0], cq[0][1] + cq[1][1]);
-      *reinterpret_cast<float2*>(&w.dq[(g + 8) * LD + 2 * t]) = make_float2(cq[0][2] + cq[1][2], cq[0][3] + cq[1][3]);
-    }
-    __syncwarp();
   }
-
-  // u of row r (both halves of the warp the same) and the outputs, column by column of A and B
-  auto load8 = [](float (&x)[GROUP], const float* from) {
-    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from);
-    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(from + 4);
+  auto store = [&](float* to, const float (&c)[2][4]) {
+    *reinterpret_cast<float2*>(&to[g * LD + 2 * t]) = make_float2(c[0][0] + c[1][0], c[0][1] + c[1][1]);
+    *reinterpret_cast<float2*>(&to[(g + 8) * LD + 2 * t]) = make_float2(c[0][2] + c[1][2], c[0][3] + c[1][3]);
   };
-  float u[GROUP], o[GROUP], c[GROUP];
-  if (kDelta) load8(u, &w.dk[r * LD]);
-  if (kFresh) load8(o, &w.dq[r * LD]);
-  load8(c, f.c);
+  if (kP) store(dk, cp);
+  if (kF) store(df, cf);
+  if (kFresh) store(dq, cq);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void load8(float (&x)[GROUP], const float* from) {
+  *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from);
+  *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(from + 4);
+}
+
+// u of row lane % 16 from S k (both halves of the warp the same); with queries the outputs, from S q to
+// `out` (a token every `step`), column by column of A and B.
+template <bool kDelta, bool kFresh, typename T>
+__device__ __forceinline__ void solve(float (&u)[GROUP], float (&o)[GROUP], const float (&c)[GROUP], const T (*v)[STRIP],
+                                      const float* beta, const float* A, const float* B, int m, T* out, int step,
+                                      float scale) {
+  const int lane = threadIdx.x & 31, r = lane & 15;
 #pragma unroll
   for (int i = 0; i < GROUP; ++i) {
-    const float v = to_f(tok.v[i][r]);
-    u[i] = kDelta ? fmaf(-c[i], u[i], v) : v;
+    const float x = to_f(v[i][r]);
+    u[i] = kDelta ? fmaf(-c[i], u[i], x) : x;
     if (kFresh) o[i] *= c[i];
-  }
-  T* out = nullptr;
-  const int step = p.H * D;
-  if (kFresh) {
-    const Place at = place_of<D>(p, strip.at);
-    out = reinterpret_cast<T*>(p.out) +
-          (((int64_t)at.n * p.fresh.rows + first) * p.H + at.h) * D + at.row0 + r;
   }
 #pragma unroll
   for (int j = 0; j < GROUP; ++j) {
     if (j >= m) break;
     float x[GROUP];
     if (kDelta) {
-      u[j] *= tok.beta[j];
-      load8(x, &f.A[j * GROUP]);
+      u[j] *= beta[j];
+      load8(x, &A[j * GROUP]);
 #pragma unroll
       for (int i = j + 1; i < GROUP; ++i) u[i] = fmaf(-x[i], u[j], u[i]);
     }
@@ -404,43 +448,49 @@ __device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& 
       load8(x, &B[j * GROUP]);
 #pragma unroll
       for (int i = j; i < GROUP; ++i) o[i] = fmaf(x[i], u[j], o[i]);
-      if (lane >> 4 == (j & 1)) *out = from_f<T>(p.scale * o[j]);
+      if (lane >> 4 == (j & 1)) *out = from_f<T>(scale * o[j]);
       out += step;
     }
   }
-  if (!update) {
-    __syncwarp();
-    return;
-  }
+}
 
-  // S = c_m S + sum_j R_mj u_j k_j^T
-  const float ce = c[GROUP - 1];
-  load8(c, f.rest);
+// u becomes the rows' weights R_mj u_j, a copy of them in shared memory.
+__device__ __forceinline__ void weights(float (&u)[GROUP], const float* rest, int m, float* to) {
+  const int lane = threadIdx.x & 31;
+  float x[GROUP];
+  load8(x, rest);
 #pragma unroll
-  for (int i = 0; i < GROUP; ++i) u[i] = i < m ? u[i] * c[i] : 0.f;
+  for (int i = 0; i < GROUP; ++i) u[i] = i < m ? u[i] * x[i] : 0.f;
   __syncwarp();
   if (lane < STRIP) {
-    *reinterpret_cast<float4*>(&w.dk[r * LD]) = make_float4(u[0], u[1], u[2], u[3]);
-    *reinterpret_cast<float4*>(&w.dk[r * LD + 4]) = make_float4(u[4], u[5], u[6], u[7]);
+    *reinterpret_cast<float4*>(&to[lane * LD]) = make_float4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<float4*>(&to[lane * LD + 4]) = make_float4(u[4], u[5], u[6], u[7]);
   }
   __syncwarp();
+}
+
+// S = c S + W K.
+template <int D, typename T>
+__device__ __forceinline__ void update(State<D>& s, float c, const float* W, const uint4 (*ks)[D / 32][32]) {
+  constexpr int NP = PLANES<T>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t a[4], last[2];     // rows g, g + 8: the first two summands as 16 columns, and the third
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float2 x = *reinterpret_cast<const float2*>(&w.dk[(g + 8 * i) * LD + 2 * t]);
+    float2 x = *reinterpret_cast<const float2*>(&W[(g + 8 * i) * LD + 2 * t]);
     a[i] = pack2(x);
     x = sub2(x, unpack2(a[i]));
     a[i + 2] = pack2(x);
     last[i] = pack2(sub2(x, unpack2(a[i + 2])));
   }
-  const float2 c2 = make_float2(ce, ce);
+  const float2 c2 = make_float2(c, c);
   const uint32_t ends[4] = {last[0], last[1], a[0], a[1]};     // the third summand, and the first once more
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
+  for (int j = 0; j < D / 32; ++j) {
     uint32_t pairs[NP][4];
 #pragma unroll
     for (int o = 0; o < NP; ++o) {
-      const uint4 k = tok.k[o][j][lane];
+      const uint4 k = ks[o][j][lane];
       pairs[o][0] = k.x; pairs[o][1] = k.y; pairs[o][2] = k.z; pairs[o][3] = k.w;
     }
 #pragma unroll
@@ -463,6 +513,98 @@ __device__ __forceinline__ void group(const DraftParams& p, const Tokens<D, T>& 
   __syncwarp();
 }
 
+// A strip's rows of the outputs from token `first` on, its lane's row.
+template <int D, typename T>
+__device__ __forceinline__ T* out_of(const DraftParams& p, unsigned strip, int first) {
+  const Place at = place_of<D>(p, strip);
+  return reinterpret_cast<T*>(p.out) +
+         (((int64_t)at.n * p.fresh.rows + first) * p.H + at.h) * D + at.row0 + (threadIdx.x & 15);
+}
+template <int D>
+__device__ __forceinline__ void store_state(const DraftParams& p, const Strip& at, const State<D>& s) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float* S = state_of<D>(p, at) + g * D + 8 * t;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) store32(S + i * 8 * D + j * 32, s[j][0][i], s[j][1][i], s[j][2][i], s[j][3][i]);
+}
+
+// Group b of up to 8 pending tokens, m of them: the state is advanced.
+template <int D, bool kDelta, typename T, typename W>
+__device__ __forceinline__ void pending(State<D>& s, W& w, int side, int b, int m) {
+  const int r = threadIdx.x & 15;
+  if (kDelta)
+    read_state<D, true, true, false, T>(s, w.pend[b].k, nullptr, nullptr, w.dk, nullptr, nullptr);
+  float u[GROUP], c[GROUP];
+  if (kDelta) load8(u, &w.dk[r * LD]);
+  load8(c, w.fp[b].c);
+  solve<kDelta, false, T>(u, u, c, w.v[side][0][b], w.pend[b].beta, w.fp[b].A, nullptr, m, nullptr, 0, 0.f);
+  weights(u, w.fp[b].rest, m, w.dk);
+  update<D, T>(s, c[GROUP - 1], w.dk, w.pend[b].k);
+}
+
+// The same for fresh ones: their outputs, and the state for the group behind them if there is one.
+template <int D, bool kDelta, typename T, typename W>
+__device__ __forceinline__ void fresh(const DraftParams& p, State<D>& s, W& w, unsigned strip, int side, int b, int first,
+                                      int m, bool more) {
+  const int r = threadIdx.x & 15;
+  read_state<D, kDelta, false, true, T>(s, nullptr, w.fresh[b].k, w.q[b], nullptr, w.dk, w.dq);
+  float u[GROUP], o[GROUP], c[GROUP];
+  if (kDelta) load8(u, &w.dk[r * LD]);
+  load8(o, &w.dq[r * LD]);
+  load8(c, w.ff[b].c);
+  solve<kDelta, true, T>(u, o, c, w.v[side][1][b], w.fresh[b].beta, w.ff[b].A, w.B[b], m, out_of<D, T>(p, strip, first),
+                         p.H * D, p.scale);
+  if (more) {
+    weights(u, w.ff[b].rest, m, w.dk);
+    update<D, T>(s, c[GROUP - 1], w.dk, w.fresh[b].k);
+  }
+  __syncwarp();
+}
+
+// A group of a pending tokens and one of m fresh ones in one pass over the state before both: with W the
+// pending rows' weights, S' x = c S x + W (K x) for the fresh k and q.
+template <int D, bool kDelta, typename T, typename W>
+__device__ __forceinline__ void both(const DraftParams& p, State<D>& s, W& w, const Strip& at, int side) {
+  const int r = threadIdx.x & 15;
+  read_state<D, kDelta, true, true, T>(s, w.pend[0].k, w.fresh[0].k, w.q[0], w.dk, w.df, w.dq);
+  float u[GROUP], c[GROUP];
+  if (kDelta) load8(u, &w.dk[r * LD]);
+  load8(c, w.fp[0].c);
+  solve<kDelta, false, T>(u, u, c, w.v[side][0][0], w.pend[0].beta, w.fp[0].A, nullptr, at.a, nullptr, 0, 0.f);
+  weights(u, w.fp[0].rest, at.a, w.dk);
+  const float ce = c[GROUP - 1];
+  update<D, T>(s, ce, w.dk, w.pend[0].k);
+  store_state<D>(p, at, s);
+
+  float f[GROUP], o[GROUP];
+  if (kDelta) load8(f, &w.df[r * LD]);
+  load8(o, &w.dq[r * LD]);
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) {
+    if (kDelta) f[i] *= ce;
+    o[i] *= ce;
+  }
+#pragma unroll
+  for (int j = 0; j < GROUP; ++j) {
+    if (j >= at.a) break;
+    float x[GROUP];
+    if (kDelta) {
+      load8(x, &w.X[0][j * GROUP]);
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) f[i] = fmaf(x[i], u[j], f[i]);
+    }
+    load8(x, &w.X[1][j * GROUP]);
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) o[i] = fmaf(x[i], u[j], o[i]);
+  }
+  load8(c, w.ff[0].c);
+  solve<kDelta, true, T>(f, o, c, w.v[side][1][0], w.fresh[0].beta, w.ff[0].A, w.B[0], at.m, out_of<D, T>(p, at.at, 0),
+                         p.H * D, p.scale);
+  __syncwarp();
+}
+
 template <int D, bool kDelta, typename T, int G>
 __global__ void __launch_bounds__(32, CTAS<D, T, G>) draft_kernel(const DraftParams p) {
   constexpr int J = D / 32;
@@ -476,9 +618,11 @@ __global__ void __launch_bounds__(32, CTAS<D, T, G>) draft_kernel(const DraftPar
   unsigned where = blockIdx.x * run;
   auto next_at = [&](unsigned x) { return (x + 1) & (run - 1) ? x + 1 : x + 1 - run + ahead; };
   Strip at = strip_at<D>(p, where, strips), next = strip_at<D>(p, next_at(where), strips);
-  // Copies are committed in the order state and pending tokens of a strip, fresh tokens of it, state of
-  // the next one, ...: each where the buffer is free, a phase or two ahead of its use.
-  fetch_state<D>(p, at, w);
+  // Copies are committed in the order of a strip's state and values, its pending tokens, its fresh
+  // tokens (the last two with the first strip of a run alone): each where the buffer is free, a phase or
+  // two ahead of its use.
+  int side = 0;
+  fetch_strip<D>(p, at, w, side);
   fetch_groups<D, kDelta, false>(p, w, at.at, at.a, true);
   fetch_groups<D, kDelta, true>(p, w, at.at, at.m, true);
   bool new_pend = true, new_fresh = true;   // the buffers hold tokens whose factors are not formed yet
@@ -488,15 +632,13 @@ __global__ void __launch_bounds__(32, CTAS<D, T, G>) draft_kernel(const DraftPar
     after.at = next_at(next.at);
     if ((after.at & (run - 1)) == 0) after = strip_at<D>(p, after.at, strips);
     if (at.m < p.fresh.rows) {
-      const Place pl = place_of<D>(p, where);
-      T* out = reinterpret_cast<T*>(p.out) +
-                           ((int64_t)pl.n * p.fresh.rows * p.H + pl.h) * D + pl.row0;
-      for (int i = at.m * STRIP + lane; i < p.fresh.rows * STRIP; i += 32)
-        out[(int64_t)(i / STRIP) * p.H * D + i % STRIP] = from_f<T>(0.f);
+      T* out = out_of<D, T>(p, where, at.m + (lane >> 4));
+      for (int i = at.m + (lane >> 4); i < p.fresh.rows; i += 2, out += 2 * p.H * D) *out = from_f<T>(0.f);
     }
-    const bool last = ((where + 1) & (run - 1)) == 0;
-    float2 s[J][4][2];
-    wait<1>();
+    const bool last = ((where + 1) & (run - 1)) == 0, one_pass = ONE_PASS<T, G> && at.a > 0 && at.m > 0;
+    State<D> s;
+    if (one_pass) wait<0>();
+    else wait<1>();
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -509,48 +651,59 @@ __global__ void __launch_bounds__(32, CTAS<D, T, G>) draft_kernel(const DraftPar
           s[j][e + 1][i] = make_float2(x.z, x.w);
         }
     __syncwarp();
-    fetch_state<D>(p, next, w);
-#pragma unroll 1
-    for (int first = 0; first < at.a; first += GROUP) {
-      const int i = first / GROUP % G, m = min(at.a - first, GROUP);
-      const bool late = first >= G * GROUP;        // a group that the buffers do not hold yet
-      if (late) {
-        fetch_tokens<D, kDelta, false>(p, p.pend, w.pend[i], w.q[0], at.at, first, at.a, true);
-        commit();
-        wait<0>();
-        __syncwarp();
+    fetch_strip<D>(p, next, w, side ^ 1);
+    if (one_pass) {
+      if constexpr (ONE_PASS<T, G>) {
+        if (new_pend) {      // (both kinds are new at once)
+          factors<D, kDelta, false>(p, w.pend[0], w.q[0], w.fp[0], w.B[0], at.at, at.a);
+          factors<D, kDelta, true>(p, w.fresh[0], w.q[0], w.ff[0], w.B[0], at.at, at.m);
+          cross_products<D, T>(w);
+        }
+        both<D, kDelta, T>(p, s, w, at, side);
+        new_pend = new_fresh = last;
+        fetch_groups<D, kDelta, false>(p, w, next.at, next.a, last);
+        fetch_groups<D, kDelta, true>(p, w, next.at, next.m, last);
       }
-      if (late || new_pend) factors<D, kDelta, false>(p, w.pend[i], w.q[0], w.fp[i], w.B[0], at.at, m);
-      group<D, kDelta, false>(p, w.pend[i], w.q[0], w.fp[i], w.B[0], s, w, at, first, m, true);
-    }
-    new_pend = last || at.a > G * GROUP;
-    fetch_groups<D, kDelta, false>(p, w, next.at, next.a, new_pend);
-    if (at.a > 0) {
-      float* S = state_of<D>(p, at) + g * D + 8 * t;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < J; ++j) store32(S + i * 8 * D + j * 32, s[j][0][i], s[j][1][i], s[j][2][i], s[j][3][i]);
-    }
-    wait<2>();
-    __syncwarp();
+    } else {
 #pragma unroll 1
-    for (int first = 0; first < at.m; first += GROUP) {
-      const int i = first / GROUP % G, m = min(at.m - first, GROUP);
-      const bool late = first >= G * GROUP;
-      if (late) {
-        fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh[i], w.q[i], at.at, first, at.m, true);
-        commit();
-        wait<0>();
-        __syncwarp();
+      for (int first = 0; first < at.a; first += GROUP) {
+        const int i = first / GROUP % G, m = min(at.a - first, GROUP);
+        const bool late = first >= G * GROUP;        // a group that the buffers do not hold yet
+        if (late) {
+          fetch_tokens<D, kDelta, false>(p, p.pend, w.pend[i], w.q[0], at.at, first, at.a);
+          fetch_values<D>(p, p.pend, w.v[side][0][i], at.at, first, at.a);
+          commit();
+          wait<0>();
+          __syncwarp();
+        }
+        if (late || new_pend) factors<D, kDelta, false>(p, w.pend[i], w.q[0], w.fp[i], w.B[0], at.at, m);
+        pending<D, kDelta, T>(s, w, side, i, m);
       }
-      if (late || new_fresh) factors<D, kDelta, true>(p, w.fresh[i], w.q[i], w.ff[i], w.B[i], at.at, m);
-      group<D, kDelta, true>(p, w.fresh[i], w.q[i], w.ff[i], w.B[i], s, w, at, first, m, first + GROUP < at.m);
+      new_pend = last || at.a > G * GROUP;
+      fetch_groups<D, kDelta, false>(p, w, next.at, next.a, new_pend);
+      if (at.a > 0) store_state<D>(p, at, s);
+      wait<2>();
+      __syncwarp();
+#pragma unroll 1
+      for (int first = 0; first < at.m; first += GROUP) {
+        const int i = first / GROUP % G, m = min(at.m - first, GROUP);
+        const bool late = first >= G * GROUP;
+        if (late) {
+          fetch_tokens<D, kDelta, true>(p, p.fresh, w.fresh[i], w.q[i], at.at, first, at.m);
+          fetch_values<D>(p, p.fresh, w.v[side][1][i], at.at, first, at.m);
+          commit();
+          wait<0>();
+          __syncwarp();
+        }
+        if (late || new_fresh) factors<D, kDelta, true>(p, w.fresh[i], w.q[i], w.ff[i], w.B[i], at.at, m);
+        fresh<D, kDelta, T>(p, s, w, at.at, side, i, first, m, first + GROUP < at.m);
+      }
+      new_fresh = last || at.m > G * GROUP;
+      fetch_groups<D, kDelta, true>(p, w, next.at, next.m, new_fresh);
     }
-    new_fresh = last || at.m > G * GROUP;
-    fetch_groups<D, kDelta, true>(p, w, next.at, next.m, new_fresh);
     at = next;
     next = after;
+    side ^= 1;
   }
 }
 
@@ -587,7 +740,7 @@ cudaError_t rule(const DraftParams& p, cudaStream_t st) {
 }
 // Two groups in shared memory where a sequence may have them: otherwise each strip would load its
 // tokens again (64 sequences of 32 heads, 16 + 16 tokens, delta rule and linear attention, BF16 92 and
-// 77 us against 86 and 69, FP32 267 and 171 against 245 and 148).
+// 77 us against 81 and 67, FP32 267 and 171 against 237 and 140).
 template <int D, typename T>
 cudaError_t groups(const DraftParams& p, cudaStream_t st) {
   return p.pend.rows > GROUP || p.fresh.rows > GROUP ? rule<D, T, 2>(p, st) : rule<D, T, 1>(p, st);

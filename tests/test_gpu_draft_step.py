@@ -117,14 +117,15 @@ def test_every_token_counts_where_no_numbers_are_given(T, dtype, D, delta):
 
 @pytest.mark.parametrize("delta", [False, True])
 def test_commit_then_draft_equals_both_in_one_call(delta):
-    """Committed by itself a state is, to the bit, what the draft step writes; the drafts from it
-    are the same to a rounding (of the state)."""
+    """Committed by itself a state is, to the bit, what the draft step writes.  The drafts of one
+    call come from the state before both: each way is within the tolerance of the exact outputs, so
+    they are within twice that of each other."""
     x = case(6, 5, 4, 4, 2, 128, BF16, delta, 3)
     y = dict(x, cache=x["cache"].clone())
     out = call(x)
     commit(y, y["pend"], y["num_pend"])
     assert torch.equal(x["cache"], y["cache"])
-    assert torch.equal(out, call(y, pending=None, num_pending=None))
+    assert err(out, f64(call(y, pending=None, num_pending=None))) <= 2 * TOL[BF16]
 
 
 @pytest.mark.parametrize("delta", [False, True])

@@ -257,3 +257,59 @@ def test_rounds_replayed_in_a_graph(delta):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and torch.equal(x["cache"], y["cache"])
+
+
+@pytest.mark.parametrize("delta", [False, True])
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 128)])
+@pytest.mark.parametrize("T,P", [(5, 4), (8, 8), (16, 12)])
+def test_rows_that_do_not_count_reach_nothing_in_short_calls(T, P, dtype, D, delta):
+    """Up to eight tokens of each kind, and up to sixteen: none counts, some do, all do."""
+    x = case(4, T, P, 2, 1, D, dtype, delta, 12)
+    x["num"] = torch.tensor([0, 3, T - 1, T], dtype=torch.int32, device="cuda")
+    x["num_pend"] = torch.tensor([P, 0, P - 1, 1], dtype=torch.int32, device="cuda")
+    ro, rc = want(x)
+    for t, num in ((x["new"], x["num"]), (x["pend"], x["num_pend"])):
+        for m in t:
+            for n in range(4):
+                t[m][n, num[n]:] = NAN if n % 2 else float("inf")
+    out = call(x, out=torch.full_like(x["new"]["v"], NAN))
+    check(x, out, ro, rc, dtype)
+
+
+@pytest.mark.parametrize("delta", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,P", [(6, 3), (6, 0), (14, 3)])
+def test_a_bad_draft_reaches_the_ones_behind_it_alone(T, P, dtype, delta):
+    """A NaN or an infinity in a draft: not the drafts before it, other heads' or sequences', nor the pool."""
+    for what, bad in (("k", NAN), ("v", float("inf")), ("q", NAN)):
+        x = case(3, T, P, 2, 2, 128, dtype, delta, 13)
+        x["num"] = None
+        y = dict(x, cache=x["cache"].clone(), new={m: t.clone() for m, t in x["new"].items()})
+        good = call(x)
+        y["new"][what][1, 4, 0, 7] = bad
+        out = call(y)
+        assert torch.equal(x["cache"], y["cache"])
+        same = torch.ones(3, T, 2, dtype=torch.bool)
+        same[1, 4:, 0] = False
+        assert torch.equal(out[same.cuda()], good[same.cuda()])
+        assert not torch.isfinite(out[1, 4, 0]).all()
+
+
+@pytest.mark.parametrize("delta", [False, True])
+def test_gates_at_their_ends_in_one_pass(delta):
+    x = case(3, 6, 5, 3, 3, 64, BF16, delta, 14)
+    ends = torch.tensor([0.0, -90.0, -float("inf")], device="cuda")
+    if delta:
+        for t in (x["new"], x["pend"]):
+            t["gate"][:] = ends
+            t["gate"][0, 1::2] = -0.5
+            t["beta"][1] = 1.0
+            t["beta"][2] = 0.0
+    else:
+        x["decay"] = ends
+    ro, rc = want(x, num=None, num_pend=None)
+    out = call(x, num_tokens=None, num_pending=None)
+    assert np.isfinite(f64(out)).all()
+    for h in range(3):
+        assert err(out[:, :, h], ro[:, :, h]) <= TOL[BF16]
+        assert err(x["cache"][x["idx"].long(), h], rc[x["idx"].tolist(), h]) <= TOL[F32]

@@ -59,7 +59,7 @@ template <typename T>
 constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;     // BF16 summands of a token
 // CTAs of one warp each on an SM; G groups of tokens in their shared memory.
 template <int D, typename T, int G>
-constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : G == 1 ? 16 : 13)
+constexpr int CTAS = sizeof(T) == 2 ? (D == 128 ? 8 : G == 1 ? 14 : 13)
                                     : (D == 128 ? (G == 1 ? 7 : 4) : G == 1 ? 12 : 7);
 // Whether pending and fresh tokens take one pass over the state (both()): at the most 8 of each, BF16.
 // (FP32 tokens, whose pass would keep more than fits in registers and shared memory: 91 -> 128 us.)

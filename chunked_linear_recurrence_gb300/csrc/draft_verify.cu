@@ -11,12 +11,12 @@
 // enough, but this machine does two FP64 operations a clock and SM, and a warp's scan in it takes
 // 1.5 us).
 //
-// Measured, 128 sequences, 7 drafts, 100003 tokens, FP32: 27 us (floor 12.9: one row of p, most of q)
+// Measured, 128 sequences, 7 drafts, 100003 tokens, FP32: 27 us (floor 12.7: one row of p, most of q)
 // of which the test 1.5, the stream 13 for the median CTA and 19 for the last one, the pick among
 // the warps 0.9, the search 3.5.  Copies of 16 bytes to shared memory against 4-byte loads to
 // registers (rows start at any multiple of an element): stream 22 -> 13-19.  Sums sent with st.async to a
-// barrier against a cluster barrier with release and acquire: 28.3 -> 26.9 us.  Five CTAs an SM:
-// 26.9; 3, 4, 6: 32.0, 27.5, 31-35 (six leave clusters for a second wave).
+// barrier against a cluster barrier with release and acquire: 28.3 -> 26.9 us.  Five CTAs of 8 warps an
+// SM: 26.9; 3, 4, 6: 32.0, 27.5, 31-35 (six leave clusters for a second wave).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -26,12 +26,16 @@
 namespace sfg {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int CTAS = 5;           // of an SM
+// CTAs of WARPS warps on an SM.  Long rows take 16 warps: fewer rows are under way at a time, and each
+// is read faster (100003 tokens, 600 sequences 125 us with 8 warps, 77 with 16; 128 sequences 27.0, 26.7;
+// of 131072 tokens 300 sequences 77, 61).  Short ones end sooner with 8 (32000, 2000 sequences 85, 104).
+template <int WARPS>
+constexpr int CTAS = WARPS == 8 ? 5 : 2;
+constexpr int LONG_ROW = 65536;
 constexpr int STAGES = 2;         // chunks of a warp's slice in flight
 constexpr int CHUNK_BYTES = 1024; // of a row
+constexpr int STAGE = STAGES * 2 * (CHUNK_BYTES + 16);
 constexpr int kSlice = 1024;      // elements that are worth a CTA
 
 constexpr int kNone = -1, kAgain = -2, kLate = -3;     // in place of the picked warp
@@ -183,10 +187,11 @@ __device__ __noinline__ Pick pick_lane(float2 mine, float2 before, float2 aim) {
   return {sum(before, shfl(excl, who)), who};
 }
 
-template <typename T>
-__global__ void __launch_bounds__(THREADS, CTAS) draft_verify_kernel(const VerifyParams p) {
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(const VerifyParams p) {
+  constexpr int THREADS = 32 * WARPS;
   constexpr int EACH = MAX_CLUSTER * WARPS / 32;     // warps of a cluster to a lane
-  __shared__ __align__(16) char stages[WARPS][STAGES * 2 * (CHUNK_BYTES + 16)];
+  extern __shared__ __align__(16) char stages[];     // STAGE bytes a warp
   __shared__ float2 sums[2][MAX_CLUSTER * WARPS];    // of every warp of the cluster, in order
   __shared__ float2 runs[WARPS];                     // of the picked slice
   __shared__ float2 found[2];                        // what lies before the picked warp, and the aim
@@ -257,9 +262,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) draft_verify_kernel(const Verif
 
   const int lo = (int)(p.V * me / workers), hi = (int)(p.V * (me + 1) / workers);
   for (int pass = 0;; ++pass) {
-    float2 s = how == kLess     ? sum_slice<T, kLess>(pr, qr, lo, hi, skip, stages[warp])
-               : how == kOthers ? sum_slice<T, kOthers>(pr, pr, lo, hi, skip, stages[warp])
-                                : sum_slice<T, kTarget>(pr, pr, lo, hi, skip, stages[warp]);
+    float2 s = how == kLess     ? sum_slice<T, kLess>(pr, qr, lo, hi, skip, stages + warp * STAGE)
+               : how == kOthers ? sum_slice<T, kOthers>(pr, pr, lo, hi, skip, stages + warp * STAGE)
+                                : sum_slice<T, kTarget>(pr, pr, lo, hi, skip, stages + warp * STAGE);
     s = warp_sum(s);
     __syncwarp();
     if (pass == 0) cluster_wait();
@@ -350,17 +355,24 @@ __global__ void __launch_bounds__(THREADS, CTAS) draft_verify_kernel(const Verif
   }
 }
 
-template <typename T>
+template <typename T, int WARPS>
 cudaError_t go(const VerifyParams& p, cudaStream_t st) {
   // as many CTAs to a sequence as one wave holds, each with a slice worth its start
   int ranks = MAX_CLUSTER;
-  const int wave = 152 * CTAS;
+  const int wave = 152 * CTAS<WARPS>;
   if (ranks > wave / p.N) ranks = wave / p.N;
   if (ranks > (p.V + kSlice - 1) / kSlice) ranks = (p.V + kSlice - 1) / kSlice;
   if (ranks < 1) ranks = 1;
+  auto kernel = draft_verify_kernel<T, WARPS>;
+  constexpr int bytes = WARPS * STAGE;
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.N * ranks));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(32 * WARPS);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -368,14 +380,18 @@ cudaError_t go(const VerifyParams& p, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, draft_verify_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <typename T>
+cudaError_t sized(const VerifyParams& p, cudaStream_t st) {
+  return p.V >= LONG_ROW ? go<T, 16>(p, st) : go<T, 8>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_draft_verify(const VerifyParams& p, bool bf16, cudaStream_t st) {
   if (p.N < 1) return cudaSuccess;
-  return bf16 ? go<__nv_bfloat16>(p, st) : go<float>(p, st);
+  return bf16 ? sized<__nv_bfloat16>(p, st) : sized<float>(p, st);
 }
 
 }  // namespace sfg

@@ -184,3 +184,12 @@ def test_replayed_in_a_graph_and_on_another_stream():
     got = call(e, stream=side)
     side.synchronize()
     check(e, got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("N,T,V", [(1, 3, 65536), (40, 2, 65537), (90, 1, 70001), (400, 1, 65535), (320, 1, 65543)])
+def test_long_rows(N, T, V, drafts, dtype):
+    """On either side of the length that takes more warps, with clusters of eight down to one."""
+    d = make(N, T, V, dtype, drafts, N + V)
+    check(d, call(d))

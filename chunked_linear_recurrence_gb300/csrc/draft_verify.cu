@@ -7,7 +7,7 @@
 //
 // The comparison and the search have to give what exact arithmetic gives, however the sums are
 // split: the test is one product in FP64 (exact for FP32 factors), and sums are two floats, a sum
-// and the rounding errors of all its additions and differences (48 bits; FP64 would be exact
+// and the rounding errors of its additions and differences (48 bits, kept over long rows by Sum; FP64 would be exact
 // enough, but this machine does two FP64 operations a clock and SM, and a warp's scan in it takes
 // 1.5 us).
 //
@@ -62,6 +62,42 @@ __device__ __forceinline__ float2 sum(float2 a, float2 b) {
   add(a, b);
   return a;
 }
+// The sum of a long run of non-negative weights.  add() rounds what the low parts gather to 24 bits, and
+// they grow with the number of additions (0.7 262144 times: off by 2^-18).  So up to 17 weights are added from
+// zero (m of them: off by m^2 2^-48 at the worst), such sums in runs of 64, the runs' sums in runs of 64, and
+// those, each with its low part brought below half a step of the high one: 64 x 2^-47 a level, 2^-38
+// in all.  (Against additions in one run 26.6 -> 26.9 us in the batch below.)
+template <bool kLong>      // (short rows, up to 65536 tokens: one level)
+struct Sum {
+  static constexpr int LEVELS = kLong ? 3 : 1;
+  float2 s[LEVELS] = {};
+  int n = 0;
+  static __device__ __forceinline__ void fold(float2& s, float2 w) {
+    add(s, w);
+    const float h = __fadd_rn(s.x, s.y);
+    s.y = __fsub_rn(s.y, __fsub_rn(h, s.x));
+    s.x = h;
+  }
+  __device__ __forceinline__ void operator+=(float2 w) {
+    fold(s[0], w);
+    if (kLong && (++n & 63) == 0) {
+      fold(s[1 % LEVELS], s[0]);
+      s[0] = make_float2(0.f, 0.f);
+      if ((n & 4095) == 0) {
+        fold(s[LEVELS - 1], s[1 % LEVELS]);
+        s[1 % LEVELS] = make_float2(0.f, 0.f);
+      }
+    }
+  }
+  __device__ __forceinline__ float2 total() const {
+    float2 t = s[0];
+    if (kLong && n >= 64) {
+      fold(t, s[1 % LEVELS]);
+      fold(t, s[LEVELS - 1]);
+    }
+    return t;
+  }
+};
 // a > b, of sums of non-negative weights; false with a NaN.
 __device__ __forceinline__ bool more(float2 a, float2 b) {
   const float ah = __fadd_rn(a.x, a.y), al = __fadd_rn(__fsub_rn(a.x, ah), a.y);
@@ -86,7 +122,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 // A warp's sum of the weights [lo, hi).  Rows start anywhere: whole chunks are copied in
 // 16-byte units from the unit that holds their first element to the one behind their last, which lie
 // within the slice because 16 bytes at least of it are left at either end; those ends are loaded.
-template <typename T, Weight how>
+template <typename T, Weight how, bool kLong>
 __device__ __forceinline__ float2 sum_slice(const T* p, const T* q, int lo, int hi, int skip, char* buf) {
   constexpr int E = 16 / sizeof(T), C = CHUNK_BYTES / sizeof(T);
   constexpr int ROW = CHUNK_BYTES + 16, UNITS = ROW / 16;
@@ -112,13 +148,15 @@ __device__ __forceinline__ float2 sum_slice(const T* p, const T* q, int lo, int 
   };
 #pragma unroll
   for (int c = 0; c < STAGES; ++c) fetch(c);
+  Sum<kLong> all;
   float2 s = make_float2(0.f, 0.f);
-  const int ends = hi - lo - chunks * C;
+  const int ends = hi - lo - chunks * C;       // (at most C + 2 E)
 #pragma unroll 4
   for (int t = lane; t < ends; t += 32) {
     const int y = lo + t + (t >= E ? chunks * C : 0);
     add(s, weight<how>(to_f(p[y]), how == kLess ? to_f(q[y]) : 0.f, y == skip));
   }
+  all += s;
   for (int c = 0; c < chunks; ++c) {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
     __syncwarp();
@@ -126,13 +164,15 @@ __device__ __forceinline__ float2 sum_slice(const T* p, const T* q, int lo, int 
     const T* a = reinterpret_cast<const T*>(at + ps) + lane;
     const T* b = reinterpret_cast<const T*>(at + ROW + qs) + lane;
     const int y = lo + E + c * C + lane;
+    s = weight<how>(to_f(a[0]), how == kLess ? to_f(b[0]) : 0.f, y == skip);
 #pragma unroll
-    for (int i = 0; i < C / 32; ++i)
+    for (int i = 1; i < C / 32; ++i)
       add(s, weight<how>(to_f(a[i * 32]), how == kLess ? to_f(b[i * 32]) : 0.f, y + i * 32 == skip));
+    all += s;
     __syncwarp();
     fetch(c + STAGES);
   }
-  return s;
+  return all.total();
 }
 
 // The CTAs of a cluster.  Arrivals order nothing by themselves: a release would wait for every store
@@ -190,6 +230,7 @@ __device__ __noinline__ Pick pick_lane(float2 mine, float2 before, float2 aim) {
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(const VerifyParams p) {
   constexpr int THREADS = 32 * WARPS;
+  constexpr bool kLong = WARPS > 8;
   constexpr int EACH = MAX_CLUSTER * WARPS / 32;     // warps of a cluster to a lane
   extern __shared__ __align__(16) char stages[];     // STAGE bytes a warp
   __shared__ float2 sums[2][MAX_CLUSTER * WARPS];    // of every warp of the cluster, in order
@@ -262,9 +303,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
 
   const int lo = (int)(p.V * me / workers), hi = (int)(p.V * (me + 1) / workers);
   for (int pass = 0;; ++pass) {
-    float2 s = how == kLess     ? sum_slice<T, kLess>(pr, qr, lo, hi, skip, stages + warp * STAGE)
-               : how == kOthers ? sum_slice<T, kOthers>(pr, pr, lo, hi, skip, stages + warp * STAGE)
-                                : sum_slice<T, kTarget>(pr, pr, lo, hi, skip, stages + warp * STAGE);
+    float2 s = how == kLess     ? sum_slice<T, kLess, kLong>(pr, qr, lo, hi, skip, stages + warp * STAGE)
+               : how == kOthers ? sum_slice<T, kOthers, kLong>(pr, pr, lo, hi, skip, stages + warp * STAGE)
+                                : sum_slice<T, kTarget, kLong>(pr, pr, lo, hi, skip, stages + warp * STAGE);
     s = warp_sum(s);
     __syncwarp();
     if (pass == 0) cluster_wait();
@@ -325,9 +366,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
     for (;;) {
       const int per = (to - from + THREADS - 1) / THREADS;
       const int b = min(from + (int)threadIdx.x * per, to), e = min(b + per, to);
-      float2 mine = make_float2(0.f, 0.f);
-#pragma unroll 8
-      for (int y = b; y < e; ++y) add(mine, one(pr, qr, y, skip, how));
+      Sum<kLong> run;
+      for (int y = b; y < e; y += 8) {
+        float2 s = one(pr, qr, y, skip, how);
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+          if (y + i < e) add(s, one(pr, qr, y + i, skip, how));
+        run += s;
+      }
+      float2 mine = run.total();
       const float2 r = warp_sum(mine);
       if (lane == 0) runs[warp] = r;
       __syncthreads();

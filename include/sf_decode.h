@@ -100,8 +100,10 @@ sf_status sf_linattn_commit(const sf_gdn_shape *shape, const void *k, const void
  *                  the number to commit of [last token, draft 0, draft 1, ...].  -1: a
  *                  kernel's bounded internal wait expired (2 s; there is no workspace to
  *                  say so in)
- * A negative weight or a NaN counts as zero.  Products and sums are exact to 2^-40 or
- * better, so that a result does not depend on how the sums are split.
+ * A negative weight or a NaN counts as zero.  The test's products are exact.  The draw's sums
+ * are exact to 2^-38 of the weights' sum at every V, for draft probabilities that are not
+ * negative and sums from 2^-100 on, so that a draw depends on how they are split only where
+ * u_T times the sum lies that near a border between two tokens.
  * N >= 0, T >= 0 (T = 0: one token is drawn from p_0), V >= 1.  Outputs overlap no input.
  * ---------------------------------------------------------------------- */
 typedef struct {

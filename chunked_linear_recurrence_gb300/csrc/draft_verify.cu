@@ -325,8 +325,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
       if (__any_sync(0xffffffffu, late)) pick = kLate;
       else if (total.x == 0.f && how != kTarget) pick = kAgain;
       else if (total.x > 0.f && isfinite(total.x) && isfinite(total.y)) {
-        const float hi_u = __fmul_rn(final_u, total.x);
-        const float2 aim = make_float2(hi_u, __fmaf_rn(final_u, total.y, __fmaf_rn(final_u, total.x, -hi_u)));
+        const float ut = final_u < -1.f ? -1.f : final_u;     // (-1 draws as any below 0, but its aim is finite)
+        const float hi_u = __fmul_rn(ut, total.x);
+        const float2 aim = make_float2(hi_u, __fmaf_rn(ut, total.y, __fmaf_rn(ut, total.x, -hi_u)));
         const Pick lanes = pick_lane(all, make_float2(0.f, 0.f), aim);
         // the same rule over the lane's own
         int at = -1;

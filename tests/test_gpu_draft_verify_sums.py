@@ -49,3 +49,15 @@ def test_weights_of_all_sizes(V):
     u = torch.rand(N, generator=torch.Generator().manual_seed(V))
     got = draws(w.float(), u)
     check(got, u, lambda y: int(run[y]), int(run[-1]))
+
+
+@pytest.mark.parametrize("V", [3000, 70001])
+def test_uniforms_far_outside_their_range(V):
+    """Whatever lies below 0 draws the first token with weight, from 1 on the last one."""
+    import chunked_linear_recurrence_gb300 as sf
+    u = [-float("inf"), -3e38, -1e30, -1e-45, 1.0, 3e38, float("inf")]
+    target = torch.zeros(len(u), 1, V, device="cuda")
+    target[:, :, 1234:1300] = 1.0
+    tokens, num = sf.sf_draft_verify(target, torch.zeros(len(u), 0, dtype=torch.int32, device="cuda"),
+                                     torch.tensor(u, device="cuda")[:, None])
+    assert tokens[:, 0].tolist() == [1234] * 4 + [1299] * 3 and num.tolist() == [1] * len(u)

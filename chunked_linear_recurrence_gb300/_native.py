@@ -36,7 +36,7 @@ EXPORTS = ("sf_last_error", "sf_version", "sf_gdn_fwd_workspace", "sf_gdn_chunk_
            "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd_workspace", "sf_qk_norm_rope_bwd",
            "sf_testing_inject_linattn_timeout",
            "sf_gdn_draft_step", "sf_linattn_draft_step", "sf_gdn_commit", "sf_linattn_commit",
-           "sf_draft_verify", "sf_state_workspace", "sf_state_copy", "sf_state_fork",
+           "sf_draft_verify", "sf_testing_inject_verify_timeout", "sf_state_workspace", "sf_state_copy", "sf_state_fork",
            "sf_state_compact")
 
 
@@ -147,13 +147,15 @@ def load(path: str = LIB_PATH):
         lib.sf_gdn_commit.argtypes = [sp, vp, vp, vp, vp, vp, vp, I, vp, vp]
         lib.sf_linattn_commit.argtypes = [sp, vp, vp, vp, vp, vp, I, vp, vp]
         lib.sf_draft_verify.argtypes = [vs, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.sf_testing_inject_verify_timeout.argtypes = [I]
         lib.sf_state_workspace.argtypes = [I, I]
         lib.sf_state_workspace.restype = sz
         lib.sf_state_copy.argtypes = [pp, vp, vp, I, vp]
         lib.sf_state_fork.argtypes = [pp, vp, I, vp, I, vp, vp, vp, sz, vp]
         lib.sf_state_compact.argtypes = [pp, vp, I, vp, vp, vp, sz, vp]
         for f in ("sf_gdn_draft_step", "sf_linattn_draft_step", "sf_gdn_commit",
-                  "sf_linattn_commit", "sf_draft_verify", "sf_state_copy", "sf_state_fork",
+                  "sf_linattn_commit", "sf_draft_verify",
+                  "sf_testing_inject_verify_timeout", "sf_state_copy", "sf_state_fork",
                   "sf_state_compact", "sf_linattn_chunk_fwd", "sf_linattn_paged_chunk_fwd", "sf_linattn_chunk_bwd",
                   "sf_linattn_step", "sf_gdn_step", "sf_qk_norm_rope_fwd", "sf_qk_norm_rope_bwd",
                   "sf_gdn_chunk_fwd", "sf_gdn_paged_chunk_fwd", "sf_gdn_segment_summary",

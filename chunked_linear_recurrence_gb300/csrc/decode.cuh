@@ -42,6 +42,8 @@ struct VerifyParams {
   int32_t* count;
   int N, T, V;
   int64_t target_seq, target_row, draft_seq, draft_row;
+  uint64_t wait_ns;     // after which an internal wait gives up
+  bool drop;            // failure-detection testing: the last CTA of a sequence sends the first one no sums
 };
 cudaError_t launch_draft_verify(const VerifyParams& p, bool bf16, cudaStream_t st);
 

@@ -309,9 +309,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
     s = warp_sum(s);
     __syncwarp();
     if (pass == 0) cluster_wait();
-    if (lane < ranks) send(&sums[pass][me], &arrived[pass], lane, s);
+    if (lane < ranks && !(p.drop && lane == 0 && rank == ranks - 1)) send(&sums[pass][me], &arrived[pass], lane, s);
     if (warp == 0) {
-      const bool late = !tc::mbar_wait(&arrived[pass], 0);
+      const bool late = !tc::mbar_wait(&arrived[pass], 0, p.wait_ns);
       __syncwarp();
       float2 v[EACH], all = make_float2(0.f, 0.f);
 #pragma unroll
@@ -353,9 +353,18 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
       how = kTarget;
       continue;
     }
-    if (picked == kNone || picked == kLate) {
-      if (threadIdx.x == 0 && (rank == 0 || picked == kLate)) tokens[a] = -1;
-      if (threadIdx.x == 0 && picked == kLate) p.count[n] = -1;
+    if (picked == kNone) {
+      if (rank == 0 && threadIdx.x == 0) tokens[a] = -1;
+      return;
+    }
+    if (picked == kLate) {
+      // A CTA that is behind still sends its sums here: this one outlives all that have not left (their
+      // waits are bounded too, and those that have left are not waited for), and what they sent last.
+      // Only then does it say so: the first CTA may not have written its number before.
+      cluster_arrive();
+      cluster_wait();
+      if (warp == 0) tc::mbar_wait(&arrived[pass], 0, p.wait_ns);
+      if (threadIdx.x == 0) p.count[n] = -1;
       return;
     }
     if (picked / WARPS != rank) return;

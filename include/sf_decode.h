@@ -99,7 +99,7 @@ sf_status sf_linattn_commit(const sf_gdn_shape *shape, const void *k, const void
  *   num_tokens     int32 [N]: accepted drafts + 1 (0 for padding): the tokens gained, and
  *                  the number to commit of [last token, draft 0, draft 1, ...].  -1: a
  *                  kernel's bounded internal wait expired (2 s; there is no workspace to
- *                  say so in)
+ *                  say so in), and the sequence's tokens are undefined
  * A negative weight or a NaN counts as zero.  The test's products are exact.  The draw's sums
  * are exact to 2^-38 of the weights' sum at every V, for draft probabilities that are not
  * negative and sums from 2^-100 on, so that a draw depends on how they are split only where
@@ -116,6 +116,12 @@ sf_status sf_draft_verify(const sf_verify_shape *shape, const void *target_probs
                           const int32_t *draft_tokens, const float *uniforms,
                           const void *draft_probs, const int32_t *num_drafts, int32_t *tokens,
                           int32_t *num_tokens, sf_stream_t stream);
+
+/* Failure-detection testing only, as sf_testing_inject_timeout: in the next sf_draft_verify on
+ * the calling host thread the last CTA of every sequence sends the first one no sums, and
+ * every internal wait gives up after that many milliseconds (1 .. 100).  num_tokens then
+ * reads -1 (0 for padding); later calls are normal. */
+sf_status sf_testing_inject_verify_timeout(int milliseconds);
 
 /* ------------------------------------------------------------------------
  * The pool's slots.  The layers of a model keep one cache each, and a slot's states lie

@@ -54,9 +54,9 @@ typedef struct {
  *   state_cache, num_slots, state_indices: as sf_gdn_step.  Padding gives zero rows.
  * 16-byte aligned tensors, a 32-byte aligned state_cache; out overlaps no input.  The
  * tokens go through the chunk form (dot products with the state before eight tokens, and a
- * triangular solve over them).  States are computed in FP32; FP32 outputs too.  Outputs of
- * BF16 tokens are rounded from FP32 sums over the state's first 16 bits.  The state left is
- * to the bit that of sf_*_commit; outputs are the same to their rounding.
+ * triangular solve over them), in FP32; BF16 outputs are rounded from that.  The state left
+ * is to the bit that of sf_*_commit, and outputs are those of the step behind it to FP32's
+ * rounding of the terms that they are summed from.
  * ---------------------------------------------------------------------- */
 sf_status sf_gdn_draft_step(const sf_gdn_shape *shape, const void *q, const void *k, const void *v,
                             const float *gate, const float *beta, const int32_t *num_tokens,

@@ -227,16 +227,18 @@ def sf_state_copy(caches, src, dst, stream=None):
                                 _stream(stream, device)))
 
 
-def _plan_args(pool, device, reserved, rows, out, ws):
+def _plan_args(pool, device, reserved, rows, out, ws, inputs):
+    """``inputs``: (address, bytes) of the indices."""
     slots = pool.num_slots
     reserved = _addr("reserved", reserved, (slots,), torch.bool)
     if out is None:
         out = torch.empty(rows, dtype=_I32, device=device)
-        to = out.data_ptr()
-        if ws is None and slots <= 4096 and rows <= 1024 and pool.num_caches <= 64:
-            return out, None, (reserved, to, None, 0)        # (none is used)
+        to, inputs = out.data_ptr(), ()
     else:
         to = _addr("out", out, (rows,), _I32)
+    if (ws is None and slots <= 4096 and rows <= 1024 and pool.num_caches <= 64
+            and not any(to < at + n and at < to + rows * 4 for at, n in inputs)):
+        return out, None, (reserved, to, None, 0)            # (none is used)
     if ws is None:
         ws = torch.empty(_workspace_bytes(slots, rows), dtype=torch.uint8, device=device)
     else:
@@ -253,7 +255,7 @@ def sf_state_fork(caches, state_indices, parents, reserved=None, out=None, ws=No
     pool, device = _state_pool(caches)
     idx, N = _vector("state_indices", state_indices)
     par, M = _vector("parents", parents)
-    out, ws, tail = _plan_args(pool, device, reserved, M, out, ws)
+    out, ws, tail = _plan_args(pool, device, reserved, M, out, ws, ((idx, N * 4), (par, M * 4)))
     _check(load().sf_state_fork(ctypes.byref(pool), idx, N, par, M, *tail, _stream(stream, device)))
     return out
 
@@ -264,6 +266,6 @@ def sf_state_compact(caches, state_indices, reserved=None, out=None, ws=None, st
     for ``reserved`` slots (bool [num_slots]), which stay.  Returns where each is then, int32 [N]."""
     pool, device = _state_pool(caches)
     idx, N = _vector("state_indices", state_indices)
-    out, ws, tail = _plan_args(pool, device, reserved, N, out, ws)
+    out, ws, tail = _plan_args(pool, device, reserved, N, out, ws, ((idx, N * 4),))
     _check(load().sf_state_compact(ctypes.byref(pool), idx, N, *tail, _stream(stream, device)))
     return out

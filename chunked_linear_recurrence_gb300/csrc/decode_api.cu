@@ -85,10 +85,21 @@ sf_status check_pool(const sf_state_pool* p, const char* fn) {
   return SF_OK;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x && y && x < y + nb && y < x + na;
+}
+
 // A plan over `rows` rows, then the copies it gives.
 sf_status planned(const char* fn, const sf_state_pool* pool, sfg::PoolPlan p, int rows, void* ws, size_t ws_bytes,
                   sf_stream_t stream) {
   p.num_slots = pool->num_slots;
+  // (a compaction's row is written when its own old index has been read, others' may not have been; a fork
+  // reads all indices before, and reserved between its rows)
+  const size_t out = (size_t)rows * 4;
+  if (p.parents ? overlap(p.out, out, p.reserved, (size_t)p.num_slots)
+                : p.out != p.idx && overlap(p.out, out, p.idx, (size_t)p.N * 4))
+    return report(SF_ERR_INVALID_ARG, "%s: new_indices overlaps an input that it is not", fn);
   if (sfg::pool_move_needs_workspace(p, pool->num_caches)) {
     const size_t need = sf_state_workspace(pool->num_slots, rows);
     if (!ws || !aligned16(ws) || ws_bytes < need)

@@ -149,8 +149,8 @@ sf_status sf_testing_inject_verify_timeout(int milliseconds);
  *   them, are brought into the lowest L that are not reserved: those above, in order, move
  *   into the gaps, in order.  new_indices[n]: where state_indices[n] is now (padding and
  *   reserved slots stay).  Sequences that name one slot go on sharing it.
- * new_indices may be state_indices (or parents).  Slots that nothing moves into keep
- * what they held.
+ * new_indices may be state_indices (or parents), and overlaps no input otherwise.  Slots that
+ * nothing moves into keep what they held.
  * ---------------------------------------------------------------------- */
 #define SF_MAX_SLOTS (1 << 18)
 

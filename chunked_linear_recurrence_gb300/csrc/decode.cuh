@@ -55,14 +55,20 @@ struct PoolPlan {
   const uint8_t* reserved;    // or NULL
   int32_t* out;
   int N, M, num_slots;
-  // workspace
+  // workspace, or NULL
   int32_t* src;               // [rows] pairs to copy ...
   int32_t* dst;
   int32_t* count;             // ... and how many
   int32_t* first;             // fork: [num_slots]
 };
-// The plan, and its copies in every cache: in one launch that needs no workspace, or in two.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x && y && x < y + nb && y < x + na;
+}
+// The plan, and its copies in every cache: in one launch that needs no workspace, or, if the plan has
+// one, in two.  Some plans need it, others are faster with it.
 bool pool_move_needs_workspace(const PoolPlan& plan, int num_caches);
+bool pool_move_likes_workspace(const PoolPlan& plan);
 cudaError_t launch_pool_move(const PoolPlan& plan, int num_caches, void* const* caches,
                              const size_t* slot_bytes, cudaStream_t st);
 // Copies of src[i] to dst[i], i < *count (or rows where count is NULL), in every cache.

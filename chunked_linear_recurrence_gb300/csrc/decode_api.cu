@@ -10,6 +10,7 @@
 using sfg::aligned16;
 using sfg::check_heads;
 using sfg::cuda_status;
+using sfg::overlap;
 using sfg::report;
 
 namespace {
@@ -85,11 +86,6 @@ sf_status check_pool(const sf_state_pool* p, const char* fn) {
   return SF_OK;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-  return x && y && x < y + nb && y < x + na;
-}
-
 // A plan over `rows` rows, then the copies it gives.
 sf_status planned(const char* fn, const sf_state_pool* pool, sfg::PoolPlan p, int rows, void* ws, size_t ws_bytes,
                   sf_stream_t stream) {
@@ -100,10 +96,11 @@ sf_status planned(const char* fn, const sf_state_pool* pool, sfg::PoolPlan p, in
   if (p.parents ? overlap(p.out, out, p.reserved, (size_t)p.num_slots)
                 : p.out != p.idx && overlap(p.out, out, p.idx, (size_t)p.N * 4))
     return report(SF_ERR_INVALID_ARG, "%s: new_indices overlaps an input that it is not", fn);
-  if (sfg::pool_move_needs_workspace(p, pool->num_caches)) {
-    const size_t need = sf_state_workspace(pool->num_slots, rows);
-    if (!ws || !aligned16(ws) || ws_bytes < need)
-      return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn, need);
+  const size_t need = sf_state_workspace(pool->num_slots, rows);
+  const bool needs = sfg::pool_move_needs_workspace(p, pool->num_caches), given = ws && aligned16(ws) && ws_bytes >= need;
+  if (needs && !given)
+    return report(SF_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 16-byte aligned", fn, need);
+  if (needs || (given && sfg::pool_move_likes_workspace(p))) {
     char* at = static_cast<char*>(ws);
     p.count = reinterpret_cast<int32_t*>(at);
     p.src = reinterpret_cast<int32_t*>(at + 256);

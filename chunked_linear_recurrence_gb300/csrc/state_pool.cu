@@ -5,14 +5,16 @@
 // slots of every cache.  The plan works on bitmaps of the slots in shared memory with a running
 // count a word, so that "the r-th free slot" is a search and not a scan; its results depend on the
 // order of rows and slots alone.  In small pools every CTA of the copy makes the plan for itself, in one
-// launch and without a workspace's traffic; where it would hold too much shared memory, or where
-// the new indices go where the old ones are read, one CTA makes it in a launch before.
+// launch and without a workspace's traffic; where that takes longer, where it would hold too much shared
+// memory, or where the new indices go where the old ones are read, one CTA makes it in a launch before.
 //
 // The copies are bound by memory.  Measured: 59 slots in 8 caches of 1 MB (990 MB) 148 us, 99 % of
 // the copy rate; a compaction's 48 (805 MB) 129 us, 92 %; one slot copied three times 4.7 us.  Pieces of
 // 16 KB, 16 CTAs of 128 threads an SM; 8 KB 153, 133; 32 KB, 8 CTAs of 256 threads 150, 130; the last
-// turn's pieces cut for the CTAs that have none 150, 130.  In two launches the smallest fork takes
-// 6.5 us.
+// turn's pieces cut for the CTAs that have none 150, 130.  One launch and two, forks of slots of 64 KB: 9
+// slots and 4 rows 3.8 and 6.0 us; 160 and 96 4.4, 6.3; 300 and 150 5.9, 6.4; 600 and 300 8.3, 7.4; 1000 and
+// 400 17.0, 8.4; 4096 and 1024 32.7, 12.0 (128 threads plan for longer, and with 25 KB eight CTAs fit an SM,
+// so that a second wave plans again); of 1 MB: 96 slots 9.4, 9.4, 300 29.3, 29.7, 600 55.7, 53.4, 1000 75.8, 69.2.
 #include "common.cuh"
 #include "decode.cuh"
 #include "linattn.cuh"
@@ -25,7 +27,8 @@ constexpr int COPY = 128;
 constexpr int PIECE = 1024;           // 16-byte units of a piece: 16 KB
 constexpr int CACHES = 64;            // caches of a copy launch
 constexpr int CTAS = 152 * 16;
-constexpr int FUSED_SLOTS = 4096, FUSED_ROWS = 1024;   // of a plan in every CTA: 28 KB
+constexpr int FUSED_SLOTS = 4096, FUSED_ROWS = 1024;   // of a plan in every CTA, at the most: 25 KB ...
+constexpr int FAST_SLOTS = 512, FAST_ROWS = 256;       // ... and where it is faster than a launch of its own
 
 // Exclusive prefix sums over a CTA's TH threads, and their total.
 template <int TH>
@@ -285,11 +288,6 @@ int copy_grid(const CopyParams& p) {
   const int64_t work = (int64_t)p.rows * p.pieces[p.caches];
   return (int)(work < CTAS ? work : CTAS);
 }
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-  return x && y && x < y + nb && y < x + na;
-}
-
 }  // namespace
 
 cudaError_t launch_pool_copy(int num_slots, int num_caches, void* const* caches,
@@ -318,11 +316,15 @@ bool pool_move_needs_workspace(const PoolPlan& plan, int num_caches) {
          overlap(plan.out, out, plan.reserved, (size_t)plan.num_slots);
 }
 
+bool pool_move_likes_workspace(const PoolPlan& plan) {
+  return plan.num_slots > FAST_SLOTS || (plan.parents ? plan.M : plan.N) > FAST_ROWS;
+}
+
 cudaError_t launch_pool_move(const PoolPlan& plan, int num_caches, void* const* caches,
                              const size_t* slot_bytes, cudaStream_t st) {
   const int words = (plan.num_slots + 31) / 32, rows = plan.parents ? plan.M : plan.N;
   const size_t bits = (size_t)words * 4 * (plan.parents ? 2 : 4), out = (size_t)rows * 4;
-  if (!pool_move_needs_workspace(plan, num_caches)) {
+  if (!plan.count) {
     const CopyParams p = copy_params(plan.num_slots, num_caches, caches, slot_bytes, rows);
     const int grid = copy_grid(p);
     const size_t bytes = bits + 2 * out + (plan.parents ? (size_t)plan.num_slots * 4 : 0);

@@ -132,9 +132,10 @@ sf_status sf_testing_inject_verify_timeout(int milliseconds);
  *                  written, moved or given out: states kept for later, sequences that
  *                  state_indices does not name.  Slot 0 is never used (padding's index).
  *   workspace      sf_state_workspace(num_slots, rows) bytes, 16-byte aligned, no initial
- *                  contents; rows: M of a fork, N of a compaction.  Not used, and may be
- *                  NULL, for up to 4096 slots, 1024 rows and 64 caches, unless
- *                  new_indices overlaps an input.
+ *                  contents; rows: M of a fork, N of a compaction.  May be NULL for up to
+ *                  4096 slots, 1024 rows and 64 caches, unless new_indices overlaps an
+ *                  input.  Up to 512 slots and 256 rows of those do not use it; larger
+ *                  plans are faster with it.
  * An index outside [1, num_slots) is padding.  num_slots <= SF_MAX_SLOTS.
  *
  * sf_state_copy: dst[i] becomes a copy of src[i] (int32 [M] device each); a pair with

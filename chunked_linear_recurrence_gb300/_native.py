@@ -147,7 +147,7 @@ def load(path: str = LIB_PATH):
         lib.sf_gdn_commit.argtypes = [sp, vp, vp, vp, vp, vp, vp, I, vp, vp]
         lib.sf_linattn_commit.argtypes = [sp, vp, vp, vp, vp, vp, I, vp, vp]
         lib.sf_draft_verify.argtypes = [vs, vp, vp, vp, vp, vp, vp, vp, vp]
-        lib.sf_testing_inject_verify_timeout.argtypes = [I]
+        lib.sf_testing_inject_verify_timeout.argtypes = []
         lib.sf_state_workspace.argtypes = [I, I]
         lib.sf_state_workspace.restype = sz
         lib.sf_state_copy.argtypes = [pp, vp, vp, I, vp]

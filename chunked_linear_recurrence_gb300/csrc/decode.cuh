@@ -42,8 +42,7 @@ struct VerifyParams {
   int32_t* count;
   int N, T, V;
   int64_t target_seq, target_row, draft_seq, draft_row;
-  uint64_t wait_ns;     // after which an internal wait gives up
-  bool drop;            // failure-detection testing: the last CTA of a sequence sends the first one no sums
+  bool give_up;         // failure-detection testing: the first CTA of a sequence gives up its wait at once
 };
 cudaError_t launch_draft_verify(const VerifyParams& p, bool bf16, cudaStream_t st);
 

@@ -17,7 +17,7 @@ namespace {
 
 static_assert(sfg::DRAFT_MAX == SF_DRAFT_MAX && sfg::MAX_SLOTS == SF_MAX_SLOTS, "limits of the header");
 
-thread_local int g_wait_ms = 0;   // sf_testing_inject_verify_timeout
+thread_local bool g_give_up = false;   // sf_testing_inject_verify_timeout
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -187,16 +187,13 @@ sf_status sf_draft_verify(const sf_verify_shape* shape, const void* target_probs
   p.N = s.N; p.T = s.T; p.V = s.V;
   p.target_seq = s.target_seq; p.target_row = s.target_row;
   p.draft_seq = s.draft_seq; p.draft_row = s.draft_row;
-  p.drop = g_wait_ms > 0;
-  p.wait_ns = p.drop ? g_wait_ms * 1000000ull : 2000000000ull;
-  g_wait_ms = 0;
+  p.give_up = g_give_up;
+  g_give_up = false;
   return cuda_status(sfg::launch_draft_verify(p, s.dtype == SF_BF16, reinterpret_cast<cudaStream_t>(stream)), fn);
 }
 
-sf_status sf_testing_inject_verify_timeout(int milliseconds) {
-  if (milliseconds < 1 || milliseconds > 100)
-    return report(SF_ERR_INVALID_ARG, "sf_testing_inject_verify_timeout: need 1 <= milliseconds <= 100");
-  g_wait_ms = milliseconds;
+sf_status sf_testing_inject_verify_timeout(void) {
+  g_give_up = true;
   return SF_OK;
 }
 

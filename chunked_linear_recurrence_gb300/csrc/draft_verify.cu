@@ -33,6 +33,7 @@ constexpr int MAX_CLUSTER = 8;
 template <int WARPS>
 constexpr int CTAS = WARPS == 8 ? 5 : 2;
 constexpr int LONG_ROW = 65536;
+constexpr int DEEP_ROW = 1 << 20;  // longer ones than that sum in three levels
 constexpr int STAGES = 2;         // chunks of a warp's slice in flight
 constexpr int CHUNK_BYTES = 1024; // of a row
 constexpr int STAGE = STAGES * 2 * (CHUNK_BYTES + 16);
@@ -66,10 +67,10 @@ __device__ __forceinline__ float2 sum(float2 a, float2 b) {
 // they grow with the number of additions (0.7 262144 times: off by 2^-18).  So up to 17 weights are added from
 // zero (m of them: off by m^2 2^-48 at the worst), such sums in runs of 64, the runs' sums in runs of 64, and
 // those, each with its low part brought below half a step of the high one: 64 x 2^-47 a level, 2^-38
-// in all.  (Against additions in one run 26.6 -> 26.9 us in the batch below.)
-template <bool kLong>      // (short rows, up to 65536 tokens: one level)
+// in all.  (Against additions in one run 26.5 -> 26.7 us in the batch below.)
+template <bool kDeep>      // (up to 2^20 tokens one level does: 256 chunks a lane)
 struct Sum {
-  static constexpr int LEVELS = kLong ? 3 : 1;
+  static constexpr int LEVELS = kDeep ? 3 : 1;
   float2 s[LEVELS] = {};
   int n = 0;
   static __device__ __forceinline__ void fold(float2& s, float2 w) {
@@ -80,7 +81,7 @@ struct Sum {
   }
   __device__ __forceinline__ void operator+=(float2 w) {
     fold(s[0], w);
-    if (kLong && (++n & 63) == 0) {
+    if (kDeep && (++n & 63) == 0) {
       fold(s[1 % LEVELS], s[0]);
       s[0] = make_float2(0.f, 0.f);
       if ((n & 4095) == 0) {
@@ -91,7 +92,7 @@ struct Sum {
   }
   __device__ __forceinline__ float2 total() const {
     float2 t = s[0];
-    if (kLong && n >= 64) {
+    if (kDeep && n >= 64) {
       fold(t, s[1 % LEVELS]);
       fold(t, s[LEVELS - 1]);
     }
@@ -122,7 +123,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 // A warp's sum of the weights [lo, hi).  Rows start anywhere: whole chunks are copied in
 // 16-byte units from the unit that holds their first element to the one behind their last, which lie
 // within the slice because 16 bytes at least of it are left at either end; those ends are loaded.
-template <typename T, Weight how, bool kLong>
+template <typename T, Weight how, bool kDeep>
 __device__ __forceinline__ float2 sum_slice(const T* p, const T* q, int lo, int hi, int skip, char* buf) {
   constexpr int E = 16 / sizeof(T), C = CHUNK_BYTES / sizeof(T);
   constexpr int ROW = CHUNK_BYTES + 16, UNITS = ROW / 16;
@@ -148,7 +149,7 @@ __device__ __forceinline__ float2 sum_slice(const T* p, const T* q, int lo, int 
   };
 #pragma unroll
   for (int c = 0; c < STAGES; ++c) fetch(c);
-  Sum<kLong> all;
+  Sum<kDeep> all;
   float2 s = make_float2(0.f, 0.f);
   const int ends = hi - lo - chunks * C;       // (at most C + 2 E)
 #pragma unroll 4
@@ -227,10 +228,9 @@ __device__ __noinline__ Pick pick_lane(float2 mine, float2 before, float2 aim) {
   return {sum(before, shfl(excl, who)), who};
 }
 
-template <typename T, int WARPS>
+template <typename T, int WARPS, bool kDeep>
 __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(const VerifyParams p) {
   constexpr int THREADS = 32 * WARPS;
-  constexpr bool kLong = WARPS > 8;
   constexpr int EACH = MAX_CLUSTER * WARPS / 32;     // warps of a cluster to a lane
   extern __shared__ __align__(16) char stages[];     // STAGE bytes a warp
   __shared__ float2 sums[2][MAX_CLUSTER * WARPS];    // of every warp of the cluster, in order
@@ -303,15 +303,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
 
   const int lo = (int)(p.V * me / workers), hi = (int)(p.V * (me + 1) / workers);
   for (int pass = 0;; ++pass) {
-    float2 s = how == kLess     ? sum_slice<T, kLess, kLong>(pr, qr, lo, hi, skip, stages + warp * STAGE)
-               : how == kOthers ? sum_slice<T, kOthers, kLong>(pr, pr, lo, hi, skip, stages + warp * STAGE)
-                                : sum_slice<T, kTarget, kLong>(pr, pr, lo, hi, skip, stages + warp * STAGE);
+    float2 s = how == kLess     ? sum_slice<T, kLess, kDeep>(pr, qr, lo, hi, skip, stages + warp * STAGE)
+               : how == kOthers ? sum_slice<T, kOthers, kDeep>(pr, pr, lo, hi, skip, stages + warp * STAGE)
+                                : sum_slice<T, kTarget, kDeep>(pr, pr, lo, hi, skip, stages + warp * STAGE);
     s = warp_sum(s);
     __syncwarp();
     if (pass == 0) cluster_wait();
-    if (lane < ranks && !(p.drop && lane == 0 && rank == ranks - 1)) send(&sums[pass][me], &arrived[pass], lane, s);
+    if (lane < ranks) send(&sums[pass][me], &arrived[pass], lane, s);
     if (warp == 0) {
-      const bool late = !tc::mbar_wait(&arrived[pass], 0, p.wait_ns);
+      const bool late = (p.give_up && rank == 0) || !tc::mbar_wait(&arrived[pass], 0);
       __syncwarp();
       float2 v[EACH], all = make_float2(0.f, 0.f);
 #pragma unroll
@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
       // Only then does it say so: the first CTA may not have written its number before.
       cluster_arrive();
       cluster_wait();
-      if (warp == 0) tc::mbar_wait(&arrived[pass], 0, p.wait_ns);
+      for (int b = 0; b < 2; ++b)
+        for (int i = 0; i < 1000 && !tc::mbar_try_wait(&arrived[b], 0); ++i) {}
       if (threadIdx.x == 0) p.count[n] = -1;
       return;
     }
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
     for (;;) {
       const int per = (to - from + THREADS - 1) / THREADS;
       const int b = min(from + (int)threadIdx.x * per, to), e = min(b + per, to);
-      Sum<kLong> run;
+      Sum<kDeep> run;
       for (int y = b; y < e; y += 8) {
         float2 s = one(pr, qr, y, skip, how);
 #pragma unroll
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS<WARPS>) draft_verify_kernel(c
   }
 }
 
-template <typename T, int WARPS>
+template <typename T, int WARPS, bool kDeep>
 cudaError_t go(const VerifyParams& p, cudaStream_t st) {
   // as many CTAs to a sequence as one wave holds, each with a slice worth its start
   int ranks = MAX_CLUSTER;
@@ -420,7 +421,7 @@ cudaError_t go(const VerifyParams& p, cudaStream_t st) {
   if (ranks > wave / p.N) ranks = wave / p.N;
   if (ranks > (p.V + kSlice - 1) / kSlice) ranks = (p.V + kSlice - 1) / kSlice;
   if (ranks < 1) ranks = 1;
-  auto kernel = draft_verify_kernel<T, WARPS>;
+  auto kernel = draft_verify_kernel<T, WARPS, kDeep>;
   constexpr int bytes = WARPS * STAGE;
   if (bytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -441,7 +442,7 @@ cudaError_t go(const VerifyParams& p, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t sized(const VerifyParams& p, cudaStream_t st) {
-  return p.V >= LONG_ROW ? go<T, 16>(p, st) : go<T, 8>(p, st);
+  return p.V > DEEP_ROW ? go<T, 16, true>(p, st) : p.V >= LONG_ROW ? go<T, 16, false>(p, st) : go<T, 8, false>(p, st);
 }
 
 }  // namespace

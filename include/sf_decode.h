@@ -118,10 +118,9 @@ sf_status sf_draft_verify(const sf_verify_shape *shape, const void *target_probs
                           int32_t *num_tokens, sf_stream_t stream);
 
 /* Failure-detection testing only, as sf_testing_inject_timeout: in the next sf_draft_verify on
- * the calling host thread the last CTA of every sequence sends the first one no sums, and
- * every internal wait gives up after that many milliseconds (1 .. 100).  num_tokens then
- * reads -1 (0 for padding); later calls are normal. */
-sf_status sf_testing_inject_verify_timeout(int milliseconds);
+ * the calling host thread the first CTA of every sequence gives up its wait for the others'
+ * sums at once.  num_tokens then reads -1 (0 for padding); later calls are normal. */
+sf_status sf_testing_inject_verify_timeout(void);
 
 /* ------------------------------------------------------------------------
  * The pool's slots.  The layers of a model keep one cache each, and a slot's states lie

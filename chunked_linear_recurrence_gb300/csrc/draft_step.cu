@@ -25,8 +25,8 @@
 // summands (24 bits), and the update's sum is formed apart and added to the state by one FP32
 // multiply-add with rounding to nearest, so that the state has no bias of the tensor core's sums.
 // (Drafts that read two summands, 16 bits, lose what cancels: where a token takes the place of one 2^13
-// times larger, outputs were off by 2.0e-2 for 1.1e-3.  128 sequences, 5 + 5 tokens 93.4 -> 94.4 us, 16 + 16
-// tokens below 81 -> 87.)  FP32 tokens are split into three summands themselves, and the six products
+// times larger, outputs were off by 2.0e-2 for 1.1e-3.  128 sequences, 5 + 5 tokens 93.4 -> 94.3 us, 64 with
+// 16 + 16 79 -> 86.)  FP32 tokens are split into three summands themselves, and the six products
 // down to 2^-24 are formed everywhere.
 //
 // A warp takes four strips of a head in a row, with their tokens and what those are to each other in
@@ -34,17 +34,17 @@
 // through the pool as one window.
 //
 // Bound by memory, 4 V K bytes read and as many written (if a token was accepted), and by the chain
-// of a strip's steps (1250 instructions with both kinds of tokens, two warps to a scheduler).  Measured,
-// K = 128: 128 sequences of 32 heads, 5 + 5 tokens 93.5 us (537 MB, 5.85 TB/s, 86 % of the copy rate),
-// 256 of 16 heads, 8 + 8 tokens by linear attention 96 us, a commit of 8 tokens 92 us; one sequence
+// of a strip's steps (1270 instructions with both kinds of tokens, two warps to a scheduler).  Measured,
+// K = 128: 128 sequences of 32 heads, 5 + 5 tokens 94.3 us (537 MB, 5.8 TB/s, 85 % of the copy rate),
+// 256 of 16 heads, 8 + 8 tokens by linear attention 96.5 us, a commit of 8 tokens 92 us, 5 tokens with
+// nothing pending 56 us and by linear attention 52 (of 40 for the states' bytes); one sequence
 // of 16 heads 4.5 us.  The same movement without any tokens' work takes 88 us.  What it came
 // from: FP32 pipes with shared-memory tokens 156, 148, 120 us; states loaded where they are used
 // 164, 149, 113; copied ahead 158, 146, 121; factors and tokens of a run of strips kept 100, 114,
 // 102; whole rows to a copy and whole lines to a store, eight warps an SM and a window 96-98, 98, 92;
-// one pass for both kinds of tokens 93.5, 96.  Twelve warps an SM (168 registers, some spilled) 98, 109,
-// 95; runs of one strip 115, 102, 88; summands by truncation and byte permutes instead of
-// conversions: the same.  FP32 tokens, 64 sequences of 32 heads: 5 + 5 tokens 88 us, a commit of
-// 8 52 us (on the FP32 pipes 85, 68; floor 41).
+// one pass for both kinds of tokens 93.5, 96; the state read in three summands 94.3, 96.5.  With two:
+// twelve warps an SM (168 registers, some spilled) 98, 109, 95; runs of one strip 115, 102, 88; summands by
+// truncation and byte permutes instead of conversions: the same.  FP32 tokens, 64 sequences of 32 heads: 5 + 5 tokens 88 us, a commit of 8 51 us (on the FP32 pipes 85, 68; floor 41).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -711,8 +711,11 @@ __global__ void __launch_bounds__(32, CTAS<D, T, G>) draft_kernel(const DraftPar
 template <int D, bool kDelta, typename T, int G>
 cudaError_t go(DraftParams p, cudaStream_t st) {
   const int strips = p.N * p.H * (D / STRIP);
-  // Strips in a row save work (128 sequences of 32 heads, 5 + 5 tokens: runs of one 115 us, two 102,
-  // four 96), but the CTAs take whole runs in turns.
+  // Strips in a row save work, but the CTAs take whole runs in turns.  The costs of a strip in runs of one
+  // and two, to those in runs of four, are those of 5 + 5 BF16 tokens, K = 128 (1.17, 1.02 by other sizes; 115
+  // us, 102, 96 as first measured).  Others differ, measured with 64 or 96 sequences of 32 heads: 16 + 16 tokens
+  // 1.15, 1.07; linear attention 1.09, 0.98; drafts alone 1.10, 0.99; commits 0.97, 0.96; K = 64 1.16, 1.01; FP32
+  // 1.43, 1.17, and 1.65, 1.29 with two groups.
   constexpr int kSlots = 152 * CTAS<D, T, G>;
   double best = 0;
   for (int run = 1; run <= RUN; run *= 2) {
@@ -740,8 +743,8 @@ cudaError_t rule(const DraftParams& p, cudaStream_t st) {
   return p.decay ? go<D, false, T, G>(p, st) : go<D, true, T, G>(p, st);
 }
 // Two groups in shared memory where a sequence may have them: otherwise each strip would load its
-// tokens again (64 sequences of 32 heads, 16 + 16 tokens, delta rule and linear attention, BF16 92 and
-// 77 us against 81 and 67, FP32 267 and 171 against 237 and 140).
+// tokens again (64 sequences of 32 heads, 16 + 16 tokens, delta rule and linear attention, BF16 93 and
+// 75 us against 86 and 66, FP32 268 and 164 against 222 and 136).
 template <int D, typename T>
 cudaError_t groups(const DraftParams& p, cudaStream_t st) {
   return p.pend.rows > GROUP || p.fresh.rows > GROUP ? rule<D, T, 2>(p, st) : rule<D, T, 1>(p, st);

@@ -11,12 +11,16 @@
 // enough, but this machine does two FP64 operations a clock and SM, and a warp's scan in it takes
 // 1.5 us).
 //
-// Measured, 128 sequences, 7 drafts, 100003 tokens, FP32: 27 us (floor 12.7: one row of p, most of q)
-// of which the test 1.5, the stream 13 for the median CTA and 19 for the last one, the pick among
-// the warps 0.9, the search 3.5.  Copies of 16 bytes to shared memory against 4-byte loads to
-// registers (rows start at any multiple of an element): stream 22 -> 13-19.  Sums sent with st.async to a
-// barrier against a cluster barrier with release and acquire: 28.3 -> 26.9 us.  Five CTAs of 8 warps an
-// SM: 26.9; 3, 4, 6: 32.0, 27.5, 31-35 (six leave clusters for a second wave).
+// Measured, 128 sequences, 7 drafts, 100003 tokens, FP32: 26.8 us (floor 13.0: one row of p, most of q)
+// of which, by the clock of its CTAs (two of 16 warps a sequence), the test 1.5, the stream 13 for the
+// median CTA and 18 for the last one, the sums' way and the pick among the warps 2, the search 3.5.
+// Rows of BF16 23 us, of looked-up drafts 22 and (BF16) 20.  Of many rows
+// instructions take more: 600 sequences with 2 drafts 76 us (floor 46), 45 M instructions, 59 % of the issue slots;
+// in BF16 59 us (floor 23), 42 M, 72 %.
+// With 8 warps: copies of 16 bytes to shared memory against 4-byte loads to registers (rows start at any
+// multiple of an element) stream 22 -> 13-19; sums sent with st.async to a barrier against a cluster barrier
+// with release and acquire 28.3 -> 26.9 us; five CTAs an SM 26.9, 3, 4, 6: 32.0, 27.5, 31-35 (six leave
+// clusters for a second wave).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -28,8 +32,9 @@ namespace {
 
 constexpr int MAX_CLUSTER = 8;
 // CTAs of WARPS warps on an SM.  Long rows take 16 warps: fewer rows are under way at a time, and each
-// is read faster (100003 tokens, 600 sequences 125 us with 8 warps, 77 with 16; 128 sequences 27.0, 26.7;
-// of 131072 tokens 300 sequences 77, 61).  Short ones end sooner with 8 (32000, 2000 sequences 85, 104).
+// is read faster (600 sequences of 100003 tokens 117 us with 8 warps, 73 with 16; of 65536 72, 53; 128
+// sequences the same either way).  Short ones end sooner with 8 (32000 tokens, 600 sequences 32, 36; 2000 82,
+// 104).  Of 50000 tokens 600 sequences take 51, 44, 2000 128, 118: many rows could change over from there on.
 template <int WARPS>
 constexpr int CTAS = WARPS == 8 ? 5 : 2;
 constexpr int LONG_ROW = 65536;

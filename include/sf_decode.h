@@ -95,7 +95,8 @@ sf_status sf_linattn_commit(const sf_gdn_shape *shape, const void *k, const void
  *                  draws the first token with weight, from 1 on and as a NaN the last)
  *   num_drafts     int32 [N] or NULL (T); at most T of them count; negative: padding
  *   tokens         int32 [N,T+1]: the accepted drafts, the drawn token, then -1.  The
- *                  drawn token is -1 where the weights' sum is not positive and finite.
+ *                  drawn token is -1 where the weights' sum is not positive or not finite
+ *                  in FP32.
  *   num_tokens     int32 [N]: accepted drafts + 1 (0 for padding): the tokens gained, and
  *                  the number to commit of [last token, draft 0, draft 1, ...].  -1: a
  *                  kernel's bounded internal wait expired (2 s; there is no workspace to

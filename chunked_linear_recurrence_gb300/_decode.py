@@ -236,7 +236,7 @@ def _plan_args(pool, device, reserved, rows, out, ws, inputs):
         to, inputs = out.data_ptr(), ()
     else:
         to = _addr("out", out, (rows,), _I32)
-    if (ws is None and slots <= 512 and rows <= 256 and pool.num_caches <= 64
+    if (ws is None and slots <= 4096 and rows <= 256 and pool.num_caches <= 64
             and not any(to < at + n and at < to + rows * 4 for at, n in inputs)):
         return out, None, (reserved, to, None, 0)            # (none is used)
     if ws is None:

@@ -12,9 +12,10 @@
 // the copy rate; a compaction's 48 (805 MB) 129 us, 92 %; one slot copied three times 4.7 us.  Pieces of
 // 16 KB, 16 CTAs of 128 threads an SM; 8 KB 153, 133; 32 KB, 8 CTAs of 256 threads 150, 130; the last
 // turn's pieces cut for the CTAs that have none 150, 130.  One launch and two, forks of slots of 64 KB: 9
-// slots and 4 rows 3.8 and 6.0 us; 160 and 96 4.4, 6.3; 300 and 150 5.9, 6.4; 600 and 300 8.3, 7.4; 1000 and
-// 400 17.0, 8.4; 4096 and 1024 32.7, 12.0 (128 threads plan for longer, and with 25 KB eight CTAs fit an SM,
-// so that a second wave plans again); of 1 MB: 96 slots 9.4, 9.4, 300 29.3, 29.7, 600 55.7, 53.4, 1000 75.8, 69.2.
+// slots and 4 rows 3.8 and 6.0 us; 160 and 96 4.4, 6.3; 4096 and 64 4.8, 6.4; 300 and 150 5.9, 6.4; 4096 and 256 8.0,
+// 7.9; 400 and 300 8.6, 7.5; 1000 and 400 17.0, 8.4; 4096 and 1024 32.7, 12.0 (128 threads plan for longer,
+// and with 25 KB eight CTAs fit an SM, so that a second wave plans again); of 1 MB: 96 slots, 48 rows 9.4, 9.4;
+// 300 and 150 29.3, 29.7; 600 and 300 55.7, 53.4; 1000 and 400 75.8, 69.2.
 #include "common.cuh"
 #include "decode.cuh"
 #include "linattn.cuh"
@@ -28,7 +29,7 @@ constexpr int PIECE = 1024;           // 16-byte units of a piece: 16 KB
 constexpr int CACHES = 64;            // caches of a copy launch
 constexpr int CTAS = 152 * 16;
 constexpr int FUSED_SLOTS = 4096, FUSED_ROWS = 1024;   // of a plan in every CTA, at the most: 25 KB ...
-constexpr int FAST_SLOTS = 512, FAST_ROWS = 256;       // ... and where it is faster than a launch of its own
+constexpr int FAST_ROWS = 256;                         // ... and where it is faster than a launch of its own
 
 // Exclusive prefix sums over a CTA's TH threads, and their total.
 template <int TH>
@@ -317,7 +318,7 @@ bool pool_move_needs_workspace(const PoolPlan& plan, int num_caches) {
 }
 
 bool pool_move_likes_workspace(const PoolPlan& plan) {
-  return plan.num_slots > FAST_SLOTS || (plan.parents ? plan.M : plan.N) > FAST_ROWS;
+  return (plan.parents ? plan.M : plan.N) > FAST_ROWS;
 }
 
 cudaError_t launch_pool_move(const PoolPlan& plan, int num_caches, void* const* caches,

@@ -134,8 +134,7 @@ sf_status sf_testing_inject_verify_timeout(void);
  *   workspace      sf_state_workspace(num_slots, rows) bytes, 16-byte aligned, no initial
  *                  contents; rows: M of a fork, N of a compaction.  May be NULL for up to
  *                  4096 slots, 1024 rows and 64 caches, unless new_indices overlaps an
- *                  input.  Up to 512 slots and 256 rows of those do not use it; larger
- *                  plans are faster with it.
+ *                  input.  Up to 256 rows of those do not use it; more are faster with it.
  * An index outside [1, num_slots) is padding.  num_slots <= SF_MAX_SLOTS.
  *
  * sf_state_copy: dst[i] becomes a copy of src[i] (int32 [M] device each); a pair with

@@ -20,6 +20,16 @@ def made(monkeypatch):
     return got
 
 
+@pytest.mark.parametrize("rows,used", [(256, False), (257, True)])
+def test_many_rows_have_a_workspace(made, rows, used):
+    import chunked_linear_recurrence_gb300 as sf
+    cache, idx = torch.zeros(4096, 8), torch.zeros(rows, dtype=torch.int32)
+    for call in (lambda: sf.sf_state_fork(cache, idx[:3], idx), lambda: sf.sf_state_compact(cache, idx)):
+        made.clear()
+        call()
+        assert (torch.uint8 in made) == used
+
+
 @pytest.mark.parametrize("out", ["none", "apart", "beside", "indices", "parents", "overlapping"])
 @pytest.mark.parametrize("slots", [40, 5000])
 def test_a_workspace_is_made_where_one_is_used(made, out, slots):

@@ -22,7 +22,7 @@ def without(caches, fn, *args):
     assert getattr(sf.load(), fn)(ctypes.byref(pool), *at, None, 0, stream) == 0
 
 
-@pytest.mark.parametrize("slots,rows", [(512, 256), (513, 256), (512, 257), (700, 90), (3000, 1000), (4096, 1024)])
+@pytest.mark.parametrize("slots,rows", [(512, 256), (4096, 256), (512, 257), (700, 90), (3000, 1000), (4096, 1024)])
 @pytest.mark.parametrize("caches", [1, 3])
 def test_both_forms_give_the_same(slots, rows, caches):
     import chunked_linear_recurrence_gb300 as sf
